@@ -332,6 +332,159 @@ flce_status flce_selftest_wait_timeout(int32_t* err_word, int32_t* result,
                                        double budget_s, void* stream);
 
 /* ------------------------------------------------------------------------
+ * The norm of a set of gradients taken together, and clipping by it: what a
+ * training step does with the gradients of the losses above and of the rest
+ * of its model.
+ *
+ *   norm = (sum |g|^p)^(1/p) over every element of every gradient (p = 1, 2),
+ *          or max |g| (inf)
+ *   dst  = g * min(1, max_norm / (norm + eps))        (a NaN norm gives NaN)
+ *
+ * Sums are held in 64 bits above 64-element parts, with no 32-bit overflow or
+ * underflow in between; the result is the same in every run. Products are
+ * rounded once, to dst's type. Each gradient is `rows` runs of `cols`
+ * contiguous elements, `src_pitch` (`dst_pitch`) elements from run to run; a
+ * dense tensor of any shape is one run. Tensors may start at any address that
+ * their element type allows; 16-byte aligned runs are fastest.
+ */
+typedef enum flce_norm { FLCE_NORM_L1 = 1, FLCE_NORM_L2 = 2, FLCE_NORM_INF = 3 } flce_norm;
+
+typedef struct flce_grad {
+  const void* src;
+  void* dst;           /* may be src; ignored by flce_grad_norm */
+  int64_t rows, cols;  /* either may be 0: nothing there */
+  int64_t src_pitch, dst_pitch;
+  int32_t src_dtype;   /* flce_dtype */
+  int32_t dst_dtype;   /* src_dtype or FLCE_F32 */
+} flce_grad;
+
+/* Bytes of device workspace that both calls need for `count` gradients. */
+size_t flce_grad_workspace_size(int64_t count);
+
+/* norm_out: fp32 device scalar. `grads` is a host array, read during the call
+ * only, of any length. No gradients: the norm is 0. */
+flce_status flce_grad_norm(const flce_grad* grads, int64_t count, int32_t norm,
+                           float* norm_out, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/* The same, and dst = clipped src for every gradient. Where the factor is 1
+ * and every dst is its src, nothing is written. Memory that the call writes
+ * must not overlap what it reads or writes for another gradient
+ * (FLCE_ERR_INVALID_ARG). max_norm and eps are finite and >= 0. */
+flce_status flce_grad_clip(const flce_grad* grads, int64_t count, int32_t norm,
+                           float max_norm, float eps, float* norm_out,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * One step of a beam search over the vocabulary.
+ *
+ *   s_bkv = beam_scores_bk + z_bkv - log sum_u e^{z_bku}
+ *
+ * and, for each prompt b, the `candidates` largest of its K * V scores, best
+ * first; equal scores in the order of k * V + v. The comparison is in 64 bits
+ * on row sums of 32-bit exponentials; the scores are rounded to fp32.
+ *   - allowed (bytes, nullable): a token whose byte is 0 counts as z = -inf,
+ *     whatever its logit holds: it is neither offered nor in the sum.
+ *   - finished (bytes, nullable): a beam whose byte is not 0 offers itself
+ *     alone, with its score unchanged, under pad_token; its logits are not read.
+ *   - A beam with score -inf, or with no token left, offers nothing.
+ *   - Places that nothing fills hold score -inf, parent 0 and pad_token.
+ *   - An allowed logit that is NaN or +inf, or a beam score that is, sets
+ *     FLCE_DEVERR_NOT_FINITE, and that beam offers nothing.
+ * Rows of logits are V contiguous elements; strides are in elements (bytes of
+ * `allowed`), 0 where an axis shares one row.
+ */
+#define FLCE_DEVERR_NOT_FINITE 4
+#define FLCE_DEVERR_PARENT_RANGE 8
+
+typedef struct flce_beam_problem {
+  int64_t batch, beams, v;     /* batch >= 0; 1 <= beams <= 1024 */
+  int64_t candidates;          /* 1 to 256 */
+  int64_t stride_batch, stride_beam;
+  int64_t allowed_stride_batch, allowed_stride_beam;
+  int64_t pad_token;           /* in [0, v) */
+  int32_t dtype;               /* of the logits */
+  int32_t reserved;            /* 0 */
+} flce_beam_problem;
+
+/* Bytes of device workspace flce_beam_select() needs (0 if `p` is invalid). */
+size_t flce_beam_select_workspace_size(const flce_beam_problem* p);
+
+/* beam_scores [batch][beams]; finished [batch][beams]; the outputs
+ * [batch][candidates]. */
+flce_status flce_beam_select(const flce_beam_problem* p, const void* logits,
+                             const float* beam_scores, const uint8_t* finished,
+                             const uint8_t* allowed, float* scores_out,
+                             int64_t* parents_out, int64_t* tokens_out,
+                             int32_t* err_word, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/* In-place reordering of what a beam search keeps for each beam (caches,
+ * token histories, scores):
+ *
+ *   state[b * beams + j] = state[b * beams + parents[b * beams + j]]
+ *
+ * for every state, as if all were read before any is written. A state is
+ * batch * beams beams, beam_stride bytes apart, each of size[0] x ... x
+ * size[3] runs of run_bytes contiguous bytes, stride[d] bytes apart. Its
+ * elements do not overlap, and no two states do. 16-byte aligned runs and
+ * strides are fastest. A parent outside [0, beams) sets
+ * FLCE_DEVERR_PARENT_RANGE and leaves its beam as it is. beams <= 64. */
+typedef struct flce_beam_state {
+  void* data;
+  int64_t beam_stride;
+  int64_t size[4];   /* 1 where unused */
+  int64_t stride[4];
+  int64_t run_bytes;
+} flce_beam_state;
+
+flce_status flce_beam_reorder(const flce_beam_state* states, int64_t count,
+                              const int64_t* parents, int64_t batch,
+                              int64_t beams, int32_t* err_word, void* stream);
+
+/* ------------------------------------------------------------------------
+ * A linear layer in 8-bit integers (a head for answering, not for training).
+ *
+ *   scale_i = max_h |x_ih| / 127,  q_ih = round(x_ih / scale_i)   (halves to even)
+ *   lin_ij  = scale_i * weight_scale_j * sum_h q_ih * w_jh + bias_j
+ *   u_ij    = logit_scale * lin_ij
+ *   out_ij  = softcap * tanh(u_ij / softcap)   if softcap > 0, else u_ij
+ *
+ * A row of zeros has scale 0; a row that holds a NaN or an infinity gives
+ * NaN. Products are exact, sums are held in 32 bits: the integer paths are
+ * exact, and the tensor-core path rounds only sums beyond 2^24. Rows lie
+ * `pitch` elements apart.
+ */
+typedef enum flce_qdtype { FLCE_Q_I8 = 3 } flce_qdtype; /* beside flce_dtype, for x */
+
+/* x [n][h] -> q [n][h] (int8) and scale [n] (fp32). */
+flce_status flce_quantize_rows(const void* x, int32_t dtype, int64_t n, int64_t h,
+                               int64_t x_pitch, int8_t* q, int64_t q_pitch,
+                               float* scale, void* stream);
+
+typedef struct flce_qproblem {
+  int64_t n, h, v;                      /* n, v >= 0; 1 <= h <= 131071 */
+  int64_t x_pitch, weight_pitch, out_pitch;
+  int32_t x_dtype;     /* an flce_dtype (quantised within the call), or FLCE_Q_I8 */
+  int32_t out_dtype;   /* flce_dtype of out */
+  int32_t bias_dtype;  /* flce_dtype of bias */
+  int32_t has_bias;    /* 0 or 1 */
+  float logit_scale;   /* finite */
+  float softcap;       /* > 0 enables it */
+} flce_qproblem;
+
+/* Bytes of device workspace flce_qlinear() needs (0 if `p` is invalid). */
+size_t flce_qlinear_workspace_size(const flce_qproblem* p);
+
+/* x_scale [n]: with FLCE_Q_I8 only, else NULL. weight int8 [v][h] with
+ * weight_scale fp32 [v]. Weight rows that start at multiples of 16 bytes are
+ * read as they are; others are first laid out in the workspace. */
+flce_status flce_qlinear(const flce_qproblem* p, const void* x, const float* x_scale,
+                         const int8_t* weight, const float* weight_scale,
+                         const void* bias, void* out, int32_t* err_word,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
  * Per-kernel timing, for measurement tools (not part of the method; the
  * pages describe no profiler). While enabled, every kernel launch made by
  * flce_forward / flce_backward on the calling process is bracketed by two

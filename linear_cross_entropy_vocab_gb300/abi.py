@@ -33,6 +33,8 @@ FLCE_SKIP_IGNORED_ROWS = 1
 
 FLCE_DEVERR_TARGET_RANGE = 1
 FLCE_DEVERR_TIMEOUT = 2
+FLCE_DEVERR_NOT_FINITE = 4
+FLCE_DEVERR_PARENT_RANGE = 8
 
 REDUCTIONS = {"none": FLCE_RED_NONE, "sum": FLCE_RED_SUM, "mean": FLCE_RED_MEAN}
 
@@ -43,6 +45,14 @@ FLCE_KL_MEAN = 3
 
 KL_REDUCTIONS = {"none": FLCE_KL_NONE, "sum": FLCE_KL_SUM, "batchmean": FLCE_KL_BATCHMEAN,
                  "mean": FLCE_KL_MEAN}
+
+FLCE_NORM_L1 = 1
+FLCE_NORM_L2 = 2
+FLCE_NORM_INF = 3
+
+FLCE_Q_I8 = 3
+
+BEAM_STATE_DIMS = 4
 
 # Every symbol include/flce.h declares.
 EXPORTS = (
@@ -55,6 +65,15 @@ EXPORTS = (
     "flce_kl_forward",
     "flce_kl_backward_workspace_size",
     "flce_kl_backward",
+    "flce_grad_workspace_size",
+    "flce_grad_norm",
+    "flce_grad_clip",
+    "flce_beam_select_workspace_size",
+    "flce_beam_select",
+    "flce_beam_reorder",
+    "flce_quantize_rows",
+    "flce_qlinear_workspace_size",
+    "flce_qlinear",
     "flce_selftest_wait_timeout",
     "flce_status_string",
     "flce_last_error",
@@ -102,6 +121,62 @@ class flce_kl_problem(ctypes.Structure):  # noqa: N801  (C name)
         ("vocab_chunk", ctypes.c_int64),
         ("flags", ctypes.c_int32),
         ("reserved", ctypes.c_int32),
+    ]
+
+
+class flce_grad(ctypes.Structure):  # noqa: N801  (C name)
+    _fields_ = [
+        ("src", ctypes.c_void_p),
+        ("dst", ctypes.c_void_p),
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("src_pitch", ctypes.c_int64),
+        ("dst_pitch", ctypes.c_int64),
+        ("src_dtype", ctypes.c_int32),
+        ("dst_dtype", ctypes.c_int32),
+    ]
+
+
+class flce_beam_problem(ctypes.Structure):  # noqa: N801  (C name)
+    _fields_ = [
+        ("batch", ctypes.c_int64),
+        ("beams", ctypes.c_int64),
+        ("v", ctypes.c_int64),
+        ("candidates", ctypes.c_int64),
+        ("stride_batch", ctypes.c_int64),
+        ("stride_beam", ctypes.c_int64),
+        ("allowed_stride_batch", ctypes.c_int64),
+        ("allowed_stride_beam", ctypes.c_int64),
+        ("pad_token", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class flce_beam_state(ctypes.Structure):  # noqa: N801  (C name)
+    _fields_ = [
+        ("data", ctypes.c_void_p),
+        ("beam_stride", ctypes.c_int64),
+        ("size", ctypes.c_int64 * BEAM_STATE_DIMS),
+        ("stride", ctypes.c_int64 * BEAM_STATE_DIMS),
+        ("run_bytes", ctypes.c_int64),
+    ]
+
+
+class flce_qproblem(ctypes.Structure):  # noqa: N801  (C name)
+    _fields_ = [
+        ("n", ctypes.c_int64),
+        ("h", ctypes.c_int64),
+        ("v", ctypes.c_int64),
+        ("x_pitch", ctypes.c_int64),
+        ("weight_pitch", ctypes.c_int64),
+        ("out_pitch", ctypes.c_int64),
+        ("x_dtype", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32),
+        ("bias_dtype", ctypes.c_int32),
+        ("has_bias", ctypes.c_int32),
+        ("logit_scale", ctypes.c_float),
+        ("softcap", ctypes.c_float),
     ]
 
 
@@ -165,6 +240,30 @@ def load() -> ctypes.CDLL:
         lib.flce_kl_backward.argtypes = [_KLPROB] + [_P] * 16
         lib.flce_kl_backward.argtypes[-2] = ctypes.c_size_t
         lib.flce_kl_backward.restype = ctypes.c_int
+        lib.flce_grad_workspace_size.argtypes = [ctypes.c_int64]
+        lib.flce_grad_workspace_size.restype = ctypes.c_size_t
+        lib.flce_grad_norm.argtypes = [_P, ctypes.c_int64, ctypes.c_int32, _P, _P,
+                                       ctypes.c_size_t, _P]
+        lib.flce_grad_norm.restype = ctypes.c_int
+        lib.flce_grad_clip.argtypes = [_P, ctypes.c_int64, ctypes.c_int32, ctypes.c_float,
+                                       ctypes.c_float, _P, _P, ctypes.c_size_t, _P]
+        lib.flce_grad_clip.restype = ctypes.c_int
+        lib.flce_beam_select_workspace_size.argtypes = [ctypes.POINTER(flce_beam_problem)]
+        lib.flce_beam_select_workspace_size.restype = ctypes.c_size_t
+        lib.flce_beam_select.argtypes = [ctypes.POINTER(flce_beam_problem)] + [_P] * 9 + [
+            ctypes.c_size_t, _P]
+        lib.flce_beam_select.restype = ctypes.c_int
+        lib.flce_beam_reorder.argtypes = [_P, ctypes.c_int64, _P, ctypes.c_int64, ctypes.c_int64,
+                                          _P, _P]
+        lib.flce_beam_reorder.restype = ctypes.c_int
+        lib.flce_quantize_rows.argtypes = [_P, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64,
+                                           ctypes.c_int64, _P, ctypes.c_int64, _P, _P]
+        lib.flce_quantize_rows.restype = ctypes.c_int
+        lib.flce_qlinear_workspace_size.argtypes = [ctypes.POINTER(flce_qproblem)]
+        lib.flce_qlinear_workspace_size.restype = ctypes.c_size_t
+        lib.flce_qlinear.argtypes = [ctypes.POINTER(flce_qproblem)] + [_P] * 8 + [
+            ctypes.c_size_t, _P]
+        lib.flce_qlinear.restype = ctypes.c_int
         lib.flce_selftest_wait_timeout.argtypes = [_P, _P, ctypes.c_double, _P]
         lib.flce_selftest_wait_timeout.restype = ctypes.c_int
         lib.flce_status_string.argtypes = [ctypes.c_int]
@@ -300,6 +399,72 @@ def flce_kl_backward(p, hidden, weight, bias, target_probs, labels, lse_rows, qs
                                  stream)
     if check:
         _check(st, "flce_kl_backward")
+    return st
+
+
+def flce_grad_workspace_size(count: int) -> int:
+    return load().flce_grad_workspace_size(count)
+
+
+def flce_grad_norm(grads, count, norm, norm_out, workspace, workspace_bytes, stream,
+                   check=True) -> int:
+    """``grads`` is the address of ``count`` flce_grad structs in host memory."""
+    st = load().flce_grad_norm(grads, count, norm, norm_out, workspace, workspace_bytes, stream)
+    if check:
+        _check(st, "flce_grad_norm")
+    return st
+
+
+def flce_grad_clip(grads, count, norm, max_norm, eps, norm_out, workspace, workspace_bytes,
+                   stream, check=True) -> int:
+    st = load().flce_grad_clip(grads, count, norm, max_norm, eps, norm_out, workspace,
+                               workspace_bytes, stream)
+    if check:
+        _check(st, "flce_grad_clip")
+    return st
+
+
+def flce_beam_select_workspace_size(p: flce_beam_problem) -> int:
+    return load().flce_beam_select_workspace_size(ctypes.byref(p))
+
+
+def flce_beam_select(p, logits, beam_scores, finished, allowed, scores_out, parents_out,
+                     tokens_out, err_word, workspace, workspace_bytes, stream,
+                     check=True) -> int:
+    st = load().flce_beam_select(ctypes.byref(p), logits, beam_scores, finished, allowed,
+                                 scores_out, parents_out, tokens_out, err_word, workspace,
+                                 workspace_bytes, stream)
+    if check:
+        _check(st, "flce_beam_select")
+    return st
+
+
+def flce_beam_reorder(states, count, parents, batch, beams, err_word, stream,
+                      check=True) -> int:
+    """``states`` is the address of ``count`` flce_beam_state structs in host memory."""
+    st = load().flce_beam_reorder(states, count, parents, batch, beams, err_word, stream)
+    if check:
+        _check(st, "flce_beam_reorder")
+    return st
+
+
+def flce_quantize_rows(x, dtype, n, h, x_pitch, q, q_pitch, scale, stream, check=True) -> int:
+    st = load().flce_quantize_rows(x, dtype, n, h, x_pitch, q, q_pitch, scale, stream)
+    if check:
+        _check(st, "flce_quantize_rows")
+    return st
+
+
+def flce_qlinear_workspace_size(p: flce_qproblem) -> int:
+    return load().flce_qlinear_workspace_size(ctypes.byref(p))
+
+
+def flce_qlinear(p, x, x_scale, weight, weight_scale, bias, out, err_word, workspace,
+                 workspace_bytes, stream, check=True) -> int:
+    st = load().flce_qlinear(ctypes.byref(p), x, x_scale, weight, weight_scale, bias, out,
+                             err_word, workspace, workspace_bytes, stream)
+    if check:
+        _check(st, "flce_qlinear")
     return st
 
 

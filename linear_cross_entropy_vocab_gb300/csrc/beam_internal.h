@@ -1,0 +1,72 @@
+// Parameters of the beam search kernels (kernels_beam.cu), filled in by the
+// entry points in beam_api.cu.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "flce.h"
+
+namespace flce {
+
+constexpr int kBeamMaxCandidates = 256;
+constexpr int kBeamMaxBeams = 64;  // of a reordering; a selection takes more (its scores are staged)
+constexpr int kBeamMaxSelectBeams = 1024;
+
+// Logits per thread of a selection CTA (256 threads): a slice of 2048 or of 8192.
+constexpr int kSliceSmall = 2048;
+constexpr int kSliceLarge = 8192;
+
+struct BeamSelectParams {
+  const void* logits;
+  int64_t stride_b, stride_k;  // elements
+  const uint8_t* allowed;      // or null
+  int64_t allowed_b, allowed_k;
+  const float* beam_scores;    // [B][K]
+  const uint8_t* finished;     // [B][K] or null
+  int32_t batch, beams, m, splits;
+  int64_t v;
+  int64_t pad_token;
+  // per (row, slice): its M best keys, best first, 0 where there are fewer,
+  // and its maximum and sum of exponentials
+  uint64_t* keys;
+  float2* stats;
+  float* scores_out;      // [B][M]
+  int64_t* parents_out;   // [B][M]
+  int64_t* tokens_out;    // [B][M]
+  int32_t* err_word;
+};
+
+cudaError_t launch_beam_select(const BeamSelectParams& p, int dtype, bool large,
+                               cudaStream_t s);
+
+constexpr int kReorderDims = 4;
+constexpr int kReorderTable = 64;
+
+// One state: rows of `vecs` vectors of the launch's width, at the places that
+// the (at most 4) outer extents and strides give, for each of batch x beams
+// beams `beam_stride` bytes apart.
+struct ReorderEntry {
+  uint8_t* data;
+  int64_t beam_stride;
+  int64_t stride[kReorderDims];  // bytes, outermost first
+  uint32_t size[kReorderDims];   // 1 where unused
+  uint32_t run;                  // vectors in one contiguous run
+  uint32_t total;                // vectors of one beam
+};
+
+struct ReorderTable {
+  ReorderEntry e[kReorderTable];
+  uint32_t first[kReorderTable + 1];  // first block of each state
+  int32_t count;
+  int32_t batch, beams;
+  const int64_t* parents;
+  int32_t* err_word;
+};
+
+cudaError_t launch_beam_reorder(const ReorderTable& t, int width, int64_t blocks, cudaStream_t s);
+
+// Vectors of one beam that a block takes.
+constexpr int kReorderBlock = 256;
+
+}  // namespace flce

@@ -17,6 +17,7 @@
 
 #include "flce.h"
 #include "flce_internal.h"
+#include "host_common.h"
 
 namespace {
 
@@ -1196,6 +1197,33 @@ flce_status static_scratch(void** out) {
 }
 
 }  // namespace
+
+// ------------------------------------------- shared with the other entry points
+namespace flce {
+namespace host {
+
+flce_status fail(flce_status s, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_err, sizeof(g_err), fmt, ap);
+  va_end(ap);
+  return s;
+}
+flce_status cuda_fail(cudaError_t e, const char* what) { return ::cuda_fail(e, what); }
+void clear_error() { g_err[0] = 0; }
+flce_status check_device(int* sms) {
+  DeviceInfo d;
+  const flce_status st = ::check_device(&d);
+  if (st == FLCE_OK) *sms = d.sms;
+  return st;
+}
+flce_status check_workspace(void* ws, size_t have, size_t need) {
+  return ::check_workspace(ws, have, need);
+}
+EncodeTiledFn tensor_map_encoder() { return encoder(); }
+
+}  // namespace host
+}  // namespace flce
 
 extern "C" {
 

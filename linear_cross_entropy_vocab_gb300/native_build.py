@@ -19,7 +19,9 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libflce.so")
 
-SOURCES = ["flce_api.cu", "kernels_tc.cu", "kernels_simt.cu", "kernels_rows.cu"]
+SOURCES = ["flce_api.cu", "kernels_tc.cu", "kernels_simt.cu", "kernels_rows.cu",
+           "grads_api.cu", "kernels_grads.cu", "beam_api.cu", "kernels_beam.cu",
+           "int8_api.cu", "kernels_int8.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
                      "-I", INCLUDE, "-I", CSRC]
