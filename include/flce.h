@@ -451,9 +451,9 @@ flce_status flce_beam_reorder(const flce_beam_state* states, int64_t count,
  *   out_ij  = softcap * tanh(u_ij / softcap)   if softcap > 0, else u_ij
  *
  * A row of zeros has scale 0; a row that holds a NaN or an infinity gives
- * NaN. Products are exact, sums are held in 32 bits: the integer paths are
- * exact, and the tensor-core path rounds only sums beyond 2^24. Rows lie
- * `pitch` elements apart.
+ * NaN. Products are exact and sums are held in 32-bit floating point: they are
+ * exact up to 2^24, and beyond it rounded at each of the h / 16 steps of the
+ * tensor core. Rows lie `pitch` elements apart.
  */
 typedef enum flce_qdtype { FLCE_Q_I8 = 3 } flce_qdtype; /* beside flce_dtype, for x */
 
@@ -471,14 +471,22 @@ typedef struct flce_qproblem {
   int32_t has_bias;    /* 0 or 1 */
   float logit_scale;   /* finite */
   float softcap;       /* > 0 enables it */
+  int32_t flags;       /* OR of FLCE_Q_LAY_OUT_WEIGHT; 0 for none */
+  int32_t reserved;    /* 0 */
 } flce_qproblem;
+
+/* Lay the weight out in the workspace first, one more pass over it. It is
+ * implied by a weight_pitch that is no multiple of 16, and a caller sets it
+ * for a weight that does not start at a multiple of 16 bytes (such a call is
+ * FLCE_ERR_UNSUPPORTED without it). */
+#define FLCE_Q_LAY_OUT_WEIGHT 1
 
 /* Bytes of device workspace flce_qlinear() needs (0 if `p` is invalid). */
 size_t flce_qlinear_workspace_size(const flce_qproblem* p);
 
 /* x_scale [n]: with FLCE_Q_I8 only, else NULL. weight int8 [v][h] with
  * weight_scale fp32 [v]. Weight rows that start at multiples of 16 bytes are
- * read as they are; others are first laid out in the workspace. */
+ * read where they are (see FLCE_Q_LAY_OUT_WEIGHT for others). */
 flce_status flce_qlinear(const flce_qproblem* p, const void* x, const float* x_scale,
                          const int8_t* weight, const float* weight_scale,
                          const void* bias, void* out, int32_t* err_word,

@@ -51,6 +51,7 @@ FLCE_NORM_L2 = 2
 FLCE_NORM_INF = 3
 
 FLCE_Q_I8 = 3
+FLCE_Q_LAY_OUT_WEIGHT = 1
 
 BEAM_STATE_DIMS = 4
 
@@ -177,6 +178,8 @@ class flce_qproblem(ctypes.Structure):  # noqa: N801  (C name)
         ("has_bias", ctypes.c_int32),
         ("logit_scale", ctypes.c_float),
         ("softcap", ctypes.c_float),
+        ("flags", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
     ]
 
 

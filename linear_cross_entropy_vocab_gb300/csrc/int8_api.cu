@@ -36,22 +36,71 @@ flce_status check_qproblem(const flce_qproblem* p) {
     return fail(FLCE_ERR_INVALID_ARG, "a pitch is smaller than its rows");
   if (!std::isfinite(p->logit_scale) || !std::isfinite(p->softcap))
     return fail(FLCE_ERR_INVALID_ARG, "logit_scale and softcap must be finite");
+  if ((p->flags & ~FLCE_Q_LAY_OUT_WEIGHT) != 0 || p->reserved != 0)
+    return fail(FLCE_ERR_INVALID_ARG, "unknown flags, or reserved is not 0");
   return FLCE_OK;
 }
 
-struct QPlan {
-  size_t q, scale, total;
-  int64_t q_pitch;
+// Rows of x that a tile takes, and whether CTA pairs take it. A tile of up to
+// 128 rows runs on single CTAs, whose accumulator drains behind the next
+// tile's products; more rows run on pairs, which share the tile of x, in the
+// fewest tiles of at most 256 rows, each as small as that many allow.
+struct QTile {
+  int cg;
+  int64_t nt, n_tiles;
 };
 
+QTile tile_of(int64_t n) {
+  QTile t;
+  t.cg = n <= 128 ? 1 : 2;
+  t.n_tiles = ceil_div(n, t.cg == 1 ? 128 : 256);
+  const int64_t step = 16 * t.cg;
+  t.nt = ceil_div(ceil_div(n, t.n_tiles), step) * step;
+  t.n_tiles = ceil_div(n, t.nt);
+  return t;
+}
+
+struct QPlan {
+  size_t wide, scale, weight, total;
+  int64_t wide_pitch, weight_pitch;
+  bool align;  // the weight is laid out in the workspace first
+};
+
+// TMA reads rows that start at multiples of 16 bytes: others are laid out
+// anew, which reads and writes the weight once more.
 QPlan plan_qlinear(const flce_qproblem* p) {
   QPlan q{};
-  q.q_pitch = (p->h + 15) / 16 * 16;
-  if (p->x_dtype != FLCE_Q_I8) {
-    q.scale = align_256(static_cast<size_t>(p->n) * static_cast<size_t>(q.q_pitch));
-    q.total = q.scale + align_256(static_cast<size_t>(p->n) * 4);
-  }
+  const bool align = p->weight_pitch % 16 != 0 || (p->flags & FLCE_Q_LAY_OUT_WEIGHT) != 0;
+  q.align = align;
+  q.wide_pitch = ceil_div(p->h, 64) * 64;
+  q.scale = align_256(static_cast<size_t>(p->n) * static_cast<size_t>(q.wide_pitch) * 2);
+  q.weight = q.scale + align_256(static_cast<size_t>(p->n) * 4);
+  q.weight_pitch = align ? ceil_div(p->h, 16) * 16 : p->weight_pitch;
+  q.total = q.weight +
+            (align ? align_256(static_cast<size_t>(p->v) * static_cast<size_t>(q.weight_pitch)) : 0);
   return q;
+}
+
+bool make_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, int64_t inner,
+              int64_t outer, int64_t pitch_bytes, uint32_t box_inner, uint32_t box_outer) {
+  const EncodeTiledFn enc = tensor_map_encoder();
+  if (enc == nullptr) {
+    fail(FLCE_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    return false;
+  }
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch_bytes)};
+  const cuuint32_t box[2] = {box_inner, box_outer};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = enc(map, type, 2, const_cast<void*>(base), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    fail(FLCE_ERR_CUDA, "cuTensorMapEncodeTiled failed with CUresult %d (%lld x %lld, pitch %lld)",
+         static_cast<int>(r), (long long)inner, (long long)outer, (long long)pitch_bytes);
+    return false;
+  }
+  return true;
 }
 
 }  // namespace
@@ -74,7 +123,14 @@ flce_status flce_quantize_rows(const void* x, int32_t dtype, int64_t n, int64_t 
   int sms = 0;
   const flce_status st = check_device(&sms);
   if (st != FLCE_OK || n == 0) return st;
-  const flce::QuantParams k{x, n, h, x_pitch, q, q_pitch, scale};
+  flce::QuantParams k{};
+  k.x = x;
+  k.n = n;
+  k.h = h;
+  k.x_pitch = x_pitch;
+  k.q = q;
+  k.q_pitch = q_pitch;
+  k.scale = scale;
   const cudaError_t e = flce::launch_quantize_rows(k, dtype, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FLCE_OK : cuda_fail(e, "row quantisation kernel");
 }
@@ -105,6 +161,9 @@ flce_status flce_qlinear(const flce_qproblem* p, const void* x, const float* x_s
       return fail(FLCE_ERR_UNSUPPORTED, "a pointer is misaligned for its type");
   }
   const QPlan plan = plan_qlinear(p);
+  if (p->n > 0 && p->v > 0 && !plan.align && !aligned_to(weight, 16))
+    return fail(FLCE_ERR_UNSUPPORTED,
+                "weight does not start at a multiple of 16 bytes (FLCE_Q_LAY_OUT_WEIGHT)");
   st = check_workspace(workspace, workspace_bytes, plan.total);
   if (st != FLCE_OK) return st;
   int sms = 0;
@@ -112,36 +171,52 @@ flce_status flce_qlinear(const flce_qproblem* p, const void* x, const float* x_s
   if (st != FLCE_OK || p->n == 0 || p->v == 0) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint8_t* const ws = static_cast<uint8_t*>(workspace);
-  flce::QLinearParams k{};
-  if (dynamic) {
-    const flce::QuantParams q{x, p->n, p->h, p->x_pitch, reinterpret_cast<int8_t*>(ws + plan.q),
-                              plan.q_pitch, reinterpret_cast<float*>(ws + plan.scale)};
-    const cudaError_t e = flce::launch_quantize_rows(q, p->x_dtype, s);
-    if (e != cudaSuccess) return cuda_fail(e, "row quantisation kernel");
-    k.x = q.q;
-    k.x_scale = q.scale;
-    k.x_pitch = q.q_pitch;
-  } else {
-    k.x = static_cast<const int8_t*>(x);
-    k.x_scale = x_scale;
-    k.x_pitch = p->x_pitch;
+  cudaError_t e;
+  if (plan.align) {
+    int8_t* const laid = reinterpret_cast<int8_t*>(ws + plan.weight);
+    e = flce::launch_align_rows(weight, p->v, p->h, p->weight_pitch, laid, plan.weight_pitch, s);
+    if (e != cudaSuccess) return cuda_fail(e, "weight layout kernel");
+    weight = laid;
   }
-  k.weight = weight;
+  flce::QuantParams q{};
+  q.x = x;
+  q.n = p->n;
+  q.h = p->h;
+  q.x_pitch = p->x_pitch;
+  q.wide = ws + plan.wide;
+  q.wide_pitch = plan.wide_pitch;
+  q.scale = reinterpret_cast<float*>(ws + plan.scale);
+  e = flce::launch_widen_rows(q, p->x_dtype, s);
+  if (e != cudaSuccess) return cuda_fail(e, "row quantisation kernel");
+
+  const QTile tile = tile_of(p->n);
+  flce::QLinearTcParams k{};
+  if (!make_map(&k.w_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, weight, p->h, p->v, plan.weight_pitch,
+                128, 128) ||
+      !make_map(&k.x_map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, q.wide, plan.wide_pitch, p->n,
+                plan.wide_pitch * 2, 64, static_cast<uint32_t>(tile.nt / tile.cg)))
+    return FLCE_ERR_CUDA;
+  const int64_t v_tiles = ceil_div(p->v, 128 * tile.cg);
+  if (v_tiles * tile.n_tiles > 0x7fffffff)
+    return fail(FLCE_ERR_UNSUPPORTED, "more than 2^31 output tiles");
+  k.x_scale = dynamic ? q.scale : x_scale;
   k.weight_scale = weight_scale;
   k.bias = bias;
   k.out = out;
   k.n = p->n;
-  k.h = p->h;
   k.v = p->v;
-  k.weight_pitch = p->weight_pitch;
   k.out_pitch = p->out_pitch;
-  k.out_dtype = p->out_dtype;
   k.bias_dtype = p->bias_dtype;
+  k.nt = static_cast<int32_t>(tile.nt);
+  k.n_tiles = static_cast<int32_t>(tile.n_tiles);
+  k.v_tiles = static_cast<int32_t>(v_tiles);
+  k.k_blocks = static_cast<int32_t>(ceil_div(p->h, 64));
+  k.err_word = err_word;
   k.xf.scale = p->logit_scale;
   k.xf.has_cap = p->softcap > 0.0f ? 1 : 0;
   k.xf.softcap = k.xf.has_cap ? p->softcap : 1.0f;
   k.xf.inv_softcap = 1.0f / k.xf.softcap;
-  const cudaError_t e = flce::launch_qlinear_simple(k, s);
+  e = flce::launch_qlinear_tc(k, tile.cg, p->out_dtype, sms, s);
   return e == cudaSuccess ? FLCE_OK : cuda_fail(e, "8-bit linear kernel");
 }
 

@@ -1,0 +1,478 @@
+// The linear layer on 8-bit integer rows, on the tensor cores:
+//
+//   out_ij = f(x_scale_i * weight_scale_j * sum_h q_ih w_jh + bias_j)
+//
+// The tensor cores of this GPU have no 8-bit integer rate worth using, but a
+// half-precision number holds every 8-bit integer, its products are exact and
+// the accumulators are 32 bits wide: sums up to 2^24 are exact too. So the
+// weight travels from memory to the SM in 8 bits, which is what bounds a call
+// with few rows, and is widened on the way into the MMA; the few rows of x are
+// widened once, by a kernel of their own.
+//
+// The weight is the A operand (its rows are the accumulator's lanes) and is
+// read by the MMA from tensor memory: widening warps take the bytes from the
+// shared memory that TMA filled, turn each into a half and store them with
+// tcgen05.st. Shared memory then carries the weight in 8 bits only, and
+// the MMA reads only x from it. A byte b becomes a half by b xor 0x6480, which is
+// 1024 + 128 + b, minus 1152. Bytes 0 and 2 of a word make one pair and 1 and
+// 3 the other, without a permutation: x is laid out in that order
+// (k = 0, 2, 1, 3 in each four) by the kernel that widens it.
+//
+// Tiles are 128 weight rows (CG = 1) or 256 over a pair of CTAs (CG = 2) by
+// `nt` rows of x, a multiple of 16 (32) that the launch chooses so that the
+// last tile is not mostly empty. A CTA stays on its SM and takes tile after
+// tile. Tensor memory: columns [0, 256) the accumulators (two when nt <= 128,
+// so that one drains while the other fills), [256, 512) eight 64-deep slices
+// of widened weight.
+//
+// Roles (19 warps): 0 loads the weight, 1 issues the MMAs, 2 loads x, 3-10
+// widen (two groups of four; each takes 64 of a stage's 128 bytes), 11-18
+// run the epilogue (two per lane quarter, half of the columns each).
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "int8_internal.h"
+#include "tc_gemm.cuh"
+
+namespace flce {
+namespace {
+
+constexpr int kWStageBytes = 128 * 128;  // 128 weight rows x 128 bytes
+constexpr int kMaxWStages = 12;
+constexpr int kMaxXStages = 24;
+constexpr int kASlots = 8;
+constexpr int kACols = 32;        // tensor-memory columns of a 64-deep slice
+constexpr int kABase = 256;       // first of them
+constexpr int kWidenWarps = 8;
+constexpr int kEpilogueWarps = 8;
+constexpr int kFirstWiden = 3;
+constexpr int kFirstEpilogue = kFirstWiden + kWidenWarps;
+constexpr int kThreads = 32 * (kFirstEpilogue + kEpilogueWarps);
+constexpr int kSmemBudget = 220 * 1024;
+
+struct Ctl {
+  uint64_t w_full[kMaxWStages], w_empty[kMaxWStages];
+  uint64_t x_full[kMaxXStages], x_empty[kMaxXStages];
+  uint64_t a_full[kASlots], a_empty[kASlots];
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t mma_done;
+  uint32_t tmem_base;
+  int abort;
+};
+
+// D (+)= A * B^T with A in tensor memory, fp16 inputs, fp32 accumulators.
+template <int CG>
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t accumulate) {
+  if constexpr (CG == 1)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// 32 columns of this warp's 32 lanes.
+__device__ __forceinline__ void tmem_store_32cols(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n\t"
+      "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+// Bytes (0, 2) and (1, 3) of a word of four signed 8-bit integers as halves.
+__device__ __forceinline__ void widen(uint32_t w, uint32_t& even, uint32_t& odd) {
+  const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+  uint32_t e = (w & 0x00ff00ffu) ^ 0x64806480u;
+  uint32_t o = ((w >> 8) & 0x00ff00ffu) ^ 0x64806480u;
+  const __half2 eh = __hsub2(*reinterpret_cast<__half2*>(&e), bias);
+  const __half2 oh = __hsub2(*reinterpret_cast<__half2*>(&o), bias);
+  even = *reinterpret_cast<const uint32_t*>(&eh);
+  odd = *reinterpret_cast<const uint32_t*>(&oh);
+}
+
+// An mbarrier arrive on the pair's even CTA.
+template <int CG>
+__device__ __forceinline__ void arrive_leader(uint32_t bar, bool leader) {
+  if (CG == 1 || leader)
+    mbar_arrive(bar);
+  else
+    mbar_arrive_cluster(map_to_rank(bar, 0));
+}
+
+template <int CG>
+__device__ __forceinline__ void commit(uint32_t bar) {
+  if constexpr (CG == 1)
+    umma_commit(bar);
+  else
+    umma_commit_pair(bar, 0x3);
+}
+
+__device__ __forceinline__ float bias_at(const void* p, int dtype, int64_t i) {
+  if (dtype == FLCE_F32) return static_cast<const float*>(p)[i];
+  if (dtype == FLCE_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+  return __half2float(static_cast<const __half*>(p)[i]);
+}
+__device__ __forceinline__ void store(float* p, float x) { *p = x; }
+__device__ __forceinline__ void store(__nv_bfloat16* p, float x) { *p = __float2bfloat16(x); }
+__device__ __forceinline__ void store(__half* p, float x) { *p = __float2half(x); }
+
+template <int CG, class T>
+__global__ void __launch_bounds__(kThreads, 1)
+    qlinear_kernel(const __grid_constant__ QLinearTcParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Ctl ctl;
+  const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
+  const uint32_t x_base = base + static_cast<uint32_t>(p.w_stages) * kWStageBytes;
+  const uint32_t x_bytes = static_cast<uint32_t>(p.nt / CG) * 128u;
+  const int warp = static_cast<int>(threadIdx.x >> 5);
+  const int lane = static_cast<int>(threadIdx.x & 31);
+  const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;
+  const bool leader = rank == 0;
+  const int unit0 = static_cast<int>(blockIdx.x) / CG;
+  const int units = static_cast<int>(gridDim.x) / CG;
+  const int total = p.n_tiles * p.v_tiles;
+  volatile int* const abort_flag = &ctl.abort;
+  int* const err_word = p.err_word;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.w_stages; ++s) {
+      mbar_init(smem_addr(&ctl.w_full[s]), 1);
+      mbar_init(smem_addr(&ctl.w_empty[s]), kWidenWarps);
+    }
+    for (int s = 0; s < p.x_stages; ++s) {
+      mbar_init(smem_addr(&ctl.x_full[s]), 1);
+      mbar_init(smem_addr(&ctl.x_empty[s]), 1);
+    }
+    for (int s = 0; s < kASlots; ++s) {
+      mbar_init(smem_addr(&ctl.a_full[s]), (kWidenWarps / 2) * CG);
+      mbar_init(smem_addr(&ctl.a_empty[s]), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(smem_addr(&ctl.acc_full[s]), 1);
+      mbar_init(smem_addr(&ctl.acc_empty[s]), kEpilogueWarps * CG);
+    }
+    mbar_init(smem_addr(&ctl.mma_done), 1);
+    ctl.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&p.w_map);
+    tma_prefetch_desc(&p.x_map);
+  }
+  if (warp == 1) {
+    if constexpr (CG == 1) {
+      tmem_alloc(smem_addr(&ctl.tmem_base), 512);
+      tmem_relinquish();
+    } else {
+      tmem_alloc_pair(smem_addr(&ctl.tmem_base), 512);
+      tmem_relinquish_pair();
+    }
+  }
+  tc_fence_before_sync();
+  if constexpr (CG == 1)
+    __syncthreads();
+  else
+    cluster_sync();
+  tc_fence_after_sync();
+  const uint32_t tmem = ctl.tmem_base;
+  const int bufs = p.nt <= 128 ? 2 : 1;
+  const int w_iters = (p.k_blocks + 1) / 2;  // 128-byte stages of a tile
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------ weight loads
+      int s = 0;
+      uint32_t phase = 0, armed = 0, last_phase = 0;
+      bool ok = true;
+      for (int u = unit0; ok && u < total; u += units) {
+        const int row = (u / p.n_tiles) * (128 * CG) + static_cast<int>(rank) * 128;
+        for (int i = 0; i < w_iters; ++i) {
+          if (!mbar_wait(smem_addr(&ctl.w_empty[s]), phase ^ 1u, abort_flag, err_word)) {
+            ok = false;
+            break;
+          }
+          const uint32_t full = smem_addr(&ctl.w_full[s]);
+          mbar_arrive_expect_tx(full, kWStageBytes);
+          tma_load_2d(base + static_cast<uint32_t>(s) * kWStageBytes, &p.w_map, full, i * 128, row);
+          armed |= 1u << s;
+          last_phase = (last_phase & ~(1u << s)) | (phase << s);
+          if (++s == p.w_stages) {
+            s = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok)  // copies in flight land before the CTA leaves
+        for (int q = 0; q < p.w_stages; ++q)
+          if (armed & (1u << q)) drain_wait(smem_addr(&ctl.w_full[q]), (last_phase >> q) & 1u);
+    }
+  } else if (warp == 2) {
+    if (lane == 0) {
+      // ------------------------------------------------ loads of x
+      grid_dependency_wait();  // x is widened by the kernel before this one
+      int s = 0;
+      uint32_t phase = 0, armed = 0, last_phase = 0;
+      bool ok = true;
+      for (int u = unit0; ok && u < total; u += units) {
+        const int row = (u % p.n_tiles) * p.nt + static_cast<int>(rank) * (p.nt / CG);
+        for (int k = 0; k < p.k_blocks; ++k) {
+          if (!wait_bar<CG>(smem_addr(&ctl.x_empty[s]), phase ^ 1u, abort_flag, err_word)) {
+            ok = false;
+            break;
+          }
+          const uint32_t local = smem_addr(&ctl.x_full[s]);
+          const uint32_t dst = x_base + static_cast<uint32_t>(s) * x_bytes;
+          if (leader) mbar_arrive_expect_tx(local, CG * x_bytes);
+          if constexpr (CG == 1)
+            tma_load_2d(dst, &p.x_map, local, k * 64, row);
+          else
+            tma_load_2d_pair(dst, &p.x_map, map_to_rank(local, 0), k * 64, row);
+          armed |= 1u << s;
+          last_phase = (last_phase & ~(1u << s)) | (phase << s);
+          if (++s == p.x_stages) {
+            s = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok && leader)
+        for (int q = 0; q < p.x_stages; ++q)
+          if (armed & (1u << q)) drain_wait(smem_addr(&ctl.x_full[q]), (last_phase >> q) & 1u);
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && leader) {
+      // ------------------------------------------------ MMA issuer
+      const uint32_t idesc = idesc_f16kind_f32(128 * CG, p.nt, 0, 0, 0u);
+      int xs = 0, as = 0;
+      uint32_t x_phase = 0, a_phase = 0;
+      bool ok = true;
+      int it = 0;
+      for (int u = unit0; ok && u < total; u += units, ++it) {
+        const int buf = bufs == 2 ? it & 1 : 0;
+        const uint32_t use = static_cast<uint32_t>(bufs == 2 ? it >> 1 : it) & 1u;
+        if (!wait_bar<CG>(smem_addr(&ctl.acc_empty[buf]), use ^ 1u, abort_flag, err_word)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        const uint32_t d = tmem + static_cast<uint32_t>(buf * 128);
+        for (int k = 0; k < p.k_blocks; ++k) {
+          if (!wait_bar<CG>(smem_addr(&ctl.x_full[xs]), x_phase, abort_flag, err_word) ||
+              !wait_bar<CG>(smem_addr(&ctl.a_full[as]), a_phase, abort_flag, err_word)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const uint32_t a = tmem + static_cast<uint32_t>(kABase + as * kACols);
+          const uint32_t b = x_base + static_cast<uint32_t>(xs) * x_bytes;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_ts<CG>(d, a + static_cast<uint32_t>(kk * 8), smem_desc_sw128(b + kk * 32, 16, 1024),
+                        idesc, (k | kk) != 0 ? 1u : 0u);
+          commit<CG>(smem_addr(&ctl.x_empty[xs]));
+          commit<CG>(smem_addr(&ctl.a_empty[as]));
+          if (++xs == p.x_stages) {
+            xs = 0;
+            x_phase ^= 1u;
+          }
+          if (++as == kASlots) {
+            as = 0;
+            a_phase ^= 1u;
+          }
+        }
+        if (ok) commit<CG>(smem_addr(&ctl.acc_full[buf]));
+      }
+      commit<CG>(smem_addr(&ctl.mma_done));
+      drain_wait(smem_addr(&ctl.mma_done), 0);
+    } else if (lane == 0 && CG == 2) {
+      drain_wait(smem_addr(&ctl.mma_done), 0);  // the even CTA's MMAs write this CTA's TMEM
+    }
+  } else if (warp < kFirstEpilogue) {
+    // -------------------------------------------------- widening warps
+    const int quarter = warp & 3;
+    const int group = (warp - kFirstWiden) >> 2;
+    const int row = quarter * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    int s = 0;
+    uint32_t phase = 0;
+    uint32_t block0 = 0;  // 64-deep blocks of the tiles before this one
+    bool ok = true;
+    for (int u = unit0; ok && u < total; u += units, block0 += static_cast<uint32_t>(p.k_blocks)) {
+      for (int i = 0; i < w_iters; ++i) {
+        ok = mbar_wait(smem_addr(&ctl.w_full[s]), phase, abort_flag, err_word);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        const int k = 2 * i + group;
+        const bool some = k < p.k_blocks;
+        uint32_t w[16];
+        if (some) {
+          // 16-byte piece c of a row lies at c xor (row mod 8): TMA's 128-byte swizzle
+          const uint32_t at = base + static_cast<uint32_t>(s) * kWStageBytes +
+                              static_cast<uint32_t>(row) * 128u;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[4 * c]), "=r"(w[4 * c + 1]), "=r"(w[4 * c + 2]),
+                           "=r"(w[4 * c + 3])
+                         : "r"(at + static_cast<uint32_t>(((group * 4 + c) ^ (row & 7)) * 16))
+                         : "memory");
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&ctl.w_empty[s]));
+        if (++s == p.w_stages) {
+          s = 0;
+          phase ^= 1u;
+        }
+        if (!some) continue;
+        uint32_t h[32];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) widen(w[j], h[2 * j], h[2 * j + 1]);
+        const uint32_t block = block0 + static_cast<uint32_t>(k);
+        const uint32_t as = block % kASlots;
+        ok = wait_bar<CG>(smem_addr(&ctl.a_empty[as]), ((block / kASlots) & 1u) ^ 1u, abort_flag,
+                          err_word);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        tmem_store_32cols(tmem + lanes + kABase + as * kACols, h);
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) arrive_leader<CG>(smem_addr(&ctl.a_full[as]), leader);
+      }
+    }
+  } else {
+    // -------------------------------------------------- epilogue warps
+    const int quarter = warp & 3;
+    const int half = (warp - kFirstEpilogue) >> 2;
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    T* const out = static_cast<T*>(p.out);
+    grid_dependency_wait();  // x_scale may come from the kernel before this one
+    int it = 0;
+    for (int u = unit0; u < total; u += units, ++it) {
+      const int buf = bufs == 2 ? it & 1 : 0;
+      const uint32_t use = static_cast<uint32_t>(bufs == 2 ? it >> 1 : it) & 1u;
+      const int64_t v = static_cast<int64_t>(u / p.n_tiles) * (128 * CG) +
+                        static_cast<int64_t>(rank) * 128 + quarter * 32 + lane;
+      const int64_t n0 = static_cast<int64_t>(u % p.n_tiles) * p.nt;
+      const bool mine = v < p.v;
+      const float ws = mine ? __ldg(p.weight_scale + v) : 0.0f;
+      const float b = mine && p.bias != nullptr ? bias_at(p.bias, p.bias_dtype, v) : 0.0f;
+      const bool ok =
+          wait_bar<CG>(smem_addr(&ctl.acc_full[buf]), use, abort_flag, err_word);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after_sync();
+      const int cols = static_cast<int>(p.n - n0 < p.nt ? p.n - n0 : p.nt);
+      const int chunks = (cols + 31) / 32;
+      // this warp's 32-column chunks: the first or the second half of them
+      const int c0 = half == 0 ? 0 : (chunks + 1) / 2;
+      const int c1 = half == 0 ? (chunks + 1) / 2 : chunks;
+      for (int c = c0; c < c1; ++c) {
+        float z[32];
+        tmem_load_32cols(tmem + lanes + static_cast<uint32_t>(buf * 128 + c * 32), z);
+        const int64_t n = n0 + c * 32;
+        T* o = out + n * p.out_pitch + v;
+        const int m = cols - c * 32;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          if (j < m) {
+            const float x = p.xf(z[j] * ws * __ldg(p.x_scale + n + j), b);
+            if (mine) store(o, x);
+            o += p.out_pitch;
+          }
+        }
+      }
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) arrive_leader<CG>(smem_addr(&ctl.acc_empty[buf]), leader);
+    }
+  }
+
+  tc_fence_before_sync();
+  __syncwarp();
+  if constexpr (CG == 1)
+    __syncthreads();
+  else
+    cluster_sync();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after_sync();
+    if constexpr (CG == 1)
+      tmem_dealloc(tmem, 512);
+    else
+      tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+template <int CG, class T>
+cudaError_t launch_typed(QLinearTcParams p, int sms, cudaStream_t s) {
+  const int x_bytes = p.nt / CG * 128;
+  int w = kSmemBudget / (kWStageBytes + 2 * x_bytes);
+  if (w > kMaxWStages) w = kMaxWStages;
+  p.w_stages = w;
+  p.x_stages = 2 * w;
+  const int smem = w * (kWStageBytes + 2 * x_bytes) + 1024;
+  auto kern = qlinear_kernel<CG, T>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kSmemBudget + 1024);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  // the kernel that widens x lets this one start: it loads weights meanwhile
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.numAttrs = 1;
+  if constexpr (CG == 2) {
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+  }
+  const int64_t tiles = static_cast<int64_t>(p.n_tiles) * p.v_tiles;
+  const int64_t units = sms / CG;
+  cfg.gridDim = dim3(static_cast<unsigned>((tiles < units ? tiles : units) * CG), 1, 1);
+  e = cudaLaunchKernelEx(&cfg, kern, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int CG>
+cudaError_t launch_cg(const QLinearTcParams& p, int out_dtype, int sms, cudaStream_t s) {
+  if (out_dtype == FLCE_F32) return launch_typed<CG, float>(p, sms, s);
+  if (out_dtype == FLCE_BF16) return launch_typed<CG, __nv_bfloat16>(p, sms, s);
+  return launch_typed<CG, __half>(p, sms, s);
+}
+
+}  // namespace
+
+cudaError_t launch_qlinear_tc(const QLinearTcParams& p, int cg, int out_dtype, int sms,
+                              cudaStream_t s) {
+  return cg == 1 ? launch_cg<1>(p, out_dtype, sms, s) : launch_cg<2>(p, out_dtype, sms, s);
+}
+
+}  // namespace flce

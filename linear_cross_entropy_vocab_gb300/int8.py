@@ -69,6 +69,8 @@ def int8_linear(x: torch.Tensor, weight: torch.Tensor, weight_scale: torch.Tenso
     ``x_scale`` [...] float32 from :func:`quantize_rows`. ``bias`` [V] is a float tensor.
     ``logit_scale`` and ``softcap`` are the losses'. The result is ``out_dtype``, by default x's
     type (float32 for int8). It has no gradient: inputs that ask for one are refused.
+    Weight rows that start at multiples of 16 bytes, as quantize_rows makes them, are read where
+    they are; others are laid out anew in every call.
     """
     if weight.dim() != 2 or x.dim() < 1 or x.shape[-1] != weight.shape[1]:
         raise ValueError("x must be (..., H) and weight (V, H)")
@@ -120,7 +122,8 @@ def int8_linear(x: torch.Tensor, weight: torch.Tensor, weight_scale: torch.Tenso
     prob = abi.flce_qproblem(n, h, v, x_pitch, w_pitch, v, code, _DTYPES[out_dtype],
                              0 if bias is None else _DTYPES[bias.dtype],
                              0 if bias is None else 1, float(logit_scale),
-                             0.0 if softcap is None else float(softcap))
+                             0.0 if softcap is None else float(softcap),
+                             abi.FLCE_Q_LAY_OUT_WEIGHT if weight.data_ptr() % 16 else 0, 0)
     with torch.cuda.device(dev):
         ws_bytes = abi.flce_qlinear_workspace_size(prob)
         ws = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=dev)

@@ -21,7 +21,7 @@ LIB = os.path.join(BUILD, "libflce.so")
 
 SOURCES = ["flce_api.cu", "kernels_tc.cu", "kernels_simt.cu", "kernels_rows.cu",
            "grads_api.cu", "kernels_grads.cu", "beam_api.cu", "kernels_beam.cu",
-           "int8_api.cu", "kernels_int8.cu"]
+           "int8_api.cu", "kernels_int8.cu", "kernels_qlinear.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
                      "-I", INCLUDE, "-I", CSRC]

@@ -24,7 +24,7 @@ def test_struct_layouts():
     assert ctypes.sizeof(abi.flce_grad) == 56
     assert ctypes.sizeof(abi.flce_beam_problem) == 80
     assert ctypes.sizeof(abi.flce_beam_state) == 88
-    assert ctypes.sizeof(abi.flce_qproblem) == 72
+    assert ctypes.sizeof(abi.flce_qproblem) == 80
 
 
 # ------------------------------------------------------------- gradients
@@ -184,7 +184,8 @@ def test_beam_python_refusals():
 # ------------------------------------------------------------------ 8 bits
 def _qlinear(ws_bytes=1 << 40, workspace=FAKE, **kw):
     prob = dict(n=5, h=64, v=100, x_pitch=64, weight_pitch=64, out_pitch=100, x_dtype=0,
-                out_dtype=0, bias_dtype=0, has_bias=0, logit_scale=1.0, softcap=0.0)
+                out_dtype=0, bias_dtype=0, has_bias=0, logit_scale=1.0, softcap=0.0, flags=0,
+                reserved=0)
     ptr = dict(x=FAKE, x_scale=None, weight=FAKE, weight_scale=FAKE, bias=None, out=FAKE,
                err_word=None)
     for k in kw:
@@ -199,10 +200,10 @@ def test_qlinear_refusals():
                 dict(x_pitch=63), dict(weight_pitch=63), dict(out_pitch=99),
                 dict(logit_scale=math.nan), dict(softcap=math.inf), dict(x=None),
                 dict(weight=None), dict(weight_scale=None), dict(out=None), dict(x_scale=FAKE),
-                dict(x_dtype=abi.FLCE_Q_I8)):
+                dict(x_dtype=abi.FLCE_Q_I8), dict(flags=2), dict(reserved=1)):
         assert _qlinear(**bad) == INVALID, bad
     for bad in (dict(h=0), dict(h=131072, x_pitch=131072, weight_pitch=131072),
-                dict(x=FAKE + 2), dict(out=FAKE + 1), dict(weight_scale=FAKE + 2),
+                dict(x=FAKE + 2), dict(weight=FAKE + 8), dict(out=FAKE + 1), dict(weight_scale=FAKE + 2),
                 dict(has_bias=1, bias=FAKE + 2)):
         assert _qlinear(**bad) == UNSUPPORTED, bad
     assert _qlinear(ws_bytes=16) == WORKSPACE
