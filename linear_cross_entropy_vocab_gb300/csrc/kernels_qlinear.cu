@@ -22,12 +22,12 @@
 // `nt` rows of x, a multiple of 16 (32) that the launch chooses so that the
 // last tile is not mostly empty. A CTA stays on its SM and takes tile after
 // tile. Tensor memory: columns [0, 256) the accumulators (two when nt <= 128,
-// so that one drains while the other fills), [256, 512) eight 64-deep slices
+// so that one drains while the other fills), [256, 512) four 128-deep slices
 // of widened weight.
 //
 // Roles (19 warps): 0 loads the weight, 1 issues the MMAs, 2 loads x, 3-10
-// widen (two groups of four; each takes 64 of a stage's 128 bytes), 11-18
-// run the epilogue (two per lane quarter, half of the columns each).
+// widen (two groups of four that take 128-byte stages in turn), 11-18 run the
+// epilogue (two per lane quarter, half of the columns each).
 #include <cstdint>
 
 #include <cuda_bf16.h>
@@ -41,11 +41,12 @@ namespace {
 
 constexpr int kWStageBytes = 128 * 128;  // 128 weight rows x 128 bytes
 constexpr int kMaxWStages = 12;
-constexpr int kMaxXStages = 24;
-constexpr int kASlots = 8;
-constexpr int kACols = 32;        // tensor-memory columns of a 64-deep slice
+constexpr int kMaxXStages = kMaxWStages;
+constexpr int kASlots = 4;
+constexpr int kACols = 64;        // tensor-memory columns of a 128-deep slice
 constexpr int kABase = 256;       // first of them
-constexpr int kWidenWarps = 8;
+constexpr int kWidenGroups = 2;
+constexpr int kWidenWarps = 4 * kWidenGroups;
 constexpr int kEpilogueWarps = 8;
 constexpr int kFirstWiden = 3;
 constexpr int kFirstEpilogue = kFirstWiden + kWidenWarps;
@@ -87,14 +88,17 @@ __device__ __forceinline__ void tmem_store_32cols(uint32_t taddr, const uint32_t
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
       "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n\t"
-      "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
       "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
       "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
       "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
+}
+
+__device__ __forceinline__ void tmem_store_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
 // Bytes (0, 2) and (1, 3) of a word of four signed 8-bit integers as halves.
@@ -141,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ Ctl ctl;
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
   const uint32_t x_base = base + static_cast<uint32_t>(p.w_stages) * kWStageBytes;
-  const uint32_t x_bytes = static_cast<uint32_t>(p.nt / CG) * 128u;
+  const uint32_t x_bytes = static_cast<uint32_t>(p.nt / CG) * 128u;  // of one 64-deep box
   const int warp = static_cast<int>(threadIdx.x >> 5);
   const int lane = static_cast<int>(threadIdx.x & 31);
   const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;
@@ -155,14 +159,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.w_stages; ++s) {
       mbar_init(smem_addr(&ctl.w_full[s]), 1);
-      mbar_init(smem_addr(&ctl.w_empty[s]), kWidenWarps);
+      mbar_init(smem_addr(&ctl.w_empty[s]), 4);
     }
     for (int s = 0; s < p.x_stages; ++s) {
       mbar_init(smem_addr(&ctl.x_full[s]), 1);
       mbar_init(smem_addr(&ctl.x_empty[s]), 1);
     }
     for (int s = 0; s < kASlots; ++s) {
-      mbar_init(smem_addr(&ctl.a_full[s]), (kWidenWarps / 2) * CG);
+      mbar_init(smem_addr(&ctl.a_full[s]), 4 * CG);
       mbar_init(smem_addr(&ctl.a_empty[s]), 1);
     }
     for (int s = 0; s < 2; ++s) {
@@ -194,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after_sync();
   const uint32_t tmem = ctl.tmem_base;
   const int bufs = p.nt <= 128 ? 2 : 1;
-  const int w_iters = (p.k_blocks + 1) / 2;  // 128-byte stages of a tile
+  const int k_iters = (p.k_blocks + 1) / 2;  // 128-deep stages of a tile; the last may be half
 
   if (warp == 0) {
     if (lane == 0) {
@@ -204,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int u = unit0; ok && u < total; u += units) {
         const int row = (u / p.n_tiles) * (128 * CG) + static_cast<int>(rank) * 128;
-        for (int i = 0; i < w_iters; ++i) {
+        for (int i = 0; i < k_iters; ++i) {
           if (!mbar_wait(smem_addr(&ctl.w_empty[s]), phase ^ 1u, abort_flag, err_word)) {
             ok = false;
             break;
@@ -233,18 +237,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int u = unit0; ok && u < total; u += units) {
         const int row = (u % p.n_tiles) * p.nt + static_cast<int>(rank) * (p.nt / CG);
-        for (int k = 0; k < p.k_blocks; ++k) {
+        for (int i = 0; i < k_iters; ++i) {
           if (!wait_bar<CG>(smem_addr(&ctl.x_empty[s]), phase ^ 1u, abort_flag, err_word)) {
             ok = false;
             break;
           }
           const uint32_t local = smem_addr(&ctl.x_full[s]);
-          const uint32_t dst = x_base + static_cast<uint32_t>(s) * x_bytes;
-          if (leader) mbar_arrive_expect_tx(local, CG * x_bytes);
-          if constexpr (CG == 1)
-            tma_load_2d(dst, &p.x_map, local, k * 64, row);
-          else
-            tma_load_2d_pair(dst, &p.x_map, map_to_rank(local, 0), k * 64, row);
+          const int boxes = 2 * i + 1 < p.k_blocks ? 2 : 1;
+          if (leader) mbar_arrive_expect_tx(local, static_cast<uint32_t>(boxes) * CG * x_bytes);
+          for (int j = 0; j < boxes; ++j) {
+            const uint32_t dst = x_base + static_cast<uint32_t>(2 * s + j) * x_bytes;
+            if constexpr (CG == 1)
+              tma_load_2d(dst, &p.x_map, local, (2 * i + j) * 64, row);
+            else
+              tma_load_2d_pair(dst, &p.x_map, map_to_rank(local, 0), (2 * i + j) * 64, row);
+          }
           armed |= 1u << s;
           last_phase = (last_phase & ~(1u << s)) | (phase << s);
           if (++s == p.x_stages) {
@@ -274,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after_sync();
         const uint32_t d = tmem + static_cast<uint32_t>(buf * 128);
-        for (int k = 0; k < p.k_blocks; ++k) {
+        for (int i = 0; i < k_iters; ++i) {
           if (!wait_bar<CG>(smem_addr(&ctl.x_full[xs]), x_phase, abort_flag, err_word) ||
               !wait_bar<CG>(smem_addr(&ctl.a_full[as]), a_phase, abort_flag, err_word)) {
             ok = false;
@@ -282,11 +289,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc_fence_after_sync();
           const uint32_t a = tmem + static_cast<uint32_t>(kABase + as * kACols);
-          const uint32_t b = x_base + static_cast<uint32_t>(xs) * x_bytes;
+          const uint32_t b = x_base + static_cast<uint32_t>(2 * xs) * x_bytes;
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             umma_ts<CG>(d, a + static_cast<uint32_t>(kk * 8), smem_desc_sw128(b + kk * 32, 16, 1024),
-                        idesc, (k | kk) != 0 ? 1u : 0u);
+                        idesc, (i | kk) != 0 ? 1u : 0u);
+          if (2 * i + 1 < p.k_blocks) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma_ts<CG>(d, a + static_cast<uint32_t>(32 + kk * 8),
+                          smem_desc_sw128(b + x_bytes + kk * 32, 16, 1024), idesc, 1u);
+          }
           commit<CG>(smem_addr(&ctl.x_empty[xs]));
           commit<CG>(smem_addr(&ctl.a_empty[as]));
           if (++xs == p.x_stages) {
@@ -311,55 +324,51 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int group = (warp - kFirstWiden) >> 2;
     const int row = quarter * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-    int s = 0;
-    uint32_t phase = 0;
-    uint32_t block0 = 0;  // 64-deep blocks of the tiles before this one
     bool ok = true;
-    for (int u = unit0; ok && u < total; u += units, block0 += static_cast<uint32_t>(p.k_blocks)) {
-      for (int i = 0; i < w_iters; ++i) {
-        ok = mbar_wait(smem_addr(&ctl.w_full[s]), phase, abort_flag, err_word);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
-        const int k = 2 * i + group;
-        const bool some = k < p.k_blocks;
-        uint32_t w[16];
-        if (some) {
-          // 16-byte piece c of a row lies at c xor (row mod 8): TMA's 128-byte swizzle
-          const uint32_t at = base + static_cast<uint32_t>(s) * kWStageBytes +
-                              static_cast<uint32_t>(row) * 128u;
+    // stages of all this CTA's tiles, counted through; group g takes g, g + 2, ...
+    const int64_t stages =
+        static_cast<int64_t>(total > unit0 ? (total - unit0 - 1) / units + 1 : 0) * k_iters;
+    int s = group, as = group;
+    uint32_t phase = 0, a_phase = 1;
+    for (int64_t i = group; i < stages; i += kWidenGroups) {
+      ok = mbar_wait(smem_addr(&ctl.w_full[s]), phase, abort_flag, err_word);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      // 16-byte piece c of a row lies at c xor (row mod 8): TMA's 128-byte swizzle
+      const uint32_t at = base + static_cast<uint32_t>(s) * kWStageBytes +
+                          static_cast<uint32_t>(row) * 128u;
+      uint32_t w[32];
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(w[4 * c]), "=r"(w[4 * c + 1]), "=r"(w[4 * c + 2]),
-                           "=r"(w[4 * c + 3])
-                         : "r"(at + static_cast<uint32_t>(((group * 4 + c) ^ (row & 7)) * 16))
-                         : "memory");
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&ctl.w_empty[s]));
-        if (++s == p.w_stages) {
-          s = 0;
-          phase ^= 1u;
-        }
-        if (!some) continue;
-        uint32_t h[32];
+      for (int c = 0; c < 8; ++c)
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[4 * c]), "=r"(w[4 * c + 1]), "=r"(w[4 * c + 2]), "=r"(w[4 * c + 3])
+                     : "r"(at + static_cast<uint32_t>((c ^ (row & 7)) * 16))
+                     : "memory");
+      uint32_t h[32];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) widen(w[j], h[2 * j], h[2 * j + 1]);
-        const uint32_t block = block0 + static_cast<uint32_t>(k);
-        const uint32_t as = block % kASlots;
-        ok = wait_bar<CG>(smem_addr(&ctl.a_empty[as]), ((block / kASlots) & 1u) ^ 1u, abort_flag,
-                          err_word);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after_sync();
-        tmem_store_32cols(tmem + lanes + kABase + as * kACols, h);
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) arrive_leader<CG>(smem_addr(&ctl.a_full[as]), leader);
+      for (int j = 0; j < 16; ++j) widen(w[j], h[2 * j], h[2 * j + 1]);
+      ok = wait_bar<CG>(smem_addr(&ctl.a_empty[as]), a_phase, abort_flag, err_word);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&ctl.w_empty[s]));  // all lanes have read their bytes
+      tc_fence_after_sync();
+      const uint32_t dst = tmem + lanes + static_cast<uint32_t>(kABase + as * kACols);
+      tmem_store_32cols(dst, h);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) widen(w[16 + j], h[2 * j], h[2 * j + 1]);
+      tmem_store_32cols(dst + 32, h);
+      tmem_store_wait();
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) arrive_leader<CG>(smem_addr(&ctl.a_full[as]), leader);
+      s += kWidenGroups;
+      if (s >= p.w_stages) {
+        s -= p.w_stages;
+        phase ^= 1u;
+      }
+      as += kWidenGroups;
+      if (as >= kASlots) {
+        as -= kASlots;
+        a_phase ^= 1u;
       }
     }
   } else {
@@ -388,24 +397,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       // this warp's 32-column chunks: the first or the second half of them
       const int c0 = half == 0 ? 0 : (chunks + 1) / 2;
       const int c1 = half == 0 ? (chunks + 1) / 2 : chunks;
+      if (c0 >= c1) {
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) arrive_leader<CG>(smem_addr(&ctl.acc_empty[buf]), leader);
+      }
       for (int c = c0; c < c1; ++c) {
         float z[32];
         tmem_load_32cols(tmem + lanes + static_cast<uint32_t>(buf * 128 + c * 32), z);
+        if (c == c1 - 1) {  // the accumulator has been read
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) arrive_leader<CG>(smem_addr(&ctl.acc_empty[buf]), leader);
+        }
         const int64_t n = n0 + c * 32;
-        T* o = out + n * p.out_pitch + v;
         const int m = cols - c * 32;
+        const float xs = lane < m ? __ldg(p.x_scale + n + lane) : 0.0f;
+        T* o = out + n * p.out_pitch + v;
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
-          if (j < m) {
-            const float x = p.xf(z[j] * ws * __ldg(p.x_scale + n + j), b);
-            if (mine) store(o, x);
-            o += p.out_pitch;
-          }
+          const float x = p.xf(z[j] * ws * __shfl_sync(0xffffffffu, xs, j), b);
+          if (mine && j < m) store(o, x);
+          o += p.out_pitch;
         }
       }
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) arrive_leader<CG>(smem_addr(&ctl.acc_empty[buf]), leader);
     }
   }
 
@@ -431,7 +446,7 @@ cudaError_t launch_typed(QLinearTcParams p, int sms, cudaStream_t s) {
   int w = kSmemBudget / (kWStageBytes + 2 * x_bytes);
   if (w > kMaxWStages) w = kMaxWStages;
   p.w_stages = w;
-  p.x_stages = 2 * w;
+  p.x_stages = w;
   const int smem = w * (kWStageBytes + 2 * x_bytes) + 1024;
   auto kern = qlinear_kernel<CG, T>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
