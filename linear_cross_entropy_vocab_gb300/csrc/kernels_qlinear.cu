@@ -112,6 +112,17 @@ __device__ __forceinline__ void widen(uint32_t w, uint32_t& even, uint32_t& odd)
   odd = *reinterpret_cast<const uint32_t*>(&oh);
 }
 
+// True on one lane of a converged warp, which the compiler knows to be one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
 // An mbarrier arrive on the pair's even CTA.
 template <int CG>
 __device__ __forceinline__ void arrive_leader(uint32_t bar, bool leader) {
@@ -146,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
   const uint32_t x_base = base + static_cast<uint32_t>(p.w_stages) * kWStageBytes;
   const uint32_t x_bytes = static_cast<uint32_t>(p.nt / CG) * 128u;  // of one 64-deep box
-  const int warp = static_cast<int>(threadIdx.x >> 5);
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
   const int lane = static_cast<int>(threadIdx.x & 31);
   const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;
   const bool leader = rank == 0;
@@ -265,9 +276,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (armed & (1u << q)) drain_wait(smem_addr(&ctl.x_full[q]), (last_phase >> q) & 1u);
     }
   } else if (warp == 1) {
-    if (lane == 0 && leader) {
+    if (leader) {
       // ------------------------------------------------ MMA issuer
+      // The whole warp walks the stages and one elected lane issues: the
+      // operands are then uniform registers, and an MMA takes 9 cycles to
+      // issue. From code that one lane runs alone it takes 46, more than a
+      // product with few rows of x.
       const uint32_t idesc = idesc_f16kind_f32(128 * CG, p.nt, 0, 0, 0u);
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint64_t desc0 = smem_desc_sw128(__shfl_sync(0xffffffffu, x_base, 0), 16, 1024);
+      const uint32_t box = x_bytes >> 4;  // of a 64-deep box, in descriptor units
       int xs = 0, as = 0;
       uint32_t x_phase = 0, a_phase = 0;
       bool ok = true;
@@ -275,33 +293,40 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int u = unit0; ok && u < total; u += units, ++it) {
         const int buf = bufs == 2 ? it & 1 : 0;
         const uint32_t use = static_cast<uint32_t>(bufs == 2 ? it >> 1 : it) & 1u;
-        if (!wait_bar<CG>(smem_addr(&ctl.acc_empty[buf]), use ^ 1u, abort_flag, err_word)) {
+        ok = wait_bar<CG>(smem_addr(&ctl.acc_empty[buf]), use ^ 1u, abort_flag, err_word);
+        if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
         }
         tc_fence_after_sync();
-        const uint32_t d = tmem + static_cast<uint32_t>(buf * 128);
+        const uint32_t d = tm + static_cast<uint32_t>(buf * 128);
         for (int i = 0; i < k_iters; ++i) {
-          if (!wait_bar<CG>(smem_addr(&ctl.x_full[xs]), x_phase, abort_flag, err_word) ||
-              !wait_bar<CG>(smem_addr(&ctl.a_full[as]), a_phase, abort_flag, err_word)) {
+          ok = wait_bar<CG>(smem_addr(&ctl.x_full[xs]), x_phase, abort_flag, err_word) &&
+               wait_bar<CG>(smem_addr(&ctl.a_full[as]), a_phase, abort_flag, err_word);
+          if (!__all_sync(0xffffffffu, ok)) {
             ok = false;
             break;
           }
           tc_fence_after_sync();
-          const uint32_t a = tmem + static_cast<uint32_t>(kABase + as * kACols);
-          const uint32_t b = x_base + static_cast<uint32_t>(2 * xs) * x_bytes;
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_ts<CG>(d, a + static_cast<uint32_t>(kk * 8), smem_desc_sw128(b + kk * 32, 16, 1024),
-                        idesc, (i | kk) != 0 ? 1u : 0u);
-          if (2 * i + 1 < p.k_blocks) {
+          if (elect_one()) {
+            const uint32_t a = tm + static_cast<uint32_t>(kABase + as * kACols);
+            const uint64_t b = desc0 + static_cast<uint64_t>(static_cast<uint32_t>(2 * xs) * box);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              umma_ts<CG>(d, a + static_cast<uint32_t>(32 + kk * 8),
-                          smem_desc_sw128(b + x_bytes + kk * 32, 16, 1024), idesc, 1u);
+              umma_ts<CG>(d, a + static_cast<uint32_t>(kk * 8), b + static_cast<uint64_t>(kk * 2),
+                          idesc, (i | kk) != 0 ? 1u : 0u);
+            if (2 * i + 1 < p.k_blocks) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                umma_ts<CG>(d, a + static_cast<uint32_t>(32 + kk * 8),
+                            b + static_cast<uint64_t>(box + static_cast<uint32_t>(kk * 2)), idesc,
+                            1u);
+            }
+            commit<CG>(smem_addr(&ctl.x_empty[xs]));
+            commit<CG>(smem_addr(&ctl.a_empty[as]));
+            if (i == k_iters - 1) commit<CG>(smem_addr(&ctl.acc_full[buf]));
           }
-          commit<CG>(smem_addr(&ctl.x_empty[xs]));
-          commit<CG>(smem_addr(&ctl.a_empty[as]));
+          __syncwarp();
           if (++xs == p.x_stages) {
             xs = 0;
             x_phase ^= 1u;
@@ -311,10 +336,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             a_phase ^= 1u;
           }
         }
-        if (ok) commit<CG>(smem_addr(&ctl.acc_full[buf]));
       }
-      commit<CG>(smem_addr(&ctl.mma_done));
-      drain_wait(smem_addr(&ctl.mma_done), 0);
+      if (elect_one()) {
+        commit<CG>(smem_addr(&ctl.mma_done));
+        drain_wait(smem_addr(&ctl.mma_done), 0);
+      }
     } else if (lane == 0 && CG == 2) {
       drain_wait(smem_addr(&ctl.mma_done), 0);  // the even CTA's MMAs write this CTA's TMEM
     }
@@ -376,49 +402,65 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int quarter = warp & 3;
     const int half = (warp - kFirstEpilogue) >> 2;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-    T* const out = static_cast<T*>(p.out);
+    // an address is a uniform pointer to a row of the tile plus this lane's offset
+    const uint32_t in_tile = rank * 128u + static_cast<uint32_t>(quarter * 32 + lane);
+    const int64_t pitch = p.out_pitch * static_cast<int64_t>(sizeof(T));
     grid_dependency_wait();  // x_scale may come from the kernel before this one
     int it = 0;
     for (int u = unit0; u < total; u += units, ++it) {
       const int buf = bufs == 2 ? it & 1 : 0;
       const uint32_t use = static_cast<uint32_t>(bufs == 2 ? it >> 1 : it) & 1u;
-      const int64_t v = static_cast<int64_t>(u / p.n_tiles) * (128 * CG) +
-                        static_cast<int64_t>(rank) * 128 + quarter * 32 + lane;
+      const int64_t v0 = static_cast<int64_t>(u / p.n_tiles) * (128 * CG);
       const int64_t n0 = static_cast<int64_t>(u % p.n_tiles) * p.nt;
-      const bool mine = v < p.v;
-      const float ws = mine ? __ldg(p.weight_scale + v) : 0.0f;
-      const float b = mine && p.bias != nullptr ? bias_at(p.bias, p.bias_dtype, v) : 0.0f;
-      const bool ok =
-          wait_bar<CG>(smem_addr(&ctl.acc_full[buf]), use, abort_flag, err_word);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      tc_fence_after_sync();
+      const bool mine = v0 + in_tile < p.v;
+      // u_ij = acc * x_scale * (weight_scale * logit_scale) + bias * logit_scale
+      const float ws = (mine ? __ldg(p.weight_scale + v0 + in_tile) : 0.0f) * p.xf.scale;
+      const float b = mine && p.bias != nullptr
+                          ? bias_at(p.bias, p.bias_dtype, v0 + in_tile) * p.xf.scale
+                          : 0.0f;
       const int cols = static_cast<int>(p.n - n0 < p.nt ? p.n - n0 : p.nt);
       const int chunks = (cols + 31) / 32;
       // this warp's 32-column chunks: the first or the second half of them
       const int c0 = half == 0 ? 0 : (chunks + 1) / 2;
       const int c1 = half == 0 ? (chunks + 1) / 2 : chunks;
-      if (c0 >= c1) {
+      auto scales = [&](int c) {
+        return c * 32 + lane < cols ? __ldg(p.x_scale + n0 + c * 32 + lane) : 0.0f;
+      };
+      float xs_next = scales(c0);
+      const bool ok = wait_bar<CG>(smem_addr(&ctl.acc_full[buf]), use, abort_flag, err_word);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after_sync();
+      auto release = [&] {
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) arrive_leader<CG>(smem_addr(&ctl.acc_empty[buf]), leader);
-      }
+      };
+      if (c0 >= c1) release();
       for (int c = c0; c < c1; ++c) {
         float z[32];
         tmem_load_32cols(tmem + lanes + static_cast<uint32_t>(buf * 128 + c * 32), z);
-        if (c == c1 - 1) {  // the accumulator has been read
-          tc_fence_before_sync();
-          __syncwarp();
-          if (lane == 0) arrive_leader<CG>(smem_addr(&ctl.acc_empty[buf]), leader);
-        }
-        const int64_t n = n0 + c * 32;
+        if (c == c1 - 1) release();  // the accumulator has been read
+        const float xs = xs_next;
+        if (c + 1 < c1) xs_next = scales(c + 1);
         const int m = cols - c * 32;
-        const float xs = lane < m ? __ldg(p.x_scale + n + lane) : 0.0f;
-        T* o = out + n * p.out_pitch + v;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const float x = p.xf(z[j] * ws * __shfl_sync(0xffffffffu, xs, j), b);
-          if (mine && j < m) store(o, x);
-          o += p.out_pitch;
+        for (int j = 0; j < 32; ++j) z[j] = fmaf(z[j] * __shfl_sync(0xffffffffu, xs, j), ws, b);
+        if (p.xf.has_cap) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) z[j] = p.xf.softcap * tanh_exp2(z[j] * p.xf.inv_softcap);
+        }
+        uint8_t* const row0 = static_cast<uint8_t*>(p.out) +
+                              ((n0 + c * 32) * p.out_pitch + v0) * static_cast<int64_t>(sizeof(T));
+        const uint32_t off = in_tile * static_cast<uint32_t>(sizeof(T));
+        if (mine) {
+          if (m >= 32) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) store(reinterpret_cast<T*>(row0 + j * pitch + off), z[j]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (j < m) store(reinterpret_cast<T*>(row0 + j * pitch + off), z[j]);
+          }
         }
       }
     }
