@@ -25,9 +25,11 @@
 // so that one drains while the other fills), [256, 512) four 128-deep slices
 // of widened weight.
 //
-// Roles (19 warps): 0 loads the weight, 1 issues the MMAs, 2 loads x, 3-10
-// widen (two groups of four that take 128-byte stages in turn), 11-18 run the
-// epilogue (two per lane quarter, half of the columns each).
+// Roles (23 warps): 0 loads the weight, 1 issues the MMAs, 2 loads x, 3-14
+// widen (three groups of four that take 128-byte stages in turn: with two the
+// widening took longer than the MMAs, 5.5 ms against 4.7 for 8192 rows of the
+// Llama-3 head; a fourth gains nothing), 15-22 run the epilogue (two per lane
+// quarter, half of the columns each).
 #include <cstdint>
 
 #include <cuda_bf16.h>
@@ -45,13 +47,13 @@ constexpr int kMaxXStages = kMaxWStages;
 constexpr int kASlots = 4;
 constexpr int kACols = 64;        // tensor-memory columns of a 128-deep slice
 constexpr int kABase = 256;       // first of them
-constexpr int kWidenGroups = 2;
+constexpr int kWidenGroups = 3;
 constexpr int kWidenWarps = 4 * kWidenGroups;
 constexpr int kEpilogueWarps = 8;
 constexpr int kFirstWiden = 3;
 constexpr int kFirstEpilogue = kFirstWiden + kWidenWarps;
 constexpr int kThreads = 32 * (kFirstEpilogue + kEpilogueWarps);
-constexpr int kSmemBudget = 220 * 1024;
+constexpr int kSmemBudget = 224 * 1024;
 
 struct Ctl {
   uint64_t w_full[kMaxWStages], w_empty[kMaxWStages];
@@ -484,12 +486,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int CG, class T>
 cudaError_t launch_typed(QLinearTcParams p, int sms, cudaStream_t s) {
-  const int x_bytes = p.nt / CG * 128;
-  int w = kSmemBudget / (kWStageBytes + 2 * x_bytes);
-  if (w > kMaxWStages) w = kMaxWStages;
+  const int x_bytes = 2 * (p.nt / CG * 128);
+  // The most weight stages that leave room for four of x and that are safe.
+  // A widening group that waits for stage j has to find stage j - w of the
+  // same buffer landed, or the parity that it waits for is the one before
+  // last. Copies land in any order, so this holds where j - w was the group's
+  // own (w a multiple of the groups), or where an MMA on a later stage is done:
+  // the group's last stage, j - groups, had its slot freed by the MMAs up to
+  // j - groups - slots.
+  int w = kMaxWStages;
+  while (w > kWidenGroups &&
+         ((w % kWidenGroups != 0 && w < kWidenGroups + kASlots) ||
+          kSmemBudget - w * kWStageBytes < 4 * x_bytes))
+    --w;
   p.w_stages = w;
-  p.x_stages = w;
-  const int smem = w * (kWStageBytes + 2 * x_bytes) + 1024;
+  p.x_stages = (kSmemBudget - w * kWStageBytes) / x_bytes;
+  if (p.x_stages > kMaxXStages) p.x_stages = kMaxXStages;
+  const int smem = w * kWStageBytes + p.x_stages * x_bytes + 1024;
   auto kern = qlinear_kernel<CG, T>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        kSmemBudget + 1024);
