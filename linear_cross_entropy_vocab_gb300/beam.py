@@ -13,6 +13,7 @@ from typing import Iterable, NamedTuple, Optional, Union
 import torch
 
 from . import abi
+from ._stream import on_device, raw_stream
 
 __all__ = ["BeamSelection", "beam_select", "beam_reorder_"]
 
@@ -112,12 +113,12 @@ def beam_select(logits: torch.Tensor, beam_scores: torch.Tensor,
     if m < 1:
         raise ValueError("num_candidates must be at least 1")
     scores = torch.empty(b, m, dtype=torch.float32, device=dev)
-    chosen = torch.empty(2, b, m, dtype=torch.int64, device=dev)
-    parents, tokens = chosen.unbind(0)
-    with torch.cuda.device(dev):
+    parents = torch.empty(b, m, dtype=torch.int64, device=dev)
+    tokens = torch.empty(b, m, dtype=torch.int64, device=dev)
+    with on_device(dev):
         ws_bytes = abi.flce_beam_select_workspace_size(prob)
         ws = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=dev)
-        stream = torch.cuda.current_stream(dev).cuda_stream
+        stream = raw_stream(dev)
         abi.flce_beam_select(prob, logits.data_ptr(), beam_scores.data_ptr(), fin_ptr, ok_ptr,
                              scores.data_ptr(), parents.data_ptr(), tokens.data_ptr(),
                              _err_ptr(err_word, dev), ws.data_ptr(), ws_bytes, stream)
@@ -180,7 +181,7 @@ def beam_reorder_(states: Union[torch.Tensor, Iterable[torch.Tensor]], parents: 
         _on(f"state {i}", t, dev)
         words += _state_words(i, t, dim, b * k)
     table = array.array("q", words)
-    with torch.cuda.device(dev):
-        stream = torch.cuda.current_stream(dev).cuda_stream
+    with on_device(dev):
+        stream = raw_stream(dev)
         abi.flce_beam_reorder(table.buffer_info()[0] if states else None, len(states),
                               parents.data_ptr(), b, k, _err_ptr(err_word, dev), stream)

@@ -11,13 +11,16 @@ namespace {
 
 using namespace flce::host;
 
-// The widest slice is for selections that fill the GPU with it; below two
-// such CTAs for each of the 152 SMs a quarter of the width shortens the call.
-constexpr int64_t kFillCtas = 304;
+// CTAs that a selection is cut into: several waves of the three that an SM
+// holds, so that the tail is short; the fewer, the less there is to choose
+// from afterwards. A call that cannot have so many with large tiles takes
+// small ones.
+constexpr int64_t kSelectCtas = 1368;
+constexpr int64_t kFewCtas = 304;
 
 struct SelectPlan {
   bool large;
-  int64_t splits;
+  int64_t splits, slice_len;
   size_t stats, total;  // offset of the slice statistics; bytes in all
 };
 
@@ -47,8 +50,15 @@ flce_status check_select(const flce_beam_problem* p) {
 SelectPlan plan_select(const flce_beam_problem* p) {
   SelectPlan q;
   const int64_t rows = p->batch * p->beams;
-  q.large = rows * ceil_div(p->v, flce::kSliceLarge) >= kFillCtas;
-  q.splits = ceil_div(p->v, q.large ? flce::kSliceLarge : flce::kSliceSmall);
+  const int64_t es = p->dtype == FLCE_F32 ? 4 : 2;
+  q.large = rows * ceil_div(p->v * es, flce::kTileLargeBytes) >= kFewCtas;
+  const int64_t tile = (q.large ? flce::kTileLargeBytes : flce::kTileSmallBytes) / es;
+  const int64_t tiles = ceil_div(p->v, tile);
+  // slices of whole tiles, as equal as that allows
+  q.splits = std::max<int64_t>(1, std::min(tiles, ceil_div(kSelectCtas, std::max<int64_t>(rows, 1))));
+  q.slice_len = ceil_div(tiles, q.splits) * tile;
+  if (q.splits == tiles) q.slice_len = ceil_div(ceil_div(p->v, tiles), 8) * 8;  // alike
+  q.splits = ceil_div(p->v, q.slice_len);
   q.stats = align_256(static_cast<size_t>(rows * q.splits * p->candidates) * sizeof(uint64_t));
   q.total = q.stats + align_256(static_cast<size_t>(rows * q.splits) * sizeof(float2));
   return q;
@@ -139,6 +149,8 @@ flce_status flce_beam_select(const flce_beam_problem* p, const void* logits,
   if (st != FLCE_OK) return st;
   if (p->batch * p->beams * plan.splits > 0x7fffffffll)
     return fail(FLCE_ERR_UNSUPPORTED, "more than 2^31 row slices");
+  if (p->beams * plan.splits * p->candidates > 0x7fffffffll)
+    return fail(FLCE_ERR_UNSUPPORTED, "more than 2^31 candidates of a prompt's slices");
   int sms = 0;
   st = check_device(&sms);
   if (st != FLCE_OK || p->batch == 0) return st;
@@ -155,6 +167,9 @@ flce_status flce_beam_select(const flce_beam_problem* p, const void* logits,
   k.beams = static_cast<int32_t>(p->beams);
   k.m = static_cast<int32_t>(p->candidates);
   k.splits = static_cast<int32_t>(plan.splits);
+  k.groups = 1;
+  while (k.groups < k.m) k.groups *= 2;
+  k.slice_len = static_cast<int32_t>(plan.slice_len);
   k.v = p->v;
   k.pad_token = p->pad_token;
   k.keys = static_cast<uint64_t*>(workspace);

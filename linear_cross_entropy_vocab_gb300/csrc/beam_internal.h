@@ -13,9 +13,11 @@ constexpr int kBeamMaxCandidates = 256;
 constexpr int kBeamMaxBeams = 64;  // of a reordering; a selection takes more (its scores are staged)
 constexpr int kBeamMaxSelectBeams = 1024;
 
-// Logits per thread of a selection CTA (256 threads): a slice of 2048 or of 8192.
-constexpr int kSliceSmall = 2048;
-constexpr int kSliceLarge = 8192;
+// A selection CTA (256 threads) holds tiles of 1 or kPiecesLarge pieces of 16
+// bytes for each thread.
+constexpr int kPiecesLarge = 4;
+constexpr int kTileSmallBytes = 256 * 16;
+constexpr int kTileLargeBytes = kTileSmallBytes * kPiecesLarge;
 
 struct BeamSelectParams {
   const void* logits;
@@ -25,6 +27,8 @@ struct BeamSelectParams {
   const float* beam_scores;    // [B][K]
   const uint8_t* finished;     // [B][K] or null
   int32_t batch, beams, m, splits;
+  int32_t slice_len;           // logits of a slice, a multiple of 8 (the last may be shorter)
+  int32_t groups;              // the power of two from m on, at most 256
   int64_t v;
   int64_t pad_token;
   // per (row, slice): its M best keys, best first, 0 where there are fewer,

@@ -13,16 +13,23 @@
 // K x slices x M survivors in 64 bits (what is chosen hangs on comparisons
 // that 32 bits would decide by rounding), and the M best of them.
 //
-// Finding the M best without sorting: the threads are put into G >= M groups;
-// the smallest of the groups' maxima has at least M values at or above it, and
+// Finding the M best of a tile: the threads are put into G >= M groups; the
+// smallest of the groups' maxima has at least M values at or above it, and
 // about G ln G of them for values in no particular order. Those few go into a
-// buffer, and a key's place is the number of larger keys in it. Keys hold the
-// value's order and the complement of the index, so they are all different
-// and ties go to the lowest index. Where the buffer would overflow (thousands
-// of equal logits at the top), the M best are taken one after the other.
+// buffer and are sorted there: up to 128 by counting, for each key, the keys
+// above it, more by a bitonic network. Keys hold the value's order and the
+// complement of the index, so they are all different and ties go to the lowest
+// index. A slice is several tiles; after 1, 2, 4, ... of them the threshold
+// becomes the M-th best so far, so that about M values pass it between two
+// such points. Where the buffer would overflow (thousands of equal logits at
+// the top), the M best of the slice are taken one after the other.
 //
-// Bound: the logits are read once. A thread holds its part of the slice in
-// registers, so that nothing is read a second time.
+// Bound: the logits are read once, each thread's 16-byte pieces of the next
+// tile while it works on this one. Per logit there are two additions, a
+// product, an exponential and a maximum; whether a value reaches the threshold
+// is asked once for a piece. Issuing those bounds large calls: 64 x 8 rows of
+// 128256 fp32 logits take 59 us, 4.1 TB/s, with half of the issue slots used;
+// small ones are bound by the chain from the loads through two launches.
 //
 // Reordering. state[b K + j] = state[b K + parent_bj], in place: a thread owns
 // the same 16 bytes (or less, by alignment) of all K beams of a prompt, reads
@@ -41,7 +48,9 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBuffer = 2048;  // keys that may pass a slice's threshold
+constexpr int kBuffer = 4096;  // keys that may pass a slice's threshold
+constexpr int kChoiceBuffer = 2048;
+constexpr int kHeld = 4;       // candidates that a thread of the choice keeps in registers
 
 // Order-preserving bits of a float that is not NaN (-0 counts as +0).
 __device__ __forceinline__ uint32_t order_bits(float x) {
@@ -55,22 +64,24 @@ __device__ __forceinline__ uint64_t make_key(float x, uint32_t index) {
   return (static_cast<uint64_t>(order_bits(x)) << 32) | (0xffffffffu - index);
 }
 
+// 16 bytes of logits as floats, and one logit.
 template <class T>
-struct Load8;
+struct Piece;
 template <>
-struct Load8<float> {
-  static __device__ __forceinline__ void vec(const float* p, float (&x)[8]) {
-    const float4 a = __ldcs(reinterpret_cast<const float4*>(p));
-    const float4 b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+struct Piece<float> {
+  static constexpr int kElems = 4;
+  static __device__ __forceinline__ void unpack(const uint4& q, float (&x)[4]) {
+    x[0] = __uint_as_float(q.x);
+    x[1] = __uint_as_float(q.y);
+    x[2] = __uint_as_float(q.z);
+    x[3] = __uint_as_float(q.w);
   }
-  static __device__ __forceinline__ float one(const float* p) { return __ldcs(p); }
+  static __device__ __forceinline__ float one(const float* p) { return *p; }
 };
 template <>
-struct Load8<__nv_bfloat16> {
-  static __device__ __forceinline__ void vec(const __nv_bfloat16* p, float (&x)[8]) {
-    const uint4 q = __ldcs(reinterpret_cast<const uint4*>(p));
+struct Piece<__nv_bfloat16> {
+  static constexpr int kElems = 8;
+  static __device__ __forceinline__ void unpack(const uint4& q, float (&x)[8]) {
     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -83,9 +94,9 @@ struct Load8<__nv_bfloat16> {
   }
 };
 template <>
-struct Load8<__half> {
-  static __device__ __forceinline__ void vec(const __half* p, float (&x)[8]) {
-    const uint4 q = __ldcs(reinterpret_cast<const uint4*>(p));
+struct Piece<__half> {
+  static constexpr int kElems = 8;
+  static __device__ __forceinline__ void unpack(const uint4& q, float (&x)[8]) {
     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -97,22 +108,41 @@ struct Load8<__half> {
   static __device__ __forceinline__ float one(const __half* p) { return __half2float(*p); }
 };
 
-// A value with its place in the order of all candidates: larger scores first,
-// then lower indices.
+// A score with its place in the order of all candidates: larger scores first,
+// then lower indices. Scores are kept as the order of their 64 bits (integer
+// comparisons; this GPU compares few doubles a cycle).
 struct Scored {
-  double s;
-  uint64_t at;
+  uint64_t s;   // 0: nothing
+  uint64_t at;  // beam in the upper 32 bits, token in the lower
 };
+__device__ __forceinline__ uint64_t order_bits64(double x) {
+  const uint64_t u = static_cast<uint64_t>(__double_as_longlong(x + 0.0));
+  return u ^ ((u >> 63) ? ~0ull : 0x8000000000000000ull);
+}
+__device__ __forceinline__ double from_order_bits64(uint64_t o) {
+  return __longlong_as_double(
+      static_cast<long long>(o ^ ((o >> 63) ? 0x8000000000000000ull : ~0ull)));
+}
 __device__ __forceinline__ bool better(const Scored& a, const Scored& b) {
   return a.s > b.s || (a.s == b.s && a.at < b.at);
 }
 __device__ __forceinline__ bool better(uint64_t a, uint64_t b) { return a > b; }
+__device__ __forceinline__ Scored nothing(const Scored&) { return Scored{0, ~0ull}; }
+__device__ __forceinline__ uint64_t nothing(uint64_t) { return 0; }
 
 __device__ __forceinline__ Scored shfl_xor(const Scored& a, int o) {
   return Scored{__shfl_xor_sync(0xffffffffu, a.s, o), __shfl_xor_sync(0xffffffffu, a.at, o)};
 }
 __device__ __forceinline__ uint64_t shfl_xor(uint64_t a, int o) {
   return __shfl_xor_sync(0xffffffffu, a, o);
+}
+
+// A place in a shared list. Few lanes come here at a time: an atomic of each
+// is shorter than agreeing on one.
+__device__ __forceinline__ uint32_t take_place(int* count) {
+  uint32_t r;
+  asm volatile("atom.shared.add.u32 %0, [%1], 1;" : "=r"(r) : "r"(smem_addr(count)) : "memory");
+  return r;
 }
 
 template <class K>
@@ -132,16 +162,46 @@ __device__ __forceinline__ K block_best(K x, K* warp_buf) {
   return x;
 }
 
-// Places of the n <= kBuffer different keys in buf: out(rank, key) for the
-// ranks below m.
+// Sorts the n keys in buf, which has room for the next power of two: a bitonic
+// network. All threads of the CTA.
+template <class K>
+__device__ __forceinline__ void sort_keys(K* buf, int n) {
+  int len = 256;
+  while (len < n) len <<= 1;
+  for (int i = n + static_cast<int>(threadIdx.x); i < len; i += kThreads) buf[i] = nothing(buf[0]);
+  for (int size = 2; size <= len; size <<= 1)
+    for (int step = size >> 1; step > 0; step >>= 1) {
+      __syncthreads();
+      for (int q = static_cast<int>(threadIdx.x); q < len / 2; q += kThreads) {
+        const int i = 2 * q - (q & (step - 1)), j = i + step;
+        const K x = buf[i], y = buf[j];
+        if (better(y, x) == ((i & size) == 0)) {
+          buf[i] = y;
+          buf[j] = x;
+        }
+      }
+    }
+  __syncthreads();
+}
+
+// The first m of the n different keys in buf (with room for the next power of
+// two), in order:
+// out(rank, key) for the ranks below m and n.
 template <class K, class Out>
-__device__ __forceinline__ void rank_keys(const K* buf, int n, int m, Out out) {
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const K mine = buf[i];
-    int rank = 0;
-    for (int j = 0; j < n; ++j) rank += better(buf[j], mine) ? 1 : 0;
-    if (rank < m) out(rank, mine);
+__device__ __forceinline__ void rank_keys(K* buf, int n, int m, Out out) {
+  if (n <= 128) {
+    const int i = static_cast<int>(threadIdx.x);
+    if (i < n) {
+      const K mine = buf[i];
+      int rank = 0;
+#pragma unroll 8
+      for (int j = 0; j < n; ++j) rank += better(buf[j], mine) ? 1 : 0;
+      if (rank < m) out(rank, mine);
+    }
+    return;
   }
+  sort_keys(buf, n);
+  for (int i = static_cast<int>(threadIdx.x); i < m && i < n; i += kThreads) out(i, buf[i]);
 }
 
 // The warps of a group of 256 / g threads (g a power of two, at most 256) and
@@ -173,149 +233,234 @@ __device__ __forceinline__ uint32_t group_floor(uint32_t x, int g, uint32_t* war
   return t;
 }
 
-__device__ __forceinline__ int groups_for(int m) {
-  int g = 1;
-  while (g < m) g <<= 1;
-  return g;
-}
+// One slice of a row as the threads of a CTA see it; places count from its start.
+template <class T>
+struct Slice {
+  static constexpr int E = Piece<T>::kElems;
+  const T* z;
+  const uint8_t* ok;  // or null
+  int len;
+  bool z16, ok_vec;   // 16-byte (E-byte) loads are aligned
+
+  __device__ __forceinline__ uint4 raw(int v) const {
+    return __ldcs(reinterpret_cast<const uint4*>(z + v));
+  }
+  // What lies past the end, and where the mask says so, is -infinity.
+  __device__ __forceinline__ void mask(int v, float (&x)[E]) const {
+    if (ok_vec && v + E <= len) {
+      uint32_t a[2];
+      a[0] = __ldg(reinterpret_cast<const uint32_t*>(ok + v));
+      a[1] = E == 8 ? __ldg(reinterpret_cast<const uint32_t*>(ok + v) + 1) : 0;
+#pragma unroll
+      for (int j = 0; j < E; ++j)
+        if (((a[j >> 2] >> (8 * (j & 3))) & 0xffu) == 0) x[j] = -INFINITY;
+    } else {
+#pragma unroll
+      for (int j = 0; j < E; ++j)
+        if (v + j < len && ok[v + j] == 0) x[j] = -INFINITY;
+    }
+  }
+  __device__ __forceinline__ void load(int v, float (&x)[E]) const {
+    if (z16 && v + E <= len) {
+      Piece<T>::unpack(raw(v), x);
+    } else {
+#pragma unroll
+      for (int j = 0; j < E; ++j) x[j] = v + j < len ? Piece<T>::one(z + v + j) : -INFINITY;
+    }
+    if (ok != nullptr) mask(v, x);
+  }
+};
 
 // One slice of one row: its M best logits, maximum and sum of exponentials.
-// VECS groups of 8 logits per thread.
-template <class T, int VECS>
-__global__ void __launch_bounds__(kThreads, VECS == 1 ? 6 : 3)
+// A tile is N pieces of 16 bytes per thread; the next tile's are on their way
+// while one is worked on.
+template <class T, int N>
+__global__ void __launch_bounds__(kThreads, N == 1 ? 6 : 3)
     beam_slices_kernel(const BeamSelectParams p) {
+  constexpr int E = Piece<T>::kElems;
+  constexpr int kTile = kThreads * E * N;
   __shared__ uint64_t buf[kBuffer];
+  __shared__ uint64_t kept[kBeamMaxCandidates];
   __shared__ uint64_t warp_key[kWarps];
   __shared__ uint32_t warp_u32[kWarps];
-  __shared__ float warp_f32[kWarps];
+  __shared__ float2 warp_stat[kWarps];
   __shared__ int count;
-  const int64_t row = blockIdx.x / p.splits;
-  const int slice = static_cast<int>(blockIdx.x - row * p.splits);
-  const int b = static_cast<int>(row / p.beams), k = static_cast<int>(row - b * static_cast<int64_t>(p.beams));
+  grid_launch_dependents();
+  const uint32_t row = blockIdx.x / static_cast<uint32_t>(p.splits);
+  const uint32_t slice = blockIdx.x - row * static_cast<uint32_t>(p.splits);
+  const uint32_t b = row / static_cast<uint32_t>(p.beams);
+  const uint32_t k = row - b * static_cast<uint32_t>(p.beams);
   const float score = p.beam_scores[row];
   // a finished beam and one that cannot be continued need none of their logits
   if (p.finished != nullptr && p.finished[row] != 0) return;
   if (score == -INFINITY) return;
-  const T* const z = static_cast<const T*>(p.logits) + b * p.stride_b + k * p.stride_k;
-  const uint8_t* const ok =
-      p.allowed != nullptr ? p.allowed + b * p.allowed_b + k * p.allowed_k : nullptr;
-  const int64_t v0 = static_cast<int64_t>(slice) * (kThreads * 8 * VECS);
-  const bool z16 = (reinterpret_cast<uintptr_t>(z) & 15u) == 0;
-  const bool ok8 = ok != nullptr && (reinterpret_cast<uintptr_t>(ok) & 7u) == 0;
-  float x[VECS][8];
-#pragma unroll
-  for (int i = 0; i < VECS; ++i) {
-    const int64_t v = v0 + (static_cast<int64_t>(i) * kThreads + threadIdx.x) * 8;
-    if (z16 && v + 8 <= p.v) {
-      Load8<T>::vec(z + v, x[i]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[i][j] = v + j < p.v ? Load8<T>::one(z + v + j) : -INFINITY;
-    }
-  }
-  if (ok != nullptr) {
-#pragma unroll
-    for (int i = 0; i < VECS; ++i) {
-      const int64_t v = v0 + (static_cast<int64_t>(i) * kThreads + threadIdx.x) * 8;
-      if (ok8 && v + 8 <= p.v) {
-        const uint2 a = __ldg(reinterpret_cast<const uint2*>(ok + v));
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if ((((j < 4 ? a.x : a.y) >> (8 * (j & 3))) & 0xffu) == 0) x[i][j] = -INFINITY;
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (v + j < p.v && ok[v + j] == 0) x[i][j] = -INFINITY;
-      }
-    }
-  }
+  const int64_t v0 = static_cast<int64_t>(slice) * p.slice_len;
+  const uint32_t v0_32 = static_cast<uint32_t>(v0);
+  Slice<T> in;
+  in.z = static_cast<const T*>(p.logits) + b * p.stride_b + k * p.stride_k + v0;
+  in.ok = p.allowed != nullptr ? p.allowed + b * p.allowed_b + k * p.allowed_k + v0 : nullptr;
+  in.len = static_cast<int>(v0 + p.slice_len < p.v ? p.slice_len : p.v - v0);
+  in.z16 = (reinterpret_cast<uintptr_t>(in.z) & 15u) == 0;
+  in.ok_vec = (reinterpret_cast<uintptr_t>(in.ok) & 3u) == 0;
   if (threadIdx.x == 0) count = 0;
 
-  // maximum (NaN and +infinity make the row invalid: the stats say so)
-  float top = -INFINITY;
-  bool bad = false;
+  // the thread's maximum so far and its sum of e^(z - maximum); NaN and
+  // +infinity make the sum NaN
+  float top = -INFINITY, sum = 0.0f;
+  uint32_t floor_bits = 0;  // below every value's order
+  bool full = false;
+  int tiles = 0;
+  uint4 next[N];
+  const int mine = static_cast<int>(threadIdx.x) * E;
+  // tiles that end at or before this place are loaded ahead
+  const int ahead = in.z16 ? in.len : 0;
+  if (kTile <= ahead) {
 #pragma unroll
-  for (int i = 0; i < VECS; ++i)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      top = fmaxf(top, x[i][j]);
-      bad |= !(x[i][j] < INFINITY);
-    }
-  bad = __syncthreads_or(bad ? 1 : 0) != 0;
-  const int64_t out = row * p.splits + slice;
-  uint64_t* const keys = p.keys + out * p.m;
-  if (bad) {
-    if (threadIdx.x == 0) p.stats[out] = make_float2(NAN, 0.0f);
-    for (int i = threadIdx.x; i < p.m; i += kThreads) keys[i] = 0;
-    return;
+    for (int i = 0; i < N; ++i) next[i] = in.raw(mine + i * kThreads * E);
   }
-  const uint32_t floor_bits = group_floor(order_bits(top), groups_for(p.m), warp_u32);
-  float row_top = top;
+  for (int t0 = 0; t0 < in.len; t0 += kTile) {
+    float x[N][E];
+    if (t0 + kTile <= ahead) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    row_top = fmaxf(row_top, __shfl_xor_sync(0xffffffffu, row_top, o));
-  if ((threadIdx.x & 31) == 0) warp_f32[threadIdx.x >> 5] = row_top;
-  __syncthreads();
+      for (int i = 0; i < N; ++i) Piece<T>::unpack(next[i], x[i]);
+      if (in.ok != nullptr) {
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) row_top = fmaxf(row_top, warp_f32[w]);
+        for (int i = 0; i < N; ++i) in.mask(t0 + mine + i * kThreads * E, x[i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) in.load(t0 + mine + i * kThreads * E, x[i]);
+    }
+    if (t0 + 2 * kTile <= ahead) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) next[i] = in.raw(t0 + kTile + mine + i * kThreads * E);
+    }
+    float piece_top[N], tile_top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      piece_top[i] = x[i][0];
+#pragma unroll
+      for (int j = 1; j < E; ++j) piece_top[i] = fmaxf(piece_top[i], x[i][j]);
+      tile_top = fmaxf(tile_top, piece_top[i]);
+    }
+    if (tile_top > top) {
+      sum *= ex2_approx((top - tile_top) * kLog2e);  // 0 while top is -infinity
+      top = tile_top;
+    }
+    {
+      // the difference first: a rounded maximum times log2(e) would shift
+      // every term alike
+      const float base = top == -INFINITY ? 0.0f : top;
+      float part[2] = {0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int j = 0; j < E; ++j) part[j & 1] += ex2_approx((x[i][j] - base) * kLog2e);
+      sum += part[0] + part[1];
+    }
 
-  // what reaches the threshold, and the sum of exponentials
-  const float at_least = from_order_bits(floor_bits);
-  // the difference first: a rounded row_top * log2(e) would shift every term alike
-  const float base = row_top == -INFINITY ? 0.0f : row_top;
-  float sum = 0.0f;
+    // what reaches the threshold: the M-th best so far, once there are M
+    if (!full) floor_bits = max(floor_bits, group_floor(order_bits(tile_top), p.groups, warp_u32));
+    const float at_least = floor_bits == 0 ? -INFINITY : from_order_bits(floor_bits);
+    if (tile_top >= at_least && tile_top > -INFINITY) {
 #pragma unroll
-  for (int i = 0; i < VECS; ++i) {
-    float part = 0.0f;
+      for (int i = 0; i < N; ++i)
+        if (piece_top[i] >= at_least) {
+          const uint32_t v = v0_32 + static_cast<uint32_t>(t0 + mine + i * kThreads * E);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      part += ex2_approx((x[i][j] - base) * kLog2e);
-      if (x[i][j] >= at_least && x[i][j] > -INFINITY) {
-        const int place = atomicAdd(&count, 1);
-        const int64_t v = v0 + (static_cast<int64_t>(i) * kThreads + threadIdx.x) * 8 + j;
-        if (place < kBuffer) buf[place] = make_key(x[i][j], static_cast<uint32_t>(v));
+          for (int j = 0; j < E; ++j)
+            if (x[i][j] >= at_least && x[i][j] > -INFINITY) {
+              const uint32_t place = take_place(&count);
+              if (place < kBuffer) buf[place] = make_key(x[i][j], v + j);
+            }
+        }
+    }
+    // after every tile until there are M, then after 2, 4, 8, ... of them
+    ++tiles;
+    if (t0 + kTile < in.len && (!full || (tiles & (tiles - 1)) == 0)) {
+      __syncthreads();
+      const int n = count;
+      __syncthreads();
+      if (n > kBuffer) break;  // taken one after the other below
+      if (n >= p.m && (!full || n > p.m)) {
+        rank_keys(buf, n, p.m, [&](int rank, uint64_t key) { kept[rank] = key; });
+        __syncthreads();
+        if (static_cast<int>(threadIdx.x) < p.m) buf[threadIdx.x] = kept[threadIdx.x];
+        floor_bits = static_cast<uint32_t>(kept[p.m - 1] >> 32);
+        full = true;
+        if (threadIdx.x == 0) count = p.m;
+        __syncthreads();
       }
     }
-    sum += part;
   }
+
+  // the slice's statistics
+  const bool bad = sum != sum;
+  float all_top = top;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    all_top = fmaxf(all_top, __shfl_xor_sync(0xffffffffu, all_top, o));
+  if (all_top > -INFINITY && !bad) sum *= ex2_approx((top - all_top) * kLog2e);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  __syncthreads();  // row_top has been read by all
-  if ((threadIdx.x & 31) == 0) warp_f32[threadIdx.x >> 5] = sum;
+  if ((threadIdx.x & 31) == 0) warp_stat[threadIdx.x >> 5] = make_float2(all_top, sum);
   __syncthreads();
-  if (threadIdx.x == 0) {
-    float s = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) s += warp_f32[w];
-    p.stats[out] = make_float2(row_top, s);
-  }
+  const int64_t out = static_cast<int64_t>(row) * p.splits + slice;
+  uint64_t* const keys = p.keys + out * p.m;
   const int n = count;
+  if (threadIdx.x == 0) {
+    float m = -INFINITY, total = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, warp_stat[w].x);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w)
+      total += warp_stat[w].x > -INFINITY || warp_stat[w].y != warp_stat[w].y
+                   ? warp_stat[w].y * ex2_approx((warp_stat[w].x - m) * kLog2e)
+                   : 0.0f;
+    p.stats[out] = total == total && m < INFINITY ? make_float2(m, total) : make_float2(NAN, 0.0f);
+  }
   if (n <= kBuffer) {
     rank_keys(buf, n, p.m, [&](int rank, uint64_t key) { keys[rank] = key; });
-    for (int i = n + threadIdx.x; i < p.m; i += kThreads) keys[i] = 0;
+    for (int i = n + static_cast<int>(threadIdx.x); i < p.m; i += kThreads) keys[i] = 0;
     return;
   }
   // more equal values than the buffer holds: one after the other
   uint64_t last = ~0ull;
   for (int r = 0; r < p.m; ++r) {
     uint64_t best = 0;
+    for (int v = mine; v < in.len; v += kThreads * E) {
+      float x[E];
+      in.load(v, x);
 #pragma unroll
-    for (int i = 0; i < VECS; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int64_t v = v0 + (static_cast<int64_t>(i) * kThreads + threadIdx.x) * 8 + j;
-        const uint64_t key = make_key(x[i][j], static_cast<uint32_t>(v));
-        if (x[i][j] > -INFINITY && key < last && key > best) best = key;
+      for (int j = 0; j < E; ++j) {
+        const uint64_t key = make_key(x[j], v0_32 + static_cast<uint32_t>(v + j));
+        if (x[j] > -INFINITY && key < last && key > best) best = key;
       }
+    }
     best = block_best(best, warp_key);
     if (threadIdx.x == 0) keys[r] = best;
     last = best;
   }
 }
 
+// log(s / 2^31) within 2^-24: the exponent's part in 64 bits, and a 32-bit
+// logarithm of what is within a factor of sqrt(2) of 1.
+__device__ __forceinline__ double log_of(unsigned long long s) {
+  const float f = __ull2float_rn(s);
+  const float rest = static_cast<float>(static_cast<long long>(s - __float2ull_rn(f))) / f;
+  int e = static_cast<int>(__float_as_uint(f) >> 23) - 127;
+  float m = __uint_as_float((__float_as_uint(f) & 0x007fffffu) | 0x3f800000u);
+  if (m > 1.41421356f) {
+    m *= 0.5f;
+    ++e;
+  }
+  return static_cast<double>(e - 31) * 0.693147180559945309 +
+         static_cast<double>(logf(m) + rest);
+}
+
 // The M best of one prompt from its beams' slices.
 __global__ void __launch_bounds__(kThreads) beam_choose_kernel(const BeamSelectParams p) {
-  __shared__ Scored buf[kBuffer];
+  __shared__ Scored buf[kChoiceBuffer];
   __shared__ Scored warp_best[kWarps];
   // lse = top + log_sum of each beam, kept apart: next to a large top the sum's
   // logarithm would be lost even in 64 bits
@@ -323,10 +468,13 @@ __global__ void __launch_bounds__(kThreads) beam_choose_kernel(const BeamSelectP
   __shared__ float row_top[kBeamMaxSelectBeams];
   __shared__ int count;
   const int b = blockIdx.x;
+  const int lane = static_cast<int>(threadIdx.x & 31);
   if (threadIdx.x == 0) count = 0;
-  // log_sum is NaN for a beam that offers nothing, +infinity for a finished one
+  grid_dependency_wait();
+  // A warp takes a beam. log_sum is NaN for one that offers nothing, +infinity
+  // for a finished one.
   int err = 0;
-  for (int k = threadIdx.x; k < p.beams; k += kThreads) {
+  for (int k = static_cast<int>(threadIdx.x >> 5); k < p.beams; k += kWarps) {
     const int64_t row = static_cast<int64_t>(b) * p.beams + k;
     const float score = p.beam_scores[row];
     double l = NAN;
@@ -338,64 +486,86 @@ __global__ void __launch_bounds__(kThreads) beam_choose_kernel(const BeamSelectP
         l = INFINITY;
       } else {
         bool bad = false;
-        for (int i = 0; i < p.splits; ++i) {
+        for (int i = lane; i < p.splits; i += 32) {
           const float m = p.stats[row * p.splits + i].x;
           bad |= !(m < INFINITY);
           top = fmaxf(top, m);
         }
+        bad = __any_sync(0xffffffffu, bad);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         if (bad) {
           err |= FLCE_DEVERR_NOT_FINITE;
         } else if (top > -INFINITY) {
-          double s = 0.0;
-          for (int i = 0; i < p.splits; ++i) {
+          // At most 2^31 terms of at most 1, in steps of 2^-31: the sum is exact
+          // and in any order the same.
+          unsigned long long s = 0;
+          for (int i = lane; i < p.splits; i += 32) {
             const float2 st = p.stats[row * p.splits + i];
-            if (st.x > -INFINITY)
-              s += static_cast<double>(st.y) * exp(static_cast<double>(st.x) - static_cast<double>(top));
+            s += __float2ull_rn(st.y * ex2_approx((st.x - top) * kLog2e) * 2147483648.0f);
           }
-          l = log(s);
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+          l = log_of(s);
         }
       }
     }
-    log_sum[k] = l;
-    row_top[k] = top;
+    if (lane == 0) {
+      log_sum[k] = l;
+      row_top[k] = top;
+    }
   }
-  if (err != 0 && p.err_word != nullptr) atomicOr(p.err_word, err);
+  if (err != 0 && lane == 0 && p.err_word != nullptr) atomicOr(p.err_word, err);
   __syncthreads();
 
   const int per_beam = p.splits * p.m;
-  const int64_t total = static_cast<int64_t>(p.beams) * per_beam;
-  const Scored none{-INFINITY, ~0ull};
-  auto candidate = [&](int64_t c) -> Scored {
-    const int k = static_cast<int>(c / per_beam);
+  const int total = p.beams * per_beam;
+  const Scored none{0, ~0ull};
+  // The c-th candidate. Keys of beams that were not read are loaded and not used.
+  auto candidate = [&](int c) -> Scored {
+    const int k = c / per_beam;
     const int64_t row = static_cast<int64_t>(b) * p.beams + k;
+    const uint64_t key = p.keys[row * per_beam + (c - k * per_beam)];
     const double l = log_sum[k];
-    if (isnan(l)) return none;
     const double score = static_cast<double>(p.beam_scores[row]);
-    if (isinf(l))
-      return c == static_cast<int64_t>(k) * per_beam
-                 ? Scored{score, static_cast<uint64_t>(k) * p.v + p.pad_token}
-                 : none;
-    const uint64_t key = p.keys[row * per_beam + (c - static_cast<int64_t>(k) * per_beam)];
-    if (key == 0) return none;
     const double zv = static_cast<double>(from_order_bits(static_cast<uint32_t>(key >> 32)));
     const uint32_t v = 0xffffffffu - static_cast<uint32_t>(key);
-    return Scored{score + ((zv - static_cast<double>(row_top[k])) - l), static_cast<uint64_t>(k) * p.v + v};
+    Scored x{order_bits64(score + ((zv - static_cast<double>(row_top[k])) - l)),
+             (static_cast<uint64_t>(k) << 32) | v};
+    if (key == 0 || isnan(l)) x = none;
+    if (isinf(l))
+      x = c == k * per_beam
+              ? Scored{order_bits64(score), (static_cast<uint64_t>(k) << 32) |
+                                                static_cast<uint64_t>(p.pad_token)}
+              : none;
+    return x;
   };
   // the thread's candidates: a rotation, because the keys of a slice are in
   // order and the groups shall see all ranks alike
-  auto place_of = [&](int64_t round) -> int64_t {
-    return round * kThreads + ((threadIdx.x + static_cast<unsigned>(round) * 97u) & (kThreads - 1));
+  auto place_of = [&](int round) -> int {
+    return round * kThreads +
+           static_cast<int>((threadIdx.x + static_cast<unsigned>(round) * 97u) & (kThreads - 1));
   };
-  const int64_t rounds = (total + kThreads - 1) / kThreads;
+  const int rounds = (total + kThreads - 1) / kThreads;
+  // the first of them stay in registers
+  Scored mine[kHeld];
   Scored best = none;
-  for (int64_t r = 0; r < rounds; ++r) {
-    const int64_t c = place_of(r);
-    if (c >= total) continue;
-    const Scored x = candidate(c);
+#pragma unroll
+  for (int r = 0; r < kHeld; ++r) {
+    mine[r] = none;
+    if (r < rounds) {
+      const int c = place_of(r);
+      if (c < total) mine[r] = candidate(c);
+      if (better(mine[r], best)) best = mine[r];
+    }
+  }
+  for (int r = kHeld; r < rounds; ++r) {
+    const int c = place_of(r);
+    const Scored x = c < total ? candidate(c) : none;
     if (better(x, best)) best = x;
   }
   // the smallest of the groups' best
-  const int width = kThreads / groups_for(p.m);
+  const int width = kThreads / p.groups;
   for (int o = 1; o < 32 && o < width; o <<= 1) {
     const Scored y = shfl_xor(best, o);
     if (better(y, best)) best = y;
@@ -407,7 +577,7 @@ __global__ void __launch_bounds__(kThreads) beam_choose_kernel(const BeamSelectP
       if (better(best, y)) best = y;
     }
   }
-  if ((threadIdx.x & 31) == 0) warp_best[threadIdx.x >> 5] = best;
+  if (lane == 0) warp_best[threadIdx.x >> 5] = best;
   __syncthreads();
   const int per = width > 32 ? width / 32 : 1;
   Scored floor_at = none;
@@ -417,22 +587,23 @@ __global__ void __launch_bounds__(kThreads) beam_choose_kernel(const BeamSelectP
       if (better(warp_best[w], m)) m = warp_best[w];
     if (a == 0 || better(floor_at, m)) floor_at = m;
   }
-  for (int64_t r = 0; r < rounds; ++r) {
-    const int64_t c = place_of(r);
-    if (c >= total) continue;
-    const Scored x = candidate(c);
-    if (x.s > -INFINITY && !better(floor_at, x)) {
-      const int place = atomicAdd(&count, 1);
-      if (place < kBuffer) buf[place] = x;
-    }
+  auto push = [&](const Scored& x) {
+    if (x.s == 0 || better(floor_at, x)) return;
+    const uint32_t place = take_place(&count);
+    if (place < kChoiceBuffer) buf[place] = x;
+  };
+#pragma unroll
+  for (int r = 0; r < kHeld; ++r) push(mine[r]);
+  for (int r = kHeld; r < rounds; ++r) {
+    const int c = place_of(r);
+    if (c < total) push(candidate(c));
   }
   __syncthreads();
   const int64_t o0 = static_cast<int64_t>(b) * p.m;
   auto emit = [&](int rank, const Scored& x) {
-    const uint64_t k = x.at / static_cast<uint64_t>(p.v);
-    p.scores_out[o0 + rank] = static_cast<float>(x.s);
-    p.parents_out[o0 + rank] = static_cast<int64_t>(k);
-    p.tokens_out[o0 + rank] = static_cast<int64_t>(x.at - k * static_cast<uint64_t>(p.v));
+    p.scores_out[o0 + rank] = static_cast<float>(from_order_bits64(x.s));
+    p.parents_out[o0 + rank] = static_cast<int64_t>(x.at >> 32);
+    p.tokens_out[o0 + rank] = static_cast<int64_t>(x.at & 0xffffffffu);
   };
   auto emit_none = [&](int rank) {
     p.scores_out[o0 + rank] = -INFINITY;
@@ -440,23 +611,22 @@ __global__ void __launch_bounds__(kThreads) beam_choose_kernel(const BeamSelectP
     p.tokens_out[o0 + rank] = p.pad_token;
   };
   const int n = count;
-  if (n <= kBuffer) {
+  if (n <= kChoiceBuffer) {
     rank_keys(buf, n, p.m, emit);
-    for (int i = n + threadIdx.x; i < p.m; i += kThreads) emit_none(i);
+    for (int i = n + static_cast<int>(threadIdx.x); i < p.m; i += kThreads) emit_none(i);
     return;
   }
-  Scored last{INFINITY, 0};
+  Scored last{~0ull, 0};
   for (int r = 0; r < p.m; ++r) {
     Scored x = none;
-    for (int64_t q = 0; q < rounds; ++q) {
-      const int64_t c = place_of(q);
-      if (c >= total) continue;
-      const Scored y = candidate(c);
+    for (int q = 0; q < rounds; ++q) {
+      const int c = place_of(q);
+      const Scored y = c < total ? candidate(c) : none;
       if (better(last, y) && better(y, x)) x = y;
     }
     x = block_best(x, warp_best);
     if (threadIdx.x == 0) {
-      if (x.s > -INFINITY)
+      if (x.s != 0)
         emit(r, x);
       else
         emit_none(r);
@@ -469,15 +639,23 @@ template <class T>
 cudaError_t launch_select(const BeamSelectParams& p, bool large, cudaStream_t s) {
   const int64_t blocks = static_cast<int64_t>(p.batch) * p.beams * p.splits;
   if (large)
-    beam_slices_kernel<T, kSliceLarge / (8 * kThreads)>
-        <<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(p);
+    beam_slices_kernel<T, kPiecesLarge><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(p);
   else
-    beam_slices_kernel<T, kSliceSmall / (8 * kThreads)>
-        <<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(p);
+    beam_slices_kernel<T, 1><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  beam_choose_kernel<<<static_cast<unsigned>(p.batch), kThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  // may be placed while the slices run, and waits for them
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3(static_cast<unsigned>(p.batch), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.stream = s;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, beam_choose_kernel, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 // ------------------------------------------------------------- reordering

@@ -17,6 +17,7 @@ from typing import Iterable, Optional, Sequence
 import torch
 
 from . import abi
+from ._stream import on_device, raw_stream
 
 __all__ = ["grad_norm", "clip_grads_", "clip_grads", "clip_grad_norm_"]
 
@@ -109,11 +110,11 @@ def _run(grads, out, norm_type, max_norm, eps) -> torch.Tensor:
         device = torch.device("cuda", torch.cuda.current_device())
     count = len(table) // 7
     address = table.buffer_info()[0] if count else None
-    with torch.cuda.device(device):
+    with on_device(device):
         norm = torch.empty((), dtype=torch.float32, device=device)
         ws_bytes = abi.flce_grad_workspace_size(count)
         ws = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
-        stream = torch.cuda.current_stream(device).cuda_stream
+        stream = raw_stream(device)
         if max_norm is None:
             abi.flce_grad_norm(address, count, code, norm.data_ptr(), ws.data_ptr(), ws_bytes,
                                stream)

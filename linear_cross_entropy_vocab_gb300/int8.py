@@ -14,6 +14,7 @@ from typing import Optional, Tuple
 import torch
 
 from . import abi
+from ._stream import on_device, raw_stream
 
 __all__ = ["quantize_rows", "int8_linear"]
 
@@ -48,8 +49,8 @@ def quantize_rows(x: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
     q_pitch = (h + 15) // 16 * 16
     q = torch.empty(n, q_pitch, dtype=torch.int8, device=x.device)
     scale = torch.empty(n, dtype=torch.float32, device=x.device)
-    with torch.cuda.device(x.device):
-        stream = torch.cuda.current_stream(x.device).cuda_stream
+    with on_device(x.device):
+        stream = raw_stream(x.device)
         abi.flce_quantize_rows(x.data_ptr(), code, n, h, pitch, q.data_ptr(), q_pitch,
                                scale.data_ptr(), stream)
     q = q[:, :h]
@@ -124,10 +125,10 @@ def int8_linear(x: torch.Tensor, weight: torch.Tensor, weight_scale: torch.Tenso
                              0 if bias is None else 1, float(logit_scale),
                              0.0 if softcap is None else float(softcap),
                              abi.FLCE_Q_LAY_OUT_WEIGHT if weight.data_ptr() % 16 else 0, 0)
-    with torch.cuda.device(dev):
+    with on_device(dev):
         ws_bytes = abi.flce_qlinear_workspace_size(prob)
         ws = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=dev)
-        stream = torch.cuda.current_stream(dev).cuda_stream
+        stream = raw_stream(dev)
         abi.flce_qlinear(prob, x.data_ptr(), None if x_scale is None else x_scale.data_ptr(),
                          weight.data_ptr(), weight_scale.data_ptr(),
                          None if bias is None else bias.data_ptr(), out.data_ptr(),
