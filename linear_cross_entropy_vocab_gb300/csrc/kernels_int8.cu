@@ -3,9 +3,15 @@
 //   scale_i = max_h |x_ih| / 127,  q_ih = round(x_ih / scale_i)
 //
 // as bytes for the caller, or as halves in the operand order of the linear
-// kernel (kernels_qlinear.cu). Bound by memory: a CTA takes one row, keeps up
-// to 4096 values of it in registers between the maximum and the rounding, and
-// reads longer rows a second time, from L2.
+// kernel (kernels_qlinear.cu).
+//
+// Bound by memory: a CTA takes one row, keeps up to 4096 values of it in
+// registers, as they came, between the maximum and the rounding, and reads
+// longer rows a second time, from L2. What keeps it near that bound is the
+// number of instructions for a value: the maximum is taken on the raw bits, two
+// 16-bit values at a time; the quotient is a product with the reciprocal and one
+// correction; and adding 1.5 * 2^23 rounds it and leaves the integer in the low
+// byte.
 #include <cstdint>
 
 #include <cuda_bf16.h>
@@ -20,103 +26,156 @@ constexpr int kThreads = 128;
 constexpr int kVecs = 4;  // groups of 8 values per thread and sweep
 constexpr int kSweep = kThreads * kVecs * 8;
 
+// A group of 8 values: how it is loaded, its largest magnitude by the order of
+// the bits (NaN is above infinity), and its values.
 template <class T>
-__device__ __forceinline__ float to_float(T x);
+struct Group;
 template <>
-__device__ __forceinline__ float to_float(float x) { return x; }
-template <>
-__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
-template <>
-__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
-template <>
-__device__ __forceinline__ float to_float(int8_t x) { return static_cast<float>(x); }
-
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-  const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 q = __ldg(reinterpret_cast<const uint4*>(p));
-  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+struct Group<float> {
+  static constexpr int kAlign = 16;
+  uint4 q[2];
+  __device__ __forceinline__ void load(const float* p) {
+    q[0] = __ldg(reinterpret_cast<const uint4*>(p));
+    q[1] = __ldg(reinterpret_cast<const uint4*>(p) + 1);
   }
-}
-__device__ __forceinline__ void load8(const __half* p, float (&x)[8]) {
-  const uint4 q = __ldg(reinterpret_cast<const uint4*>(p));
-  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  __device__ __forceinline__ void load_some(const float* p, int64_t n) {
+    uint32_t w[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
+    for (int j = 0; j < 8; ++j) w[j] = j < n ? __float_as_uint(p[j]) : 0u;
+    q[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    q[1] = make_uint4(w[4], w[5], w[6], w[7]);
   }
-}
-__device__ __forceinline__ void load8(const int8_t* p, float (&x)[8]) {
-  const uint2 q = __ldg(reinterpret_cast<const uint2*>(p));
+  __device__ __forceinline__ uint32_t peak(uint32_t m) const {
+    const uint32_t w[8] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w};
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    x[i] = static_cast<float>(static_cast<int8_t>((i < 4 ? q.x : q.y) >> (8 * (i & 3))));
-}
-
-// 8 values from element e of a row of h; zeros past its end.
-template <class T>
-__device__ __forceinline__ void load_group(const T* row, int64_t e, int64_t h, bool vec,
-                                           float (&x)[8]) {
-  if (vec && e + 8 <= h) {
-    load8(row + e, x);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = e + j < h ? to_float(row[e + j]) : 0.0f;
+    for (int j = 0; j < 8; ++j) m = max(m, w[j] & 0x7fffffffu);
+    return m;
   }
-}
+  static __device__ __forceinline__ float peak_value(uint32_t m) { return __uint_as_float(m); }
+  __device__ __forceinline__ void values(float (&x)[8]) const {
+    const uint32_t w[8] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(w[j]);
+  }
+};
 
-// round(x / scale), halves to even. The product with the reciprocal is within
-// 2^-16 of the quotient (at most 127, two roundings): only near a half does
-// the division decide.
+// The same for 16-bit types, two values in a word.
+struct Group16 {
+  static constexpr int kAlign = 16;
+  uint4 q;
+  __device__ __forceinline__ void load(const void* p) {
+    q = __ldg(reinterpret_cast<const uint4*>(p));
+  }
+  __device__ __forceinline__ void load_some(const void* p, int64_t n) {
+    const uint16_t* const u = static_cast<const uint16_t*>(p);
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      w[j] = (2 * j < n ? u[2 * j] : 0u) | ((2 * j + 1 < n ? u[2 * j + 1] : 0u) << 16);
+    q = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __device__ __forceinline__ uint32_t peak(uint32_t m) const {
+    m = __vmaxu2(m, q.x & 0x7fff7fffu);
+    m = __vmaxu2(m, q.y & 0x7fff7fffu);
+    m = __vmaxu2(m, q.z & 0x7fff7fffu);
+    return __vmaxu2(m, q.w & 0x7fff7fffu);
+  }
+};
+template <>
+struct Group<__nv_bfloat16> : Group16 {
+  static __device__ __forceinline__ float peak_value(uint32_t m) {
+    return __uint_as_float(max(m >> 16, m & 0xffffu) << 16);
+  }
+  __device__ __forceinline__ void values(float (&x)[8]) const {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+};
+template <>
+struct Group<__half> : Group16 {
+  static __device__ __forceinline__ float peak_value(uint32_t m) {
+    return __half2float(__ushort_as_half(static_cast<unsigned short>(max(m >> 16, m & 0xffffu))));
+  }
+  __device__ __forceinline__ void values(float (&x)[8]) const {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      x[2 * i] = f.x;
+      x[2 * i + 1] = f.y;
+    }
+  }
+};
+// Integers already: nothing to scale.
+template <>
+struct Group<int8_t> {
+  static constexpr int kAlign = 8;
+  uint2 q;
+  __device__ __forceinline__ void load(const int8_t* p) {
+    q = __ldg(reinterpret_cast<const uint2*>(p));
+  }
+  __device__ __forceinline__ void load_some(const int8_t* p, int64_t n) {
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < n) w[j >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(p[j])) << (8 * (j & 3));
+    q = make_uint2(w[0], w[1]);
+  }
+  __device__ __forceinline__ uint32_t peak(uint32_t m) const { return m; }
+  static __device__ __forceinline__ float peak_value(uint32_t) { return 0.0f; }
+  __device__ __forceinline__ void values(float (&x)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      x[j] = static_cast<float>(static_cast<int8_t>((j < 4 ? q.x : q.y) >> (8 * (j & 3))));
+  }
+};
+
+constexpr float kToInt = 12582912.0f;  // 1.5 * 2^23: adding it rounds to whole numbers
+
+// x / scale rounded to whole numbers, halves to even, plus kToInt (the integer
+// is in the low byte). Values of a short type are multiples of few scales, and
+// halves are common: the quotient has to be the correctly rounded one. It is,
+// from a product with the correctly rounded reciprocal and one correction by
+// the exact remainder (Markstein 1990, theorem on division), where nothing
+// leaves the normal range: quotients below a half need no more than to stay
+// there.
 __device__ __forceinline__ void round8(float (&x)[8], float scale, float inv) {
-  if (!(scale > 0.0f)) {
+  if (scale >= 1.0e-28f) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = 0.0f;
+    for (int j = 0; j < 8; ++j) {
+      const float q = x[j] * inv;
+      x[j] = fmaf(fmaf(-q, scale, x[j]), inv, q) + kToInt;
+    }
     return;
   }
-  bool close = scale < 1.0e-37f;  // its reciprocal may overflow
-  float r[8];
+  // a tiny scale, 0 or NaN
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const float y = x[j] * inv;
-    r[j] = rintf(y);
-    close |= fabsf(y - r[j]) > 0.4999f;
+    const float q = scale > 0.0f ? rintf(__fdiv_rn(x[j], scale)) : 0.0f;
+    x[j] = fminf(127.0f, fmaxf(-127.0f, q)) + kToInt;
   }
-  if (close) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) r[j] = rintf(__fdiv_rn(x[j], scale));
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) x[j] = fminf(127.0f, fmaxf(-127.0f, r[j]));
 }
 
 __device__ __forceinline__ void put_bytes(int8_t* q, int64_t e, int64_t h, bool vec,
                                           const float (&x)[8]) {
-  if (vec && e + 8 <= h) {
-    uint32_t w[2];
+  uint32_t w[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t b0 = static_cast<uint32_t>(__float2int_rn(x[4 * i])) & 0xffu;
-      const uint32_t b1 = static_cast<uint32_t>(__float2int_rn(x[4 * i + 1])) & 0xffu;
-      const uint32_t b2 = static_cast<uint32_t>(__float2int_rn(x[4 * i + 2])) & 0xffu;
-      const uint32_t b3 = static_cast<uint32_t>(__float2int_rn(x[4 * i + 3]));
-      w[i] = b0 | (b1 << 8) | (b2 << 16) | (b3 << 24);
-    }
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t lo = __byte_perm(__float_as_uint(x[4 * i]), __float_as_uint(x[4 * i + 1]), 0x40);
+    const uint32_t hi =
+        __byte_perm(__float_as_uint(x[4 * i + 2]), __float_as_uint(x[4 * i + 3]), 0x40);
+    w[i] = __byte_perm(lo, hi, 0x5410);
+  }
+  if (vec && e + 8 <= h) {
     *reinterpret_cast<uint2*>(q + e) = make_uint2(w[0], w[1]);
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (e + j < h) q[e + j] = static_cast<int8_t>(__float2int_rn(x[j]));
+      if (e + j < h) q[e + j] = static_cast<int8_t>(w[j >> 2] >> (8 * (j & 3)));
   }
 }
 
@@ -140,27 +199,32 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const QuantPara
   constexpr bool kInt = sizeof(T) == 1;
   const int64_t row = blockIdx.x;
   const T* const x0 = static_cast<const T*>(p.x) + row * p.x_pitch;
-  const bool vec = (reinterpret_cast<uintptr_t>(x0) & (kInt ? 7u : 15u)) == 0;
+  const bool vec = (reinterpret_cast<uintptr_t>(x0) & (Group<T>::kAlign - 1)) == 0;
   int8_t* const q0 = WIDE ? nullptr : p.q + row * p.q_pitch;
   const bool qvec = (reinterpret_cast<uintptr_t>(q0) & 7u) == 0;
   __half* const w0 = WIDE ? static_cast<__half*>(p.wide) + row * p.wide_pitch : nullptr;
   const int64_t end = WIDE ? p.wide_pitch : p.h;
-  float x[kVecs][8];
+  Group<T> g[kVecs];
+  // the thread's groups of the sweep from e0 on; zeros past the row's end
+  auto load = [&](int64_t e0) {
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      const int64_t e = e0 + (i * kThreads + static_cast<int>(threadIdx.x)) * 8;
+      if (vec && e + 8 <= p.h)
+        g[i].load(x0 + e);
+      else
+        g[i].load_some(x0 + e, p.h - e);
+    }
+  };
   float scale = 1.0f, inv = 1.0f;
   if constexpr (!kInt) {
-    // largest magnitude by the order of the bits: NaN is above infinity
     uint32_t m = 0;
     for (int64_t e0 = 0; e0 < p.h; e0 += kSweep) {
+      load(e0);
 #pragma unroll
-      for (int i = 0; i < kVecs; ++i) {
-        const int64_t e = e0 + (static_cast<int64_t>(i) * kThreads + threadIdx.x) * 8;
-        load_group(x0, e, p.h, vec, x[i]);
-      }
-#pragma unroll
-      for (int i = 0; i < kVecs; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(x[i][j]) & 0x7fffffffu);
+      for (int i = 0; i < kVecs; ++i) m = g[i].peak(m);
     }
+    m = __float_as_uint(Group<T>::peak_value(m));
     m = __reduce_max_sync(0xffffffffu, m);
     if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = m;
     __syncthreads();
@@ -173,16 +237,24 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const QuantPara
     if (threadIdx.x == 0) p.scale[row] = scale;
   }
   for (int64_t e0 = 0; e0 < end; e0 += kSweep) {
+    if (kInt || p.h > kSweep) load(e0);
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
-      const int64_t e = e0 + (static_cast<int64_t>(i) * kThreads + threadIdx.x) * 8;
+      const int64_t e = e0 + (i * kThreads + static_cast<int>(threadIdx.x)) * 8;
       if (e >= end) break;
-      if (kInt || p.h > kSweep) load_group(x0, e, p.h, vec, x[i]);
-      if constexpr (!kInt) round8(x[i], scale, inv);
+      float x[8];
+      g[i].values(x);
+      if constexpr (!kInt) {
+        round8(x, scale, inv);
+        if constexpr (WIDE) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[j] -= kToInt;
+        }
+      }
       if constexpr (WIDE)
-        put_halves(w0, e, x[i]);
+        put_halves(w0, e, x);
       else
-        put_bytes(q0, e, p.h, qvec, x[i]);
+        put_bytes(q0, e, p.h, qvec, x);
     }
   }
 }
