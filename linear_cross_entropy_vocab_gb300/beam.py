@@ -125,6 +125,9 @@ def beam_select(logits: torch.Tensor, beam_scores: torch.Tensor,
     return BeamSelection(scores, parents, tokens)
 
 
+_NO_STATE = (0, 0, 1, 1, 1, 1, 0, 0, 0, 0, 0)  # nothing to move
+
+
 def _state_words(i: int, t: torch.Tensor, dim: int, rows: int) -> tuple:
     """The flce_beam_state of a tensor whose axis ``dim`` counts the beams."""
     if not -t.dim() <= dim < t.dim():
@@ -133,24 +136,33 @@ def _state_words(i: int, t: torch.Tensor, dim: int, rows: int) -> tuple:
     if t.shape[dim] != rows:
         raise ValueError(f"state {i} has {t.shape[dim]} rows along dimension {dim}, not {rows}")
     es = t.element_size()
-    if t.numel() == 0:
-        return (0, 0) + (1,) * abi.BEAM_STATE_DIMS + (0,) * abi.BEAM_STATE_DIMS + (0,)
-    dims = sorted(((st, s) for d, (s, st) in enumerate(zip(t.shape, t.stride()))
-                   if d != dim and s > 1), reverse=True)
+    strides = t.stride()
+    # (stride, size) of the other axes from the widest stride to the narrowest, neighbours that
+    # make one axis joined
+    dims = [(st, s) for d, (s, st) in enumerate(zip(t.shape, strides)) if d != dim and s != 1]
+    if any(s == 0 for _, s in dims) or rows == 0:
+        return _NO_STATE
+    dims.sort(reverse=True)
     merged: list = []
     for st, s in dims:
         if merged and merged[-1][0] == st * s:
             merged[-1] = (st, merged[-1][1] * s)
         else:
             merged.append((st, s))
-    run = 1
+    run = es
     if merged and merged[-1][0] == 1:
-        run = merged.pop()[1]
-    pad = abi.BEAM_STATE_DIMS - len(merged)
+        run = merged.pop()[1] * es
+    n = len(merged)
+    if n == 0:
+        return (t.data_ptr(), strides[dim] * es, 1, 1, 1, 1, 0, 0, 0, 0, run)
+    if n == 1:
+        (st, s), = merged
+        return (t.data_ptr(), strides[dim] * es, 1, 1, 1, s, 0, 0, 0, st * es, run)
+    pad = abi.BEAM_STATE_DIMS - n
     if pad < 0:
         raise ValueError(f"state {i} lies in too many separate pieces: make it contiguous")
-    return ((t.data_ptr(), t.stride(dim) * es) + (1,) * pad + tuple(s for _, s in merged)
-            + (0,) * pad + tuple(st * es for st, _ in merged) + (run * es,))
+    return (t.data_ptr(), strides[dim] * es, *(1,) * pad, *(s for _, s in merged),
+            *(0,) * pad, *(st * es for st, _ in merged), run)
 
 
 def beam_reorder_(states: Union[torch.Tensor, Iterable[torch.Tensor]], parents: torch.Tensor,

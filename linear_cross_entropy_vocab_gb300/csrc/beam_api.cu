@@ -64,8 +64,8 @@ SelectPlan plan_select(const flce_beam_problem* p) {
   return q;
 }
 
-// The states of one launch share a vector width: the widest that divides the
-// address, every stride and the contiguous run.
+// Bytes that a thread moves at a time: the widest that divides the address,
+// every stride and the contiguous run.
 int width_of(const flce_beam_state& s) {
   uint64_t bits = reinterpret_cast<uintptr_t>(s.data) | static_cast<uint64_t>(s.beam_stride) |
                   static_cast<uint64_t>(s.run_bytes);
@@ -113,6 +113,54 @@ flce_status check_state(const flce_beam_state& s, int64_t i, int64_t rows, bool*
     if (size[a] > (int64_t(1) << 46) / stride[a])
       return fail(FLCE_ERR_UNSUPPORTED, "state %lld is too large", (long long)i);
     span += (size[a] - 1) * stride[a];
+  }
+  return FLCE_OK;
+}
+
+// Launches for states that have been checked, each with as many as fit.
+template <int CAP>
+flce_status reorder(const flce_beam_state* states, int64_t count, const int64_t* parents,
+                    int64_t batch, int64_t beams, int max_width, int32_t* err_word,
+                    cudaStream_t stream) {
+  flce::ReorderTable<CAP> t;
+  t.batch = static_cast<int32_t>(batch);
+  t.beams = static_cast<int32_t>(beams);
+  t.parents = parents;
+  t.err_word = err_word;
+  t.count = 0;
+  int64_t blocks = 0;
+  for (int64_t i = 0; i <= count; ++i) {
+    int64_t vecs = 0, need = 0;
+    int width = 1;
+    if (i < count) {
+      vecs = states[i].run_bytes;
+      for (int d = 0; d < flce::kReorderDims; ++d) vecs *= states[i].size[d];
+      if (vecs == 0) continue;
+      width = std::min(max_width, width_of(states[i]));
+      vecs /= width;
+      need = ceil_div(vecs, flce::kReorderBlock) * batch;
+    }
+    if (t.count > 0 && (i == count || t.count == CAP || blocks + need > 0x7fffffffll)) {
+      t.first[t.count] = static_cast<uint32_t>(blocks);
+      const cudaError_t e = flce::launch_beam_reorder(t, blocks, stream);
+      if (e != cudaSuccess) return cuda_fail(e, "beam reordering kernel");
+      t.count = 0;
+      blocks = 0;
+    }
+    if (i == count) break;
+    const flce_beam_state& s = states[i];
+    flce::ReorderEntry& r = t.e[t.count];
+    r.data = static_cast<uint8_t*>(s.data);
+    r.beam_stride = s.beam_stride;
+    for (int d = 0; d < flce::kReorderDims; ++d) {
+      r.size[d] = static_cast<uint32_t>(s.size[d]);
+      r.stride[d] = s.stride[d];
+    }
+    r.run = static_cast<uint32_t>(s.run_bytes / width);
+    r.total = static_cast<uint32_t>(vecs);
+    r.width = static_cast<uint32_t>(width);
+    t.first[t.count++] = static_cast<uint32_t>(blocks);
+    blocks += need;
   }
   return FLCE_OK;
 }
@@ -211,51 +259,11 @@ flce_status flce_beam_reorder(const flce_beam_state* states, int64_t count,
   int sms = 0;
   const flce_status dev = check_device(&sms);
   if (dev != FLCE_OK || batch == 0) return dev;
-  // one launch for each width that occurs, and for each 64 states of it
-  for (int width = max_width; width >= 1; width /= 2) {
-    flce::ReorderTable t;
-    t.batch = static_cast<int32_t>(batch);
-    t.beams = static_cast<int32_t>(beams);
-    t.parents = parents;
-    t.err_word = err_word;
-    t.count = 0;
-    int64_t blocks = 0;
-    auto launch = [&]() -> cudaError_t {
-      if (t.count == 0) return cudaSuccess;
-      t.first[t.count] = static_cast<uint32_t>(blocks);
-      const cudaError_t e =
-          flce::launch_beam_reorder(t, width, blocks, static_cast<cudaStream_t>(stream));
-      t.count = 0;
-      blocks = 0;
-      return e;
-    };
-    for (int64_t i = 0; i < count; ++i) {
-      const flce_beam_state& s = states[i];
-      int64_t vecs = s.run_bytes;
-      for (int d = 0; d < flce::kReorderDims; ++d) vecs *= s.size[d];
-      if (vecs == 0 || std::min(max_width, width_of(s)) != width) continue;
-      vecs /= width;
-      const int64_t need = ceil_div(vecs, flce::kReorderBlock) * batch;
-      if (t.count == flce::kReorderTable || blocks + need > 0x7fffffffll) {
-        const cudaError_t e = launch();
-        if (e != cudaSuccess) return cuda_fail(e, "beam reordering kernel");
-      }
-      flce::ReorderEntry& r = t.e[t.count];
-      r.data = static_cast<uint8_t*>(s.data);
-      r.beam_stride = s.beam_stride;
-      for (int d = 0; d < flce::kReorderDims; ++d) {
-        r.size[d] = static_cast<uint32_t>(s.size[d]);
-        r.stride[d] = s.stride[d];
-      }
-      r.run = static_cast<uint32_t>(s.run_bytes / width);
-      r.total = static_cast<uint32_t>(vecs);
-      t.first[t.count++] = static_cast<uint32_t>(blocks);
-      blocks += need;
-    }
-    const cudaError_t e = launch();
-    if (e != cudaSuccess) return cuda_fail(e, "beam reordering kernel");
-  }
-  return FLCE_OK;
+  if (count <= flce::kReorderSmall)
+    return reorder<flce::kReorderSmall>(states, count, parents, batch, beams, max_width, err_word,
+                                        static_cast<cudaStream_t>(stream));
+  return reorder<flce::kReorderLarge>(states, count, parents, batch, beams, max_width, err_word,
+                                      static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -45,11 +45,14 @@ cudaError_t launch_beam_select(const BeamSelectParams& p, int dtype, bool large,
                                cudaStream_t s);
 
 constexpr int kReorderDims = 4;
-constexpr int kReorderTable = 64;
+// States of one launch: the small table keeps the parameters of a call with
+// few states short.
+constexpr int kReorderSmall = 8;
+constexpr int kReorderLarge = 256;
 
-// One state: rows of `vecs` vectors of the launch's width, at the places that
-// the (at most 4) outer extents and strides give, for each of batch x beams
-// beams `beam_stride` bytes apart.
+// One state: `total` vectors of `width` bytes in runs of `run`, at the places
+// that the (at most 4) outer extents and strides give, for each of
+// batch x beams beams `beam_stride` bytes apart.
 struct ReorderEntry {
   uint8_t* data;
   int64_t beam_stride;
@@ -57,18 +60,22 @@ struct ReorderEntry {
   uint32_t size[kReorderDims];   // 1 where unused
   uint32_t run;                  // vectors in one contiguous run
   uint32_t total;                // vectors of one beam
+  uint32_t width;                // 16 (at most 32 beams), 8, 4, 2 or 1
 };
 
+template <int CAP>
 struct ReorderTable {
-  ReorderEntry e[kReorderTable];
-  uint32_t first[kReorderTable + 1];  // first block of each state
+  ReorderEntry e[CAP];
+  uint32_t first[CAP + 1];  // first block of each state
   int32_t count;
   int32_t batch, beams;
   const int64_t* parents;
   int32_t* err_word;
 };
+static_assert(sizeof(ReorderTable<kReorderLarge>) <= 32764, "kernel parameters");
 
-cudaError_t launch_beam_reorder(const ReorderTable& t, int width, int64_t blocks, cudaStream_t s);
+template <int CAP>
+cudaError_t launch_beam_reorder(const ReorderTable<CAP>& t, int64_t blocks, cudaStream_t s);
 
 // Vectors of one beam that a block takes.
 constexpr int kReorderBlock = 256;

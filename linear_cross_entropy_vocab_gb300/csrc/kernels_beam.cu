@@ -672,10 +672,26 @@ struct Vec<2> { using T = uint16_t; };
 template <>
 struct Vec<1> { using T = uint8_t; };
 
-// KM: an upper bound of the beams; a thread holds one vector of each.
+// One vector of W bytes of each of a prompt's beams, `at` bytes from base:
+// all that moves is read before anything is written.
 template <int W, int KM>
-__global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const __grid_constant__ ReorderTable t) {
+__device__ __forceinline__ void move_beams(uint8_t* base, int64_t beam_stride, int beams,
+                                           const int* parent) {
   using V = typename Vec<W>::T;
+  V v[KM];
+#pragma unroll
+  for (int j = 0; j < KM; ++j)
+    if (j < beams && parent[j] != j)
+      v[j] = *reinterpret_cast<const V*>(base + parent[j] * beam_stride);
+#pragma unroll
+  for (int j = 0; j < KM; ++j)
+    if (j < beams && parent[j] != j) *reinterpret_cast<V*>(base + j * beam_stride) = v[j];
+}
+
+// KM: an upper bound of the beams; a thread holds one vector of each.
+template <int KM, int CAP>
+__global__ void __launch_bounds__(kThreads)
+    beam_reorder_kernel(const __grid_constant__ ReorderTable<CAP> t) {
   __shared__ int parent[KM];
   int lo = 0, hi = t.count;  // the state of this block
   while (hi - lo > 1) {
@@ -700,7 +716,7 @@ __global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const __grid_con
   __syncthreads();
   if (c >= e.total) return;
   uint32_t outer = c / e.run;
-  int64_t at = static_cast<int64_t>(c - outer * e.run) * W;
+  int64_t at = static_cast<int64_t>(c - outer * e.run) * e.width;
 #pragma unroll
   for (int d = kReorderDims - 1; d >= 0; --d) {
     if (e.size[d] > 1) {
@@ -710,31 +726,17 @@ __global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const __grid_con
     }
   }
   uint8_t* const base = e.data + static_cast<int64_t>(b) * t.beams * e.beam_stride + at;
-  V v[KM];
-#pragma unroll
-  for (int j = 0; j < KM; ++j)
-    if (j < t.beams && parent[j] != j)
-      v[j] = *reinterpret_cast<const V*>(base + parent[j] * e.beam_stride);
-#pragma unroll
-  for (int j = 0; j < KM; ++j)
-    if (j < t.beams && parent[j] != j) *reinterpret_cast<V*>(base + j * e.beam_stride) = v[j];
-}
-
-template <int W>
-cudaError_t launch_reorder(const ReorderTable& t, unsigned blocks, cudaStream_t s) {
-  if (t.beams <= 4)
-    beam_reorder_kernel<W, 4><<<blocks, kThreads, 0, s>>>(t);
-  else if (t.beams <= 8)
-    beam_reorder_kernel<W, 8><<<blocks, kThreads, 0, s>>>(t);
-  else if (t.beams <= 16)
-    beam_reorder_kernel<W, 16><<<blocks, kThreads, 0, s>>>(t);
-  else if (t.beams <= 32)
-    beam_reorder_kernel<W, 32><<<blocks, kThreads, 0, s>>>(t);
-  else if constexpr (W <= 8)
-    beam_reorder_kernel<W, 64><<<blocks, kThreads, 0, s>>>(t);
-  else
-    return cudaErrorInvalidValue;
-  return cudaGetLastError();
+  if (e.width == 16) {
+    if constexpr (KM <= 32) move_beams<16, KM>(base, e.beam_stride, t.beams, parent);
+  } else if (e.width == 8) {
+    move_beams<8, KM>(base, e.beam_stride, t.beams, parent);
+  } else if (e.width == 4) {
+    move_beams<4, KM>(base, e.beam_stride, t.beams, parent);
+  } else if (e.width == 2) {
+    move_beams<2, KM>(base, e.beam_stride, t.beams, parent);
+  } else {
+    move_beams<1, KM>(base, e.beam_stride, t.beams, parent);
+  }
 }
 
 }  // namespace
@@ -746,16 +748,23 @@ cudaError_t launch_beam_select(const BeamSelectParams& p, int dtype, bool large,
   return launch_select<__half>(p, large, s);
 }
 
-cudaError_t launch_beam_reorder(const ReorderTable& t, int width, int64_t blocks,
-                                cudaStream_t s) {
+template <int CAP>
+cudaError_t launch_beam_reorder(const ReorderTable<CAP>& t, int64_t blocks, cudaStream_t s) {
   const unsigned n = static_cast<unsigned>(blocks);
-  switch (width) {
-    case 16: return launch_reorder<16>(t, n, s);
-    case 8: return launch_reorder<8>(t, n, s);
-    case 4: return launch_reorder<4>(t, n, s);
-    case 2: return launch_reorder<2>(t, n, s);
-    default: return launch_reorder<1>(t, n, s);
-  }
+  if (t.beams <= 4)
+    beam_reorder_kernel<4, CAP><<<n, kThreads, 0, s>>>(t);
+  else if (t.beams <= 8)
+    beam_reorder_kernel<8, CAP><<<n, kThreads, 0, s>>>(t);
+  else if (t.beams <= 16)
+    beam_reorder_kernel<16, CAP><<<n, kThreads, 0, s>>>(t);
+  else if (t.beams <= 32)
+    beam_reorder_kernel<32, CAP><<<n, kThreads, 0, s>>>(t);
+  else
+    beam_reorder_kernel<64, CAP><<<n, kThreads, 0, s>>>(t);
+  return cudaGetLastError();
 }
+
+template cudaError_t launch_beam_reorder(const ReorderTable<kReorderSmall>&, int64_t, cudaStream_t);
+template cudaError_t launch_beam_reorder(const ReorderTable<kReorderLarge>&, int64_t, cudaStream_t);
 
 }  // namespace flce
