@@ -445,7 +445,8 @@ flce_status flce_beam_reorder(const flce_beam_state* states, int64_t count,
 /* ------------------------------------------------------------------------
  * A linear layer in 8-bit integers (a head for answering, not for training).
  *
- *   scale_i = max_h |x_ih| / 127,  q_ih = round(x_ih / scale_i)   (halves to even)
+ *   scale_i = max_h |x_ih| * (1/127)   (both rounded to fp32)
+ *   q_ih    = round(x_ih / scale_i)    (the quotient rounded to fp32, halves to even)
  *   lin_ij  = scale_i * weight_scale_j * sum_h q_ih * w_jh + bias_j
  *   u_ij    = logit_scale * lin_ij
  *   out_ij  = softcap * tanh(u_ij / softcap)   if softcap > 0, else u_ij

@@ -1,6 +1,6 @@
 // 8-bit integer rows with a scale each:
 //
-//   scale_i = max_h |x_ih| / 127,  q_ih = round(x_ih / scale_i)
+//   scale_i = max_h |x_ih| * (1/127),  q_ih = round(x_ih / scale_i)
 //
 // as bytes for the caller, or as halves in the operand order of the linear
 // kernel (kernels_qlinear.cu).
@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const QuantPara
     for (int w = 0; w < kThreads / 32; ++w) m = max(m, buf[w]);
     const float peak = __uint_as_float(m);
     // NaN and infinity: the scale is NaN, and so is every product with it
-    scale = peak < INFINITY ? __fdiv_rn(peak, 127.0f) : NAN;
+    scale = peak < INFINITY ? peak * (1.0f / 127.0f) : NAN;
     inv = __fdiv_rn(1.0f, scale);
     if (threadIdx.x == 0) p.scale[row] = scale;
   }
@@ -259,21 +259,43 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const QuantPara
   }
 }
 
-// Four bytes at a time into aligned rows; the source may start anywhere.
+// Rows that start anywhere into rows that start at multiples of 16 bytes: a
+// thread makes 16 bytes from the five aligned words that hold them. At the
+// buffer's two ends, where such a word would reach past it, and in a row's
+// last bytes it takes them one by one.
 __global__ void __launch_bounds__(256)
     align_rows_kernel(const int8_t* src, int64_t rows, int64_t h, int64_t src_pitch, int8_t* dst,
                       int64_t dst_pitch) {
-  const int64_t words = dst_pitch / 4;
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
-    const int8_t* const s = src + row * src_pitch;
-    for (int64_t w = threadIdx.x; w < words; w += 256) {
-      uint32_t v = 0;
+  const int64_t per_row = dst_pitch / 16;
+  const int64_t total = rows * per_row;
+  const uintptr_t begin = reinterpret_cast<uintptr_t>(src);
+  const uintptr_t end = begin + static_cast<uintptr_t>((rows - 1) * src_pitch + h);
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total;
+       i += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t row = total <= 0xffffffffll
+                            ? static_cast<uint32_t>(i) / static_cast<uint32_t>(per_row)
+                            : i / per_row;
+    const int64_t c = (i - row * per_row) * 16;
+    const int8_t* const s = src + row * src_pitch + c;
+    const uintptr_t word = reinterpret_cast<uintptr_t>(s) & ~uintptr_t(3);
+    uint32_t v[4] = {0, 0, 0, 0};
+    if (c + 16 <= h && word >= begin && word + 20 <= end) {
+      const uint32_t* const w = reinterpret_cast<const uint32_t*>(word);
+      const uint32_t shift = 8u * static_cast<uint32_t>(reinterpret_cast<uintptr_t>(s) & 3u);
+      uint32_t lo = __ldg(w);
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (4 * w + j < h)
-          v |= static_cast<uint32_t>(static_cast<uint8_t>(s[4 * w + j])) << (8 * j);
-      reinterpret_cast<uint32_t*>(dst + row * dst_pitch)[w] = v;
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t hi = __ldg(w + j + 1);
+        v[j] = __funnelshift_r(lo, hi, shift);
+        lo = hi;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (c + j < h)
+          v[j >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(s[j])) << (8 * (j & 3));
     }
+    *reinterpret_cast<uint4*>(dst + row * dst_pitch + c) = make_uint4(v[0], v[1], v[2], v[3]);
   }
 }
 
@@ -303,7 +325,8 @@ cudaError_t launch_widen_rows(const QuantParams& p, int dtype, cudaStream_t s) {
 
 cudaError_t launch_align_rows(const int8_t* src, int64_t rows, int64_t h, int64_t src_pitch,
                               int8_t* dst, int64_t dst_pitch, cudaStream_t s) {
-  const unsigned grid = rows < 65536 ? static_cast<unsigned>(rows) : 65536u;
+  const int64_t blocks = (rows * (dst_pitch / 16) + 255) / 256;
+  const unsigned grid = blocks < (1 << 20) ? static_cast<unsigned>(blocks) : 1u << 20;
   align_rows_kernel<<<grid, 256, 0, s>>>(src, rows, h, src_pitch, dst, dst_pitch);
   return cudaGetLastError();
 }

@@ -1,7 +1,7 @@
 """Rows in 8-bit integers with a scale each, and the linear layer on them: a head for answering,
 at half the memory and half the memory traffic of a 16-bit one.
 
-    scale[i] = max |x[i]| / 127,   q[i] = round(x[i] / scale[i])
+    scale[i] = max |x[i]| * (1/127),   q[i] = round(x[i] / scale[i])
     u = logit_scale * (scale[:, None] * weight_scale * (q @ weight.T) + bias)
     out = softcap * tanh(u / softcap)   if softcap, else u
 

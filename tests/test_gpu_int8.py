@@ -19,7 +19,7 @@ def _quantize(x):
     """The definition in 32 bits on the host, where each operation rounds once."""
     x = x.float().cpu()
     peak = x.abs().amax(-1)
-    scale = torch.where(torch.isfinite(peak), peak / 127.0, math.nan)
+    scale = torch.where(torch.isfinite(peak), peak * (torch.ones(()) / 127.0), math.nan)
     s = scale.unsqueeze(-1)
     q = torch.where(s > 0, x / s, torch.zeros(())).nan_to_num().round().clamp(-127, 127)
     return q.to(torch.int8), scale
