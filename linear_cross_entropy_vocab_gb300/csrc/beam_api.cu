@@ -11,11 +11,11 @@ namespace {
 
 using namespace flce::host;
 
-// CTAs that a selection is cut into: several waves of the three that an SM
-// holds, so that the tail is short; the fewer, the less there is to choose
-// from afterwards. A call that cannot have so many with large tiles takes
-// small ones.
-constexpr int64_t kSelectCtas = 1368;
+// CTAs that a selection is cut into: two waves of the three or four that an SM
+// holds. Fewer leave SMs without work; more spend their time on the start and
+// the end of a slice (64 x 8 rows of 128256 fp32: 1024 CTAs 94 us, 1536 108,
+// 2560 115). A call that cannot have kFewCtas large tiles takes small ones.
+constexpr int64_t kSelectCtas = 912;
 constexpr int64_t kFewCtas = 304;
 
 struct SelectPlan {

@@ -275,7 +275,7 @@ struct Slice {
 // A tile is N pieces of 16 bytes per thread; the next tile's are on their way
 // while one is worked on.
 template <class T, int N>
-__global__ void __launch_bounds__(kThreads, N == 1 ? 6 : 3)
+__global__ void __launch_bounds__(kThreads, N == 1 ? 6 : Piece<T>::kElems == 4 ? 4 : 3)
     beam_slices_kernel(const BeamSelectParams p) {
   constexpr int E = Piece<T>::kElems;
   constexpr int kTile = kThreads * E * N;
