@@ -41,6 +41,10 @@ cudaError_t launch_grad_partials(const GradTable<CAP>& tab, int p, int max_ctas,
                                  int* n_partials, cudaStream_t s);
 cudaError_t launch_grad_norm(const double* partials, int n, int p, float* norm_out,
                              cudaStream_t s);
+// Norm and clip in one launch, by a cluster of kGradCluster CTAs.
+constexpr int kGradCluster = 8;
+cudaError_t launch_grad_clip_cluster(const GradTable<kGradTableSmall>& tab, int p, float max_norm,
+                                     float eps, float* norm_out, cudaStream_t s);
 template <int CAP>
 cudaError_t launch_grad_clip(const GradTable<CAP>& tab, const double* partials, int n, int p,
                              float max_norm, float eps, float* norm_out, bool write_norm,

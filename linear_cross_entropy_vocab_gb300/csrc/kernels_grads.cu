@@ -6,7 +6,9 @@
 // over every element of every tensor. Two launches: each CTA of the first
 // leaves one 64-bit partial; each CTA of the second adds all partials in the
 // same order (so all get the same norm, and the same in every run), and the
-// clip scales with it. Nothing is read back to the host.
+// clip scales with it. Nothing is read back to the host. A clip of little data
+// is one launch of a cluster of eight CTAs, which exchange their partials
+// through each other's shared memory.
 //
 // Both are bound by memory: the norm reads each gradient once, the clip reads
 // and writes it once more. The tensors are cut into chunks of 32 KB of source
@@ -272,10 +274,21 @@ __device__ __forceinline__ void chunk_range(const GradEntry& t, uint32_t c, uint
   e1 = e0 + len < t.n ? e0 + len : t.n;
 }
 
+template <int P>
+__device__ __forceinline__ void any_chunk_norm(const GradEntry& t, int64_t e0, int64_t e1,
+                                               double& sum, uint32_t& peak) {
+  if (t.src_dtype == FLCE_F32)
+    chunk_norm<P, FLCE_F32>(t, e0, e1, sum, peak);
+  else if (t.src_dtype == FLCE_BF16)
+    chunk_norm<P, FLCE_BF16>(t, e0, e1, sum, peak);
+  else
+    chunk_norm<P, FLCE_F16>(t, e0, e1, sum, peak);
+}
+
 // partials[blockIdx.x]: the sum of powers of this CTA's chunks, or for
 // P = 0 the bits of their largest magnitude.
 template <int P, int CAP>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, 3)
     grad_partials_kernel(const __grid_constant__ GradTable<CAP> tab, double* partials) {
   __shared__ double buf[kThreads / 32];
   double sum = 0.0;
@@ -285,12 +298,7 @@ __global__ void __launch_bounds__(kThreads, 4)
     const GradEntry& t = tab.t[i];
     int64_t e0, e1;
     chunk_range(t, c, tab.first[i], e0, e1);
-    if (t.src_dtype == FLCE_F32)
-      chunk_norm<P, FLCE_F32>(t, e0, e1, sum, peak);
-    else if (t.src_dtype == FLCE_BF16)
-      chunk_norm<P, FLCE_BF16>(t, e0, e1, sum, peak);
-    else
-      chunk_norm<P, FLCE_F16>(t, e0, e1, sum, peak);
+    any_chunk_norm<P>(t, e0, e1, sum, peak);
   }
   if constexpr (P == 0) {
     peak = block_max(peak, reinterpret_cast<uint32_t*>(buf));
@@ -381,6 +389,22 @@ __device__ __forceinline__ void chunk_scale(const GradEntry& t, int64_t e0, int6
   if (static_cast<int>(threadIdx.x) < rest) store_one(t.dst, t.dst_dtype, e0 + ei, edge * coef);
 }
 
+__device__ __forceinline__ void any_chunk_scale(const GradEntry& t, int64_t e0, int64_t e1,
+                                                float coef) {
+  if (t.src_dtype == FLCE_F32)
+    chunk_scale<FLCE_F32>(t, e0, e1, coef);
+  else if (t.src_dtype == FLCE_BF16)
+    chunk_scale<FLCE_BF16>(t, e0, e1, coef);
+  else
+    chunk_scale<FLCE_F16>(t, e0, e1, coef);
+}
+
+// min(1, max_norm / (norm + eps)); NaN stays NaN.
+__device__ __forceinline__ float clip_factor(float norm, float max_norm, float eps) {
+  const float coef = max_norm / (norm + eps);
+  return coef > 1.0f ? 1.0f : coef;
+}
+
 template <int CAP>
 __global__ void __launch_bounds__(kThreads, 4)
     grad_clip_kernel(const __grid_constant__ GradTable<CAP> tab, const double* partials, int n,
@@ -388,8 +412,7 @@ __global__ void __launch_bounds__(kThreads, 4)
   __shared__ double buf[kThreads / 32];
   const float norm = norm_of(partials, n, p, buf);
   if (write_norm && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = norm;
-  float coef = max_norm / (norm + eps);
-  if (coef > 1.0f) coef = 1.0f;  // a NaN stays one
+  const float coef = clip_factor(norm, max_norm, eps);
   if (tab.in_place && coef == 1.0f) return;
   const uint32_t total = tab.first[tab.count];
   for (uint32_t k = blockIdx.x; k < total; k += gridDim.x) {
@@ -398,12 +421,53 @@ __global__ void __launch_bounds__(kThreads, 4)
     const GradEntry& t = tab.t[i];
     int64_t e0, e1;
     chunk_range(t, c, tab.first[i], e0, e1);
-    if (t.src_dtype == FLCE_F32)
-      chunk_scale<FLCE_F32>(t, e0, e1, coef);
-    else if (t.src_dtype == FLCE_BF16)
-      chunk_scale<FLCE_BF16>(t, e0, e1, coef);
+    any_chunk_scale(t, e0, e1, coef);
+  }
+}
+
+// Norm and clip in one launch of one cluster: rank r takes chunks r, r + 8, ...
+template <int P, int CAP>
+__global__ void __launch_bounds__(kThreads)
+    grad_clip_cluster_kernel(const __grid_constant__ GradTable<CAP> tab, float max_norm, float eps,
+                             float* norm_out) {
+  __shared__ double buf[kThreads / 32];
+  __shared__ double all[kGradCluster];  // every rank's partial
+  const uint32_t rank = cluster_ctarank();
+  const uint32_t total = tab.first[tab.count];
+  double sum = 0.0;
+  uint32_t peak = 0;
+  for (uint32_t c = rank; c < total; c += kGradCluster) {
+    const int i = find_tensor(tab, c);
+    int64_t e0, e1;
+    chunk_range(tab.t[i], c, tab.first[i], e0, e1);
+    any_chunk_norm<P>(tab.t[i], e0, e1, sum, peak);
+  }
+  if constexpr (P == 0)
+    sum = static_cast<double>(__uint_as_float(block_max(peak, reinterpret_cast<uint32_t*>(buf))));
+  else
+    sum = block_sum(sum, buf);
+  if (threadIdx.x < kGradCluster) {
+    const uint32_t to = map_to_rank(smem_addr(&all[rank]), threadIdx.x);
+    asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(to), "d"(sum) : "memory");
+  }
+  cluster_sync();
+  double t = all[0];
+#pragma unroll
+  for (int r = 1; r < kGradCluster; ++r) {
+    if constexpr (P == 0)  // magnitudes, NaN above infinity
+      t = __double_as_longlong(all[r]) > __double_as_longlong(t) ? all[r] : t;
     else
-      chunk_scale<FLCE_F16>(t, e0, e1, coef);
+      t += all[r];
+  }
+  const float norm = static_cast<float>(P == 2 ? sqrt(t) : t);
+  if (rank == 0 && threadIdx.x == 0) *norm_out = norm;
+  const float coef = clip_factor(norm, max_norm, eps);
+  if (tab.in_place && coef == 1.0f) return;
+  for (uint32_t c = rank; c < total; c += kGradCluster) {
+    const int i = find_tensor(tab, c);
+    int64_t e0, e1;
+    chunk_range(tab.t[i], c, tab.first[i], e0, e1);
+    any_chunk_scale(tab.t[i], e0, e1, coef);
   }
 }
 
@@ -442,6 +506,26 @@ cudaError_t launch_grad_clip(const GradTable<CAP>& tab, const double* partials, 
   grad_clip_kernel<CAP><<<grid_of(tab, max_ctas), kThreads, 0, s>>>(
       tab, partials, n, p, max_norm, eps, norm_out, write_norm ? 1 : 0);
   return cudaGetLastError();
+}
+
+cudaError_t launch_grad_clip_cluster(const GradTable<kGradTableSmall>& tab, int p, float max_norm,
+                                     float eps, float* norm_out, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3(kGradCluster, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.stream = s;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kGradCluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  auto kern = p == 0   ? grad_clip_cluster_kernel<0, kGradTableSmall>
+              : p == 1 ? grad_clip_cluster_kernel<1, kGradTableSmall>
+                       : grad_clip_cluster_kernel<2, kGradTableSmall>;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tab, max_norm, eps, norm_out);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template cudaError_t launch_grad_partials(const GradTable<kGradTableSmall>&, int, int, double*,
