@@ -381,8 +381,12 @@ __global__ void __launch_bounds__(kThreads, N == 1 ? 6 : Piece<T>::kElems == 4 ?
       __syncthreads();
       const int n = count;
       __syncthreads();
-      if (n > kBuffer) break;  // taken one after the other below
-      if (n >= p.m && (!full || n > p.m)) {
+      if (n > kBuffer) {
+        // taken one after the other below: the rest is only summed (this floor
+        // stands for a NaN, which nothing reaches)
+        floor_bits = 0xffffffffu;
+        full = true;
+      } else if (n >= p.m && (!full || n > p.m)) {
         rank_keys(buf, n, p.m, [&](int rank, uint64_t key) { kept[rank] = key; });
         __syncthreads();
         if (static_cast<int>(threadIdx.x) < p.m) buf[threadIdx.x] = kept[threadIdx.x];

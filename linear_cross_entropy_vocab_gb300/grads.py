@@ -150,7 +150,11 @@ def clip_grads_(grads: Iterable[torch.Tensor], max_norm: float, norm_type: float
     enough already, nothing is written. A NaN norm makes every gradient NaN, an infinite one makes
     the finite ones 0."""
     max_norm, eps = _limits(max_norm, eps)
-    return _run(_listed(grads), None, norm_type, max_norm, eps)
+    grads = _listed(grads)
+    norm = _run(grads, None, norm_type, max_norm, eps)
+    if grads and not grads[0].is_inference():
+        torch.autograd.graph.increment_version(grads)
+    return norm
 
 
 def clip_grads(grads: Iterable[torch.Tensor], max_norm: float, norm_type: float = 2.0, *,
@@ -161,7 +165,10 @@ def clip_grads(grads: Iterable[torch.Tensor], max_norm: float, norm_type: float 
     grads, out = _listed(grads), _listed(out)
     if len(out) != len(grads):
         raise ValueError(f"{len(grads)} gradients and {len(out)} outputs")
-    return _run(grads, out, norm_type, max_norm, eps)
+    norm = _run(grads, out, norm_type, max_norm, eps)
+    if out and not out[0].is_inference():
+        torch.autograd.graph.increment_version(out)
+    return norm
 
 
 def clip_grad_norm_(parameters: Iterable[torch.Tensor], max_norm: float, norm_type: float = 2.0,

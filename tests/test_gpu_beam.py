@@ -141,6 +141,35 @@ def test_equal_scores_take_the_lowest_index():
     assert torch.equal(got.parents * 5000 + got.tokens, order)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_long_slices(dtype):
+    """Slices of several tiles: equal logits that overflow the list of candidates, logits that only
+    rise and only fall, a mask that opens late, and ordinary ones."""
+    b, k, v, m = 64, 8, 40000, 16
+    logits, scores, g = _make(b, k, v, dtype)
+    _check(beam_select(logits, scores, m), _scores64(logits, scores), m)
+    late = torch.arange(v, device="cuda") >= v - 3000
+    _check(beam_select(logits, scores, m, allowed=late),
+           _scores64(logits, scores, allowed=late.expand(b, k, v)), m)
+    few = torch.arange(v, device="cuda") % 4099 == 7
+    _check(beam_select(logits, scores, m, allowed=few),
+           _scores64(logits, scores, allowed=few.expand(b, k, v)), m)
+    scores = scores - 100.0 * torch.arange(k, device="cuda")  # the first beam alone counts
+    logits[:, :2] = 1.5
+    got = beam_select(logits, scores, m)
+    assert got.tokens.tolist() == [list(range(m))] * b and not bool(got.parents.any())
+    _check(got, _scores64(logits, scores), m)
+    logits[:, 0] = torch.linspace(-9, 9, v, device="cuda").to(dtype)
+    _check(beam_select(logits, scores, m), _scores64(logits, scores), m)
+    logits[:, 0] = logits[:, 0].flip(1)
+    _check(beam_select(logits, scores, m), _scores64(logits, scores), m)
+    logits[:, 0] = -math.inf
+    logits[:, 0, -1] = 0.25
+    got = beam_select(logits, scores, m)
+    assert got.tokens[:, 0].tolist() == [v - 1] * b
+    _check(got, _scores64(logits, scores), m)
+
+
 def test_strided_logits():
     """The last position of a longer output, a padded vocabulary, rows at odd addresses."""
     g = torch.Generator("cuda").manual_seed(5)

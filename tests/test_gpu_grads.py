@@ -233,6 +233,15 @@ def test_after_the_loss():
     assert abs(_norm64([hidden.grad, weight.grad], 2.0) - 0.01) < 0.01 * 2.0 ** -8
 
 
+def test_autograd_sees_the_change():
+    g = _make([(100,), (200,)], torch.float32)
+    versions = [x._version for x in g]
+    clip_grads_(g, 1.0)
+    assert [x._version for x in g] == [v + 1 for v in versions]
+    with torch.inference_mode():
+        clip_grads_([torch.ones(100, device="cuda")], 1.0)
+
+
 def test_refusals():
     a = torch.zeros(100, device="cuda")
     with pytest.raises(RuntimeError, match="overlap"):
