@@ -11,11 +11,12 @@ namespace {
 
 using namespace flce::host;
 
-// CTAs that a selection is cut into: two waves of the three or four that an SM
-// holds. Fewer leave SMs without work; more spend their time on the start and
-// the end of a slice (64 x 8 rows of 128256 fp32: 1024 CTAs 94 us, 1536 108,
-// 2560 115). A call that cannot have kFewCtas large tiles takes small ones.
-constexpr int64_t kSelectCtas = 912;
+// CTAs that a selection is cut into: most of what the GPU holds at a time (four
+// on an SM for fp32, six for 16-bit types). Fewer leave SMs without work; more
+// spend their time on the start and the end of a slice (64 x 8 rows of 128256,
+// fp32 and bf16: 512 CTAs 85 and 77 us, 1024 92 and 82, 1536 108 and 107). A
+// call that cannot have kFewCtas large tiles takes small ones.
+constexpr int64_t kSelectCtas = 512;
 constexpr int64_t kFewCtas = 304;
 
 struct SelectPlan {
@@ -51,8 +52,8 @@ SelectPlan plan_select(const flce_beam_problem* p) {
   SelectPlan q;
   const int64_t rows = p->batch * p->beams;
   const int64_t es = p->dtype == FLCE_F32 ? 4 : 2;
-  q.large = rows * ceil_div(p->v * es, flce::kTileLargeBytes) >= kFewCtas;
-  const int64_t tile = (q.large ? flce::kTileLargeBytes : flce::kTileSmallBytes) / es;
+  q.large = rows * ceil_div(p->v, flce::kTileLarge) >= kFewCtas;
+  const int64_t tile = q.large ? flce::kTileLarge : flce::kTileSmallBytes / es;
   const int64_t tiles = ceil_div(p->v, tile);
   // slices of whole tiles, as equal as that allows
   q.splits = std::max<int64_t>(1, std::min(tiles, ceil_div(kSelectCtas, std::max<int64_t>(rows, 1))));

@@ -13,11 +13,10 @@ constexpr int kBeamMaxCandidates = 256;
 constexpr int kBeamMaxBeams = 64;  // of a reordering; a selection takes more (its scores are staged)
 constexpr int kBeamMaxSelectBeams = 1024;
 
-// A selection CTA (256 threads) holds tiles of 1 or kPiecesLarge pieces of 16
-// bytes for each thread.
-constexpr int kPiecesLarge = 4;
+// A selection CTA (256 threads) holds tiles of 16 bytes or of 16 logits for
+// each thread.
 constexpr int kTileSmallBytes = 256 * 16;
-constexpr int kTileLargeBytes = kTileSmallBytes * kPiecesLarge;
+constexpr int kTileLarge = 256 * 16;
 
 struct BeamSelectParams {
   const void* logits;

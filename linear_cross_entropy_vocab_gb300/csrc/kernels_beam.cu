@@ -27,9 +27,10 @@
 // Bound: the logits are read once, each thread's 16-byte pieces of the next
 // tile while it works on this one. Per logit there are two additions, a
 // product, an exponential and a maximum; whether a value reaches the threshold
-// is asked once for a piece. Issuing those bounds large calls: 64 x 8 rows of
-// 128256 fp32 logits take 59 us, 4.1 TB/s, with half of the issue slots used;
-// small ones are bound by the chain from the loads through two launches.
+// is asked once for a piece. With half of the issue slots used, what bounds a
+// large call is the CTAs' progress from tile to tile (more loads on their way,
+// through registers or shared memory, gained nothing); a small one is bound by
+// the chain from the loads through two launches.
 //
 // Reordering. state[b K + j] = state[b K + parent_bj], in place: a thread owns
 // the same 16 bytes (or less, by alignment) of all K beams of a prompt, reads
@@ -275,7 +276,7 @@ struct Slice {
 // A tile is N pieces of 16 bytes per thread; the next tile's are on their way
 // while one is worked on.
 template <class T, int N>
-__global__ void __launch_bounds__(kThreads, N == 1 ? 6 : Piece<T>::kElems == 4 ? 4 : 3)
+__global__ void __launch_bounds__(kThreads, N == 4 ? 4 : 6)
     beam_slices_kernel(const BeamSelectParams p) {
   constexpr int E = Piece<T>::kElems;
   constexpr int kTile = kThreads * E * N;
@@ -643,7 +644,8 @@ template <class T>
 cudaError_t launch_select(const BeamSelectParams& p, bool large, cudaStream_t s) {
   const int64_t blocks = static_cast<int64_t>(p.batch) * p.beams * p.splits;
   if (large)
-    beam_slices_kernel<T, kPiecesLarge><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(p);
+    beam_slices_kernel<T, kTileLarge / (kThreads * Piece<T>::kElems)>
+        <<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(p);
   else
     beam_slices_kernel<T, 1><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(p);
   cudaError_t e = cudaGetLastError();
