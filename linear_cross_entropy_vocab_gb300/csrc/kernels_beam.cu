@@ -128,6 +128,7 @@ __device__ __forceinline__ bool better(const Scored& a, const Scored& b) {
   return a.s > b.s || (a.s == b.s && a.at < b.at);
 }
 __device__ __forceinline__ bool better(uint64_t a, uint64_t b) { return a > b; }
+__device__ __forceinline__ bool better(uint32_t a, uint32_t b) { return a > b; }
 __device__ __forceinline__ Scored nothing(const Scored&) { return Scored{0, ~0ull}; }
 __device__ __forceinline__ uint64_t nothing(uint64_t) { return 0; }
 
@@ -135,6 +136,9 @@ __device__ __forceinline__ Scored shfl_xor(const Scored& a, int o) {
   return Scored{__shfl_xor_sync(0xffffffffu, a.s, o), __shfl_xor_sync(0xffffffffu, a.at, o)};
 }
 __device__ __forceinline__ uint64_t shfl_xor(uint64_t a, int o) {
+  return __shfl_xor_sync(0xffffffffu, a, o);
+}
+__device__ __forceinline__ uint32_t shfl_xor(uint32_t a, int o) {
   return __shfl_xor_sync(0xffffffffu, a, o);
 }
 
@@ -205,33 +209,36 @@ __device__ __forceinline__ void rank_keys(K* buf, int n, int m, Out out) {
   for (int i = static_cast<int>(threadIdx.x); i < m && i < n; i += kThreads) out(i, buf[i]);
 }
 
-// The warps of a group of 256 / g threads (g a power of two, at most 256) and
-// the smallest of the groups' maxima, for a 32-bit order: on every thread.
-__device__ __forceinline__ uint32_t group_floor(uint32_t x, int g, uint32_t* warp_buf) {
-  const int width = kThreads / g;  // threads per group
-  for (int o = 1; o < 32 && o < width; o <<= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
-  if (width <= 32) {
-    x = __reduce_min_sync(0xffffffffu, x);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) warp_buf[threadIdx.x >> 5] = x;
-    __syncthreads();
-    uint32_t t = warp_buf[0];
+// The smallest of the maxima of g groups of threads (g a power of two, at most
+// 256), on every thread. Thread t is in group t mod g: threads without a value
+// lie together, at the end of a short slice, and leave no group empty. `red`
+// has a place for each lane of each warp.
+template <class K>
+__device__ __forceinline__ K group_floor(K x, int g, K (*red)[32]) {
+  const int lane = static_cast<int>(threadIdx.x & 31), warp = static_cast<int>(threadIdx.x >> 5);
+  for (int o = 16; o >= g; o >>= 1) {
+    const K y = shfl_xor(x, o);
+    if (better(y, x)) x = y;
+  }
+  __syncthreads();
+  red[warp][lane] = x;
+  __syncthreads();
+  const int classes = g > 32 ? g / 32 : 1;  // warps w and w + classes share their groups
+  K floor_at = x;
+  for (int c = 0; c < classes; ++c) {
+    K m = red[c][lane];
+    for (int w = c + classes; w < kWarps; w += classes) {
+      const K y = red[w][lane];
+      if (better(y, m)) m = y;
+    }
+    if (c == 0 || better(floor_at, m)) floor_at = m;
+  }
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) t = min(t, warp_buf[w]);
-    return t;
+  for (int o = 16; o > 0; o >>= 1) {
+    const K y = shfl_xor(floor_at, o);
+    if (better(floor_at, y)) floor_at = y;
   }
-  // fewer groups than warps: the maximum of each run of width / 32 warps
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) warp_buf[threadIdx.x >> 5] = x;
-  __syncthreads();
-  uint32_t t = 0xffffffffu;
-  const int per = width / 32;
-  for (int a = 0; a < kWarps; a += per) {
-    uint32_t m = 0;
-    for (int w = a; w < a + per; ++w) m = max(m, warp_buf[w]);
-    t = min(t, m);
-  }
-  return t;
+  return floor_at;
 }
 
 // One slice of a row as the threads of a CTA see it; places count from its start.
@@ -283,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, N == 4 ? 4 : 6)
   __shared__ uint64_t buf[kBuffer];
   __shared__ uint64_t kept[kBeamMaxCandidates];
   __shared__ uint64_t warp_key[kWarps];
-  __shared__ uint32_t warp_u32[kWarps];
+  __shared__ uint32_t red[kWarps][32];
   __shared__ float2 warp_stat[kWarps];
   __shared__ int count;
   grid_launch_dependents();
@@ -361,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, N == 4 ? 4 : 6)
     }
 
     // what reaches the threshold: the M-th best so far, once there are M
-    if (!full) floor_bits = max(floor_bits, group_floor(order_bits(tile_top), p.groups, warp_u32));
+    if (!full) floor_bits = max(floor_bits, group_floor(order_bits(tile_top), p.groups, red));
     const float at_least = floor_bits == 0 ? -INFINITY : from_order_bits(floor_bits);
     if (tile_top >= at_least && tile_top > -INFINITY) {
 #pragma unroll
@@ -545,11 +552,11 @@ __global__ void __launch_bounds__(kThreads) beam_choose_kernel(const BeamSelectP
               : none;
     return x;
   };
-  // the thread's candidates: a rotation, because the keys of a slice are in
-  // order and the groups shall see all ranks alike
+  // the thread's candidates: rotated in each 16, because the keys of a slice
+  // are in order and the groups shall see all ranks alike
   auto place_of = [&](int round) -> int {
-    return round * kThreads +
-           static_cast<int>((threadIdx.x + static_cast<unsigned>(round) * 97u) & (kThreads - 1));
+    const int t = static_cast<int>(threadIdx.x);
+    return round * kThreads + (t & ~15) + ((t + (t >> 4) + 5 * round) & 15);
   };
   const int rounds = (total + kThreads - 1) / kThreads;
   // the first of them stay in registers
@@ -569,29 +576,8 @@ __global__ void __launch_bounds__(kThreads) beam_choose_kernel(const BeamSelectP
     const Scored x = c < total ? candidate(c) : none;
     if (better(x, best)) best = x;
   }
-  // the smallest of the groups' best
-  const int width = kThreads / p.groups;
-  for (int o = 1; o < 32 && o < width; o <<= 1) {
-    const Scored y = shfl_xor(best, o);
-    if (better(y, best)) best = y;
-  }
-  if (width <= 32) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const Scored y = shfl_xor(best, o);
-      if (better(best, y)) best = y;
-    }
-  }
-  if (lane == 0) warp_best[threadIdx.x >> 5] = best;
-  __syncthreads();
-  const int per = width > 32 ? width / 32 : 1;
-  Scored floor_at = none;
-  for (int a = 0; a < kWarps; a += per) {
-    Scored m = warp_best[a];
-    for (int w = a + 1; w < a + per; ++w)
-      if (better(warp_best[w], m)) m = warp_best[w];
-    if (a == 0 || better(floor_at, m)) floor_at = m;
-  }
+  const Scored floor_at = group_floor(best, p.groups, reinterpret_cast<Scored(*)[32]>(buf));
+  __syncthreads();  // its part of buf has been read
   auto push = [&](const Scored& x) {
     if (x.s == 0 || better(floor_at, x)) return;
     const uint32_t place = take_place(&count);
