@@ -125,13 +125,18 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
-// An mbarrier arrive on the pair's even CTA.
+// An mbarrier arrive on the pair's even CTA. What the arrival announces lies in
+// tensor memory, written or read by tcgen05 instructions that have completed
+// and are ordered by tcgen05.fence; no other memory is handed over. So the
+// arrival needs no release at cluster scope, and the waits below no acquire
+// there: each costs hundreds of nanoseconds, once for a stage.
 template <int CG>
 __device__ __forceinline__ void arrive_leader(uint32_t bar, bool leader) {
   if (CG == 1 || leader)
     mbar_arrive(bar);
   else
-    mbar_arrive_cluster(map_to_rank(bar, 0));
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(map_to_rank(bar, 0))
+                 : "memory");
 }
 
 template <int CG>
@@ -251,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int u = unit0; ok && u < total; u += units) {
         const int row = (u % p.n_tiles) * p.nt + static_cast<int>(rank) * (p.nt / CG);
         for (int i = 0; i < k_iters; ++i) {
-          if (!wait_bar<CG>(smem_addr(&ctl.x_empty[s]), phase ^ 1u, abort_flag, err_word)) {
+          if (!mbar_wait(smem_addr(&ctl.x_empty[s]), phase ^ 1u, abort_flag, err_word)) {
             ok = false;
             break;
           }
@@ -295,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int u = unit0; ok && u < total; u += units, ++it) {
         const int buf = bufs == 2 ? it & 1 : 0;
         const uint32_t use = static_cast<uint32_t>(bufs == 2 ? it >> 1 : it) & 1u;
-        ok = wait_bar<CG>(smem_addr(&ctl.acc_empty[buf]), use ^ 1u, abort_flag, err_word);
+        ok = mbar_wait(smem_addr(&ctl.acc_empty[buf]), use ^ 1u, abort_flag, err_word);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
@@ -303,8 +308,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after_sync();
         const uint32_t d = tm + static_cast<uint32_t>(buf * 128);
         for (int i = 0; i < k_iters; ++i) {
-          ok = wait_bar<CG>(smem_addr(&ctl.x_full[xs]), x_phase, abort_flag, err_word) &&
-               wait_bar<CG>(smem_addr(&ctl.a_full[as]), a_phase, abort_flag, err_word);
+          ok = mbar_wait(smem_addr(&ctl.x_full[xs]), x_phase, abort_flag, err_word) &&
+               mbar_wait(smem_addr(&ctl.a_full[as]), a_phase, abort_flag, err_word);
           if (!__all_sync(0xffffffffu, ok)) {
             ok = false;
             break;
@@ -374,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t h[32];
 #pragma unroll
       for (int j = 0; j < 16; ++j) widen(w[j], h[2 * j], h[2 * j + 1]);
-      ok = wait_bar<CG>(smem_addr(&ctl.a_empty[as]), a_phase, abort_flag, err_word);
+      ok = mbar_wait(smem_addr(&ctl.a_empty[as]), a_phase, abort_flag, err_word);
       if (!__all_sync(0xffffffffu, ok)) break;
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&ctl.w_empty[s]));  // all lanes have read their bytes
@@ -429,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return c * 32 + lane < cols ? __ldg(p.x_scale + n0 + c * 32 + lane) : 0.0f;
       };
       float xs_next = scales(c0);
-      const bool ok = wait_bar<CG>(smem_addr(&ctl.acc_full[buf]), use, abort_flag, err_word);
+      const bool ok = mbar_wait(smem_addr(&ctl.acc_full[buf]), use, abort_flag, err_word);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after_sync();
       auto release = [&] {
