@@ -291,6 +291,7 @@ template <int P, int CAP>
 __global__ void __launch_bounds__(kThreads, 3)
     grad_partials_kernel(const __grid_constant__ GradTable<CAP> tab, double* partials) {
   __shared__ double buf[kThreads / 32];
+  grid_launch_dependents();
   double sum = 0.0;
   uint32_t peak = 0;
   for (uint32_t c = blockIdx.x; c < tab.first[tab.count]; c += gridDim.x) {
@@ -327,6 +328,7 @@ __device__ __forceinline__ float norm_of(const double* partials, int n, int p, d
 __global__ void __launch_bounds__(kThreads)
     grad_norm_kernel(const double* partials, int n, int p, float* norm_out) {
   __shared__ double buf[kThreads / 32];
+  grid_dependency_wait();
   const float norm = norm_of(partials, n, p, buf);
   if (threadIdx.x == 0) *norm_out = norm;
 }
@@ -410,6 +412,7 @@ __global__ void __launch_bounds__(kThreads, 4)
     grad_clip_kernel(const __grid_constant__ GradTable<CAP> tab, const double* partials, int n,
                      int p, float max_norm, float eps, float* norm_out, int write_norm) {
   __shared__ double buf[kThreads / 32];
+  grid_dependency_wait();
   const float norm = norm_of(partials, n, p, buf);
   if (write_norm && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = norm;
   const float coef = clip_factor(norm, max_norm, eps);
@@ -471,6 +474,23 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
+// A launch that may be placed while the kernel before it drains; it waits for
+// that kernel's end before it reads anything.
+template <class... P, class... A>
+cudaError_t launch_after(void (*kern)(P...), unsigned grid, cudaStream_t s, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.stream = s;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 template <int CAP>
 unsigned grid_of(const GradTable<CAP>& tab, int max_ctas) {
   const uint32_t chunks = tab.first[tab.count];
@@ -495,17 +515,15 @@ cudaError_t launch_grad_partials(const GradTable<CAP>& tab, int p, int max_ctas,
 
 cudaError_t launch_grad_norm(const double* partials, int n, int p, float* norm_out,
                              cudaStream_t s) {
-  grad_norm_kernel<<<1, kThreads, 0, s>>>(partials, n, p, norm_out);
-  return cudaGetLastError();
+  return launch_after(grad_norm_kernel, 1, s, partials, n, p, norm_out);
 }
 
 template <int CAP>
 cudaError_t launch_grad_clip(const GradTable<CAP>& tab, const double* partials, int n, int p,
                              float max_norm, float eps, float* norm_out, bool write_norm,
                              int max_ctas, cudaStream_t s) {
-  grad_clip_kernel<CAP><<<grid_of(tab, max_ctas), kThreads, 0, s>>>(
-      tab, partials, n, p, max_norm, eps, norm_out, write_norm ? 1 : 0);
-  return cudaGetLastError();
+  return launch_after(grad_clip_kernel<CAP>, grid_of(tab, max_ctas), s, tab, partials, n, p,
+                      max_norm, eps, norm_out, write_norm ? 1 : 0);
 }
 
 cudaError_t launch_grad_clip_cluster(const GradTable<kGradTableSmall>& tab, int p, float max_norm,
