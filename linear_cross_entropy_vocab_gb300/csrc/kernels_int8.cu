@@ -5,9 +5,13 @@
 // as bytes for the caller, or as halves in the operand order of the linear
 // kernel (kernels_qlinear.cu).
 //
-// Bound by memory: a CTA takes one row, keeps up to 4096 values of it in
-// registers, as they came, between the maximum and the rounding, and reads
-// longer rows a second time, from L2. What keeps it near that bound is the
+// Bound by memory: a team of threads takes one row, keeps it in registers, as
+// it came, between the maximum and the rounding, and reads rows of more than
+// 4096 values a second time, from L2. The team is 8 threads for rows of up to
+// 256 values, a warp up to 2048, a CTA beyond: 128256 bf16 rows of 128 take
+// 32 us with 8 threads each and 54 with 32; rows of 2048 144 with a warp and
+// 192 with a CTA; rows of 4096 266 with a CTA and 314 with a warp (calls with
+// their host side). What keeps it near that bound is the
 // number of instructions for a value: the maximum is taken on the raw bits, two
 // 16-bit values at a time; the quotient is a product with the reciprocal and one
 // correction; and adding 1.5 * 2^23 rounds it and leaves the integer in the low
@@ -23,8 +27,6 @@ namespace flce {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kVecs = 4;  // groups of 8 values per thread and sweep
-constexpr int kSweep = kThreads * kVecs * 8;
 
 // A group of 8 values: how it is loaded, its largest magnitude by the order of
 // the bits (NaN is above infinity), and its values.
@@ -69,9 +71,14 @@ struct Group16 {
   __device__ __forceinline__ void load_some(const void* p, int64_t n) {
     const uint16_t* const u = static_cast<const uint16_t*>(p);
     uint32_t w[4];
+    if (n >= 8 && (reinterpret_cast<uintptr_t>(p) & 3u) == 0) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      w[j] = (2 * j < n ? u[2 * j] : 0u) | ((2 * j + 1 < n ? u[2 * j + 1] : 0u) << 16);
+      for (int j = 0; j < 4; ++j) w[j] = __ldg(static_cast<const uint32_t*>(p) + j);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        w[j] = (2 * j < n ? u[2 * j] : 0u) | ((2 * j + 1 < n ? u[2 * j + 1] : 0u) << 16);
+    }
     q = make_uint4(w[0], w[1], w[2], w[3]);
   }
   __device__ __forceinline__ uint32_t peak(uint32_t m) const {
@@ -191,29 +198,36 @@ __device__ __forceinline__ void put_halves(__half* wide, int64_t e, const float 
   *reinterpret_cast<uint4*>(wide + e) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// One CTA per row; WIDE: halves in operand order instead of bytes.
-template <class T, bool WIDE>
+// One row per team of TEAM threads; WIDE: halves in operand order instead of
+// bytes.
+template <class T, bool WIDE, int TEAM, int VECS>
 __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const QuantParams p) {
   __shared__ uint32_t buf[kThreads / 32];
   if (WIDE) grid_launch_dependents();
   constexpr bool kInt = sizeof(T) == 1;
-  const int64_t row = blockIdx.x;
+  constexpr int kSweep = TEAM * VECS * 8;
+  const int in_team = static_cast<int>(threadIdx.x) % TEAM;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kThreads / TEAM) +
+                      static_cast<int>(threadIdx.x) / TEAM;
+  if (TEAM < kThreads && row >= p.n) return;
   const T* const x0 = static_cast<const T*>(p.x) + row * p.x_pitch;
   const bool vec = (reinterpret_cast<uintptr_t>(x0) & (Group<T>::kAlign - 1)) == 0;
   int8_t* const q0 = WIDE ? nullptr : p.q + row * p.q_pitch;
   const bool qvec = (reinterpret_cast<uintptr_t>(q0) & 7u) == 0;
   __half* const w0 = WIDE ? static_cast<__half*>(p.wide) + row * p.wide_pitch : nullptr;
   const int64_t end = WIDE ? p.wide_pitch : p.h;
-  Group<T> g[kVecs];
+  Group<T> g[VECS];
   // the thread's groups of the sweep from e0 on; zeros past the row's end
   auto load = [&](int64_t e0) {
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      const int64_t e = e0 + (i * kThreads + static_cast<int>(threadIdx.x)) * 8;
+    for (int i = 0; i < VECS; ++i) {
+      const int64_t e = e0 + (i * TEAM + in_team) * 8;
       if (vec && e + 8 <= p.h)
         g[i].load(x0 + e);
-      else
+      else if (e < p.h)
         g[i].load_some(x0 + e, p.h - e);
+      else
+        g[i] = Group<T>{};
     }
   };
   float scale = 1.0f, inv = 1.0f;
@@ -222,25 +236,33 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const QuantPara
     for (int64_t e0 = 0; e0 < p.h; e0 += kSweep) {
       load(e0);
 #pragma unroll
-      for (int i = 0; i < kVecs; ++i) m = g[i].peak(m);
+      for (int i = 0; i < VECS; ++i) m = g[i].peak(m);
     }
     m = __float_as_uint(Group<T>::peak_value(m));
-    m = __reduce_max_sync(0xffffffffu, m);
-    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = m;
-    __syncthreads();
+    if constexpr (TEAM < 32) {
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) m = max(m, buf[w]);
+      for (int o = TEAM / 2; o > 0; o >>= 1)
+        m = max(m, __shfl_xor_sync(0xffu << (threadIdx.x & 24u), m, o, TEAM));
+    } else {
+      m = __reduce_max_sync(0xffffffffu, m);
+    }
+    if constexpr (TEAM == kThreads) {
+      if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = m;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < kThreads / 32; ++w) m = max(m, buf[w]);
+    }
     const float peak = __uint_as_float(m);
     // NaN and infinity: the scale is NaN, and so is every product with it
     scale = peak < INFINITY ? peak * (1.0f / 127.0f) : NAN;
     inv = __fdiv_rn(1.0f, scale);
-    if (threadIdx.x == 0) p.scale[row] = scale;
+    if (in_team == 0) p.scale[row] = scale;
   }
   for (int64_t e0 = 0; e0 < end; e0 += kSweep) {
     if (kInt || p.h > kSweep) load(e0);
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      const int64_t e = e0 + (i * kThreads + static_cast<int>(threadIdx.x)) * 8;
+    for (int i = 0; i < VECS; ++i) {
+      const int64_t e = e0 + (i * TEAM + in_team) * 8;
       if (e >= end) break;
       float x[8];
       g[i].values(x);
@@ -299,18 +321,30 @@ __global__ void __launch_bounds__(256)
   }
 }
 
+template <class T, bool WIDE, int TEAM, int VECS>
+cudaError_t launch_team(const QuantParams& p, cudaStream_t s) {
+  const int64_t rows = kThreads / TEAM;  // of a CTA
+  const unsigned grid = static_cast<unsigned>((p.n + rows - 1) / rows);
+  quantize_rows_kernel<T, WIDE, TEAM, VECS><<<grid, kThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+template <class T, bool WIDE>
+cudaError_t launch_typed(const QuantParams& p, cudaStream_t s) {
+  const int64_t len = WIDE ? p.wide_pitch : p.h;
+  if (len <= 256) return launch_team<T, WIDE, 8, 4>(p, s);
+  if (len <= 1024) return launch_team<T, WIDE, 32, 4>(p, s);
+  if (len <= 2048) return launch_team<T, WIDE, 32, 8>(p, s);
+  return launch_team<T, WIDE, kThreads, 4>(p, s);
+}
+
 template <bool WIDE>
 cudaError_t launch_rows(const QuantParams& p, int dtype, cudaStream_t s) {
-  const unsigned grid = static_cast<unsigned>(p.n);
-  if (dtype == FLCE_F32)
-    quantize_rows_kernel<float, WIDE><<<grid, kThreads, 0, s>>>(p);
-  else if (dtype == FLCE_BF16)
-    quantize_rows_kernel<__nv_bfloat16, WIDE><<<grid, kThreads, 0, s>>>(p);
-  else if (dtype == FLCE_F16)
-    quantize_rows_kernel<__half, WIDE><<<grid, kThreads, 0, s>>>(p);
-  else if constexpr (WIDE)
-    quantize_rows_kernel<int8_t, WIDE><<<grid, kThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  if (dtype == FLCE_F32) return launch_typed<float, WIDE>(p, s);
+  if (dtype == FLCE_BF16) return launch_typed<__nv_bfloat16, WIDE>(p, s);
+  if (dtype == FLCE_F16) return launch_typed<__half, WIDE>(p, s);
+  if constexpr (WIDE) return launch_typed<int8_t, WIDE>(p, s);
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace

@@ -53,10 +53,11 @@ def quantize_rows(x: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
         stream = raw_stream(x.device)
         abi.flce_quantize_rows(x.data_ptr(), code, n, h, pitch, q.data_ptr(), q_pitch,
                                scale.data_ptr(), stream)
-    q = q[:, :h]
-    if len(lead) != 1:
-        q = q.unflatten(0, lead) if lead else q[0]
-    return q, scale.reshape(lead)
+    if q_pitch != h:
+        q = q[:, :h]
+    if len(lead) == 1:
+        return q, scale
+    return q.unflatten(0, lead) if lead else q[0], scale.reshape(lead)
 
 
 def int8_linear(x: torch.Tensor, weight: torch.Tensor, weight_scale: torch.Tensor,

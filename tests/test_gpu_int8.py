@@ -31,7 +31,8 @@ def _same(a, b):
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("n,h", [(1, 1), (3, 7), (5, 16), (130, 100), (2, 1023), (7, 1024),
-                                 (3, 4096), (2, 4097), (3, 20001)])
+                                 (3, 4096), (2, 4097), (3, 20001), (33, 255), (17, 256),
+                                 (9, 257), (5, 2047), (6, 2048), (3, 2049), (1000, 40)])
 def test_quantize(n, h, dtype):
     x = torch.randn(n, h, generator=torch.Generator().manual_seed(h)).to(dtype)
     q, scale = quantize_rows(x.cuda())
