@@ -41,6 +41,7 @@ struct QLinearTcParams {
   int32_t bias_dtype;
   int32_t nt;                 // rows of x in a tile
   int32_t n_tiles, v_tiles;   // tiles along x and along the weight
+  int32_t band;               // tiles of x that run through the weight together
   int32_t k_blocks;           // 64-deep blocks of h
   int32_t w_stages, x_stages; // set by the launcher
   int* err_word;

@@ -156,6 +156,18 @@ __device__ __forceinline__ void store(float* p, float x) { *p = x; }
 __device__ __forceinline__ void store(__nv_bfloat16* p, float x) { *p = __float2bfloat16(x); }
 __device__ __forceinline__ void store(__half* p, float x) { *p = __float2half(x); }
 
+// Tile u of a launch: its place along x and along the weight. Tiles of x run
+// fastest, `band` of them at a time, so that what the tiles in flight share of
+// x stays in L2 over the whole weight.
+__device__ __forceinline__ void tile_place(const QLinearTcParams& p, int u, int& n, int& v) {
+  const int per_band = p.band * p.v_tiles;
+  const int first = (u / per_band) * p.band;
+  const int wide = p.n_tiles - first < p.band ? p.n_tiles - first : p.band;
+  const int r = u % per_band;
+  n = first + r % wide;
+  v = r / wide;
+}
+
 template <int CG, class T>
 __global__ void __launch_bounds__(kThreads, 1)
     qlinear_kernel(const __grid_constant__ QLinearTcParams p) {
@@ -225,7 +237,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t phase = 0, armed = 0, last_phase = 0;
       bool ok = true;
       for (int u = unit0; ok && u < total; u += units) {
-        const int row = (u / p.n_tiles) * (128 * CG) + static_cast<int>(rank) * 128;
+        int n, v;
+        tile_place(p, u, n, v);
+        const int row = v * (128 * CG) + static_cast<int>(rank) * 128;
         for (int i = 0; i < k_iters; ++i) {
           if (!mbar_wait(smem_addr(&ctl.w_empty[s]), phase ^ 1u, abort_flag, err_word)) {
             ok = false;
@@ -254,7 +268,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t phase = 0, armed = 0, last_phase = 0;
       bool ok = true;
       for (int u = unit0; ok && u < total; u += units) {
-        const int row = (u % p.n_tiles) * p.nt + static_cast<int>(rank) * (p.nt / CG);
+        int n, v;
+        tile_place(p, u, n, v);
+        const int row = n * p.nt + static_cast<int>(rank) * (p.nt / CG);
         for (int i = 0; i < k_iters; ++i) {
           if (!mbar_wait(smem_addr(&ctl.x_empty[s]), phase ^ 1u, abort_flag, err_word)) {
             ok = false;
@@ -417,8 +433,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int u = unit0; u < total; u += units, ++it) {
       const int buf = bufs == 2 ? it & 1 : 0;
       const uint32_t use = static_cast<uint32_t>(bufs == 2 ? it >> 1 : it) & 1u;
-      const int64_t v0 = static_cast<int64_t>(u / p.n_tiles) * (128 * CG);
-      const int64_t n0 = static_cast<int64_t>(u % p.n_tiles) * p.nt;
+      int tile_n, tile_v;
+      tile_place(p, u, tile_n, tile_v);
+      const int64_t v0 = static_cast<int64_t>(tile_v) * (128 * CG);
+      const int64_t n0 = static_cast<int64_t>(tile_n) * p.nt;
       const bool mine = v0 + in_tile < p.v;
       // u_ij = acc * x_scale * (weight_scale * logit_scale) + bias * logit_scale
       const float ws = (mine ? __ldg(p.weight_scale + v0 + in_tile) : 0.0f) * p.xf.scale;

@@ -111,7 +111,8 @@ def _make(n, h, v, dtype, seed=0):
 SIZES = [(1, 1, 1), (1, 16, 5), (3, 100, 130), (8, 64, 128), (16, 128, 129), (17, 96, 300),
          (32, 1024, 127), (33, 257, 1000), (64, 512, 256), (65, 80, 515), (128, 4096, 200),
          (129, 144, 640), (200, 1008, 333), (256, 64, 1024), (257, 112, 257), (500, 513, 700),
-         (1030, 256, 400)]
+         (1030, 256, 400),
+         (4700, 4096, 300)]  # more rows of x than run through the weight together
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
