@@ -218,6 +218,9 @@ flce_status flce_beam_select(const flce_beam_problem* p, const void* logits,
   k.beams = static_cast<int32_t>(p->beams);
   k.m = static_cast<int32_t>(p->candidates);
   k.splits = static_cast<int32_t>(plan.splits);
+  const int64_t es = p->dtype == FLCE_F32 ? 4 : 2;
+  k.shifted = !aligned_to(logits, 16) || (p->batch > 1 && p->stride_batch * es % 16 != 0) ||
+              (p->beams > 1 && p->stride_beam * es % 16 != 0);
   k.groups = 1;
   while (k.groups < k.m) k.groups *= 2;
   k.slice_len = static_cast<int32_t>(plan.slice_len);

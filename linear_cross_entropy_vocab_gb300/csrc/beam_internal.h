@@ -28,6 +28,7 @@ struct BeamSelectParams {
   int32_t batch, beams, m, splits;
   int32_t slice_len;           // logits of a slice, a multiple of 8 (the last may be shorter)
   int32_t groups;              // the power of two from m on, at most 256
+  int32_t shifted;             // some row starts elsewhere than at a multiple of 16 bytes
   int64_t v;
   int64_t pad_token;
   // per (row, slice): its M best keys, best first, 0 where there are fewer,

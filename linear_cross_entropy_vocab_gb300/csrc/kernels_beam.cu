@@ -241,6 +241,18 @@ __device__ __forceinline__ K group_floor(K x, int g, K (*red)[32]) {
   return floor_at;
 }
 
+// The 16 bytes that start `s` bytes (0 to 15) into the 32 of a and b.
+__device__ __forceinline__ uint4 shift_bytes(const uint4& a, const uint4& b, uint32_t s) {
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int j = 0; j < 6; ++j) w[j] = (s & 8u) ? w[j + 2] : w[j];
+#pragma unroll
+  for (int j = 0; j < 5; ++j) w[j] = (s & 4u) ? w[j + 1] : w[j];
+  const uint32_t bits = 8u * (s & 3u);
+  return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                    __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+}
+
 // One slice of a row as the threads of a CTA see it; places count from its start.
 template <class T>
 struct Slice {
@@ -249,10 +261,14 @@ struct Slice {
   const uint8_t* ok;  // or null
   int len;
   bool z16, ok_vec;   // 16-byte (E-byte) loads are aligned
+  uint32_t shift;     // bytes from a multiple of 16 to the slice's start; 0 without SHIFT
 
-  __device__ __forceinline__ uint4 raw(int v) const {
-    return __ldcs(reinterpret_cast<const uint4*>(z + v));
+  // The aligned 16 bytes that hold the first of the logits from v on (v a
+  // multiple of E).
+  __device__ __forceinline__ const uint4* chunk(int v) const {
+    return reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(z + v) - shift);
   }
+  __device__ __forceinline__ uint4 raw(int v) const { return __ldcs(chunk(v)); }
   // What lies past the end, and where the mask says so, is -infinity.
   __device__ __forceinline__ void mask(int v, float (&x)[E]) const {
     if (ok_vec && v + E <= len) {
@@ -281,9 +297,11 @@ struct Slice {
 
 // One slice of one row: its M best logits, maximum and sum of exponentials.
 // A tile is N pieces of 16 bytes per thread; the next tile's are on their way
-// while one is worked on.
-template <class T, int N>
-__global__ void __launch_bounds__(kThreads, N == 4 ? 4 : 6)
+// while one is worked on. SHIFT: rows may start anywhere, and a thread's logits
+// come from two aligned pieces (64 x 8 rows of 128255 bf16: 58 us, value by
+// value 80; of 128256 as aligned ones 46, by the shifting kernel 50).
+template <class T, int N, bool SHIFT>
+__global__ void __launch_bounds__(kThreads, N == 4 ? 4 : N == 2 && SHIFT ? 5 : 6)
     beam_slices_kernel(const BeamSelectParams p) {
   constexpr int E = Piece<T>::kElems;
   constexpr int kTile = kThreads * E * N;
@@ -308,8 +326,9 @@ __global__ void __launch_bounds__(kThreads, N == 4 ? 4 : 6)
   in.z = static_cast<const T*>(p.logits) + b * p.stride_b + k * p.stride_k + v0;
   in.ok = p.allowed != nullptr ? p.allowed + b * p.allowed_b + k * p.allowed_k + v0 : nullptr;
   in.len = static_cast<int>(v0 + p.slice_len < p.v ? p.slice_len : p.v - v0);
-  in.z16 = (reinterpret_cast<uintptr_t>(in.z) & 15u) == 0;
+  in.z16 = !SHIFT || (reinterpret_cast<uintptr_t>(in.z) & 15u) == 0;
   in.ok_vec = (reinterpret_cast<uintptr_t>(in.ok) & 3u) == 0;
+  in.shift = SHIFT ? static_cast<uint32_t>(reinterpret_cast<uintptr_t>(in.z) & 15u) : 0u;
   if (threadIdx.x == 0) count = 0;
 
   // the thread's maximum so far and its sum of e^(z - maximum); NaN and
@@ -320,15 +339,26 @@ __global__ void __launch_bounds__(kThreads, N == 4 ? 4 : 6)
   int tiles = 0;
   uint4 next[N];
   const int mine = static_cast<int>(threadIdx.x) * E;
-  // tiles that end at or before this place are loaded ahead
-  const int ahead = in.z16 ? in.len : 0;
-  if (kTile <= ahead) {
+  // Whether the tile at t0 is loaded in 16 bytes, ahead of time: it is whole,
+  // and in a row that starts elsewhere than at a multiple of 16 bytes, where a
+  // thread's logits come from two such pieces, neither reaches past the row.
+  const int64_t rest = p.v - v0 - E;
+  const int limit = !SHIFT || in.z16 || rest >= in.len ? in.len : static_cast<int>(rest);
+  const int start = !SHIFT || in.z16 || v0 > 0 ? 0 : 1;
+  auto ahead = [&](int t0) { return t0 >= start && t0 + kTile <= limit; };
+  if (ahead(0)) {
 #pragma unroll
     for (int i = 0; i < N; ++i) next[i] = in.raw(mine + i * kThreads * E);
   }
   for (int t0 = 0; t0 < in.len; t0 += kTile) {
     float x[N][E];
-    if (t0 + kTile <= ahead) {
+    if (ahead(t0)) {
+      if (SHIFT && !in.z16) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          next[i] = shift_bytes(next[i], __ldg(in.chunk(t0 + mine + i * kThreads * E) + 1),
+                                in.shift);
+      }
 #pragma unroll
       for (int i = 0; i < N; ++i) Piece<T>::unpack(next[i], x[i]);
       if (in.ok != nullptr) {
@@ -339,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, N == 4 ? 4 : 6)
 #pragma unroll
       for (int i = 0; i < N; ++i) in.load(t0 + mine + i * kThreads * E, x[i]);
     }
-    if (t0 + 2 * kTile <= ahead) {
+    if (ahead(t0 + kTile)) {
 #pragma unroll
       for (int i = 0; i < N; ++i) next[i] = in.raw(t0 + kTile + mine + i * kThreads * E);
     }
@@ -629,11 +659,19 @@ __global__ void __launch_bounds__(kThreads) beam_choose_kernel(const BeamSelectP
 template <class T>
 cudaError_t launch_select(const BeamSelectParams& p, bool large, cudaStream_t s) {
   const int64_t blocks = static_cast<int64_t>(p.batch) * p.beams * p.splits;
-  if (large)
-    beam_slices_kernel<T, kTileLarge / (kThreads * Piece<T>::kElems)>
-        <<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(p);
-  else
-    beam_slices_kernel<T, 1><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(p);
+  const unsigned grid = static_cast<unsigned>(blocks);
+  constexpr int kLarge = kTileLarge / (kThreads * Piece<T>::kElems);
+  if (p.shifted) {
+    if (large)
+      beam_slices_kernel<T, kLarge, true><<<grid, kThreads, 0, s>>>(p);
+    else
+      beam_slices_kernel<T, 1, true><<<grid, kThreads, 0, s>>>(p);
+  } else {
+    if (large)
+      beam_slices_kernel<T, kLarge, false><<<grid, kThreads, 0, s>>>(p);
+    else
+      beam_slices_kernel<T, 1, false><<<grid, kThreads, 0, s>>>(p);
+  }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // may be placed while the slices run, and waits for them
