@@ -20,8 +20,12 @@ using namespace flce::host;
 
 // Upper bound of the CTAs of one launch: the workspace holds one partial each.
 constexpr int kMaxCtas = 1024;
-// Resident CTAs per SM of the gradient kernels (256 threads, at most 64 registers).
-constexpr int kCtasPerSm = 4;
+// CTAs per SM of the norm and of the clip. The clip holds a chunk's 16-byte
+// loads and the places of its stores, 128 registers a thread; four CTAs of 64
+// spill, and 640 MB read and written take 270 us in fp32 and 216 in bf16,
+// against 209 and 212 with two.
+constexpr int kNormCtasPerSm = 4;
+constexpr int kClipCtasPerSm = 2;
 
 // Chunks of 32 KB up to which the cluster of eight CTAs takes a clip by itself.
 // On the device that is the shorter way up to 16 (two fp32 tensors: 128 KB 5.4
@@ -190,7 +194,9 @@ flce_status fill(GradTable<CAP>& tab, const flce_grad* g, int64_t count, int64_t
 
 template <int CAP>
 flce_status run(const flce_grad* g, int64_t count, int p, bool clip, float max_norm, float eps,
-                float* norm_out, double* partials, int max_ctas, cudaStream_t s) {
+                float* norm_out, double* partials, int sms, cudaStream_t s) {
+  const int norm_ctas = std::min(kMaxCtas, kNormCtasPerSm * sms);
+  const int clip_ctas = std::min(kMaxCtas, kClipCtasPerSm * sms);
   GradTable<CAP> tab;
   int n_partials = 0;
   for (int64_t next = 0; next < count;) {
@@ -206,7 +212,7 @@ flce_status run(const flce_grad* g, int64_t count, int p, bool clip, float max_n
     }
     int n = 0;
     const cudaError_t e =
-        flce::launch_grad_partials(tab, p, max_ctas, partials + n_partials, &n, s);
+        flce::launch_grad_partials(tab, p, norm_ctas, partials + n_partials, &n, s);
     if (e != cudaSuccess) return cuda_fail(e, "gradient norm kernel");
     n_partials += n;
   }
@@ -220,7 +226,7 @@ flce_status run(const flce_grad* g, int64_t count, int p, bool clip, float max_n
     if (st != FLCE_OK) return st;
     if (tab.count == 0) continue;
     const cudaError_t e = flce::launch_grad_clip(tab, partials, n_partials, p, max_norm, eps,
-                                                 norm_out, first, max_ctas, s);
+                                                 norm_out, first, clip_ctas, s);
     if (e != cudaSuccess) return cuda_fail(e, "gradient clip kernel");
     first = false;
   }
@@ -240,13 +246,12 @@ flce_status enter(const flce_grad* g, int64_t count, int32_t norm, bool clip, fl
   int sms = 0;
   st = check_device(&sms);
   if (st != FLCE_OK) return st;
-  const int max_ctas = std::min(kMaxCtas, kCtasPerSm * sms);
   double* const partials = static_cast<double*>(workspace);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int p = norm_code(norm);
   if (count <= kGradTableSmall)
-    return run<kGradTableSmall>(g, count, p, clip, max_norm, eps, norm_out, partials, max_ctas, s);
-  return run<kGradTableLarge>(g, count, p, clip, max_norm, eps, norm_out, partials, max_ctas, s);
+    return run<kGradTableSmall>(g, count, p, clip, max_norm, eps, norm_out, partials, sms, s);
+  return run<kGradTableLarge>(g, count, p, clip, max_norm, eps, norm_out, partials, sms, s);
 }
 
 }  // namespace

@@ -144,6 +144,15 @@ __device__ __forceinline__ double term64(float x) {
   return P == 1 ? fabs(d) : d * d;
 }
 
+// Elements from p to the next 128-byte line, at most n: the 16-byte accesses of
+// a warp then cover whole lines.
+template <class T>
+__device__ __forceinline__ int to_line(const T* p, int n) {
+  const int head =
+      static_cast<int>(((128u - (reinterpret_cast<uintptr_t>(p) & 127u)) & 127u) / sizeof(T));
+  return head < n ? head : n;
+}
+
 // The partial of one chunk: elements [e0, e1) of tensor t.
 template <int P, int DT>
 __device__ __forceinline__ void chunk_norm(const GradEntry& t, int64_t e0, int64_t e1,
@@ -167,11 +176,10 @@ __device__ __forceinline__ void chunk_norm(const GradEntry& t, int64_t e0, int64
     peak = max(peak, a.m);
     return;
   }
-  // elements before the first 16-byte boundary, whole groups, and the rest
+  // elements before the first line, whole groups of 16 bytes, and the rest
   const T* const p = src + e0;
   const int n = static_cast<int>(e1 - e0);
-  int head = static_cast<int>(((16u - (reinterpret_cast<uintptr_t>(p) & 15u)) & 15u) / sizeof(T));
-  head = head < n ? head : n;
+  const int head = to_line(p, n);
   const int groups = (n - head) / N;
   const uint4* const v = reinterpret_cast<const uint4*>(p + head);
   uint4 q[kVecs];
@@ -180,7 +188,7 @@ __device__ __forceinline__ void chunk_norm(const GradEntry& t, int64_t e0, int64
     const int g = static_cast<int>(threadIdx.x) + i * kThreads;
     q[i] = g < groups ? __ldg(v + g) : make_uint4(0, 0, 0, 0);
   }
-  const int rest = n - groups * N;  // head and tail elements: at most 2 N - 2
+  const int rest = n - groups * N;  // head and tail elements: at most 70
   float edge = 0.0f;
   if (static_cast<int>(threadIdx.x) < rest) {
     const int i = static_cast<int>(threadIdx.x);
@@ -349,8 +357,7 @@ __device__ __forceinline__ void chunk_scale(const GradEntry& t, int64_t e0, int6
   }
   const T* const p = src + e0;
   const int n = static_cast<int>(e1 - e0);
-  int head = static_cast<int>(((16u - (reinterpret_cast<uintptr_t>(p) & 15u)) & 15u) / sizeof(T));
-  head = head < n ? head : n;
+  const int head = to_line(p, n);
   const int groups = (n - head) / N;
   const uint4* const v = reinterpret_cast<const uint4*>(p + head);
   uint4 q[kVecs];
@@ -369,24 +376,34 @@ __device__ __forceinline__ void chunk_scale(const GradEntry& t, int64_t e0, int6
   const bool vec = same && ((reinterpret_cast<uintptr_t>(t.dst) + d0 * sizeof(T)) & 15u) == 0;
   const bool wide = !same && t.dst_dtype == FLCE_F32 &&
                     ((reinterpret_cast<uintptr_t>(t.dst) + d0 * 4) & 15u) == 0;
+  // each kind of store in a loop of its own: merged, they become single ones
+  auto each = [&](auto put) {
 #pragma unroll
-  for (int i = 0; i < kVecs; ++i) {
-    const int g = static_cast<int>(threadIdx.x) + i * kThreads;
-    if (g >= groups) break;
-    float x[N];
-    E::unpack(q[i], x);
+    for (int i = 0; i < kVecs; ++i) {
+      const int g = static_cast<int>(threadIdx.x) + i * kThreads;
+      if (g >= groups) break;
+      float x[N];
+      E::unpack(q[i], x);
 #pragma unroll
-    for (int j = 0; j < N; ++j) x[j] *= coef;
-    if (vec) {
-      reinterpret_cast<uint4*>(static_cast<T*>(t.dst) + d0)[g] = E::pack(x);
-    } else if (wide) {
-      float4* o = reinterpret_cast<float4*>(static_cast<float*>(t.dst) + d0) + g * (N / 4);
+      for (int j = 0; j < N; ++j) x[j] *= coef;
+      put(g, x);
+    }
+  };
+  if (vec) {
+    uint4* const o = reinterpret_cast<uint4*>(static_cast<T*>(t.dst) + d0);
+    each([&](int g, const float(&x)[N]) { o[g] = E::pack(x); });
+  } else if (wide) {
+    float4* const o = reinterpret_cast<float4*>(static_cast<float*>(t.dst) + d0);
+    each([&](int g, const float(&x)[N]) {
 #pragma unroll
-      for (int j = 0; j < N; j += 4) o[j / 4] = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
-    } else {
+      for (int j = 0; j < N; j += 4)
+        o[g * (N / 4) + j / 4] = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+    });
+  } else {
+    each([&](int g, const float(&x)[N]) {
 #pragma unroll
       for (int j = 0; j < N; ++j) store_one(t.dst, t.dst_dtype, d0 + g * N + j, x[j]);
-    }
+    });
   }
   if (static_cast<int>(threadIdx.x) < rest) store_one(t.dst, t.dst_dtype, e0 + ei, edge * coef);
 }
@@ -408,7 +425,7 @@ __device__ __forceinline__ float clip_factor(float norm, float max_norm, float e
 }
 
 template <int CAP>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, 2)
     grad_clip_kernel(const __grid_constant__ GradTable<CAP> tab, const double* partials, int n,
                      int p, float max_norm, float eps, float* norm_out, int write_norm) {
   __shared__ double buf[kThreads / 32];
@@ -430,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 4)
 
 // Norm and clip in one launch of one cluster: rank r takes chunks r, r + 8, ...
 template <int P, int CAP>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 1)
     grad_clip_cluster_kernel(const __grid_constant__ GradTable<CAP> tab, float max_norm, float eps,
                              float* norm_out) {
   __shared__ double buf[kThreads / 32];
