@@ -452,6 +452,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                              float* norm_out) {
   __shared__ double buf[kThreads / 32];
   __shared__ double all[kGradCluster];  // every rank's partial
+  // every CTA of the cluster has started before any writes to another's memory
+  asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
   const uint32_t rank = cluster_ctarank();
   const uint32_t total = tab.first[tab.count];
   double sum = 0.0;
@@ -466,6 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     sum = static_cast<double>(__uint_as_float(block_max(peak, reinterpret_cast<uint32_t*>(buf))));
   else
     sum = block_sum(sum, buf);
+  asm volatile("barrier.cluster.wait;" ::: "memory");
   if (threadIdx.x < kGradCluster) {
     const uint32_t to = map_to_rank(smem_addr(&all[rank]), threadIdx.x);
     asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(to), "d"(sum) : "memory");
