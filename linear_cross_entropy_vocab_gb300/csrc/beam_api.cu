@@ -58,7 +58,8 @@ SelectPlan plan_select(const flce_beam_problem* p) {
   const int64_t tile = q.large ? flce::kTileLarge : flce::kTileSmallBytes / es;
   const int64_t tiles = ceil_div(p->v, tile);
   // slices of whole tiles, as equal as that allows
-  q.splits = std::max<int64_t>(1, std::min(tiles, ceil_div(kSelectCtas, std::max<int64_t>(rows, 1))));
+  const int64_t wanted = ceil_div(kSelectCtas, std::max<int64_t>(rows, 1));
+  q.splits = std::max<int64_t>(1, std::min(tiles, wanted));
   q.slice_len = ceil_div(tiles, q.splits) * tile;
   if (q.splits == tiles) q.slice_len = ceil_div(ceil_div(p->v, tiles), 8) * 8;  // alike
   q.splits = ceil_div(p->v, q.slice_len);
@@ -90,7 +91,8 @@ flce_status check_state(const flce_beam_state& s, int64_t i, int64_t rows, bool*
   }
   *empty = total == 0 || rows == 0;
   if (*empty) return FLCE_OK;
-  if (s.data == nullptr) return fail(FLCE_ERR_INVALID_ARG, "state %lld: data is NULL", (long long)i);
+  if (s.data == nullptr)
+    return fail(FLCE_ERR_INVALID_ARG, "state %lld: data is NULL", (long long)i);
   // every beam's bytes lie apart: sorted by stride, each axis steps over all
   // that the axes inside it span
   int64_t size[flce::kReorderDims + 1], stride[flce::kReorderDims + 1];

@@ -10,7 +10,7 @@
 namespace flce {
 
 constexpr int kBeamMaxCandidates = 256;
-constexpr int kBeamMaxBeams = 64;  // of a reordering; a selection takes more (its scores are staged)
+constexpr int kBeamMaxBeams = 64;  // of a reordering
 constexpr int kBeamMaxSelectBeams = 1024;
 
 // A selection CTA (256 threads) holds tiles of 16 bytes or of 16 logits for

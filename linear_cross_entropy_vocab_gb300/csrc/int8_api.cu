@@ -13,7 +13,7 @@ namespace {
 using namespace flce::host;
 
 constexpr int64_t kMaxH = 131071;  // 128 * 128 * h stays below 2^31
-constexpr int64_t kMaxRows = 0x7fffffff;
+constexpr int64_t kMaxRows = 0x7fffff00;  // a tile may end 255 rows further
 
 bool float_type(int32_t d) { return d == FLCE_F32 || d == FLCE_BF16 || d == FLCE_F16; }
 size_t size_of(int32_t d) { return d == FLCE_F32 ? 4 : d == FLCE_Q_I8 ? 1 : 2; }
@@ -84,7 +84,8 @@ QPlan plan_qlinear(const flce_qproblem* p) {
   q.weight = q.scale + align_256(static_cast<size_t>(p->n) * 4);
   q.weight_pitch = align ? ceil_div(p->h, 16) * 16 : p->weight_pitch;
   q.total = q.weight +
-            (align ? align_256(static_cast<size_t>(p->v) * static_cast<size_t>(q.weight_pitch)) : 0);
+            (align ? align_256(static_cast<size_t>(p->v) * static_cast<size_t>(q.weight_pitch))
+                   : 0);
   return q;
 }
 

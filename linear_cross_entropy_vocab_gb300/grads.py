@@ -35,7 +35,8 @@ def _norm_code(norm_type) -> int:
 
 
 def _runs(g: torch.Tensor, o: torch.Tensor):
-    """(byte offset in g, in o, rows, cols, pitch of g, of o) that cover two tensors of one shape."""
+    """(byte offset in g, in o, rows, cols, pitch of g, of o) that cover two tensors of one
+    shape."""
     dims = sorted(((s, a, b) for s, a, b in zip(g.shape, g.stride(), o.stride()) if s > 1),
                   key=lambda d: (-d[1], -d[2]))
     merged: list = []
