@@ -15,6 +15,7 @@ namespace {
 using flce::GradEntry;
 using flce::GradTable;
 using flce::kGradTableLarge;
+using flce::kGradTableMedium;
 using flce::kGradTableSmall;
 using namespace flce::host;
 
@@ -251,6 +252,8 @@ flce_status enter(const flce_grad* g, int64_t count, int32_t norm, bool clip, fl
   const int p = norm_code(norm);
   if (count <= kGradTableSmall)
     return run<kGradTableSmall>(g, count, p, clip, max_norm, eps, norm_out, partials, sms, s);
+  if (count <= kGradTableMedium)
+    return run<kGradTableMedium>(g, count, p, clip, max_norm, eps, norm_out, partials, sms, s);
   return run<kGradTableLarge>(g, count, p, clip, max_norm, eps, norm_out, partials, sms, s);
 }
 
@@ -260,7 +263,7 @@ extern "C" {
 
 size_t flce_grad_workspace_size(int64_t count) {
   if (count < 0) return 0;
-  const int64_t launches = count <= kGradTableSmall ? 1 : ceil_div(count, kGradTableLarge);
+  const int64_t launches = ceil_div(std::max<int64_t>(count, 1), kGradTableLarge);
   return static_cast<size_t>(launches) * kMaxCtas * sizeof(double);
 }
 

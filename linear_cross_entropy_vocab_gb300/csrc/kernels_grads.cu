@@ -568,9 +568,13 @@ cudaError_t launch_grad_clip_cluster(const GradTable<kGradTableSmall>& tab, int 
 
 template cudaError_t launch_grad_partials(const GradTable<kGradTableSmall>&, int, int, double*,
                                           int*, cudaStream_t);
+template cudaError_t launch_grad_partials(const GradTable<kGradTableMedium>&, int, int, double*,
+                                          int*, cudaStream_t);
 template cudaError_t launch_grad_partials(const GradTable<kGradTableLarge>&, int, int, double*,
                                           int*, cudaStream_t);
 template cudaError_t launch_grad_clip(const GradTable<kGradTableSmall>&, const double*, int, int,
+                                      float, float, float*, bool, int, cudaStream_t);
+template cudaError_t launch_grad_clip(const GradTable<kGradTableMedium>&, const double*, int, int,
                                       float, float, float*, bool, int, cudaStream_t);
 template cudaError_t launch_grad_clip(const GradTable<kGradTableLarge>&, const double*, int, int,
                                       float, float, float*, bool, int, cudaStream_t);

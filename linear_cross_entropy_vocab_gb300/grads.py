@@ -63,44 +63,47 @@ def _runs(g: torch.Tensor, o: torch.Tensor):
 def _table(grads: Sequence[torch.Tensor], out: Optional[Sequence[torch.Tensor]]):
     """The flce_grad structs of the gradients as 64-bit words, and the gradients' device."""
     words: list = []
-    device = grads[0].device if grads else None
+    if not grads:
+        return array.array("q"), None
+    device, index = grads[0].device, grads[0].get_device()
+    add, code_of = words.extend, _DTYPES.get
     for i, g in enumerate(grads):
-        code = _DTYPES.get(g.dtype)
+        code = code_of(g.dtype)
         if code is None:
             raise TypeError(f"gradient {i} is {g.dtype}: use float32, bfloat16 or float16")
         if not g.is_cuda:
             raise ValueError(f"gradient {i} must be a CUDA tensor")
-        if g.device != device:
+        if g.get_device() != index:
             raise ValueError(f"gradient {i} is on {g.device}, the first on {device}")
-        if g.layout != torch.strided:
+        if g.layout is not torch.strided:
             raise ValueError(f"gradient {i} must be a dense tensor, not {g.layout}")
         n = g.numel()
-        src = g.data_ptr()
         if out is None:
             if n == 0:
                 continue
+            src = g.data_ptr()
             if g.is_contiguous():
-                words += (src, src, 1, n, n, n, code | code << 32)
+                add((src, src, 1, n, n, n, code | code << 32))
             else:
                 for x, y, rows, cols, pg, po in _runs(g, g):
-                    words += (src + x, src + y, rows, cols, pg, po, code | code << 32)
+                    add((src + x, src + y, rows, cols, pg, po, code | code << 32))
             continue
         o = out[i]
         if o.shape != g.shape:
             raise ValueError(f"out {i} is {tuple(o.shape)}, its gradient {tuple(g.shape)}")
-        if o.dtype != g.dtype and o.dtype != torch.float32:
+        out_code = code_of(o.dtype)
+        if out_code != code and out_code != abi.FLCE_F32:
             raise TypeError(f"out {i} must be {g.dtype} or float32, not {o.dtype}")
-        if o.device != device or o.layout != torch.strided:
+        if o.get_device() != index or o.layout is not torch.strided:
             raise ValueError(f"out {i} must be a dense tensor on {device}")
         if n == 0:
             continue
-        dst = o.data_ptr()
-        codes = code | _DTYPES[o.dtype] << 32
+        src, dst, codes = g.data_ptr(), o.data_ptr(), code | out_code << 32
         if g.is_contiguous() and o.is_contiguous():
-            words += (src, dst, 1, n, n, n, codes)
+            add((src, dst, 1, n, n, n, codes))
         else:
             for x, y, rows, cols, pg, po in _runs(g, o):
-                words += (src + x, dst + y, rows, cols, pg, po, codes)
+                add((src + x, dst + y, rows, cols, pg, po, codes))
     return array.array("q", words), device
 
 
