@@ -30,10 +30,11 @@ namespace flce {
 constexpr float kLog2e = 1.4426950408889634f;
 
 // tanh from its exponential form tanh(x) = (e^{2x} - 1) / (e^{2x} + 1),
-// with |x| clamped to 9 (tanh(9) rounds to 1 in fp32). Absolute error is a
-// few 1e-7.
+// with x clamped to 9 from above (tanh(9) rounds to 1 in fp32; below -9 the
+// form itself gives -1). The clamp keeps a NaN, which fminf would turn into 9.
+// Absolute error is a few 1e-7.
 __device__ __forceinline__ float tanh_exp2(float x) {
-  x = fminf(fmaxf(x, -9.0f), 9.0f);
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(9.0f));
   const float e = ex2_approx(x * (2.0f * kLog2e));
   return __fdividef(e - 1.0f, e + 1.0f);
 }

@@ -243,3 +243,28 @@ def test_refusals():
         int8_linear(x, wq, ws, bias[:49])
     with pytest.raises(ValueError):
         int8_linear(x, wq.cpu(), ws)
+
+
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("n", [6, 300])  # one CTA a tile, and pairs
+def test_softcap_keeps_nan(n, out_dtype):
+    """A NaN anywhere in a logit stays NaN under the cap; the other logits are the capped ones,
+    large ones of either sign among them."""
+    x, wq, ws, bias = _make(n, 200, 300, torch.float32)
+    x[1, 7] = math.nan
+    x[2, 8] = math.inf
+    x[3] *= 1e6
+    ws[40] = math.nan
+    bias[50] = math.nan
+    got = int8_linear(x, wq, ws, bias, softcap=20.0, out_dtype=out_dtype)
+    rows = torch.arange(n, device="cuda")
+    rows = (rows != 1) & (rows != 2)
+    cols = torch.arange(300, device="cuda")
+    cols = (cols != 40) & (cols != 50)
+    assert bool(got[~rows].isnan().all()) and bool(got[:, ~cols].isnan().all())
+    q, scale = quantize_rows(x)
+    _check(got[rows][:, cols], q[rows], scale[rows], wq[cols], ws[cols], bias[cols], softcap=20.0)
+    assert bool((got[3, cols] > 19.9).any()) and bool((got[3, cols] < -19.9).any())
+    scale[4] = math.nan
+    got = int8_linear(q, wq, ws, bias, x_scale=scale, softcap=20.0, out_dtype=out_dtype)
+    assert bool(got[4].isnan().all())

@@ -228,3 +228,24 @@ def test_two_threads_two_streams_match_sequential():
     for a, b in zip(seq, res):
         for u, v in zip(a, b):
             assert torch.equal(u.cpu(), v.cpu())
+
+
+@pytest.mark.parametrize("softcap", [None, 30.0])
+@pytest.mark.parametrize("dtype,n,h,v", [
+    (torch.float32, 16, 20, 50), (torch.float32, 256, 256, 1000), (torch.bfloat16, 256, 256, 1000),
+    (torch.float16, 40, 64, 600)])
+def test_a_nan_reaches_the_loss(dtype, n, h, v, softcap):
+    """A row of hidden that holds a NaN has a NaN loss and gradient, with a softcap as without one,
+    and leaves the other rows' losses alone."""
+    g = torch.Generator("cuda").manual_seed(0)
+    hidden = torch.randn(n, h, generator=g, device="cuda").to(dtype)
+    weight = (torch.randn(v, h, generator=g, device="cuda") * h ** -0.5).to(dtype)
+    targets = torch.randint(0, v, (n,), generator=g, device="cuda")
+    clean = fused_linear_cross_entropy(hidden, weight, targets, softcap=softcap, reduction="none")
+    hidden[3, 5] = float("nan")
+    hidden.requires_grad_(True)
+    rows = fused_linear_cross_entropy(hidden, weight, targets, softcap=softcap, reduction="none")
+    others = torch.arange(n, device="cuda") != 3
+    assert bool(rows[3].isnan()) and torch.equal(rows[others], clean[others])
+    rows.sum().backward()
+    assert bool(hidden.grad[3].isnan().all()) and not bool(hidden.grad[others].isnan().any())
