@@ -261,7 +261,9 @@ flce_status flce_beam_reorder(const flce_beam_state* states, int64_t count,
     if (empty) continue;
     int64_t vecs = states[i].run_bytes / std::min(max_width, width_of(states[i]));
     for (int d = 0; d < flce::kReorderDims; ++d) vecs *= states[i].size[d];
-    if (vecs > 0xfffffff0ll || ceil_div(vecs, flce::kReorderBlock) * batch > 0x7fffffffll)
+    // the kernel rounds a beam's vectors up to whole blocks in 32 bits
+    if (vecs > 0xffffffffll / flce::kReorderBlock * flce::kReorderBlock ||
+        ceil_div(vecs, flce::kReorderBlock) * batch > 0x7fffffffll)
       return fail(FLCE_ERR_UNSUPPORTED, "state %lld is too large", (long long)i);
   }
   int sms = 0;

@@ -235,3 +235,18 @@ def test_int8_python_refusals():
         package.int8_linear(x.double(), w, s)
     with pytest.raises(TypeError):
         package.int8_linear(x, w, s, out_dtype=torch.float64)
+
+
+@pytest.mark.parametrize("vectors", [0xffffff01, 0xfffffff0, 0xfffffff1, 1 << 32])
+def test_reorder_refuses_more_vectors_than_its_blocks_can_count(vectors):
+    """A beam's vectors, rounded up to whole blocks of 256, stay below 2^32."""
+    for width in (1, 2, 4, 8, 16):
+        stride = (vectors + 1) * width
+        assert _reorder(batch=1, beams=2, run_bytes=vectors * width, beam_stride=stride,
+                        data=FAKE + width) == UNSUPPORTED, width
+        assert "too large" in abi.flce_last_error()
+        # the same in pieces
+        if vectors % 16 == 0:
+            assert _reorder(batch=1, beams=2, run_bytes=16 * width, size=(1, 1, 1, vectors // 16),
+                            stride=(0, 0, 0, 17 * width), beam_stride=2 * stride + width,
+                            data=FAKE + width) == UNSUPPORTED, width
