@@ -398,7 +398,7 @@ flce_status flce_grad_clip(const flce_grad* grads, int64_t count, int32_t norm,
 #define FLCE_DEVERR_PARENT_RANGE 8
 
 typedef struct flce_beam_problem {
-  int64_t batch, beams, v;     /* batch >= 0; 1 <= beams <= 1024 */
+  int64_t batch, beams, v;     /* batch >= 0; 1 <= beams <= 1024; 1 <= v < 2^31 - 8192 */
   int64_t candidates;          /* 1 to 256 */
   int64_t stride_batch, stride_beam;
   int64_t allowed_stride_batch, allowed_stride_beam;

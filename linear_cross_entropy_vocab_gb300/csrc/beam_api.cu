@@ -21,6 +21,10 @@ using namespace flce::host;
 constexpr int64_t kSelectCtas = 512;
 constexpr int64_t kFewCtas = 100;
 
+// A slice may be a whole row: its length in whole tiles, and the end of the tile
+// after the next, stay in 32 bits.
+constexpr int64_t kMaxV = 0x7fffffff - 2 * flce::kTileLarge;
+
 struct SelectPlan {
   bool large;
   int64_t splits, slice_len;
@@ -37,7 +41,7 @@ flce_status check_select(const flce_beam_problem* p) {
   if (p->beams < 1 || p->beams > flce::kBeamMaxSelectBeams)
     return fail(FLCE_ERR_UNSUPPORTED, "1 to %d beams are supported, not %lld",
                 flce::kBeamMaxSelectBeams, (long long)p->beams);
-  if (p->v < 1 || p->v > 0x7fffffff)
+  if (p->v < 1 || p->v > kMaxV)
     return fail(FLCE_ERR_INVALID_ARG, "vocabulary of %lld tokens", (long long)p->v);
   if (p->candidates < 1 || p->candidates > flce::kBeamMaxCandidates)
     return fail(FLCE_ERR_UNSUPPORTED, "1 to %d candidates are supported, not %lld",

@@ -250,3 +250,15 @@ def test_reorder_refuses_more_vectors_than_its_blocks_can_count(vectors):
             assert _reorder(batch=1, beams=2, run_bytes=16 * width, size=(1, 1, 1, vectors // 16),
                             stride=(0, 0, 0, 17 * width), beam_stride=2 * stride + width,
                             data=FAKE + width) == UNSUPPORTED, width
+
+
+@pytest.mark.parametrize("v", [(1 << 31) - 8192, (1 << 31) - 4096, (1 << 31) - 4095, (1 << 31) - 1])
+def test_select_refuses_rows_whose_tiles_leave_32_bits(v):
+    """Rows that share their memory make such a vocabulary one tensor of 4 GB."""
+    for dtype in (abi.FLCE_F32, abi.FLCE_BF16, abi.FLCE_F16):
+        for batch, beams in ((1, 1), (64, 8), (600, 1)):
+            at = dict(batch=batch, beams=beams, dtype=dtype, stride_batch=0, stride_beam=0)
+            assert _select(v=v, **at) == INVALID, (batch, beams)
+            last = abi.flce_beam_problem(batch=batch, beams=beams, candidates=6, dtype=dtype,
+                                         v=(1 << 31) - 8193)
+            assert abi.flce_beam_select_workspace_size(last) > 0
