@@ -448,8 +448,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // this warp's 32-column chunks: the first or the second half of them
       const int c0 = half == 0 ? 0 : (chunks + 1) / 2;
       const int c1 = half == 0 ? (chunks + 1) / 2 : chunks;
+      // an ordinary load: the kernel before this one, which wrote the scales, may
+      // have run beside it until the wait above
       auto scales = [&](int c) {
-        return c * 32 + lane < cols ? __ldg(p.x_scale + n0 + c * 32 + lane) : 0.0f;
+        return c * 32 + lane < cols ? p.x_scale[n0 + c * 32 + lane] : 0.0f;
       };
       float xs_next = scales(c0);
       const bool ok = mbar_wait(smem_addr(&ctl.acc_full[buf]), use, abort_flag, err_word);

@@ -268,3 +268,18 @@ def test_softcap_keeps_nan(n, out_dtype):
     scale[4] = math.nan
     got = int8_linear(q, wq, ws, bias, x_scale=scale, softcap=20.0, out_dtype=out_dtype)
     assert bool(got[4].isnan().all())
+
+
+@pytest.mark.parametrize("n", [1, 40, 300])
+def test_scales_of_this_call(n):
+    """Calls in a row whose scales take the same places in memory: each uses those that it made
+    itself. The layer's kernel starts while the one that writes them still runs."""
+    _, wq, ws, bias = _make(n, 96, 500, torch.float32)
+    inputs = [_make(n, 96, 1, torch.float32, seed=i)[0] * 10.0 ** (i % 7 - 3) for i in range(40)]
+    want = []
+    for x in inputs:
+        q, scale = quantize_rows(x)
+        want.append(int8_linear(q, wq, ws, bias, x_scale=scale))
+    torch.cuda.synchronize()
+    got = [int8_linear(x, wq, ws, bias) for x in inputs]
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
