@@ -153,7 +153,8 @@ __device__ __forceinline__ int to_line(const T* p, int n) {
   return head < n ? head : n;
 }
 
-// The partial of one chunk: elements [e0, e1) of tensor t.
+// The partial of one chunk: elements [e0, e1) of tensor t. Ordinary loads: the
+// cluster's kernel writes the same memory afterwards.
 template <int P, int DT>
 __device__ __forceinline__ void chunk_norm(const GradEntry& t, int64_t e0, int64_t e1,
                                            double& sum, uint32_t& peak) {
@@ -186,7 +187,7 @@ __device__ __forceinline__ void chunk_norm(const GradEntry& t, int64_t e0, int64
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
     const int g = static_cast<int>(threadIdx.x) + i * kThreads;
-    q[i] = g < groups ? __ldg(v + g) : make_uint4(0, 0, 0, 0);
+    q[i] = g < groups ? v[g] : make_uint4(0, 0, 0, 0);
   }
   const int rest = n - groups * N;  // head and tail elements: at most 70
   float edge = 0.0f;
@@ -221,7 +222,7 @@ __device__ __forceinline__ void chunk_norm(const GradEntry& t, int64_t e0, int64
         const int g = static_cast<int>(threadIdx.x) + i * kThreads;
         if (g >= groups) break;
         float x[N];
-        E::unpack(__ldg(v + g), x);
+        E::unpack(v[g], x);
 #pragma unroll
         for (int j = 0; j < N; ++j) d += term64<P>(x[j]);
       }

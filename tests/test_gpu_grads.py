@@ -260,3 +260,23 @@ def test_refusals():
         clip_grads([a], 1.0, out=[a[:5]])
     with pytest.raises(TypeError):
         clip_grads([a], 1.0, out=[torch.zeros(100, device="cuda", dtype=torch.float16)])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_small_clips_in_a_row(dtype):
+    """One launch reads the gradients for the norm and then writes them: clips in place of one
+    piece of memory, one after the other, each of what the one before left or of new values."""
+    buf = torch.empty(100003, dtype=dtype, device="cuda")
+    grads = [buf[3:40000], buf[40000:40007], buf[40007:]]
+    fresh = [_make([(100003,)], dtype, scale=10.0 ** (i % 5 - 2), seed=i)[0] for i in range(20)]
+    was, got, norms, limits = [], [], [], []
+    for x in fresh:
+        buf.copy_(x)
+        for limit in (3.0, 1.0, 0.25):
+            was.append(buf[3:].clone())
+            norms.append(clip_grads_(grads, limit))
+            got.append(buf[3:].clone())
+            limits.append(limit)
+    for w, o, norm, limit in zip(was, got, norms, limits):
+        want = _check_norm(norm, [w], 2.0)
+        _check_clipped([o], [w], want, limit)
