@@ -147,6 +147,36 @@ __device__ __forceinline__ void commit(uint32_t bar) {
     umma_commit_pair(bar, 0x3);
 }
 
+// tanh of a pair, within 10 * 2^-24 of its value: x P(t) / Q(t) with t = x^2,
+// P and Q of degree 4 fitted to tanh itself for the least relative error (below
+// 2^-26; all coefficients are positive, so that nothing cancels). The form by
+// exponentials, (e^2x - 1) / (e^2x + 1), is right to some 1e-7 absolute only: a
+// logit of a millionth of the cap loses all its bits. Beyond 8.3 tanh is 1
+// within 2^-23. The clamp keeps a NaN, which fminf and fmaxf would not.
+__device__ __forceinline__ uint64_t tanh_pair(float a, float b) {
+  constexpr float kEnd = 8.3f;
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(kEnd));
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(b) : "f"(kEnd));
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(-kEnd));
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(b) : "f"(-kEnd));
+  auto both = [](float c) { return f2_pack(c, c); };
+  const uint64_t x = f2_pack(a, b);
+  const uint64_t t = f2_mul(x, x);
+  uint64_t p = f2_fma(t, both(1.4648282e-8f), both(2.1508517e-5f));
+  uint64_t q = f2_fma(t, both(8.295119e-7f), both(3.3739527e-4f));
+  p = f2_fma(p, t, both(3.5491704e-3f));
+  q = f2_fma(q, t, both(2.6079955e-2f));
+  p = f2_fma(p, t, both(0.13425872f));
+  q = f2_fma(q, t, both(0.46759197f));
+  p = f2_fma(p, t, both(1.0f));
+  q = f2_fma(q, t, both(1.0f));
+  float r_a, r_b;
+  f2_unpack(q, r_a, r_b);
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(r_a));
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(r_b));
+  return f2_mul(f2_mul(p, x), f2_pack(r_a, r_b));
+}
+
 __device__ __forceinline__ float bias_at(const void* p, int dtype, int64_t i) {
   if (dtype == FLCE_F32) return static_cast<const float*>(p)[i];
   if (dtype == FLCE_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
@@ -473,8 +503,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int j = 0; j < 32; ++j) z[j] = fmaf(z[j] * __shfl_sync(0xffffffffu, xs, j), ws, b);
         if (p.xf.has_cap) {
+          const uint64_t inv = f2_pack(p.xf.inv_softcap, p.xf.inv_softcap);
+          const uint64_t cap = f2_pack(p.xf.softcap, p.xf.softcap);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) z[j] = p.xf.softcap * tanh_exp2(z[j] * p.xf.inv_softcap);
+          for (int j = 0; j < 32; j += 2) {
+            f2_unpack(f2_mul(f2_pack(z[j], z[j + 1]), inv), z[j], z[j + 1]);
+            f2_unpack(f2_mul(tanh_pair(z[j], z[j + 1]), cap), z[j], z[j + 1]);
+          }
         }
         uint8_t* const row0 = static_cast<uint8_t*>(p.out) +
                               ((n0 + c * 32) * p.out_pitch + v0) * static_cast<int64_t>(sizeof(T));

@@ -283,3 +283,23 @@ def test_scales_of_this_call(n):
     torch.cuda.synchronize()
     got = [int8_linear(x, wq, ws, bias) for x in inputs]
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("n", [5, 300])
+@pytest.mark.parametrize("size", [1e-6, 1e-3, 0.1, 1.0])
+def test_softcap_of_small_logits(size, n):
+    """Logits far below the cap keep their own precision: z rounds twice, its share of the cap
+    twice, the product with the cap once (2^-24 each, none of which tanh magnifies), and tanh is
+    within 10 * 2^-24: its rational form, evaluated in 32 bits over 2.2 million places on the
+    host, is within 5, and the approximate reciprocal adds 2."""
+    x, wq, ws, _ = _make(n, 128, 400, torch.float32)
+    q, scale = quantize_rows(x)
+    cap = 30.0
+    ws = ws * (size * cap / float(((q.double() @ wq.double().t()) * scale.double().unsqueeze(-1)
+                                  * ws.double()).abs().max()))
+    z, _, gross, _ = _linear64(q, scale, wq, ws, softcap=cap)
+    assert float(gross.max()) <= 2.0 ** 24  # the sums are exact
+    got = int8_linear(x, wq, ws, softcap=cap).double()
+    assert bool(((got - z).abs() <= 15 * 2.0 ** -24 * z.abs()).all())
+    half = int8_linear(x, wq, ws, softcap=cap, out_dtype=torch.bfloat16).double()
+    assert bool(((half - z).abs() <= (2.0 ** -8 + 16 * 2.0 ** -24) * z.abs()).all())
