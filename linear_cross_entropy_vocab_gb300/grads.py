@@ -178,11 +178,16 @@ def clip_grads(grads: Iterable[torch.Tensor], max_norm: float, norm_type: float 
 def clip_grad_norm_(parameters: Iterable[torch.Tensor], max_norm: float, norm_type: float = 2.0,
                     error_if_nonfinite: bool = False, *, eps: float = 1e-6) -> torch.Tensor:
     """:func:`clip_grads_` over the ``.grad`` of ``parameters`` (those without one are left out).
-    ``error_if_nonfinite`` waits for the norm and raises before anything is scaled if it is not
-    finite."""
+    A ``max_norm`` of inf sets no limit: the norm is returned and the gradients stay as they are,
+    whatever it is. ``error_if_nonfinite`` waits for the norm and raises before anything is scaled
+    if it is not finite."""
+    unlimited = max_norm == math.inf
+    _limits(0.0 if unlimited else max_norm, eps)
     grads = [p.grad for p in _listed(parameters) if p.grad is not None]
-    if error_if_nonfinite:
+    if error_if_nonfinite or unlimited:
         norm = grad_norm(grads, norm_type)
-        if not math.isfinite(float(norm)):
+        if error_if_nonfinite and not math.isfinite(float(norm)):
             raise RuntimeError(f"the gradients' norm is {float(norm)}: they are not clipped")
+        if unlimited:
+            return norm
     return clip_grads_(grads, max_norm, norm_type, eps=eps)

@@ -280,3 +280,29 @@ def test_small_clips_in_a_row(dtype):
     for w, o, norm, limit in zip(was, got, norms, limits):
         want = _check_norm(norm, [w], 2.0)
         _check_clipped([o], [w], want, limit)
+
+
+@pytest.mark.parametrize("p", [1.0, 2.0, math.inf])
+def test_no_limit(p):
+    """max_norm = inf: the norm is read and the gradients stay."""
+    grads = _make([(100,), (20000,)], torch.bfloat16)
+    params = [torch.nn.Parameter(torch.zeros_like(g)) for g in grads]
+    for bad in (None, math.inf, math.nan):
+        if bad is not None:
+            grads[1][777] = bad
+        for q, g in zip(params, grads):
+            q.grad = g.clone()
+        norm = clip_grad_norm_(params, math.inf, p)
+        if bad is None:
+            _check_norm(norm, grads, p)
+        else:
+            assert math.isnan(float(norm)) if math.isnan(bad) else float(norm) == math.inf
+            with pytest.raises(RuntimeError, match="not clipped"):
+                clip_grad_norm_(params, math.inf, p, error_if_nonfinite=True)
+        assert all(torch.equal(q.grad.view(torch.int16), g.view(torch.int16))
+                   for q, g in zip(params, grads))
+    for bad in (-1.0, math.nan, -math.inf):
+        with pytest.raises(ValueError, match="max_norm"):
+            clip_grad_norm_(params, bad, p)
+    with pytest.raises(ValueError, match="eps"):
+        clip_grad_norm_(params, math.inf, p, eps=-1.0)
