@@ -197,5 +197,4 @@ def beam_reorder_(states: Union[torch.Tensor, Iterable[torch.Tensor]], parents: 
         stream = raw_stream(dev)
         abi.flce_beam_reorder(table.buffer_info()[0] if states else None, len(states),
                               parents.data_ptr(), b, k, _err_ptr(err_word, dev), stream)
-    if states and not states[0].is_inference():
-        torch.autograd.graph.increment_version(states)
+    torch.autograd.graph.increment_version(states)

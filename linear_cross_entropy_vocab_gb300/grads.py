@@ -156,8 +156,7 @@ def clip_grads_(grads: Iterable[torch.Tensor], max_norm: float, norm_type: float
     max_norm, eps = _limits(max_norm, eps)
     grads = _listed(grads)
     norm = _run(grads, None, norm_type, max_norm, eps)
-    if grads and not grads[0].is_inference():
-        torch.autograd.graph.increment_version(grads)
+    torch.autograd.graph.increment_version(grads)
     return norm
 
 
@@ -170,8 +169,7 @@ def clip_grads(grads: Iterable[torch.Tensor], max_norm: float, norm_type: float 
     if len(out) != len(grads):
         raise ValueError(f"{len(grads)} gradients and {len(out)} outputs")
     norm = _run(grads, out, norm_type, max_norm, eps)
-    if out and not out[0].is_inference():
-        torch.autograd.graph.increment_version(out)
+    torch.autograd.graph.increment_version(out)
     return norm
 
 

@@ -349,3 +349,21 @@ def test_reorder_graph():
     parents.copy_(torch.tensor([[3, 2, 1, 0]]))
     graph.replay()
     assert state[:, 49].tolist() == [3, 2, 1, 0]
+
+
+@pytest.mark.parametrize("order", [(0, 1), (1, 0)])
+def test_reorder_autograd_sees_the_change(order):
+    """States that mix inference tensors, which have no version, with others."""
+    with torch.inference_mode():
+        plain = torch.arange(4, device="cuda")
+    a = torch.arange(4, device="cuda")
+    both = [(plain, a)[i] for i in order]
+    parents = torch.tensor([[1, 0], [1, 0]], device="cuda")
+    for inside in (False, True):
+        with torch.inference_mode(inside):
+            was = a._version
+            beam_reorder_(both, parents)
+            assert a._version == was + 1
+            beam_reorder_(plain, parents)
+    assert a.tolist() == [0, 1, 2, 3] and plain.tolist() == [0, 1, 2, 3]
+    beam_reorder_([], parents)

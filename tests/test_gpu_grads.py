@@ -306,3 +306,28 @@ def test_no_limit(p):
             clip_grad_norm_(params, bad, p)
     with pytest.raises(ValueError, match="eps"):
         clip_grad_norm_(params, math.inf, p, eps=-1.0)
+
+
+@pytest.mark.parametrize("order", [(0, 1, 2), (1, 2, 0), (2, 1, 0)])
+def test_autograd_sees_the_change_among_inference_tensors(order):
+    """Lists that mix inference tensors, which have no version, with others, in any order; inside
+    inference mode and outside."""
+    with torch.inference_mode():
+        plain = [torch.ones(50, device="cuda") for _ in range(2)]
+    a = torch.ones(50, device="cuda")
+    every = [plain[0], a, plain[1]]
+    every = [every[i] for i in order]
+    copies = [torch.empty(50, device="cuda") for _ in range(3)]
+    for inside in (False, True):
+        with torch.inference_mode(inside):
+            was = a._version
+            clip_grads_(every, 1.0)
+            assert a._version == was + 1
+            before = [c._version for c in copies]
+            clip_grads(every, 1.0, out=copies)
+            assert a._version == was + 1
+            assert [c._version for c in copies] == [v + 1 for v in before]
+            clip_grads(copies, 1.0, out=every)
+            assert a._version == was + 2
+    clip_grads_(plain, 1.0)
+    clip_grads_([], 1.0)
