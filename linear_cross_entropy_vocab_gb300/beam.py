@@ -13,6 +13,7 @@ from typing import Iterable, NamedTuple, Optional, Union
 import torch
 
 from . import abi
+from ._autograd import refuse_gradient
 from ._stream import on_device, raw_stream
 
 __all__ = ["BeamSelection", "beam_select", "beam_reorder_"]
@@ -62,7 +63,7 @@ def beam_select(logits: torch.Tensor, beam_scores: torch.Tensor,
     mask leaves nothing offer nothing; places that nothing fills hold score -inf, parent 0 and
     ``pad_token``. ``err_word`` (one int32, which the caller clears and reads) gets
     FLCE_DEVERR_NOT_FINITE where an allowed logit or a beam score is NaN or +inf; that beam
-    offers nothing.
+    offers nothing. The scores have no gradient: logits or beam scores that ask for one are refused.
     """
     if logits.dim() != 3:
         raise ValueError("logits must be (B, K, V)")
@@ -72,6 +73,7 @@ def beam_select(logits: torch.Tensor, beam_scores: torch.Tensor,
         raise TypeError(f"unsupported dtype {logits.dtype}: use float32, bfloat16 or float16")
     if k < 1 or v < 1:
         raise ValueError("logits need at least one beam and one token")
+    refuse_gradient("beam_select", logits=logits, beam_scores=beam_scores)
     dev = logits.device
     _on("logits", logits, dev)
     if beam_scores.shape != (b, k):

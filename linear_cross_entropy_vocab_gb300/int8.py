@@ -14,6 +14,7 @@ from typing import Optional, Tuple
 import torch
 
 from . import abi
+from ._autograd import refuse_gradient
 from ._stream import on_device, raw_stream
 
 __all__ = ["quantize_rows", "int8_linear"]
@@ -36,10 +37,12 @@ def quantize_rows(x: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
     """x [..., H] (float32, bfloat16 or float16) -> (q int8 [..., H], scale float32 [...]), with
     x close to q * scale. Halves round to even; a row of zeros has scale 0, and a row that holds
     a NaN or an infinity has scale NaN. q's rows start at multiples of 16 bytes, as int8_linear
-    reads them best: where H is no multiple of 16, q is a view of wider rows."""
+    reads them best: where H is no multiple of 16, q is a view of wider rows. It has no gradient:
+    an x that asks for one is refused."""
     code = _DTYPES.get(x.dtype)
     if code is None:
         raise TypeError(f"unsupported dtype {x.dtype}: use float32, bfloat16 or float16")
+    refuse_gradient("quantize_rows", x=x)
     if not x.is_cuda:
         raise ValueError("x must be a CUDA tensor")
     if x.dim() < 1 or x.shape[-1] < 1:
@@ -100,6 +103,7 @@ def int8_linear(x: torch.Tensor, weight: torch.Tensor, weight_scale: torch.Tenso
         raise TypeError(f"unsupported out_dtype {out_dtype}")
     if bias is not None and (bias.shape != (v,) or bias.dtype not in _DTYPES):
         raise ValueError("bias must be (V,), float32, bfloat16 or float16")
+    refuse_gradient("int8_linear", x=x, weight_scale=weight_scale, bias=bias, x_scale=x_scale)
     dev = x.device
     for name, t in (("x", x), ("weight", weight), ("weight_scale", weight_scale),
                     ("bias", bias), ("x_scale", x_scale), ("err_word", err_word)):
@@ -109,8 +113,6 @@ def int8_linear(x: torch.Tensor, weight: torch.Tensor, weight_scale: torch.Tenso
             raise ValueError(f"{name} must be a CUDA tensor")
         if t.device != dev:
             raise ValueError(f"{name} is on {t.device}, x on {dev}")
-        if t.requires_grad and torch.is_grad_enabled():
-            raise RuntimeError(f"int8_linear has no gradient, and {name} asks for one")
     if err_word is not None and (err_word.dtype != torch.int32 or err_word.numel() != 1):
         raise TypeError("err_word must be one int32")
     x, n, x_pitch = _rows(x)

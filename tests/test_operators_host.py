@@ -262,3 +262,35 @@ def test_select_refuses_rows_whose_tiles_leave_32_bits(v):
             last = abi.flce_beam_problem(batch=batch, beams=beams, candidates=6, dtype=dtype,
                                          v=(1 << 31) - 8193)
             assert abi.flce_beam_select_workspace_size(last) > 0
+
+
+@pytest.mark.filterwarnings("ignore:.*torch.jit:DeprecationWarning")
+def test_gradients_are_refused_not_dropped():
+    """Operators that have no gradient raise for inputs that ask for one, in reverse or forward
+    mode, and go on (here to the missing device) under no_grad."""
+    x, w, s = torch.zeros(3, 8), torch.zeros(5, 8, dtype=torch.int8), torch.zeros(5)
+    z, b = torch.zeros(2, 3, 10), torch.zeros(2, 3)
+    calls = [
+        (package.quantize_rows, (x,), {}, (0,)),
+        (package.int8_linear, (x, w, s, s.clone()), {}, (0, 2, 3)),
+        (package.beam_select, (z, b), {}, (0, 1)),
+    ]
+    for call, args, kw, floats in calls:
+        for i in floats:
+            asking = list(args)
+            asking[i] = args[i].clone().requires_grad_(True)
+            with pytest.raises(RuntimeError, match="no gradient"):
+                call(*asking, **kw)
+            with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
+                call(*asking, **kw)
+            with torch.autograd.forward_ad.dual_level():
+                asking[i] = torch.autograd.forward_ad.make_dual(args[i], torch.ones_like(args[i]))
+                with pytest.raises(RuntimeError, match="tangent"):
+                    call(*asking, **kw)
+                with torch.no_grad(), pytest.raises(RuntimeError, match="tangent"):
+                    call(*asking, **kw)
+                with pytest.raises(ValueError, match="CUDA"):
+                    call(*args, **kw)
+    q = torch.zeros(3, 8, dtype=torch.int8)
+    with pytest.raises(RuntimeError, match="no gradient"):
+        package.int8_linear(q, w, s, x_scale=torch.zeros(3, requires_grad=True))
