@@ -52,10 +52,11 @@ def beam_select(logits: torch.Tensor, beam_scores: torch.Tensor,
                 finished: Optional[torch.Tensor] = None,
                 allowed: Optional[torch.Tensor] = None, pad_token: int = 0,
                 err_word: Optional[torch.Tensor] = None) -> BeamSelection:
-    """The ``num_candidates`` (default K) best continuations of each prompt.
+    """The ``num_candidates`` (default K; at most 256) best continuations of each prompt.
 
-    logits [B, K, V] (float32, bfloat16 or float16) and beam_scores [B, K] (float32, the log
-    probability of each beam so far). Scores that are equal are taken in the order of k * V + v.
+    logits [B, K, V] (float32, bfloat16 or float16; K at most 1024, V below 2^31 - 8192) and
+    beam_scores [B, K] (float32, the log probability of each beam so far). Scores that are equal
+    are taken in the order of k * V + v.
 
     ``allowed`` (bool, broadcast to [B, K, V]): tokens that may come; the others count as logits
     of -inf, whatever they hold. ``finished`` (bool [B, K]): beams at their end; each offers
@@ -63,7 +64,8 @@ def beam_select(logits: torch.Tensor, beam_scores: torch.Tensor,
     mask leaves nothing offer nothing; places that nothing fills hold score -inf, parent 0 and
     ``pad_token``. ``err_word`` (one int32, which the caller clears and reads) gets
     FLCE_DEVERR_NOT_FINITE where an allowed logit or a beam score is NaN or +inf; that beam
-    offers nothing. The scores have no gradient: logits or beam scores that ask for one are refused.
+    offers nothing. The scores have no gradient: logits or beam scores that ask for one are
+    refused.
     """
     if logits.dim() != 3:
         raise ValueError("logits must be (B, K, V)")
@@ -174,8 +176,9 @@ def beam_reorder_(states: Union[torch.Tensor, Iterable[torch.Tensor]], parents: 
 
     ``states`` is a tensor or several, of any types, shapes and strides (views of the filled part
     of a cache among them), that share no memory; parents [B, K] int64. Beams that continue
-    themselves are neither read nor written. A parent outside [0, K) leaves its beam as it is and
-    sets FLCE_DEVERR_PARENT_RANGE in ``err_word`` (one int32, which the caller clears and reads).
+    themselves are neither read nor written. K is at most 64. A parent outside [0, K) leaves its
+    beam as it is and sets FLCE_DEVERR_PARENT_RANGE in ``err_word`` (one int32, which the caller
+    clears and reads).
     """
     if parents.dim() != 2:
         raise ValueError("parents must be (B, K)")

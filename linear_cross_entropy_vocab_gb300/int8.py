@@ -68,7 +68,8 @@ def int8_linear(x: torch.Tensor, weight: torch.Tensor, weight_scale: torch.Tenso
                 logit_scale: float = 1.0, softcap: Optional[float] = None,
                 out_dtype: Optional[torch.dtype] = None,
                 err_word: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """Logits [..., V] of x [..., H] against weight [V, H] (int8, weight_scale [V] float32).
+    """Logits [..., V] of x [..., H] against weight [V, H] (int8, weight_scale [V] float32; H at
+    most 131071).
 
     x is float32, bfloat16 or float16 and is quantised row by row within the call, or int8 with
     ``x_scale`` [...] float32 from :func:`quantize_rows`. ``bias`` [V] is a float tensor.

@@ -294,3 +294,14 @@ def test_gradients_are_refused_not_dropped():
     q = torch.zeros(3, 8, dtype=torch.int8)
     with pytest.raises(RuntimeError, match="no gradient"):
         package.int8_linear(q, w, s, x_scale=torch.zeros(3, requires_grad=True))
+
+
+def test_docstrings_name_the_limits():
+    """What the C entry points refuse for its size, a user reads beforehand."""
+    assert "at most 256" in package.beam_select.__doc__
+    assert "K at most 1024" in package.beam_select.__doc__
+    assert _select(candidates=257) == UNSUPPORTED and _select(beams=1025) == UNSUPPORTED
+    assert "K is at most 64" in package.beam_reorder_.__doc__
+    assert _reorder(beams=65) == UNSUPPORTED
+    assert "H at\n    most 131071" in package.int8_linear.__doc__
+    assert _qlinear(h=131072, x_pitch=131072, weight_pitch=131072) == UNSUPPORTED
