@@ -338,7 +338,8 @@ flce_status flce_selftest_wait_timeout(int32_t* err_word, int32_t* result,
  *
  *   norm = (sum |g|^p)^(1/p) over every element of every gradient (p = 1, 2),
  *          or max |g| (inf)
- *   dst  = g * min(1, max_norm / (norm + eps))        (a NaN norm gives NaN)
+ *   dst  = g * min(1, max_norm / (norm + eps))        (a NaN norm gives NaN;
+ *                                                      0 / 0 counts as 1)
  *
  * Sums are held in 64 bits above 64-element parts, with no 32-bit overflow or
  * underflow in between; the result is the same in every run. Products are

@@ -419,8 +419,10 @@ __device__ __forceinline__ void any_chunk_scale(const GradEntry& t, int64_t e0, 
     chunk_scale<FLCE_F16>(t, e0, e1, coef);
 }
 
-// min(1, max_norm / (norm + eps)); NaN stays NaN.
+// min(1, max_norm / (norm + eps)); NaN stays NaN. All gradients 0 and eps 0
+// leave nothing to scale, whatever max_norm is.
 __device__ __forceinline__ float clip_factor(float norm, float max_norm, float eps) {
+  if (norm + eps == 0.0f) return 1.0f;
   const float coef = max_norm / (norm + eps);
   return coef > 1.0f ? 1.0f : coef;
 }

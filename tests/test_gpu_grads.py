@@ -331,3 +331,16 @@ def test_autograd_sees_the_change_among_inference_tensors(order):
             assert a._version == was + 2
     clip_grads_(plain, 1.0)
     clip_grads_([], 1.0)
+
+
+@pytest.mark.parametrize("n", [5, 1 << 20])  # one launch, and two
+@pytest.mark.parametrize("p", [1.0, 2.0, math.inf])
+def test_zeros_without_eps(p, n):
+    """Gradients of norm 0, eps 0 and max_norm 0: the quotient has no value, the gradients do."""
+    zeros = [torch.zeros(n, device="cuda"), torch.zeros(3, dtype=torch.bfloat16, device="cuda")]
+    out = [torch.full(z.shape, 7.0, device="cuda") for z in zeros]
+    for limit in (0.0, 1.0):
+        assert float(clip_grads(zeros, limit, p, out=out, eps=0.0)) == 0.0
+        assert not any(bool(o.any()) for o in out)
+        assert float(clip_grads_(zeros, limit, p, eps=0.0)) == 0.0
+        assert not any(bool(z.any()) for z in zeros)
