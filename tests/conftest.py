@@ -15,6 +15,11 @@ def pytest_configure(config):
         "markers", "slow: full-size parity case (minutes of host fp64 work)")
 
 
+# Hand made-up addresses to the library and count on the missing device to end the call: on a GPU
+# the kernels would use them.
+WITHOUT_DEVICE = ("test_operators_host.py::test_grad_overlaps",)
+
+
 def pytest_collection_modifyitems(config, items):
     try:
         import torch
@@ -22,6 +27,10 @@ def pytest_collection_modifyitems(config, items):
     except Exception:  # pragma: no cover
         has_gpu = False
     if has_gpu:
+        skip = pytest.mark.skip(reason="passes made-up addresses, for machines without a GPU")
+        for item in items:
+            if item.nodeid.endswith(WITHOUT_DEVICE):
+                item.add_marker(skip)
         return
     skip = pytest.mark.skip(reason="no CUDA device in this process")
     for item in items:

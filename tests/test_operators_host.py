@@ -305,3 +305,26 @@ def test_docstrings_name_the_limits():
     assert _reorder(beams=65) == UNSUPPORTED
     assert "H at\n    most 131071" in package.int8_linear.__doc__
     assert _qlinear(h=131072, x_pitch=131072, weight_pitch=131072) == UNSUPPORTED
+
+
+def test_grad_overlaps_with_a_refusal_behind():
+    """Which memory counts as shared: calls without any get as far as the next check, which
+    refuses them for their max_norm, so that no made-up address reaches a device."""
+    far = 0x900000
+
+    def shared(*grads):
+        assert _clip(*grads, max_norm=-1.0) == INVALID
+        text = abi.flce_last_error()
+        assert ("overlap" in text) != ("max_norm" in text), text
+        return "overlap" in text
+
+    rows = dict(rows=9, cols=40, src_pitch=100, dst_pitch=100)
+    assert not shared(_grad(), _grad(src=FAKE + 400, dst=FAKE + 400))
+    assert not shared(_grad(dst=far), _grad(dst=far + 400))  # one source, read twice
+    assert not shared(_grad(**rows), _grad(src=FAKE + 160, dst=FAKE + 160, **rows))
+    assert not shared(_grad(rows=0), _grad())
+    assert shared(_grad(), _grad())
+    assert shared(_grad(src=far, dst=FAKE + 396), _grad())
+    assert shared(_grad(dst=FAKE + 4))
+    assert shared(_grad(**rows), _grad(src=FAKE + 156, dst=FAKE + 156, **rows))
+    assert shared(_grad(**rows), _grad(src=FAKE + 244, dst=FAKE + 244, **rows))
