@@ -21,13 +21,6 @@ using namespace flce::host;
 
 // Upper bound of the CTAs of one launch: the workspace holds one partial each.
 constexpr int kMaxCtas = 1024;
-// CTAs per SM of the norm and of the clip. The clip holds a chunk's 16-byte
-// loads and the places of its stores, 128 registers a thread; four CTAs of 64
-// spill, and 640 MB read and written take 270 us in fp32 and 216 in bf16,
-// against 209 and 212 with two.
-constexpr int kNormCtasPerSm = 4;
-constexpr int kClipCtasPerSm = 2;
-
 // Chunks of 32 KB up to which the cluster of eight CTAs takes a clip by itself.
 // On the device that is the shorter way up to 16 (two fp32 tensors: 128 KB 5.4
 // us against 7.6, 512 KB 7.3 against 8.0, 1 MB 10.4 against 8.0), and as a call
@@ -196,8 +189,8 @@ flce_status fill(GradTable<CAP>& tab, const flce_grad* g, int64_t count, int64_t
 template <int CAP>
 flce_status run(const flce_grad* g, int64_t count, int p, bool clip, float max_norm, float eps,
                 float* norm_out, double* partials, int sms, cudaStream_t s) {
-  const int norm_ctas = std::min(kMaxCtas, kNormCtasPerSm * sms);
-  const int clip_ctas = std::min(kMaxCtas, kClipCtasPerSm * sms);
+  const int norm_ctas = std::min(kMaxCtas, flce::kGradNormCtasPerSm * sms);
+  const int clip_ctas = std::min(kMaxCtas, flce::kGradClipCtasPerSm * sms);
   GradTable<CAP> tab;
   int n_partials = 0;
   for (int64_t next = 0; next < count;) {

@@ -11,6 +11,13 @@ namespace flce {
 
 // Source bytes of one chunk: what a CTA takes at a time.
 constexpr int kGradChunkBytes = 32768;
+// CTAs per SM of the norm and of the clip: the kernels are compiled to fit that
+// many, and the grids are that large. The clip holds a chunk's 16-byte loads and
+// the places of its stores, 128 registers a thread; four CTAs of 64 spill, and
+// 640 MB read and written take 270 us in fp32 and 216 in bf16, against 209 and
+// 212 with two.
+constexpr int kGradNormCtasPerSm = 4;
+constexpr int kGradClipCtasPerSm = 2;
 // Tensors in one launch. Kernel parameters end at 32,764 bytes; the smaller
 // tables keep the parameters of a call with few tensors short (59 small ones:
 // 65 us a clip in place with the medium table, 69 with the large).

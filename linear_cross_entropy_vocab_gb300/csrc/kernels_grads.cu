@@ -297,7 +297,7 @@ __device__ __forceinline__ void any_chunk_norm(const GradEntry& t, int64_t e0, i
 // partials[blockIdx.x]: the sum of powers of this CTA's chunks, or for
 // P = 0 the bits of their largest magnitude.
 template <int P, int CAP>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, kGradNormCtasPerSm)
     grad_partials_kernel(const __grid_constant__ GradTable<CAP> tab, double* partials) {
   __shared__ double buf[kThreads / 32];
   grid_launch_dependents();
@@ -428,7 +428,7 @@ __device__ __forceinline__ float clip_factor(float norm, float max_norm, float e
 }
 
 template <int CAP>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, kGradClipCtasPerSm)
     grad_clip_kernel(const __grid_constant__ GradTable<CAP> tab, const double* partials, int n,
                      int p, float max_norm, float eps, float* norm_out, int write_norm) {
   __shared__ double buf[kThreads / 32];
