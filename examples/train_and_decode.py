@@ -5,7 +5,8 @@ head's weight in 8-bit integers, and a beam search over its logits.
 
 The model is one recurrent cell over token embeddings with a head over the vocabulary. It learns
 sequences that count up by a step given at their start, and then continues such sequences with
-four beams; the training's loss falls and every continuation is right. Takes seconds on one GPU.
+four beams; the training's loss falls and most continuations are right (all 64, where it was
+tried). Takes seconds on one GPU.
 """
 import os
 import sys

@@ -343,7 +343,7 @@ flce_status flce_selftest_wait_timeout(int32_t* err_word, int32_t* result,
  *
  * Sums are held in 64 bits above 64-element parts, with no 32-bit overflow or
  * underflow in between; the result is the same in every run. Products are
- * rounded once, to dst's type. Each gradient is `rows` runs of `cols`
+ * rounded to fp32 and then to dst's type. Each gradient is `rows` runs of `cols`
  * contiguous elements, `src_pitch` (`dst_pitch`) elements from run to run; a
  * dense tensor of any shape is one run. Tensors may start at any address that
  * their element type allows; 16-byte aligned runs are fastest.
@@ -383,7 +383,10 @@ flce_status flce_grad_clip(const flce_grad* grads, int64_t count, int32_t norm,
  *
  * and, for each prompt b, the `candidates` largest of its K * V scores, best
  * first; equal scores in the order of k * V + v. The comparison is in 64 bits
- * on row sums of 32-bit exponentials; the scores are rounded to fp32.
+ * on row sums of 32-bit exponentials, which leave a beam's scores within 8e-6:
+ * candidates of two beams closer than twice that may change places, those of
+ * one beam do not. The scores are rounded to fp32. The result is the same in
+ * every run of one shape and type.
  *   - allowed (bytes, nullable): a token whose byte is 0 counts as z = -inf,
  *     whatever its logit holds: it is neither offered nor in the sum.
  *   - finished (bytes, nullable): a beam whose byte is not 0 offers itself
@@ -451,6 +454,7 @@ flce_status flce_beam_reorder(const flce_beam_state* states, int64_t count,
  *   lin_ij  = scale_i * weight_scale_j * sum_h q_ih * w_jh + bias_j
  *   u_ij    = logit_scale * lin_ij
  *   out_ij  = softcap * tanh(u_ij / softcap)   if softcap > 0, else u_ij
+ *             (tanh within 10 * 2^-24 of its value)
  *
  * A row of zeros has scale 0; a row that holds a NaN or an infinity gives
  * NaN. Products are exact and sums are held in 32-bit floating point: they are

@@ -22,10 +22,12 @@ using namespace flce::host;
 // Upper bound of the CTAs of one launch: the workspace holds one partial each.
 constexpr int kMaxCtas = 1024;
 // Chunks of 32 KB up to which the cluster of eight CTAs takes a clip by itself.
-// On the device that is the shorter way up to 16 (two fp32 tensors: 128 KB 5.4
-// us against 7.6, 512 KB 7.3 against 8.0, 1 MB 10.4 against 8.0), and as a call
-// of its own, where a second launch costs the host 5 us, up to 64 (19 us
-// against 24).
+// On the device that is the shorter way up to 8 or 12 (two tensors in a graph,
+// cluster against two launches: fp32 8 chunks 4.4 against 5.1 us, 16 5.2 / 5.1,
+// 24 5.7 / 5.1, 64 8.3 / 5.3; bf16 8 5.8 / 6.4, 16 7.3 / 6.4, 24 8.8 / 6.4, 64
+// 15.7 / 6.5). A call of its own, where a second launch costs the host 5 us,
+// takes 16.5 us instead of 21.7 at any of these sizes. Between the two, 24 gives
+// up at most 2.4 us in a graph for those 5.
 constexpr uint32_t kClusterChunks = 24;
 
 constexpr int64_t kMaxExtent = int64_t(1) << 46;

@@ -12,7 +12,10 @@ namespace {
 
 using namespace flce::host;
 
-constexpr int64_t kMaxH = 131071;  // 128 * 128 * h stays below 2^31
+// Keeps the sums of h products below 2^31, where the last place of the 32-bit
+// accumulator, which each step of 16 products may lose beyond 2^24, is at most
+// 128.
+constexpr int64_t kMaxH = 131071;
 constexpr int64_t kMaxRows = 0x7fffff00;  // a tile may end 255 rows further
 
 bool float_type(int32_t d) { return d == FLCE_F32 || d == FLCE_BF16 || d == FLCE_F16; }

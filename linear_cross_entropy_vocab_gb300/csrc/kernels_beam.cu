@@ -10,8 +10,13 @@
 // lse: it reads each logit once, keeps the M best of a slice of the row with
 // their indices, and the slice's maximum and sum of exponentials. The second
 // takes one prompt: lse of each beam from its slices, the scores of the
-// K x slices x M survivors in 64 bits (what is chosen hangs on comparisons
-// that 32 bits would decide by rounding), and the M best of them.
+// K x slices x M survivors, and the M best of them.
+//
+// A slice's sum is made of ex2.approx values (2^-22 each) added in 32 bits, so
+// that lse is right to some 1e-6 and candidates of two beams closer than 1e-5
+// may change places. What follows is in 64 bits, where scores of different
+// logits of one beam stay different: in 32 bits rounding would make them equal
+// and hand the choice to the index.
 //
 // Finding the M best of a tile: the threads are put into G >= M groups; the
 // smallest of the groups' maxima has at least M values at or above it, and
@@ -299,7 +304,10 @@ struct Slice {
 // A tile is N pieces of 16 bytes per thread; the next tile's are on their way
 // while one is worked on. SHIFT: rows may start anywhere, and a thread's logits
 // come from two aligned pieces (64 x 8 rows of 128255 bf16: 58 us, value by
-// value 80; of 128256 as aligned ones 46, by the shifting kernel 50).
+// value 80; of 128256 as aligned ones 46, by the shifting kernel 50). Two
+// 16-bit pieces at six CTAs an SM spill two bytes of the 40 registers; with
+// five and 48, which spill nothing, those aligned rows take 49 us and 32 of
+// them 19, with six 47 and 14.
 template <class T, int N, bool SHIFT>
 __global__ void __launch_bounds__(kThreads, N == 4 ? 4 : N == 2 && SHIFT ? 5 : 6)
     beam_slices_kernel(const BeamSelectParams p) {
@@ -539,8 +547,8 @@ __global__ void __launch_bounds__(kThreads) beam_choose_kernel(const BeamSelectP
         if (bad) {
           err |= FLCE_DEVERR_NOT_FINITE;
         } else if (top > -INFINITY) {
-          // At most 2^31 terms of at most 1, in steps of 2^-31: the sum is exact
-          // and in any order the same.
+          // At most 2^31 terms of at most 1, each rounded to a multiple of 2^-31:
+          // adding those is exact, and in any order the same.
           unsigned long long s = 0;
           for (int i = lane; i < p.splits; i += 32) {
             const float2 st = p.stats[row * p.splits + i];

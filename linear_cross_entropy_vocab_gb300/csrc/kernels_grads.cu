@@ -6,9 +6,9 @@
 // over every element of every tensor. Two launches: each CTA of the first
 // leaves one 64-bit partial; each CTA of the second adds all partials in the
 // same order (so all get the same norm, and the same in every run), and the
-// clip scales with it. Nothing is read back to the host. A clip of little data
-// is one launch of a cluster of eight CTAs, which exchange their partials
-// through each other's shared memory.
+// clip scales with it, rounding products to fp32 and then to the type. Nothing
+// is read back to the host. A clip of little data is one launch of a cluster of
+// eight CTAs, which exchange their partials through each other's shared memory.
 //
 // Both are bound by memory: the norm reads each gradient once, the clip reads
 // and writes it once more. The tensors are cut into chunks of 32 KB of source
@@ -20,8 +20,8 @@
 //
 // Sums: a thread adds the at most 64 terms of a chunk in 32 bits and those
 // sums in 64 bits. Where a 32-bit sum overflows or is so small that squares
-// below the normal range could matter, the thread takes the same values again
-// in 64 bits (its registers still hold them): the norm of gradients around
+// below the normal range could matter, the thread reads the same values again
+// (the caches hold them) and adds them in 64 bits: the norm of gradients around
 // 1e25 or 1e-25 is right as well.
 #include <cstdint>
 

@@ -404,7 +404,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = quarter * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     bool ok = true;
-    // stages of all this CTA's tiles, counted through; group g takes g, g + 2, ...
+    // stages of all this CTA's tiles, counted through; group g takes g,
+    // g + kWidenGroups, ...
     const int64_t stages =
         static_cast<int64_t>(total > unit0 ? (total - unit0 - 1) / units + 1 : 0) * k_iters;
     int s = group, as = group;
