@@ -476,7 +476,7 @@ typedef struct flce_qproblem {
   int32_t bias_dtype;  /* flce_dtype of bias */
   int32_t has_bias;    /* 0 or 1 */
   float logit_scale;   /* finite */
-  float softcap;       /* > 0 enables it */
+  float softcap;       /* > 0 enables it; 1 / softcap is finite */
   int32_t flags;       /* OR of FLCE_Q_LAY_OUT_WEIGHT; 0 for none */
   int32_t reserved;    /* 0 */
 } flce_qproblem;

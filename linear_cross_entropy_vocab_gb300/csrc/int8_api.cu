@@ -39,6 +39,8 @@ flce_status check_qproblem(const flce_qproblem* p) {
     return fail(FLCE_ERR_INVALID_ARG, "a pitch is smaller than its rows");
   if (!std::isfinite(p->logit_scale) || !std::isfinite(p->softcap))
     return fail(FLCE_ERR_INVALID_ARG, "logit_scale and softcap must be finite");
+  if (p->softcap > 0.0f && !std::isfinite(1.0f / p->softcap))
+    return fail(FLCE_ERR_INVALID_ARG, "softcap is too small to divide by");
   if ((p->flags & ~FLCE_Q_LAY_OUT_WEIGHT) != 0 || p->reserved != 0)
     return fail(FLCE_ERR_INVALID_ARG, "unknown flags, or reserved is not 0");
   return FLCE_OK;

@@ -328,3 +328,11 @@ def test_grad_overlaps_with_a_refusal_behind():
     assert shared(_grad(dst=FAKE + 4))
     assert shared(_grad(**rows), _grad(src=FAKE + 156, dst=FAKE + 156, **rows))
     assert shared(_grad(**rows), _grad(src=FAKE + 244, dst=FAKE + 244, **rows))
+
+
+def test_softcap_without_a_reciprocal_is_refused():
+    """The cap divides: one whose reciprocal overflows would make a logit of 0 NaN."""
+    assert _qlinear(softcap=1e-39) == INVALID
+    assert "softcap" in abi.flce_last_error()
+    assert _qlinear(softcap=3e-39, ws_bytes=16) == WORKSPACE  # as far as the next check
+    assert _qlinear(softcap=-1e-39, ws_bytes=16) == WORKSPACE  # no cap
