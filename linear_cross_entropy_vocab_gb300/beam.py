@@ -75,7 +75,7 @@ def beam_select(logits: torch.Tensor, beam_scores: torch.Tensor,
         raise TypeError(f"unsupported dtype {logits.dtype}: use float32, bfloat16 or float16")
     if k < 1 or v < 1:
         raise ValueError("logits need at least one beam and one token")
-    refuse_gradient("beam_select", logits=logits, beam_scores=beam_scores)
+    refuse_gradient("beam_select", ("logits", "beam_scores"), logits, beam_scores)
     dev = logits.device
     _on("logits", logits, dev)
     if beam_scores.shape != (b, k):

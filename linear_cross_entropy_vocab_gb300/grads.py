@@ -6,7 +6,8 @@
 
 Two kernel launches for up to 500 tensors, one for a clip of few small ones, more in steps of 500;
 the norm stays on the device and nothing waits for it, so a clip can be captured into a CUDA graph
-with the step that it belongs to. Autograd records none of it: the norm is a constant. The work runs in libflce.so (``flce_grad_norm``, ``flce_grad_clip``).
+with the step that it belongs to. Autograd records none of it: the norm is a constant. The work
+runs in libflce.so (``flce_grad_norm``, ``flce_grad_clip``).
 """
 from __future__ import annotations
 

@@ -42,7 +42,7 @@ def quantize_rows(x: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
     code = _DTYPES.get(x.dtype)
     if code is None:
         raise TypeError(f"unsupported dtype {x.dtype}: use float32, bfloat16 or float16")
-    refuse_gradient("quantize_rows", x=x)
+    refuse_gradient("quantize_rows", ("x",), x)
     if not x.is_cuda:
         raise ValueError("x must be a CUDA tensor")
     if x.dim() < 1 or x.shape[-1] < 1:
@@ -104,7 +104,8 @@ def int8_linear(x: torch.Tensor, weight: torch.Tensor, weight_scale: torch.Tenso
         raise TypeError(f"unsupported out_dtype {out_dtype}")
     if bias is not None and (bias.shape != (v,) or bias.dtype not in _DTYPES):
         raise ValueError("bias must be (V,), float32, bfloat16 or float16")
-    refuse_gradient("int8_linear", x=x, weight_scale=weight_scale, bias=bias, x_scale=x_scale)
+    refuse_gradient("int8_linear", ("x", "weight_scale", "bias", "x_scale"), x, weight_scale, bias,
+                    x_scale)
     dev = x.device
     for name, t in (("x", x), ("weight", weight), ("weight_scale", weight_scale),
                     ("bias", bias), ("x_scale", x_scale), ("err_word", err_word)):
