@@ -431,7 +431,8 @@ flce_status flce_beam_select(const flce_beam_problem* p, const void* logits,
  * for every state, as if all were read before any is written. A state is
  * batch * beams beams, beam_stride bytes apart, each of size[0] x ... x
  * size[3] runs of run_bytes contiguous bytes, stride[d] bytes apart. Its
- * elements do not overlap, and no two states do. 16-byte aligned runs and
+ * elements do not overlap, and no two states do (two that start at one address
+ * are refused, FLCE_ERR_INVALID_ARG; other sharing is not looked for). 16-byte aligned runs and
  * strides are fastest. A parent outside [0, beams) sets
  * FLCE_DEVERR_PARENT_RANGE and leaves its beam as it is. beams <= 64. */
 typedef struct flce_beam_state {

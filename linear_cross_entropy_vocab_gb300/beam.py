@@ -175,10 +175,10 @@ def beam_reorder_(states: Union[torch.Tensor, Iterable[torch.Tensor]], parents: 
     of every state, row b * K + j becomes what row b * K + parents[b, j] was.
 
     ``states`` is a tensor or several, of any types, shapes and strides (views of the filled part
-    of a cache among them), that share no memory; parents [B, K] int64. Beams that continue
-    themselves are neither read nor written. K is at most 64. A parent outside [0, K) leaves its
-    beam as it is and sets FLCE_DEVERR_PARENT_RANGE in ``err_word`` (one int32, which the caller
-    clears and reads).
+    of a cache among them), that share no memory (one that is listed twice is refused, other
+    sharing is not looked for); parents [B, K] int64. Beams that continue themselves are neither
+    read nor written. K is at most 64. A parent outside [0, K) leaves its beam as it is and sets
+    FLCE_DEVERR_PARENT_RANGE in ``err_word`` (one int32, which the caller clears and reads).
     """
     if parents.dim() != 2:
         raise ValueError("parents must be (B, K)")

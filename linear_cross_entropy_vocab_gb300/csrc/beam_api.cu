@@ -2,6 +2,7 @@
 // checks, workspace and launches. Nothing is allocated on the device and
 // nothing waits for it.
 #include <algorithm>
+#include <new>
 
 #include "beam_internal.h"
 #include "flce.h"
@@ -124,6 +125,27 @@ flce_status check_state(const flce_beam_state& s, int64_t i, int64_t rows, bool*
     span += (size[a] - 1) * stride[a];
   }
   return FLCE_OK;
+}
+
+// No two states that hold anything start at one address: the second would move
+// what the first moves, in no order. States that share memory otherwise are the
+// caller's to avoid; views that interleave in one buffer are ordinary.
+flce_status check_repeats(const flce_beam_state* states, int64_t count) {
+  constexpr int64_t kFew = 64;
+  const void* few[kFew];
+  const void** const at = count <= kFew ? few : new (std::nothrow) const void*[count];
+  if (at == nullptr)
+    return fail(FLCE_ERR_INVALID_ARG, "no host memory for %lld states", (long long)count);
+  int64_t n = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    const flce_beam_state& s = states[i];
+    if (s.run_bytes != 0 && s.size[0] != 0 && s.size[1] != 0 && s.size[2] != 0 && s.size[3] != 0)
+      at[n++] = s.data;
+  }
+  std::sort(at, at + n);
+  const bool twice = std::adjacent_find(at, at + n) != at + n;
+  if (at != few) delete[] at;
+  return twice ? fail(FLCE_ERR_INVALID_ARG, "a state is listed twice") : FLCE_OK;
 }
 
 // Launches for states that have been checked, each with as many as fit.
@@ -269,6 +291,10 @@ flce_status flce_beam_reorder(const flce_beam_state* states, int64_t count,
     if (vecs > 0xffffffffll / flce::kReorderBlock * flce::kReorderBlock ||
         ceil_div(vecs, flce::kReorderBlock) * batch > 0x7fffffffll)
       return fail(FLCE_ERR_UNSUPPORTED, "state %lld is too large", (long long)i);
+  }
+  if (batch > 0 && beams > 1 && count > 1) {
+    const flce_status st = check_repeats(states, count);
+    if (st != FLCE_OK) return st;
   }
   int sms = 0;
   const flce_status dev = check_device(&sms);

@@ -367,3 +367,20 @@ def test_reorder_autograd_sees_the_change(order):
             beam_reorder_(plain, parents)
     assert a.tolist() == [0, 1, 2, 3] and plain.tolist() == [0, 1, 2, 3]
     beam_reorder_([], parents)
+
+
+def test_reorder_states_that_interleave():
+    """Keys and values side by side in one buffer are two states; one of them twice is refused."""
+    g = torch.Generator("cuda").manual_seed(4)
+    both = torch.randn(6, 2, 4, 33, generator=g, device="cuda")
+    parents = torch.tensor([[1, 2, 0], [0, 0, 2]], device="cuda")
+    want = both[_rows(parents)]
+    was = both.clone()
+    with pytest.raises(RuntimeError, match="twice"):
+        beam_reorder_([both[:, 0], both[:, 1], both[:, 0]], parents)
+    assert torch.equal(both, was)
+    beam_reorder_([both[:, 0], both[:, 1]], parents)
+    assert torch.equal(both, want)
+    one = torch.arange(3, device="cuda")  # a single beam never moves
+    beam_reorder_([one, one], torch.zeros(3, 1, dtype=torch.int64, device="cuda"))
+    assert one.tolist() == [0, 1, 2]

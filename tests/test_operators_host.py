@@ -336,3 +336,35 @@ def test_softcap_without_a_reciprocal_is_refused():
     assert "softcap" in abi.flce_last_error()
     assert _qlinear(softcap=3e-39, ws_bytes=16) == WORKSPACE  # as far as the next check
     assert _qlinear(softcap=-1e-39, ws_bytes=16) == WORKSPACE  # no cap
+
+
+@pytest.mark.parametrize("count", [2, 5, 64, 65, 300])
+def test_reorder_refuses_a_state_that_is_listed_twice(count):
+    """Two states of one address share its byte: moved twice, in no order, they would be garbage.
+    Lists without such a pair get as far as the check of the last state, which is refused for
+    its own sake, so that no made-up address reaches a device."""
+    def call(addresses):
+        states = [(a, 1000, 1000) for a in addresses] + [(FAKE, 999, 1000)]
+        table = (abi.flce_beam_state * len(states))(*[
+            abi.flce_beam_state(a, stride, (ctypes.c_int64 * 4)(1, 1, 1, 1),
+                                (ctypes.c_int64 * 4)(0, 0, 0, 0), run)
+            for a, stride, run in states])
+        n = len(states) if addresses[0] != addresses[-1] else len(states) - 1
+        assert abi.flce_beam_reorder(ctypes.addressof(table), n, FAKE, 2, 3, None, None,
+                                     check=False) == INVALID
+        return abi.flce_last_error()
+
+    far = [0x100000 + 6000 * i for i in range(count)]
+    assert "elements overlap" in call(far)
+    assert "twice" in call(far[:-1] + far[:1])
+
+
+def test_reorder_empty_states_share_nothing():
+    """States without bytes may have any address; the last of these is refused for its own sake."""
+    states = [(FAKE, 0), (FAKE, 0), (FAKE, -1)]
+    table = (abi.flce_beam_state * 3)(*[
+        abi.flce_beam_state(a, 1000, (ctypes.c_int64 * 4)(1, 1, 1, 1),
+                            (ctypes.c_int64 * 4)(0, 0, 0, 0), run) for a, run in states])
+    assert abi.flce_beam_reorder(ctypes.addressof(table), 3, FAKE, 2, 3, None, None,
+                                 check=False) == INVALID
+    assert "run_bytes" in abi.flce_last_error()
