@@ -500,6 +500,62 @@ flce_status flce_qlinear(const flce_qproblem* p, const void* x, const float* x_s
                          void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
+ * The root-mean-square norm with the residual's addition, and its gradients.
+ *
+ *   s_ih  = x_ih + residual_ih                  (x_ih without a residual)
+ *   rstd_i = 1 / sqrt((1/h) sum_h s_ih^2 + eps)
+ *   y_ih  = s_ih * rstd_i * weight_h            (weight 1 without one)
+ *
+ * Everything is computed in fp32 (the sum of squares in fp64 where its fp32
+ * value leaves the range) from the unrounded s; y, q and sum_out are rounded
+ * once. The gradients, with unit = s * rstd taken from the stored sum and
+ * u = grad_y * weight:
+ *
+ *   grad_s = grad_sum + rstd * (u - unit * (1/h) sum_h u * unit)
+ *   grad_weight_h = sum_i grad_y_ih * unit_ih    (the same bits in every run)
+ *
+ * and grad_s is the gradient of x and of the residual. Rows of outputs and of
+ * grad_y and grad_sum lie h elements apart.
+ */
+typedef struct flce_norm_problem {
+  int64_t n, h;            /* n >= 0; 1 <= h <= 2^24 */
+  int64_t x_pitch;         /* elements between rows of x (backward: of total) */
+  int64_t residual_pitch;  /* of residual; at least h in any case */
+  int32_t dtype;           /* flce_dtype of x, y and grad_y */
+  int32_t sum_dtype;       /* of residual and sum: dtype or FLCE_F32 */
+  int32_t weight_dtype;    /* dtype or FLCE_F32 */
+  float eps;               /* finite, at least FLT_MIN */
+  int64_t reserved;        /* 0 */
+} flce_norm_problem;
+
+/* residual and sum_out go together (NULL without a residual). weight and
+ * rstd_out [n] may be NULL. Outputs share no memory with inputs. */
+flce_status flce_rms_norm(const flce_norm_problem* p, const void* x,
+                          const void* residual, const void* weight, void* y,
+                          void* sum_out, float* rstd_out, void* stream);
+
+/* The same with y in 8-bit integers, as flce_quantize_rows makes them of the
+ * unrounded y: q [n][h], rows q_pitch bytes apart, and scale [n]. */
+flce_status flce_rms_norm_quantize(const flce_norm_problem* p, const void* x,
+                                   const void* residual, const void* weight,
+                                   int8_t* q, int64_t q_pitch, float* scale,
+                                   void* sum_out, void* stream);
+
+/* Bytes of device workspace flce_rms_norm_backward() needs (0 if `p` is invalid). */
+size_t flce_rms_norm_backward_workspace_size(const flce_norm_problem* p);
+
+/* total: sum_out of the forward, or x where there was no residual (then of
+ * x's type: sum_dtype says which it is). grad_sum may be NULL (zeros), and any
+ * of the three results. grad_residual is written where sum_dtype is FLCE_F32;
+ * in one type it is grad_x. */
+flce_status flce_rms_norm_backward(const flce_norm_problem* p, const void* grad_y,
+                                   const void* grad_sum, const void* total,
+                                   const void* weight, const float* rstd,
+                                   void* grad_x, void* grad_residual,
+                                   void* grad_weight, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
  * Per-kernel timing, for measurement tools (not part of the method; the
  * pages describe no profiler). While enabled, every kernel launch made by
  * flce_forward / flce_backward on the calling process is bracketed by two

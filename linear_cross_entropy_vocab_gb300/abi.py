@@ -75,6 +75,10 @@ EXPORTS = (
     "flce_quantize_rows",
     "flce_qlinear_workspace_size",
     "flce_qlinear",
+    "flce_rms_norm",
+    "flce_rms_norm_quantize",
+    "flce_rms_norm_backward_workspace_size",
+    "flce_rms_norm_backward",
     "flce_selftest_wait_timeout",
     "flce_status_string",
     "flce_last_error",
@@ -183,6 +187,20 @@ class flce_qproblem(ctypes.Structure):  # noqa: N801  (C name)
     ]
 
 
+class flce_norm_problem(ctypes.Structure):  # noqa: N801  (C name)
+    _fields_ = [
+        ("n", ctypes.c_int64),
+        ("h", ctypes.c_int64),
+        ("x_pitch", ctypes.c_int64),
+        ("residual_pitch", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("sum_dtype", ctypes.c_int32),
+        ("weight_dtype", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+        ("reserved", ctypes.c_int64),
+    ]
+
+
 class flce_kernel_time(ctypes.Structure):  # noqa: N801  (C name)
     _fields_ = [
         ("name", ctypes.c_char * FLCE_PROFILE_NAME_LEN),
@@ -267,6 +285,16 @@ def load() -> ctypes.CDLL:
         lib.flce_qlinear.argtypes = [ctypes.POINTER(flce_qproblem)] + [_P] * 8 + [
             ctypes.c_size_t, _P]
         lib.flce_qlinear.restype = ctypes.c_int
+        lib.flce_rms_norm.argtypes = [ctypes.POINTER(flce_norm_problem)] + [_P] * 7
+        lib.flce_rms_norm.restype = ctypes.c_int
+        lib.flce_rms_norm_quantize.argtypes = [ctypes.POINTER(flce_norm_problem)] + [_P] * 4 + [
+            ctypes.c_int64, _P, _P, _P]
+        lib.flce_rms_norm_quantize.restype = ctypes.c_int
+        lib.flce_rms_norm_backward_workspace_size.argtypes = [ctypes.POINTER(flce_norm_problem)]
+        lib.flce_rms_norm_backward_workspace_size.restype = ctypes.c_size_t
+        lib.flce_rms_norm_backward.argtypes = [ctypes.POINTER(flce_norm_problem)] + [_P] * 9 + [
+            ctypes.c_size_t, _P]
+        lib.flce_rms_norm_backward.restype = ctypes.c_int
         lib.flce_selftest_wait_timeout.argtypes = [_P, _P, ctypes.c_double, _P]
         lib.flce_selftest_wait_timeout.restype = ctypes.c_int
         lib.flce_status_string.argtypes = [ctypes.c_int]
@@ -468,6 +496,36 @@ def flce_qlinear(p, x, x_scale, weight, weight_scale, bias, out, err_word, works
                              err_word, workspace, workspace_bytes, stream)
     if check:
         _check(st, "flce_qlinear")
+    return st
+
+
+def flce_rms_norm(p, x, residual, weight, y, sum_out, rstd_out, stream, check=True) -> int:
+    st = load().flce_rms_norm(ctypes.byref(p), x, residual, weight, y, sum_out, rstd_out, stream)
+    if check:
+        _check(st, "flce_rms_norm")
+    return st
+
+
+def flce_rms_norm_quantize(p, x, residual, weight, q, q_pitch, scale, sum_out, stream,
+                           check=True) -> int:
+    st = load().flce_rms_norm_quantize(ctypes.byref(p), x, residual, weight, q, q_pitch, scale,
+                                       sum_out, stream)
+    if check:
+        _check(st, "flce_rms_norm_quantize")
+    return st
+
+
+def flce_rms_norm_backward_workspace_size(p: flce_norm_problem) -> int:
+    return load().flce_rms_norm_backward_workspace_size(ctypes.byref(p))
+
+
+def flce_rms_norm_backward(p, grad_y, grad_sum, total, weight, rstd, grad_x, grad_residual,
+                           grad_weight, workspace, workspace_bytes, stream, check=True) -> int:
+    st = load().flce_rms_norm_backward(ctypes.byref(p), grad_y, grad_sum, total, weight, rstd,
+                                       grad_x, grad_residual, grad_weight, workspace,
+                                       workspace_bytes, stream)
+    if check:
+        _check(st, "flce_rms_norm_backward")
     return st
 
 

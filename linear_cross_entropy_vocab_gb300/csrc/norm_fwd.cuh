@@ -1,0 +1,190 @@
+// The forward kernel of the root-mean-square norm, with its output in the
+// input's type (kernels_norm.cu) or in 8-bit integers (kernels_norm_q.cu):
+//
+//   s = x + r,  y = s * w / sqrt(mean(s^2) + eps)
+//   scale = max|y| * (1/127),  q = round(y / scale)
+//
+// Bound by memory: one pass. A team of threads (a warp, or a CTA of 128 to 1024
+// threads) takes one row and keeps its sums in registers, in 32 bits and not
+// rounded, between the mean and the output; rows of more than 16384 values are
+// read a second time. The squares are summed in 32 bits over at most 32 values
+// a thread and then by a tree.
+#pragma once
+
+#include <cstdint>
+
+#include "int8_round.cuh"
+#include "norm_internal.h"
+#include "norm_rows.cuh"
+
+namespace flce {
+
+template <class T, bool QUANT, bool VEC, int TEAM, int VECS, int THREADS>
+__global__ void __launch_bounds__(THREADS) rms_norm_kernel(const NormParams p) {
+  static_assert(TEAM == 32 || TEAM == THREADS, "a team is a warp or the CTA");
+  using Cols = Columns<TEAM, VEC>;
+  constexpr int kWarps = THREADS / 32;
+  constexpr int kSweep = TEAM * VECS * 8;
+  __shared__ float sum_buf[kWarps];
+  __shared__ double wide_buf[kWarps];
+  __shared__ uint32_t max_buf[kWarps];
+  const int t = static_cast<int>(threadIdx.x) % TEAM;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (THREADS / TEAM) +
+                      static_cast<int>(threadIdx.x) / TEAM;
+  if (TEAM == 32 && row >= p.n) return;  // whole warps
+  const int64_t h = p.h;
+  const T* const x = static_cast<const T*>(p.x) + row * p.x_pitch;
+  float s[VECS][8];
+  auto load = [&](int64_t e0, bool keep) {
+#pragma unroll
+    for (int i = 0; i < VECS; ++i) Cols::load(x, Cols::first(e0, i, t), h, s[i]);
+    if (p.residual != nullptr) {
+      float r[VECS][8];
+#pragma unroll
+      for (int i = 0; i < VECS; ++i)
+        Cols::template load_either<T>(p.residual, row * p.residual_pitch, p.wide,
+                                      Cols::first(e0, i, t), h, r[i]);
+#pragma unroll
+      for (int i = 0; i < VECS; ++i) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[i][j] += r[i][j];
+        if (keep)
+          Cols::template store_either<T>(p.sum, row * h, p.wide, Cols::first(e0, i, t), h, s[i]);
+      }
+    }
+  };
+  float part = 0.0f;
+  for (int64_t e0 = 0; e0 < h; e0 += kSweep) {
+    load(e0, true);
+    float sweep = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VECS; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sweep = fmaf(s[i][j], s[i][j], sweep);
+    part += sweep;
+  }
+  const bool again = h > kSweep;  // the registers hold the last sweep alone
+  float square = team_all<TEAM>(part, sum_buf, SumOp{});
+  float rstd;
+  if (square < 3.0e38f && (square > 1.0e-24f || p.eps > 1.0e-24f)) {
+    rstd = __frsqrt_rn(__fdiv_rn(square, static_cast<float>(h)) + p.eps);
+  } else {
+    // squares that leave the 32-bit range, or are not finite: the same in 64 bits
+    double wide = 0.0;
+    for (int64_t e0 = 0; e0 < h; e0 += kSweep) {
+      if (again) load(e0, false);
+#pragma unroll
+      for (int i = 0; i < VECS; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) wide += static_cast<double>(s[i][j]) * s[i][j];
+    }
+    wide = team_all<TEAM>(wide, wide_buf, SumOp{});
+    rstd = static_cast<float>(1.0 / sqrt(wide / static_cast<double>(h) + p.eps));
+  }
+  if (p.rstd != nullptr && t == 0) p.rstd[row] = rstd;
+  // s becomes y in 32 bits
+  auto finish = [&](int64_t e0) {
+#pragma unroll
+    for (int i = 0; i < VECS; ++i) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[i][j] *= rstd;
+      if (p.weight != nullptr) {
+        float w[8];
+        Cols::template load_either<T>(p.weight, 0, p.weight_wide, Cols::first(e0, i, t), h, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[i][j] *= w[j];
+      }
+    }
+  };
+  if constexpr (!QUANT) {
+    for (int64_t e0 = 0; e0 < h; e0 += kSweep) {
+      if (again) load(e0, false);
+      finish(e0);
+#pragma unroll
+      for (int i = 0; i < VECS; ++i)
+        Cols::store(static_cast<T*>(p.y) + row * h, Cols::first(e0, i, t), h, s[i]);
+    }
+  } else {
+    uint32_t peak = 0;  // of the bits without the sign: NaN is above infinity
+    for (int64_t e0 = 0; e0 < h; e0 += kSweep) {
+      if (again) load(e0, false);
+      finish(e0);
+#pragma unroll
+      for (int i = 0; i < VECS; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          // columns past the end hold 0 * rstd, which is NaN where rstd is
+          const uint32_t bits = __float_as_uint(s[i][j]) & 0x7fffffffu;
+          peak = bits > peak ? bits : peak;
+        }
+    }
+    const float top = __uint_as_float(team_all<TEAM>(peak, max_buf, MaxOp{}));
+    const float scale = top < INFINITY ? top * (1.0f / 127.0f) : NAN;
+    const float inv = __fdiv_rn(1.0f, scale);
+    if (t == 0) p.scale[row] = scale;
+    int8_t* const q = p.q + row * p.q_pitch;
+    const bool qvec = (reinterpret_cast<uintptr_t>(q) & 7u) == 0;
+    for (int64_t e0 = 0; e0 < h; e0 += kSweep) {
+      if (again) {
+        load(e0, false);
+        finish(e0);
+      }
+#pragma unroll
+      for (int i = 0; i < VECS; ++i) {
+        const int64_t e = Cols::first(e0, i, t);
+        if (e >= h) continue;
+        round8(s[i], scale, inv);
+        if constexpr (VEC) {
+          put_bytes(q, e, h, qvec, s[i]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (e + j * TEAM < h)
+              q[e + j * TEAM] = static_cast<int8_t>(__float_as_uint(s[i][j]) & 0xffu);
+        }
+      }
+    }
+  }
+}
+
+template <class T, bool QUANT, bool VEC, int TEAM, int VECS, int THREADS = TEAM>
+cudaError_t launch_norm_team(const NormParams& p, cudaStream_t s) {
+  constexpr int64_t rows = THREADS / TEAM;  // of a CTA
+  const unsigned grid = static_cast<unsigned>((p.n + rows - 1) / rows);
+  rms_norm_kernel<T, QUANT, VEC, TEAM, VECS, THREADS><<<grid, THREADS, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+template <class T, bool QUANT, bool VEC>
+cudaError_t launch_norm_rows(const NormParams& p, cudaStream_t s) {
+  if (p.h <= 256) return launch_norm_team<T, QUANT, VEC, 32, 1, 128>(p, s);
+  if (p.h <= 1024) return launch_norm_team<T, QUANT, VEC, 32, 4, 128>(p, s);
+  if (p.h <= 2048) return launch_norm_team<T, QUANT, VEC, 128, 2>(p, s);
+  if (p.h <= 4096) return launch_norm_team<T, QUANT, VEC, 256, 2>(p, s);
+  if (p.h <= 8192) return launch_norm_team<T, QUANT, VEC, 512, 2>(p, s);
+  return launch_norm_team<T, QUANT, VEC, 1024, 2>(p, s);
+}
+
+// Whether every row of a tensor starts at a 16-byte boundary.
+inline bool rows_of_16(const void* p, int64_t pitch, int size) {
+  return p == nullptr || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && pitch * size % 16 == 0);
+}
+
+template <class T, bool QUANT>
+cudaError_t launch_norm_typed(const NormParams& p, cudaStream_t s) {
+  constexpr int e = sizeof(T);
+  const bool vec = p.h % 8 == 0 && rows_of_16(p.x, p.x_pitch, e) &&
+                   rows_of_16(p.residual, p.residual_pitch, p.wide ? 4 : e) &&
+                   rows_of_16(p.sum, p.h, p.wide ? 4 : e) && rows_of_16(p.weight, 0, e) &&
+                   rows_of_16(p.y, p.h, e);
+  return vec ? launch_norm_rows<T, QUANT, true>(p, s) : launch_norm_rows<T, QUANT, false>(p, s);
+}
+
+template <bool QUANT>
+cudaError_t launch_norm(const NormParams& p, int dtype, cudaStream_t s) {
+  if (dtype == FLCE_F32) return launch_norm_typed<float, QUANT>(p, s);
+  if (dtype == FLCE_BF16) return launch_norm_typed<__nv_bfloat16, QUANT>(p, s);
+  return launch_norm_typed<__half, QUANT>(p, s);
+}
+
+}  // namespace flce
