@@ -556,6 +556,44 @@ flce_status flce_rms_norm_backward(const flce_norm_problem* p, const void* grad_
                                    size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
+ * Orthogonalising matrices by Newton-Schulz products: what a matrix's singular
+ * values are is taken towards 1, its singular vectors stay.
+ *
+ *   x = src / (|src| + eps)                  |src|: root of the sum of squares
+ *   x = a x + (b (x x^T) + c (x x^T)^2) x    for each step's a, b, c
+ *
+ * (with x^T x on the other side for more rows than columns, which gives the
+ * same). The norm is held in fp64, sums in fp32; between the products x, x x^T
+ * and the polynomial are held in halves (11 bits) with a power-of-two scale of
+ * their own, so that the result is within about 1.5e-3 of itself, more where a
+ * few singular values are far above the others. A matrix that holds a NaN or
+ * an infinity gives NaN.
+ */
+typedef struct flce_ortho_problem {
+  int64_t batch;        /* matrices, at most 65535 */
+  int64_t rows, cols;   /* of each, at most 2^20 */
+  int64_t batch_stride; /* elements of src between matrices */
+  int64_t row_pitch;    /* and between rows, at least cols */
+  int32_t dtype;        /* flce_dtype of src */
+  int32_t out_dtype;    /* FLCE_BF16 or FLCE_F16 */
+  int32_t steps;        /* 1 to 64 */
+  float eps;            /* finite, at least FLT_MIN */
+  const float* coefficients; /* steps x (a, b, c), in host memory, read within the
+                                call; singular values stay in 1e-4 to 16 */
+  int64_t reserved;     /* 0 */
+} flce_ortho_problem;
+
+/* Bytes of device workspace flce_orthogonalize() needs (0 if `p` is invalid):
+ * about 4 bytes for each element of src and 4 for each of x x^T, with sides
+ * rounded up to 256. */
+size_t flce_orthogonalize_workspace_size(const flce_ortho_problem* p);
+
+/* out [batch][rows][cols], dense, sharing no memory with src. */
+flce_status flce_orthogonalize(const flce_ortho_problem* p, const void* src, void* out,
+                               int32_t* err_word, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
  * Per-kernel timing, for measurement tools (not part of the method; the
  * pages describe no profiler). While enabled, every kernel launch made by
  * flce_forward / flce_backward on the calling process is bracketed by two

@@ -79,6 +79,8 @@ EXPORTS = (
     "flce_rms_norm_quantize",
     "flce_rms_norm_backward_workspace_size",
     "flce_rms_norm_backward",
+    "flce_orthogonalize_workspace_size",
+    "flce_orthogonalize",
     "flce_selftest_wait_timeout",
     "flce_status_string",
     "flce_last_error",
@@ -201,6 +203,22 @@ class flce_norm_problem(ctypes.Structure):  # noqa: N801  (C name)
     ]
 
 
+class flce_ortho_problem(ctypes.Structure):  # noqa: N801  (C name)
+    _fields_ = [
+        ("batch", ctypes.c_int64),
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("batch_stride", ctypes.c_int64),
+        ("row_pitch", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32),
+        ("steps", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+        ("coefficients", ctypes.c_void_p),
+        ("reserved", ctypes.c_int64),
+    ]
+
+
 class flce_kernel_time(ctypes.Structure):  # noqa: N801  (C name)
     _fields_ = [
         ("name", ctypes.c_char * FLCE_PROFILE_NAME_LEN),
@@ -295,6 +313,11 @@ def load() -> ctypes.CDLL:
         lib.flce_rms_norm_backward.argtypes = [ctypes.POINTER(flce_norm_problem)] + [_P] * 9 + [
             ctypes.c_size_t, _P]
         lib.flce_rms_norm_backward.restype = ctypes.c_int
+        lib.flce_orthogonalize_workspace_size.argtypes = [ctypes.POINTER(flce_ortho_problem)]
+        lib.flce_orthogonalize_workspace_size.restype = ctypes.c_size_t
+        lib.flce_orthogonalize.argtypes = [ctypes.POINTER(flce_ortho_problem)] + [_P] * 4 + [
+            ctypes.c_size_t, _P]
+        lib.flce_orthogonalize.restype = ctypes.c_int
         lib.flce_selftest_wait_timeout.argtypes = [_P, _P, ctypes.c_double, _P]
         lib.flce_selftest_wait_timeout.restype = ctypes.c_int
         lib.flce_status_string.argtypes = [ctypes.c_int]
@@ -526,6 +549,20 @@ def flce_rms_norm_backward(p, grad_y, grad_sum, total, weight, rstd, grad_x, gra
                                        workspace_bytes, stream)
     if check:
         _check(st, "flce_rms_norm_backward")
+    return st
+
+
+def flce_orthogonalize_workspace_size(p: flce_ortho_problem) -> int:
+    return load().flce_orthogonalize_workspace_size(ctypes.byref(p))
+
+
+def flce_orthogonalize(p, src, out, err_word, workspace, workspace_bytes, stream,
+                       check=True) -> int:
+    """``p.coefficients`` is the address of 3 * steps floats in host memory."""
+    st = load().flce_orthogonalize(ctypes.byref(p), src, out, err_word, workspace,
+                                   workspace_bytes, stream)
+    if check:
+        _check(st, "flce_orthogonalize")
     return st
 
 

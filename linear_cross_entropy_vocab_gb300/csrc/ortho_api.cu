@@ -1,0 +1,291 @@
+// C entry points that orthogonalise matrices (include/flce.h): argument checks,
+// scales, workspace and launches. Nothing is allocated on the device and
+// nothing waits for it.
+#include <algorithm>
+#include <cfloat>
+#include <cmath>
+
+#include "flce.h"
+#include "host_common.h"
+#include "ortho_internal.h"
+
+namespace {
+
+using namespace flce::host;
+
+constexpr int64_t kMaxSide = 1 << 20;
+constexpr int64_t kMaxBatch = 65535;
+constexpr int64_t kMaxSteps = 64;
+
+bool float_type(int32_t d) { return d == FLCE_F32 || d == FLCE_BF16 || d == FLCE_F16; }
+size_t size_of(int32_t d) { return d == FLCE_F32 ? 4 : 2; }
+
+// The largest |a + b t + c t^2| for 0 <= t <= top.
+double poly_bound(double a, double b, double c, double top) {
+  double best = std::max(std::fabs(a), std::fabs(a + b * top + c * top * top));
+  const double t = c != 0.0 ? -b / (2.0 * c) : -1.0;
+  if (t > 0.0 && t < top) best = std::max(best, std::fabs(a + b * t + c * t * t));
+  return best;
+}
+// The largest |s (a + b s^2 + c s^4)| for 0 <= s <= top: at the end, or where
+// a + 3 b t + 5 c t^2 = 0 with t = s^2.
+double step_bound(double a, double b, double c, double top) {
+  const auto at = [&](double t) { return std::sqrt(t) * std::fabs(a + b * t + c * t * t); };
+  double best = at(top * top);
+  const auto root = [&](double t) {
+    if (t > 0.0 && t < top * top) best = std::max(best, at(t));
+  };
+  if (c != 0.0) {
+    const double d = 9.0 * b * b - 20.0 * a * c;
+    if (d >= 0.0) {
+      root((-3.0 * b + std::sqrt(d)) / (10.0 * c));
+      root((-3.0 * b - std::sqrt(d)) / (10.0 * c));
+    }
+  } else if (b != 0.0) {
+    root(-a / (3.0 * b));
+  }
+  return best;
+}
+
+// The power of two that takes values up to `bound` to at most 2^14: halves
+// reach 65504, and roundings add little to a bound.
+double scale_for(double bound) {
+  int e = 0;
+  std::frexp(bound, &e);  // bound < 2^e
+  return std::ldexp(1.0, 14 - std::max(e, -40));
+}
+
+flce_status check_problem(const flce_ortho_problem* p) {
+  if (p == nullptr) return fail(FLCE_ERR_INVALID_ARG, "problem is NULL");
+  if (p->batch < 0 || p->rows < 0 || p->cols < 0)
+    return fail(FLCE_ERR_INVALID_ARG, "batch = %lld, rows = %lld, cols = %lld",
+                (long long)p->batch, (long long)p->rows, (long long)p->cols);
+  if (p->batch > kMaxBatch || p->rows > kMaxSide || p->cols > kMaxSide)
+    return fail(FLCE_ERR_UNSUPPORTED, "at most %lld matrices of at most %lld rows and columns",
+                (long long)kMaxBatch, (long long)kMaxSide);
+  if (!float_type(p->dtype))
+    return fail(FLCE_ERR_INVALID_ARG, "dtype %d is not an flce_dtype", p->dtype);
+  if (p->out_dtype != FLCE_BF16 && p->out_dtype != FLCE_F16)
+    return fail(FLCE_ERR_INVALID_ARG, "out_dtype must be FLCE_BF16 or FLCE_F16");
+  if (p->row_pitch < p->cols || p->batch_stride < 0 || p->row_pitch > (int64_t(1) << 40) ||
+      p->batch_stride > (int64_t(1) << 46))
+    return fail(FLCE_ERR_INVALID_ARG, "row_pitch = %lld, batch_stride = %lld",
+                (long long)p->row_pitch, (long long)p->batch_stride);
+  if (!(p->eps >= FLT_MIN) || !std::isfinite(p->eps))
+    return fail(FLCE_ERR_INVALID_ARG, "eps must be finite and at least %g", (double)FLT_MIN);
+  if (p->steps < 1 || p->steps > kMaxSteps || p->coefficients == nullptr)
+    return fail(FLCE_ERR_INVALID_ARG, "1 to %lld steps, with coefficients for each",
+                (long long)kMaxSteps);
+  double bound = 1.0;  // of the singular values before each step
+  for (int k = 0; k < p->steps; ++k) {
+    const float* const abc = p->coefficients + 3 * k;
+    const double poly = poly_bound(abc[0], abc[1], abc[2], bound * bound);
+    bound = step_bound(abc[0], abc[1], abc[2], bound);
+    if (!(poly <= 1.0e4) || !(bound <= 16.0) || !(bound >= 1.0e-4))
+      return fail(FLCE_ERR_UNSUPPORTED,
+                  "the coefficients of step %d take singular values up to %g", k, bound);
+  }
+  if (p->reserved != 0) return fail(FLCE_ERR_INVALID_ARG, "reserved is not 0");
+  return FLCE_OK;
+}
+
+struct Plan {
+  int64_t m, n, m_pad, n_pad, parts;
+  size_t x[2], gram, poly, partial, factor, total;
+};
+Plan plan_of(const flce_ortho_problem* p) {
+  Plan q{};
+  q.m = std::min(p->rows, p->cols);
+  q.n = std::max(p->rows, p->cols);
+  q.m_pad = ceil_div(q.m, flce::kOrthoTile) * flce::kOrthoTile;
+  q.n_pad = ceil_div(q.n, 64) * 64;
+  // shares of at least 8192 values
+  q.parts = std::max<int64_t>(1, std::min<int64_t>(256, q.m * q.n / 8192));
+  const size_t b = static_cast<size_t>(p->batch);
+  const size_t x_bytes = align_256(b * static_cast<size_t>(q.m_pad * q.n_pad) * 2);
+  const size_t g_bytes = align_256(b * static_cast<size_t>(q.m_pad * q.m_pad) * 2);
+  q.x[0] = 0;
+  q.x[1] = x_bytes;
+  q.gram = q.x[1] + (p->steps > 1 ? x_bytes : 0);
+  q.poly = q.gram + g_bytes;
+  q.partial = q.poly + g_bytes;
+  q.factor = q.partial + align_256(b * static_cast<size_t>(q.parts) * 8);
+  q.total = q.factor + align_256(b * 4);
+  return q;
+}
+
+bool make_map(CUtensorMap* map, const void* base, int64_t inner, int64_t outer,
+              uint32_t box_inner, uint32_t box_outer, bool swizzle) {
+  const EncodeTiledFn enc = tensor_map_encoder();
+  if (enc == nullptr) {
+    fail(FLCE_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    return false;
+  }
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(inner) * 2};
+  const cuuint32_t box[2] = {box_inner, box_outer};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r =
+      enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(base), dims, strides, box,
+          estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+          swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    fail(FLCE_ERR_CUDA, "cuTensorMapEncodeTiled failed with CUresult %d (%lld x %lld)",
+         static_cast<int>(r), (long long)inner, (long long)outer);
+    return false;
+  }
+  return true;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t flce_orthogonalize_workspace_size(const flce_ortho_problem* p) {
+  if (check_problem(p) != FLCE_OK) return 0;
+  return plan_of(p).total;
+}
+
+flce_status flce_orthogonalize(const flce_ortho_problem* p, const void* src, void* out,
+                               int32_t* err_word, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+  clear_error();
+  flce_status st = check_problem(p);
+  if (st != FLCE_OK) return st;
+  const bool empty = p->batch == 0 || p->rows == 0 || p->cols == 0;
+  if (!empty && (src == nullptr || out == nullptr))
+    return fail(FLCE_ERR_INVALID_ARG, "src and out are required");
+  if (!aligned_to(src, size_of(p->dtype)) || !aligned_to(out, 2) || !aligned_to(err_word, 4))
+    return fail(FLCE_ERR_UNSUPPORTED, "a pointer is misaligned for its type");
+  const Plan plan = plan_of(p);
+  // coordinates and tile numbers are 32-bit
+  if (p->batch * plan.m_pad > (int64_t(1) << 30) ||
+      p->batch * ceil_div(plan.n, 256) * (plan.m_pad / 256) > (int64_t(1) << 30))
+    return fail(FLCE_ERR_UNSUPPORTED, "the batch has too many rows");
+  st = check_workspace(workspace, workspace_bytes, plan.total);
+  if (st != FLCE_OK) return st;
+  int sms = 0;
+  st = check_device(&sms);
+  if (st != FLCE_OK || empty) return st;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint8_t* const ws = static_cast<uint8_t*>(workspace);
+  const bool tall = p->rows > p->cols;
+
+  double bound = 1.0;
+  double x_scale = scale_for(bound);
+  flce::OrthoCopyParams c{};
+  c.src = src;
+  c.batch_stride = p->batch_stride;
+  c.row_pitch = p->row_pitch;
+  c.batch = static_cast<int32_t>(p->batch);
+  c.rows = static_cast<int32_t>(p->rows);
+  c.cols = static_cast<int32_t>(p->cols);
+  c.tall = tall ? 1 : 0;
+  c.m = static_cast<int32_t>(plan.m);
+  c.n = static_cast<int32_t>(plan.n);
+  c.m_pad = static_cast<int32_t>(plan.m_pad);
+  c.n_pad = static_cast<int32_t>(plan.n_pad);
+  c.x = ws + plan.x[0];
+  c.partial = reinterpret_cast<double*>(ws + plan.partial);
+  c.parts = static_cast<int32_t>(plan.parts);
+  c.eps = p->eps;
+  c.x_scale = static_cast<float>(x_scale);
+  c.factor = reinterpret_cast<float*>(ws + plan.factor);
+  cudaError_t e = flce::launch_ortho_norm(c, p->dtype, s);
+  if (e != cudaSuccess) return cuda_fail(e, "matrix norm kernel");
+  e = flce::launch_ortho_copy(c, p->dtype, s);
+  if (e != cudaSuccess) return cuda_fail(e, "matrix copy kernel");
+
+  // the maps of both copies, the gram and the polynomial
+  const int64_t x_rows = p->batch * plan.m_pad;
+  CUtensorMap x_along[2], x_across[2], x_store[2], g_along, g_store, p_along, p_store;
+  const int copies = p->steps > 1 ? 2 : 1;
+  for (int i = 0; i < copies; ++i) {
+    uint8_t* const x = ws + plan.x[i];
+    if (!make_map(&x_along[i], x, plan.n_pad, x_rows, 64, 128, true) ||
+        !make_map(&x_across[i], x, plan.n_pad, x_rows, 64, 64, true) ||
+        !make_map(&x_store[i], x, plan.n_pad, x_rows, 32, 32, false))
+      return FLCE_ERR_CUDA;
+  }
+  if (!make_map(&g_along, ws + plan.gram, plan.m_pad, x_rows, 64, 128, true) ||
+      !make_map(&g_store, ws + plan.gram, plan.m_pad, x_rows, 32, 32, false) ||
+      !make_map(&p_along, ws + plan.poly, plan.m_pad, x_rows, 64, 128, true) ||
+      !make_map(&p_store, ws + plan.poly, plan.m_pad, x_rows, 32, 32, false))
+    return FLCE_ERR_CUDA;
+
+  const int32_t m_tiles = static_cast<int32_t>(plan.m_pad / flce::kOrthoTile);
+  const int32_t n_tiles = static_cast<int32_t>(ceil_div(plan.n, flce::kOrthoTile));
+  const int32_t m_pad = static_cast<int32_t>(plan.m_pad);
+  for (int k = 0; k < p->steps; ++k) {
+    const float* const abc = p->coefficients + 3 * k;
+    const double g_scale = scale_for(bound * bound);
+    const double p_scale = scale_for(poly_bound(abc[0], abc[1], abc[2], bound * bound));
+    bound = step_bound(abc[0], abc[1], abc[2], bound) * (1.0 + 1.0 / 64);
+    const double next_scale = scale_for(bound);
+    const int from = k & 1;
+    const bool last = k + 1 == p->steps;
+    flce::OrthoGemmParams g{};
+    g.batch = static_cast<int32_t>(p->batch);
+    g.m_pad = m_pad;
+    g.a_stride = g.b_stride = m_pad;
+    g.err_word = err_word;
+    // the norm's factor belongs to the first step's x
+    const float* const factor = k == 0 ? c.factor : nullptr;
+
+    g.a_map = g.b_map = x_along[from];
+    g.c_map = g_store;
+    g.m_tiles = g.n_tiles = m_tiles;
+    g.cols = m_pad;
+    g.k_iters = static_cast<int32_t>(plan.n_pad / 64);
+    g.acc_scale = static_cast<float>(g_scale / (x_scale * x_scale));
+    g.factor = factor;
+    g.factor_square = 1;
+    e = flce::launch_ortho_gemm(g, flce::OrthoOp::kGram, 0, sms, s);
+    if (e != cudaSuccess) return cuda_fail(e, "gram kernel");
+
+    g.a_map = g.b_map = g_along;
+    g.c_map = p_store;
+    g.k_iters = static_cast<int32_t>(ceil_div(plan.m, 64));
+    g.acc_scale = static_cast<float>(abc[2] * p_scale / (g_scale * g_scale));
+    g.factor = nullptr;
+    g.old = ws + plan.gram;
+    g.old_scale = static_cast<float>(abc[1] * p_scale / g_scale);
+    g.diag = static_cast<float>(abc[0] * p_scale);
+    e = flce::launch_ortho_gemm(g, flce::OrthoOp::kPoly, 0, sms, s);
+    if (e != cudaSuccess) return cuda_fail(e, "polynomial kernel");
+
+    g.factor = factor;
+    g.factor_square = 0;
+    if (last && tall) {
+      g.a_map = x_across[from];
+      g.b_map = p_along;
+      g.m_tiles = n_tiles;
+      g.n_tiles = m_tiles;
+    } else {
+      g.a_map = p_along;
+      g.b_map = x_across[from];
+      g.m_tiles = m_tiles;
+      g.n_tiles = n_tiles;
+    }
+    if (last) {
+      g.acc_scale = static_cast<float>(1.0 / (x_scale * p_scale));
+      g.out = out;
+      g.rows = c.rows;
+      g.cols = c.cols;
+    } else {
+      g.acc_scale = static_cast<float>(next_scale / (x_scale * p_scale));
+      g.c_map = x_store[1 - from];
+      g.cols = c.n_pad;
+    }
+    const flce::OrthoOp op = !last ? flce::OrthoOp::kMul
+                             : tall ? flce::OrthoOp::kOutTall
+                                    : flce::OrthoOp::kOutWide;
+    e = flce::launch_ortho_gemm(g, op, p->out_dtype, sms, s);
+    if (e != cudaSuccess) return cuda_fail(e, "product kernel");
+    x_scale = next_scale;
+  }
+  return FLCE_OK;
+}
+
+}  // extern "C"

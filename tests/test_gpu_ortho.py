@@ -1,0 +1,231 @@
+"""Orthogonalised matrices against the steps in 64 bits.
+
+Tolerance, to first order in the roundings, all in the 2-norm over the entries. A step maps
+singular values by f(s) = s (a + b s^2 + c s^4); a perturbation of x grows by at most
+D = max |f'(s)| over the range [0, top] of the values. The copy, the gram A, the polynomial p and
+the new x are rounded to halves, by 2^-11 of each entry at most: A's rounding enters p by at most
+|b| + 2 |c| top^2 and then x by top, p's enters x by top. Sums of k products in 32 bits add
+k / 16 * 2^-23, and what halves cannot hold (2^-25 over the scale, which is 2^8 at least) is
+added. The result is rounded once more. Single entries are held to 16 times the mean of that
+bound, which is a sixth of an entry and less.
+"""
+import math
+
+import pytest
+import torch
+
+from linear_cross_entropy_vocab_gb300 import (clip_grads_, fused_linear_cross_entropy,
+                                              orthogonalize, rms_norm)
+from linear_cross_entropy_vocab_gb300.abi import FlceError
+from linear_cross_entropy_vocab_gb300.ortho import NEWTON_SCHULZ
+
+pytestmark = pytest.mark.gpu
+TYPES = [torch.float32, torch.bfloat16, torch.float16]
+
+
+def _steps64(g, coefficients, eps, out_dtype):
+    """(result, bound on the 2-norm of the result's error) for one matrix."""
+    g = g.double()
+    x = g / (torch.linalg.matrix_norm(g) + eps)
+    if x.shape[0] > x.shape[1]:
+        x = x.t()
+    m, n = x.shape
+    half = 2.0 ** -11 + n / 16 * 2.0 ** -23
+    floor = 2.0 ** -33 * math.sqrt(m * n)
+    delta, top = half * float(x.norm()) + floor, 1.0
+    for k, (a, b, c) in enumerate(coefficients):
+        s = torch.linspace(0, top, 4001, dtype=torch.float64)
+        grow = float((a + 3 * b * s ** 2 + 5 * c * s ** 4).abs().max())
+        top_now = top
+        top = float((s * (a + b * s ** 2 + c * s ** 4)).abs().max()) * 1.02
+        gram = x @ x.t()
+        p = a * torch.eye(m, dtype=torch.float64, device=x.device) + b * gram + c * (gram @ gram)
+        x = p @ x
+        local = top_now * (abs(b) + 2 * abs(c) * top_now ** 2) * (half * float(gram.norm()) + floor)
+        local += top_now * (half * float(p.norm()) + floor)
+        delta = grow * delta + local
+        if k + 1 < len(coefficients):
+            delta += half * float(x.norm()) + floor
+    delta += torch.finfo(out_dtype).eps / 2 * float(x.norm()) + floor
+    return (x if x.shape == g.shape else x.t()), delta
+
+
+def _check(got, g, coefficients=NEWTON_SCHULZ, eps=1e-7):
+    want, delta = _steps64(g, coefficients, eps, got.dtype)
+    if want.shape != got.shape:
+        want = want.t()
+    err = got.double() - want
+    assert float(err.norm()) <= delta, (float(err.norm()), delta, float(want.norm()))
+    assert float(err.abs().max()) <= 16 * delta / math.sqrt(want.numel())
+
+
+def _matrices(batch, m, n, dtype, seed=0, scale=1e-3):
+    g = torch.Generator("cuda").manual_seed(seed + 7 * m + n)
+    return (torch.randn(batch, m, n, generator=g, device="cuda") * scale).to(dtype)
+
+
+SIZES = [(1, 1, 1), (1, 1, 9), (2, 5, 3), (1, 64, 64), (3, 100, 300), (1, 300, 100), (2, 256, 256),
+         (1, 257, 511), (1, 130, 1000), (2, 513, 700), (1, 1000, 260), (5, 96, 64), (1, 1024, 600),
+         (1, 64, 5000), (1, 3000, 33), (40, 16, 200), (1, 770, 1300)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("batch,m,n", SIZES)
+def test_against_64_bits(batch, m, n, dtype):
+    x = _matrices(batch, m, n, dtype)
+    got = orthogonalize(x)
+    assert got.shape == x.shape and got.is_contiguous()
+    assert got.dtype == (torch.bfloat16 if dtype == torch.float32 else dtype)
+    for i in range(batch):
+        _check(got[i], x[i])
+        # matrices of a batch do not meet
+        if i in (0, batch - 1):
+            assert torch.equal(got[i], orthogonalize(x[i]))
+    assert torch.equal(got, orthogonalize(x))
+    other = torch.float16 if got.dtype == torch.bfloat16 else torch.bfloat16
+    got = orthogonalize(x, out_dtype=other)
+    assert got.dtype == other
+    _check(got[0], x[0])
+
+
+@pytest.mark.parametrize("m,n", [(70, 200), (300, 128), (257, 300)])
+def test_other_steps(m, n):
+    x = _matrices(1, m, n, torch.float32)
+    for coefficients in (((3.4445, -4.7750, 2.0315),), ((1.5, -0.5, 0.0),) * 2,
+                         ((2.0, -1.5, 0.5), (1.5, -0.5, 0.0), (1.875, -1.25, 0.375)),
+                         ((0.01, 0.0, 0.0),), ((15.0, -20.0, 8.0), (0.5, 0.0, 0.001))):
+        got = orthogonalize(x[0], coefficients=coefficients, eps=1e-3)
+        _check(got, x[0], coefficients, 1e-3)
+    # the first step's values reach 5.4, the second would take them to 45
+    with pytest.raises(FlceError, match="singular values"):
+        orthogonalize(x[0], coefficients=((15.0, -20.0, 8.0), (0.5, 0.0, 0.01)))
+    # many steps end at an orthogonal matrix: singular values at 1, to the rounding of their place
+    got = orthogonalize(x[0], coefficients=((1.5, -0.5, 0.0),) * 40, out_dtype=torch.float16)
+    values = torch.linalg.svdvals(got.double())
+    assert float((values - 1).abs().max()) < 2e-2
+
+
+def test_addresses_and_strides():
+    base = _matrices(6, 130, 400, torch.bfloat16)
+    views = [base[:, :, 1:301], base[1::2], base[:, ::3], base[:, :100, 8:308], base.transpose(1, 2),
+             base[0], base[0, :, 1:200], base.view(2, 3, 130, 400), base[:1].expand(3, 130, 400),
+             base[:, :1], base[:, :, :1], base.permute(1, 0, 2)]
+    for x in views:
+        got = orthogonalize(x)
+        assert got.shape == x.shape
+        flat, gots = x.reshape(-1, *x.shape[-2:]), got.view(-1, *x.shape[-2:])
+        for i in range(min(2, len(flat))):
+            _check(gots[i], flat[i])
+        assert torch.equal(got, orthogonalize(x.contiguous()))
+    for shape in ((0, 5, 6), (3, 0, 6), (3, 6, 0), (2, 0, 4, 4)):
+        assert orthogonalize(torch.empty(shape, device="cuda")).shape == shape
+
+
+def test_what_surrounds_the_result_stays():
+    """Sizes that end inside a tile: nothing is written past the result."""
+    for m, n in ((100, 300), (300, 100), (33, 257)):
+        x = _matrices(2, m, n, torch.bfloat16)
+        want = orthogonalize(x)
+        import linear_cross_entropy_vocab_gb300.ortho as ortho
+        room = torch.full((2 * m * n + 4096,), 7.0, dtype=torch.bfloat16, device="cuda")
+        empty = torch.empty
+
+        def placed(*a, **k):
+            if a and tuple(a[0]) == (2, m, n) if isinstance(a[0], (tuple, torch.Size)) else False:
+                return room[2048:2048 + 2 * m * n].view(2, m, n)
+            return empty(*a, **k)
+
+        try:
+            ortho.torch.empty = placed
+            got = orthogonalize(x)
+        finally:
+            ortho.torch.empty = empty
+        assert torch.equal(got, want) and got.data_ptr() == room[2048:].data_ptr()
+        assert bool((room[:2048] == 7).all()) and bool((room[2048 + 2 * m * n:] == 7).all())
+
+
+def test_extremes():
+    x = _matrices(9, 90, 200, torch.float32, scale=1.0)
+    x[0] = 0
+    x[1] *= 1e36
+    x[2] *= 1e-36
+    x[3, 5, 7] = math.nan
+    x[4, 0, 0] = math.inf
+    x[5] = 0
+    x[5, 3, 4] = -2.0
+    x[6, 1:] = 0
+    x[7] *= 1e-3
+    x[7, 0, 0] = 1e30
+    got = orthogonalize(x)
+    assert not bool(got[0].any())
+    for i in (1, 2, 5, 6, 8):
+        _check(got[i], x[i])
+    assert bool(got[3].isnan().all()) and bool(got[4].isnan().all())
+    assert bool(got[7].isfinite().all()) and abs(float(got[7, 0, 0])) > 0.6
+    # an eps beside the norm
+    got = orthogonalize(x[8:] * 1e-6, eps=1e-4)
+    _check(got[0], x[8] * 1e-6, eps=1e-4)
+    # numbers that halves cannot hold well
+    tiny = _matrices(1, 64, 64, torch.float16, scale=1e-6)
+    _check(orthogonalize(tiny)[0], tiny[0])
+
+
+def test_streams_and_graphs():
+    x = _matrices(2, 300, 520, torch.bfloat16)
+    want = orthogonalize(x)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = orthogonalize(x)
+    other = orthogonalize(x.transpose(1, 2))
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(got, want)
+    graphs, outs, ins = [], [], []
+    for i in range(2):
+        ins.append(x.clone())
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i]):
+            outs.append(orthogonalize(ins[i] if i == 0 else ins[i].transpose(1, 2)))
+    for seed in (3, 4):
+        nx = _matrices(2, 300, 520, torch.bfloat16, seed)
+        for i in range(2):
+            ins[i].copy_(nx)
+            graphs[i].replay()
+        assert torch.equal(outs[0], orthogonalize(nx))
+        assert torch.equal(outs[1], orthogonalize(nx.transpose(1, 2)))
+    assert torch.equal(other, orthogonalize(x.transpose(1, 2)))
+
+
+def test_a_training_step():
+    """Norm, head, clip and update as a training step has them, against the same in 64 bits."""
+    g = torch.Generator("cuda").manual_seed(3)
+    n, h, v = 200, 128, 1000
+
+    def rand(*shape, std=1.0):
+        return (torch.randn(*shape, generator=g, device="cuda") * std).bfloat16()
+
+    x, r, w = rand(n, h), rand(n, h), 1 + rand(h, std=0.1)
+    mix, head = rand(h, h, std=h ** -0.5), rand(v, h, std=h ** -0.5)
+    targets = torch.randint(0, v, (n,), generator=g, device="cuda")
+    leaves = [t.clone().requires_grad_() for t in (mix, head, w)]
+    y, _ = rms_norm(x @ leaves[0].t(), leaves[2], residual=r)
+    fused_linear_cross_entropy(y, leaves[1], targets).backward()
+    ref = [t.double().requires_grad_() for t in (mix, head, w)]
+    s = (x @ mix.t()).double() + r.double()  # the product as it was rounded, with its gradient
+    s = s + x.double() @ ref[0].t() - (x.double() @ ref[0].t()).detach()
+    yy = s / torch.sqrt((s * s).mean(1, keepdim=True) + 1e-6) * ref[2]
+    torch.nn.functional.cross_entropy(yy @ ref[1].t(), targets).backward()
+    for a, b in zip(leaves, ref):
+        # bf16 on the way: y, the gradients of the logits and of y, and the product's
+        assert float((a.grad.double() - b.grad).norm()) <= 4 * 2.0 ** -8 * float(b.grad.norm())
+    clip_grads_([t.grad for t in leaves], 1e-3)
+    update = orthogonalize(leaves[0].grad)
+    _check(update, leaves[0].grad)
+
+
+def test_refusals_of_gradients():
+    x = _matrices(1, 20, 30, torch.float32)[0].requires_grad_()
+    with pytest.raises(RuntimeError, match="no gradient"):
+        orthogonalize(x)
+    with torch.no_grad():
+        orthogonalize(x)
