@@ -20,7 +20,9 @@
 // 1.5e-3 of itself, where bf16 operands give 1e-2; sums are held in 32 bits.
 // The norm's factor is applied to the first step's products, in 32 bits: a
 // 16-bit input is copied without rounding.
+#include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -34,39 +36,48 @@ namespace {
 
 // ------------------------------------------------------------ norm and copy
 
-// Sums of squares of a share of a matrix's rows: 32 values in 32 bits, those
-// sums in 64, and again in 64 where a sum leaves the 32-bit range.
+// Sums of squares of a share of a matrix. Rows are read in spans of 8192
+// values, in aligned 16-byte pieces wherever a row starts (a dense matrix is
+// one long row); 32 values are summed in 32 bits, those sums in 64, and again
+// in 64 where one leaves the 32-bit range.
 template <class T>
 __global__ void __launch_bounds__(256) ortho_norm_kernel(const OrthoCopyParams p) {
   __shared__ double buf[8];
   grid_launch_dependents();
   const T* const src = static_cast<const T*>(p.src) + blockIdx.y * p.batch_stride;
-  // a share is a range of whole pieces of 32 columns x 256 threads
-  const int64_t pieces_row = (p.cols + 31) / 32;
-  const int64_t pieces = pieces_row * p.rows;
+  const bool dense = p.row_pitch == p.cols;
+  const int64_t rows = dense ? 1 : p.rows;
+  const int64_t len = dense ? int64_t(p.rows) * p.cols : p.cols;
+  const int64_t spans_row = (len + 8191 + 8) / 8192;  // a row may start 7 values into its first
   double total = 0.0;
-  for (int64_t i = blockIdx.x * int64_t(8) + (threadIdx.x >> 5); i * 32 < pieces;
-       i += int64_t(gridDim.x) * 8) {
-    // the warp's 32 pieces follow one another; its lanes read them side by side
-    float sum = 0.0f;
-    double wide = 0.0;
-    float v[32];
+  for (int64_t i = blockIdx.x; i < rows * spans_row; i += gridDim.x) {
+    const int64_t r = i / spans_row;
+    const T* const row = src + r * p.row_pitch;
+    const int phase = static_cast<int>(reinterpret_cast<uintptr_t>(row) / sizeof(T)) & 7;
+    const int64_t at = (i - r * spans_row) * 8192 - phase + threadIdx.x * 8;
+    float v[4][8];
 #pragma unroll
-    for (int k = 0; k < 32; ++k) {
-      const int64_t piece = i * 32 + k;
-      v[k] = 0.0f;
-      if (piece < pieces) {
-        const int64_t r = piece / pieces_row, c = (piece - r * pieces_row) * 32 + (threadIdx.x & 31);
-        if (c < p.cols) v[k] = to_f32(src[r * p.row_pitch + c]);
+    for (int k = 0; k < 4; ++k) {
+      const int64_t e = at + k * 2048;
+      if (e >= 0 && e + 8 <= len) {
+        load8(row + e, v[k]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[k][j] = e + j >= 0 && e + j < len ? to_f32(row[e + j]) : 0.0f;
       }
     }
+    float sum = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 32; ++k) sum = fmaf(v[k], v[k], sum);
-    wide = sum;
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum = fmaf(v[k][j], v[k][j], sum);
+    double wide = sum;
     if (!(sum < 3.0e38f && sum > 1.0e-30f)) {
       wide = 0.0;
 #pragma unroll
-      for (int k = 0; k < 32; ++k) wide += static_cast<double>(v[k]) * v[k];
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) wide += static_cast<double>(v[k][j]) * v[k][j];
     }
     total += wide;
   }
@@ -74,15 +85,21 @@ __global__ void __launch_bounds__(256) ortho_norm_kernel(const OrthoCopyParams p
   if (threadIdx.x == 0) p.partial[int64_t(blockIdx.y) * p.parts + blockIdx.x] = total;
 }
 
-// Halves of a 64 x 64 part of the padded matrix, through shared memory where it
-// is transposed.
+// Where the halves of row i from column 8 * c on lie in a 64 x 64 part in
+// shared memory: 16-byte pieces are swapped so that neither rows nor columns of
+// pieces meet in a bank.
+__device__ __forceinline__ int piece_at(int i, int c) { return i * 64 + ((c ^ (i >> 3)) & 7) * 8; }
+
+// Halves of the padded matrix, 64 x 64 at a time. The transpose of a tall
+// matrix, and rows that do not start at 16-byte boundaries, go through shared
+// memory.
 template <class T>
 __global__ void __launch_bounds__(256) ortho_copy_kernel(const OrthoCopyParams p) {
-  __shared__ __half part[64][66];
+  __shared__ __align__(16) __half part[64 * 64];
   __shared__ double buf[8];
   grid_launch_dependents();
   grid_dependency_wait();
-  const int b = blockIdx.z;
+  const int b = blockIdx.y;
   const double* const partial = p.partial + int64_t(b) * p.parts;
   double sum = 0.0;
   for (int i = threadIdx.x; i < p.parts; i += 256) sum += partial[i];
@@ -96,36 +113,72 @@ __global__ void __launch_bounds__(256) ortho_copy_kernel(const OrthoCopyParams p
     e = ilogb(norm);
     factor = static_cast<float>(scalbn(1.0 / norm, e));
   }
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) p.factor[b] = factor;
-  const int shift = -e;
+  if (blockIdx.x == 0 && threadIdx.x == 0) p.factor[b] = factor;
+  // the power of two in two factors, as one could leave the 32-bit range
+  const int shift = p.x_shift - e;
+  const float scale0 = scalbnf(1.0f, shift / 2), scale1 = scalbnf(1.0f, shift - shift / 2);
+  auto half_of = [&](float v) { return __float2half_rn(v * scale0 * scale1); };
+  auto halves_of = [&](const float(&v)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __half2 h = __floats2half2_rn(v[2 * i] * scale0 * scale1,
+                                          v[2 * i + 1] * scale0 * scale1);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  };
   const T* const src = static_cast<const T*>(p.src) + b * p.batch_stride;
   __half* const x = static_cast<__half*>(p.x) + int64_t(b) * p.m_pad * p.n_pad;
-  const int i0 = blockIdx.y * 64, j0 = blockIdx.x * 64;  // of x
-  auto half_of = [&](float v) {
-    return __float2half_rn(scalbnf(v, shift) * p.x_scale);
-  };
-  const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
-  if (p.tall) {
+  const bool aligned = reinterpret_cast<uintptr_t>(src) % 16 == 0 &&
+                       p.row_pitch * static_cast<int64_t>(sizeof(T)) % 16 == 0;
+  const int r8 = threadIdx.x >> 3, c8 = threadIdx.x & 7;
+  const int tiles_n = p.n_pad / 64, tiles = tiles_n * (p.m_rows / 64);
+  for (int u = blockIdx.x; u < tiles; u += gridDim.x) {
+    const int i0 = u / tiles_n * 64, j0 = u % tiles_n * 64;  // of x
+    const int s0 = p.tall ? j0 : i0, t0 = p.tall ? i0 : j0;  // of src
+    if (!p.tall && aligned && t0 + 64 <= p.cols) {
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const int r = j0 + ty + 4 * k, c = i0 + tx;  // of src
-      part[tx][ty + 4 * k] = r < p.rows && c < p.cols
-                                 ? half_of(to_f32(src[int64_t(r) * p.row_pitch + c]))
-                                 : __half(0.0f);
+      for (int k = 0; k < 2; ++k) {
+        const int r = s0 + r8 + 32 * k, c = t0 + c8 * 8;
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (r < p.rows) {
+          float v[8];
+          load8(src + int64_t(r) * p.row_pitch + c, v);
+          w = halves_of(v);
+        }
+        *reinterpret_cast<uint4*>(x + int64_t(r) * p.n_pad + c) = w;
+      }
+      continue;
+    }
+    __syncthreads();  // the last part has been taken
+    if (aligned && t0 + 64 <= p.cols) {  // tall
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int dr = r8 + 32 * k, r = s0 + dr;
+        float v[8] = {};
+        if (r < p.rows) load8(src + int64_t(r) * p.row_pitch + t0 + c8 * 8, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) part[piece_at(c8 * 8 + j, dr >> 3) + (dr & 7)] = half_of(v[j]);
+      }
+    } else {
+      const int dc = threadIdx.x & 63, c = t0 + dc;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const int dr = (threadIdx.x >> 6) + 4 * k, r = s0 + dr;
+        const __half v = r < p.rows && c < p.cols
+                             ? half_of(to_f32(src[int64_t(r) * p.row_pitch + c]))
+                             : __half(0.0f);
+        const int i = p.tall ? dc : dr, j = p.tall ? dr : dc;
+        part[piece_at(i, j >> 3) + (j & 7)] = v;
+      }
     }
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const int i = i0 + ty + 4 * k, j = j0 + tx;
-      x[int64_t(i) * p.n_pad + j] = part[ty + 4 * k][tx];
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const int i = i0 + ty + 4 * k, j = j0 + tx;
-      x[int64_t(i) * p.n_pad + j] = i < p.rows && j < p.cols
-                                        ? half_of(to_f32(src[int64_t(i) * p.row_pitch + j]))
-                                        : __half(0.0f);
+    for (int k = 0; k < 2; ++k) {
+      const int di = r8 + 32 * k;
+      *reinterpret_cast<uint4*>(x + int64_t(i0 + di) * p.n_pad + j0 + c8 * 8) =
+          *reinterpret_cast<const uint4*>(part + piece_at(di, c8));
     }
   }
 }
@@ -138,7 +191,8 @@ constexpr int kDepth = 64;  // of a stage: one 128-byte swizzle row of halves
 constexpr int kStages = 6;
 constexpr int kOperandBytes = kRows * kDepth * 2;
 constexpr int kStageBytes = 2 * kOperandBytes;
-constexpr int kThreads = 192;
+constexpr int kEpilogueWarps = 8;  // two a quarter of the rows, with half of the columns each
+constexpr int kThreads = 64 + 32 * kEpilogueWarps;
 constexpr int kBoxBytes = 32 * 32 * 2;
 
 struct Ctl {
@@ -149,7 +203,8 @@ struct Ctl {
   int abort;
 };
 constexpr int kSmemBytes =
-    1024 + kStages * kStageBytes + 4 * 2 * kBoxBytes + static_cast<int>(sizeof(Ctl));
+    1024 + kStages * kStageBytes + kEpilogueWarps * 2 * kBoxBytes +
+    static_cast<int>(sizeof(Ctl));
 
 template <bool ACROSS>
 __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* map, uint32_t bar,
@@ -217,22 +272,28 @@ __device__ __forceinline__ Tile tile_of(const OrthoGemmParams& p, int u) {
   return t;
 }
 
-// 32 values of a row to a dense output row of `cols` columns.
+// A box of 32 x 32 16-bit values, rows of 64 bytes: the 16-byte pieces of a row
+// are swapped by its number as the store's map expects (64-byte swizzle), so
+// that eight rows' pieces fall into different banks.
+__device__ __forceinline__ int box_at(int row, int piece) {
+  return row * 64 + ((piece ^ (row >> 1)) & 3) * 16;
+}
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int32_t x,
+                                             int32_t y, int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(src), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
 template <class T>
-__device__ __forceinline__ void store_row(T* row, int col, int cols, bool vec,
-                                          const float (&v)[32]) {
-  if (vec && col + 32 <= cols) {
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      float w[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = v[8 * g + j];
-      store8(row + col + 8 * g, w);
-    }
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if constexpr (sizeof(T) == sizeof(__half) && !std::is_same_v<T, __half>) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
   } else {
-#pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (col + j < cols) row[col + j] = from_f32<T>(v[j]);
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
   }
 }
 
@@ -247,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* const boxes = smem_raw + (base - raw) + kStages * kStageBytes;
-  Ctl* const ctl = reinterpret_cast<Ctl*>(boxes + 4 * 2 * kBoxBytes);
+  Ctl* const ctl = reinterpret_cast<Ctl*>(boxes + kEpilogueWarps * 2 * kBoxBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int per = kSymmetric ? p.m_tiles * (p.m_tiles + 1) / 2 : p.m_tiles * p.n_tiles;
   const int total = per * p.batch;
@@ -263,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_addr(&ctl->acc_full[b]), 1);
-      mbar_init(smem_addr(&ctl->acc_empty[b]), 8);  // the epilogue warps of both CTAs
+      mbar_init(smem_addr(&ctl->acc_empty[b]), 2 * kEpilogueWarps);  // of both CTAs
     }
     mbar_init(smem_addr(&ctl->done), 1);
     ctl->abort = 0;
@@ -367,7 +428,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- results: a thread has a row of the tile, 32 columns at a time
     const int quarter = warp & 3;
     const uint32_t acc_empty = map_to_rank(smem_addr(&ctl->acc_empty[0]), 0);
-    uint8_t* const box = boxes + quarter * 2 * kBoxBytes;
+    const int first = (warp - 2) >> 2 ? kCols / 64 : 0;  // of the eight pieces of 32 columns
+    uint8_t* const box = boxes + (warp - 2) * 2 * kBoxBytes;
     uint8_t* const mirror = box + kBoxBytes;
     grid_dependency_wait();  // the gram and the factors
     int it = 0;
@@ -389,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                              (int64_t(t.b) * p.m_pad + row) * p.m_pad +
                                              t.n * kOrthoTile);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) held[i] = old[i];
+        for (int i = 0; i < 4; ++i) held[i] = old[4 * first + i];
       }
       if (!__all_sync(0xffffffffu, wait_pair(smem_addr(&ctl->acc_full[buf]), (it >> 1) & 1u,
                                              abort_flag, p.err_word)))
@@ -398,8 +460,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) +
                              static_cast<uint32_t>(buf * kCols);
 #pragma unroll 1
-      for (int ch = 0; ch < kCols / 32; ++ch) {
+      for (int ch = first; ch < first + kCols / 64; ++ch) {
         const int col = t.n * kOrthoTile + ch * 32;
+        if (row0 >= p.rows || col >= p.cols) break;  // nothing is kept there
         float v[32];
         tmem_load_32cols(taddr + static_cast<uint32_t>(ch * 32), v);
 #pragma unroll
@@ -409,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                   held[1].x, held[1].y, held[1].z, held[1].w,
                                   held[2].x, held[2].y, held[2].z, held[2].w,
                                   held[3].x, held[3].y, held[3].z, held[3].w};
-          if (ch + 1 < kCols / 32) {
+          if (ch + 1 < first + kCols / 64) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) held[i] = old[4 * (ch + 1) + i];
           }
@@ -425,40 +488,45 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (row - col == j) v[j] += p.diag;
           }
         }
-        if constexpr (kOut) {
-          if (row < p.rows) {
-            T* const out = static_cast<T*>(p.out) + (int64_t(t.b) * p.rows + row) * p.cols;
-            store_row(out, col, p.cols, (reinterpret_cast<uintptr_t>(out) & 15u) == 0, v);
-          }
-        } else if (col < p.cols) {  // boxes lie in c or outside it
-          uint32_t w[16];
+        uint32_t w[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const __half2 q = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t*>(&q);
-          }
-          // the boxes' last stores have read them
-          if (lane == 0) tma_store_wait_read();
+        for (int i = 0; i < 16; ++i) w[i] = pack2<T>(v[2 * i], v[2 * i + 1]);
+        // the boxes' last contents have been taken
+        if (lane == 0) tma_store_wait_read();
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint4*>(box + box_at(lane, i)) =
+              make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        if (mirrored) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            *reinterpret_cast<uint16_t*>(mirror + box_at(i, lane >> 3) + (lane & 7) * 2) =
+                static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+        }
+        if (kOut && !p.out_mapped) {
+          // rows that no map can describe: 32 values of one after the other
           __syncwarp();
-          uint4* const mine = reinterpret_cast<uint4*>(box + lane * 64);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            mine[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-          if (mirrored) {
-            uint16_t* const to = reinterpret_cast<uint16_t*>(mirror) + lane;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              to[64 * i] = static_cast<uint16_t>(w[i]);
-              to[64 * i + 32] = static_cast<uint16_t>(w[i] >> 16);
-            }
+          T* const out = static_cast<T*>(p.out) +
+                         (int64_t(t.b) * p.rows + row0) * p.cols + col + lane;
+          const int rows = p.rows - row0 < 32 ? p.rows - row0 : 32;
+          if (col + lane < p.cols) {
+#pragma unroll 8
+            for (int r = 0; r < rows; ++r)
+              out[int64_t(r) * p.cols] = *reinterpret_cast<const T*>(
+                  box + box_at(r, lane >> 3) + (lane & 7) * 2);
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
+          continue;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (kOut)
+            tma_store_3d(&p.c_map, smem_addr(box), col, row0, t.b);
+          else
             tma_store_2d(&p.c_map, smem_addr(box), col, t.b * p.m_pad + row0);
-            if (mirrored) tma_store_2d(&p.c_map, smem_addr(mirror), row0, t.b * p.m_pad + col);
-            tma_store_commit();
-          }
+          if (mirrored) tma_store_2d(&p.c_map, smem_addr(mirror), row0, t.b * p.m_pad + col);
+          tma_store_commit();
         }
       }
       tc_fence_before_sync();
@@ -466,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0)
         mbar_arrive_cluster(acc_empty + static_cast<uint32_t>(buf * sizeof(uint64_t)));
     }
-    if (!kOut && lane == 0) tma_store_wait_all();
+    if (lane == 0) tma_store_wait_all();
   }
   tc_fence_before_sync();
   __syncwarp();
@@ -508,7 +576,10 @@ cudaError_t launch_op(const OrthoGemmParams& p, int sms, cudaStream_t s) {
 template <class T>
 cudaError_t launch_copy(const OrthoCopyParams& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.n_pad / 64), static_cast<unsigned>(p.m_pad / 64),
+  // CTAs that each find the norm once: six an SM over the batch
+  const int64_t tiles = int64_t(p.n_pad / 64) * (p.m_rows / 64);
+  const int64_t most = std::max<int64_t>(1, 6 * 152 / p.batch);
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min(tiles, most)),
                      static_cast<unsigned>(p.batch));
   cfg.blockDim = dim3(256);
   cfg.stream = s;

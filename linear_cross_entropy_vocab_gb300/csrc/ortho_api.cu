@@ -49,11 +49,12 @@ double step_bound(double a, double b, double c, double top) {
 
 // The power of two that takes values up to `bound` to at most 2^14: halves
 // reach 65504, and roundings add little to a bound.
-double scale_for(double bound) {
+int shift_for(double bound) {
   int e = 0;
   std::frexp(bound, &e);  // bound < 2^e
-  return std::ldexp(1.0, 14 - std::max(e, -40));
+  return 14 - std::max(e, -40);
 }
+double scale_for(double bound) { return std::ldexp(1.0, shift_for(bound)); }
 
 flce_status check_problem(const flce_ortho_problem* p) {
   if (p == nullptr) return fail(FLCE_ERR_INVALID_ARG, "problem is NULL");
@@ -100,7 +101,8 @@ Plan plan_of(const flce_ortho_problem* p) {
   q.m_pad = ceil_div(q.m, flce::kOrthoTile) * flce::kOrthoTile;
   q.n_pad = ceil_div(q.n, 64) * 64;
   // shares of at least 8192 values
-  q.parts = std::max<int64_t>(1, std::min<int64_t>(256, q.m * q.n / 8192));
+  q.parts = std::max<int64_t>(
+      1, std::min<int64_t>({512, q.m * q.n / 8192, 4 * 152 / std::max<int64_t>(1, p->batch)}));
   const size_t b = static_cast<size_t>(p->batch);
   const size_t x_bytes = align_256(b * static_cast<size_t>(q.m_pad * q.n_pad) * 2);
   const size_t g_bytes = align_256(b * static_cast<size_t>(q.m_pad * q.m_pad) * 2);
@@ -114,21 +116,24 @@ Plan plan_of(const flce_ortho_problem* p) {
   return q;
 }
 
+// A map of [batch][outer][inner] 16-bit values (batch 0: two dimensions).
 bool make_map(CUtensorMap* map, const void* base, int64_t inner, int64_t outer,
-              uint32_t box_inner, uint32_t box_outer, bool swizzle) {
+              uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swizzle,
+              int64_t batch = 0) {
   const EncodeTiledFn enc = tensor_map_encoder();
   if (enc == nullptr) {
     fail(FLCE_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
     return false;
   }
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(inner) * 2};
-  const cuuint32_t box[2] = {box_inner, box_outer};
-  const cuuint32_t estr[2] = {1, 1};
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer),
+                              static_cast<cuuint64_t>(batch)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(inner) * 2,
+                                 static_cast<cuuint64_t>(inner) * outer * 2};
+  const cuuint32_t box[3] = {box_inner, box_outer, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
   const CUresult r =
-      enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(base), dims, strides, box,
-          estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-          swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+      enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, batch > 0 ? 3 : 2, const_cast<void*>(base), dims,
+          strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
     fail(FLCE_ERR_CUDA, "cuTensorMapEncodeTiled failed with CUresult %d (%lld x %lld)",
@@ -137,6 +142,9 @@ bool make_map(CUtensorMap* map, const void* base, int64_t inner, int64_t outer,
   }
   return true;
 }
+
+constexpr CUtensorMapSwizzle kLoad = CU_TENSOR_MAP_SWIZZLE_128B;
+constexpr CUtensorMapSwizzle kStore = CU_TENSOR_MAP_SWIZZLE_64B;
 
 }  // namespace
 
@@ -190,7 +198,8 @@ flce_status flce_orthogonalize(const flce_ortho_problem* p, const void* src, voi
   c.partial = reinterpret_cast<double*>(ws + plan.partial);
   c.parts = static_cast<int32_t>(plan.parts);
   c.eps = p->eps;
-  c.x_scale = static_cast<float>(x_scale);
+  c.x_shift = shift_for(bound);
+  c.m_rows = static_cast<int32_t>(ceil_div(plan.m, 64) * 64);
   c.factor = reinterpret_cast<float*>(ws + plan.factor);
   cudaError_t e = flce::launch_ortho_norm(c, p->dtype, s);
   if (e != cudaSuccess) return cuda_fail(e, "matrix norm kernel");
@@ -203,15 +212,20 @@ flce_status flce_orthogonalize(const flce_ortho_problem* p, const void* src, voi
   const int copies = p->steps > 1 ? 2 : 1;
   for (int i = 0; i < copies; ++i) {
     uint8_t* const x = ws + plan.x[i];
-    if (!make_map(&x_along[i], x, plan.n_pad, x_rows, 64, 128, true) ||
-        !make_map(&x_across[i], x, plan.n_pad, x_rows, 64, 64, true) ||
-        !make_map(&x_store[i], x, plan.n_pad, x_rows, 32, 32, false))
+    if (!make_map(&x_along[i], x, plan.n_pad, x_rows, 64, 128, kLoad) ||
+        !make_map(&x_across[i], x, plan.n_pad, x_rows, 64, 64, kLoad) ||
+        !make_map(&x_store[i], x, plan.n_pad, x_rows, 32, 32, kStore))
       return FLCE_ERR_CUDA;
   }
-  if (!make_map(&g_along, ws + plan.gram, plan.m_pad, x_rows, 64, 128, true) ||
-      !make_map(&g_store, ws + plan.gram, plan.m_pad, x_rows, 32, 32, false) ||
-      !make_map(&p_along, ws + plan.poly, plan.m_pad, x_rows, 64, 128, true) ||
-      !make_map(&p_store, ws + plan.poly, plan.m_pad, x_rows, 32, 32, false))
+  if (!make_map(&g_along, ws + plan.gram, plan.m_pad, x_rows, 64, 128, kLoad) ||
+      !make_map(&g_store, ws + plan.gram, plan.m_pad, x_rows, 32, 32, kStore) ||
+      !make_map(&p_along, ws + plan.poly, plan.m_pad, x_rows, 64, 128, kLoad) ||
+      !make_map(&p_store, ws + plan.poly, plan.m_pad, x_rows, 32, 32, kStore))
+    return FLCE_ERR_CUDA;
+  // maps take rows of whole 16 bytes
+  const bool out_mapped = p->cols % 8 == 0 && aligned_to(out, 16);
+  CUtensorMap out_store{};
+  if (out_mapped && !make_map(&out_store, out, p->cols, p->rows, 32, 32, kStore, p->batch))
     return FLCE_ERR_CUDA;
 
   const int32_t m_tiles = static_cast<int32_t>(plan.m_pad / flce::kOrthoTile);
@@ -236,7 +250,7 @@ flce_status flce_orthogonalize(const flce_ortho_problem* p, const void* src, voi
     g.a_map = g.b_map = x_along[from];
     g.c_map = g_store;
     g.m_tiles = g.n_tiles = m_tiles;
-    g.cols = m_pad;
+    g.rows = g.cols = c.m_rows;
     g.k_iters = static_cast<int32_t>(plan.n_pad / 64);
     g.acc_scale = static_cast<float>(g_scale / (x_scale * x_scale));
     g.factor = factor;
@@ -271,11 +285,14 @@ flce_status flce_orthogonalize(const flce_ortho_problem* p, const void* src, voi
     if (last) {
       g.acc_scale = static_cast<float>(1.0 / (x_scale * p_scale));
       g.out = out;
+      g.c_map = out_store;
+      g.out_mapped = out_mapped ? 1 : 0;
       g.rows = c.rows;
       g.cols = c.cols;
     } else {
       g.acc_scale = static_cast<float>(next_scale / (x_scale * p_scale));
       g.c_map = x_store[1 - from];
+      g.rows = c.m_rows;
       g.cols = c.n_pad;
     }
     const flce::OrthoOp op = !last ? flce::OrthoOp::kMul

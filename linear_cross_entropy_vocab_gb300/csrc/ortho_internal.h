@@ -12,7 +12,8 @@ namespace flce {
 
 // The matrices as the caller has them, and their copy in halves: x[b] is
 // [m_pad][n_pad] with m <= n, the transpose of src[b] where `tall`, zeros
-// outside [m][n].
+// outside [m][n] up to row m_rows; what lies in the rows after that is read
+// into rows and columns of tiles that are not stored.
 struct OrthoCopyParams {
   const void* src;
   int64_t batch_stride, row_pitch;  // elements
@@ -23,7 +24,8 @@ struct OrthoCopyParams {
   double* partial;   // [batch][parts] sums of squares
   int32_t parts;
   float eps;
-  float x_scale;     // a power of two
+  int32_t x_shift;   // x holds src / norm times 2^x_shift, but for factor
+  int32_t m_rows;    // rows of x that are filled: a multiple of 64
   float* factor;     // [batch]: x = src / (norm + eps) is factor times what x holds
 };
 cudaError_t launch_ortho_norm(const OrthoCopyParams& p, int dtype, cudaStream_t s);
@@ -39,7 +41,7 @@ enum class OrthoOp {
 
 // One product over all matrices of the batch. Sides are padded to tiles; the
 // loads' maps are boxes of 64 x 128 (contraction contiguous) or 64 x 64
-// (contraction across rows), the store's 32 x 32.
+// (contraction across rows), the store's 32 x 32 with 64-byte swizzle.
 struct OrthoGemmParams {
   CUtensorMap a_map, b_map, c_map;
   int32_t batch, m_tiles, n_tiles, k_iters;
@@ -51,7 +53,8 @@ struct OrthoGemmParams {
   float old_scale, diag;       // kPoly: of the gram's halves, and on the diagonal
   const void* old;             // kPoly: the gram, rows m_pad apart
   void* out;                   // kOut*: rows x cols of out_dtype, dense
-  int32_t rows, cols;          // of out, or cols alone: of c
+  int32_t out_mapped;          // kOut*: through c_map, of out [batch][rows][cols]
+  int32_t rows, cols;          // of out, or of c: what is stored of a matrix
   int32_t* err_word;
 };
 cudaError_t launch_ortho_gemm(const OrthoGemmParams& p, OrthoOp op, int out_dtype, int sms,
