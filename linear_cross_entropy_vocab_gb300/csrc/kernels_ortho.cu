@@ -83,6 +83,8 @@ __global__ void __launch_bounds__(256) ortho_norm_kernel(const OrthoCopyParams p
   }
   total = team_all<256>(total, buf, SumOp{});
   if (threadIdx.x == 0) p.partial[int64_t(blockIdx.y) * p.parts + blockIdx.x] = total;
+  if (blockIdx.x == 0 && blockIdx.y == 0)
+    for (int i = threadIdx.x; i < p.arrived_count; i += 256) p.arrived[i] = 0;
 }
 
 // Where the halves of row i from column 8 * c on lie in a 64 x 64 part in
@@ -90,12 +92,12 @@ __global__ void __launch_bounds__(256) ortho_norm_kernel(const OrthoCopyParams p
 // pieces meet in a bank.
 __device__ __forceinline__ int piece_at(int i, int c) { return i * 64 + ((c ^ (i >> 3)) & 7) * 8; }
 
-// Halves of the padded matrix, 64 x 64 at a time. The transpose of a tall
+// Halves of the padded matrix, 64 x 128 at a time. The transpose of a tall
 // matrix, and rows that do not start at 16-byte boundaries, go through shared
 // memory.
 template <class T>
 __global__ void __launch_bounds__(256) ortho_copy_kernel(const OrthoCopyParams p) {
-  __shared__ __align__(16) __half part[64 * 64];
+  __shared__ __align__(16) __half part[2][64 * 64];
   __shared__ double buf[8];
   grid_launch_dependents();
   grid_dependency_wait();
@@ -133,52 +135,78 @@ __global__ void __launch_bounds__(256) ortho_copy_kernel(const OrthoCopyParams p
   const bool aligned = reinterpret_cast<uintptr_t>(src) % 16 == 0 &&
                        p.row_pitch * static_cast<int64_t>(sizeof(T)) % 16 == 0;
   const int r8 = threadIdx.x >> 3, c8 = threadIdx.x & 7;
-  const int tiles_n = p.n_pad / 64, tiles = tiles_n * (p.m_rows / 64);
+  const int tiles_n = (p.n_pad + 127) / 128, tiles = tiles_n * (p.m_rows / 64);
   for (int u = blockIdx.x; u < tiles; u += gridDim.x) {
-    const int i0 = u / tiles_n * 64, j0 = u % tiles_n * 64;  // of x
+    const int i0 = u / tiles_n * 64, j0 = u % tiles_n * 128;  // of x
+    const int halves = j0 + 64 < p.n_pad ? 2 : 1;
     const int s0 = p.tall ? j0 : i0, t0 = p.tall ? i0 : j0;  // of src
-    if (!p.tall && aligned && t0 + 64 <= p.cols) {
+    const bool whole = aligned && (p.tall ? t0 + 64 : t0 + 128) <= p.cols;
+    if (!p.tall && whole) {
+      uint4 w[4];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int r = s0 + r8 + 32 * k, c = t0 + c8 * 8;
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (r < p.rows) {
-          float v[8];
-          load8(src + int64_t(r) * p.row_pitch + c, v);
-          w = halves_of(v);
-        }
-        *reinterpret_cast<uint4*>(x + int64_t(r) * p.n_pad + c) = w;
+      for (int k = 0; k < 4; ++k) {
+        const int r = s0 + r8 + 32 * (k & 1), c = t0 + (k >> 1) * 64 + c8 * 8;
+        float v[8] = {};
+        if (r < p.rows) load8(src + int64_t(r) * p.row_pitch + c, v);
+        w[k] = halves_of(v);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int r = s0 + r8 + 32 * (k & 1), c = t0 + (k >> 1) * 64 + c8 * 8;
+        *reinterpret_cast<uint4*>(x + int64_t(r) * p.n_pad + c) = w[k];
       }
       continue;
     }
     __syncthreads();  // the last part has been taken
-    if (aligned && t0 + 64 <= p.cols) {  // tall
+    if (whole) {  // tall
+      float v[4][8] = {};
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int dr = r8 + 32 * k, r = s0 + dr;
-        float v[8] = {};
-        if (r < p.rows) load8(src + int64_t(r) * p.row_pitch + t0 + c8 * 8, v);
+      for (int k = 0; k < 4; ++k) {
+        const int r = s0 + r8 + 32 * k;
+        if (r < p.rows) load8(src + int64_t(r) * p.row_pitch + t0 + c8 * 8, v[k]);
+      }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) part[piece_at(c8 * 8 + j, dr >> 3) + (dr & 7)] = half_of(v[j]);
+      for (int k = 0; k < 4; ++k) {
+        const int dr = r8 + 32 * (k & 1);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          part[k >> 1][piece_at(c8 * 8 + j, dr >> 3) + (dr & 7)] = half_of(v[k][j]);
       }
     } else {
-      const int dc = threadIdx.x & 63, c = t0 + dc;
+      // rows that start anywhere: the nine aligned pieces that hold 64 values
+      for (int u9 = threadIdx.x; u9 < halves * 64 * 9; u9 += 256) {
+        const int line = u9 / 9, g = line >> 6, dr = line & 63;
+        const int r = s0 + dr + (p.tall ? 64 * g : 0), c0 = t0 + (p.tall ? 0 : 64 * g);
+        const T* const row = src + int64_t(r) * p.row_pitch;
+        const int phase = static_cast<int>(reinterpret_cast<uintptr_t>(row) / sizeof(T)) & 7;
+        const int c = c0 - ((c0 + phase) & 7) + (u9 - line * 9) * 8;
+        float v[8] = {};
+        if (r < p.rows) {
+          if (c >= 0 && c + 8 <= p.cols) {
+            load8(row + c, v);
+          } else {
 #pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const int dr = (threadIdx.x >> 6) + 4 * k, r = s0 + dr;
-        const __half v = r < p.rows && c < p.cols
-                             ? half_of(to_f32(src[int64_t(r) * p.row_pitch + c]))
-                             : __half(0.0f);
-        const int i = p.tall ? dc : dr, j = p.tall ? dr : dc;
-        part[piece_at(i, j >> 3) + (j & 7)] = v;
+            for (int j = 0; j < 8; ++j)
+              if (c + j >= 0 && c + j < p.cols) v[j] = to_f32(row[c + j]);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int dc = c + j - c0;
+          if (dc < 0 || dc >= 64) continue;
+          const int i = p.tall ? dc : dr, at = p.tall ? dr : dc;
+          part[g][piece_at(i, at >> 3) + (at & 7)] = half_of(v[j]);
+        }
       }
     }
     __syncthreads();
+    for (int g = 0; g < halves; ++g) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int di = r8 + 32 * k;
-      *reinterpret_cast<uint4*>(x + int64_t(i0 + di) * p.n_pad + j0 + c8 * 8) =
-          *reinterpret_cast<const uint4*>(part + piece_at(di, c8));
+      for (int k = 0; k < 2; ++k) {
+        const int di = r8 + 32 * k;
+        *reinterpret_cast<uint4*>(x + int64_t(i0 + di) * p.n_pad + j0 + 64 * g + c8 * 8) =
+            *reinterpret_cast<const uint4*>(part[g] + piece_at(di, c8));
+      }
     }
   }
 }
@@ -191,7 +219,7 @@ constexpr int kDepth = 64;  // of a stage: one 128-byte swizzle row of halves
 constexpr int kStages = 6;
 constexpr int kOperandBytes = kRows * kDepth * 2;
 constexpr int kStageBytes = 2 * kOperandBytes;
-constexpr int kEpilogueWarps = 8;  // two a quarter of the rows, with half of the columns each
+constexpr int kEpilogueWarps = kOrthoWarps;  // two a quarter of the rows, with half of the columns each
 constexpr int kThreads = 64 + 32 * kEpilogueWarps;
 constexpr int kBoxBytes = 32 * 32 * 2;
 
@@ -249,10 +277,10 @@ __device__ __forceinline__ void drain_pair(uint32_t bar, uint32_t parity) {
 struct Tile {
   int b, m, n;
 };
-template <bool SYMMETRIC>
+template <OrthoOp OP>
 __device__ __forceinline__ Tile tile_of(const OrthoGemmParams& p, int u) {
   Tile t;
-  if constexpr (SYMMETRIC) {
+  if constexpr (OP == OrthoOp::kGram || OP == OrthoOp::kPoly) {
     const int per = p.m_tiles * (p.m_tiles + 1) / 2;
     t.b = u / per;
     int r = u - t.b * per;
@@ -266,10 +294,53 @@ __device__ __forceinline__ Tile tile_of(const OrthoGemmParams& p, int u) {
     const int per = p.m_tiles * p.n_tiles;
     t.b = u / per;
     const int r = u - t.b * per;
-    t.n = r / p.m_tiles;
-    t.m = r - t.n * p.m_tiles;
+    if constexpr (OP == OrthoOp::kOutTall) {  // p stays in L2, x passes once
+      t.m = r / p.n_tiles;
+      t.n = r - t.m * p.n_tiles;
+    } else {
+      t.n = r / p.m_tiles;
+      t.m = r - t.n * p.m_tiles;
+    }
   }
   return t;
+}
+
+// A stretch of a tile's contraction, [k0, k1).
+struct Part {
+  int tile, k0, k1;
+};
+// The parts of one pair of CTAs. The last `split_tiles` tiles are laid end to
+// end and cut into as many equal stretches as there are pairs, so that all
+// pairs end together; the tiles before them are taken whole, one pair after the
+// other. The stretches come first: what joins their sums runs behind whole
+// tiles' products.
+struct Walk {
+  int at, end, whole;
+  static __device__ __forceinline__ int start(const OrthoGemmParams& p, int unit, int units) {
+    return unit * (p.split_tiles * p.k_iters) / units;  // the host keeps this in 31 bits
+  }
+  __device__ __forceinline__ Walk(const OrthoGemmParams& p, int unit, int units)
+      : at(start(p, unit, units)), end(start(p, unit + 1, units)), whole(unit) {}
+  __device__ __forceinline__ bool next(const OrthoGemmParams& p, int units, Part& part) {
+    if (at < end) {
+      const int t = at / p.k_iters;
+      part.tile = p.whole_tiles + t;
+      part.k0 = at - t * p.k_iters;
+      part.k1 = min(p.k_iters, part.k0 + end - at);
+      at += part.k1 - part.k0;
+      return true;
+    }
+    if (whole < p.whole_tiles) {
+      part = {whole, 0, p.k_iters};
+      whole += units;
+      return true;
+    }
+    return false;
+  }
+};
+// The pair that has iteration x of the stretches.
+__device__ __forceinline__ int owner_of(const OrthoGemmParams& p, int x, int units) {
+  return ((x + 1) * units - 1) / (p.split_tiles * p.k_iters);
 }
 
 // A box of 32 x 32 16-bit values, rows of 64 bytes: the 16-byte pieces of a row
@@ -285,6 +356,13 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t sr
           reinterpret_cast<uint64_t>(map)),
       "r"(src), "r"(x), "r"(y), "r"(z)
       : "memory");
+}
+// Where a pair leaves a warp's sums of a part: of the first part of a tile
+// (which ends the pair's stretch) or of another (which begins it).
+__device__ __forceinline__ float4* share_of(const OrthoGemmParams& p, int unit, bool first,
+                                            int rank, int warp) {
+  const int64_t slot = ((unit * 2 + (first ? 1 : 0)) * 2 + rank) * kEpilogueWarps + warp;
+  return reinterpret_cast<float4*>(p.shares) + slot * (kCols / 64 * 8 * 32);
 }
 template <class T>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
@@ -310,8 +388,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* const boxes = smem_raw + (base - raw) + kStages * kStageBytes;
   Ctl* const ctl = reinterpret_cast<Ctl*>(boxes + kEpilogueWarps * 2 * kBoxBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int per = kSymmetric ? p.m_tiles * (p.m_tiles + 1) / 2 : p.m_tiles * p.n_tiles;
-  const int total = per * p.batch;
   const int rank = static_cast<int>(cluster_ctarank());
   const bool leader = rank == 0;
   const int unit0 = blockIdx.x >> 1, units = gridDim.x >> 1;
@@ -351,12 +427,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t phase = 0, armed = 0, last = 0;
       bool ok = true;
       grid_dependency_wait();
-      for (int u = unit0; u < total && ok; u += units) {
-        const Tile t = tile_of<kSymmetric>(p, u);
+      Walk walk(p, unit0, units);
+      for (Part part; ok && walk.next(p, units, part);) {
+        const Tile t = tile_of<OP>(p, part.tile);
         const int a_side = t.m * kOrthoTile + rank * kRows;
         const int b_side = t.n * kOrthoTile + rank * kRows;
         const int a_base = t.b * p.a_stride, b_base = t.b * p.b_stride;
-        for (int k = 0; k < p.k_iters; ++k) {
+        for (int k = part.k0; k < part.k1; ++k) {
           if (!wait_pair(smem_addr(&ctl->empty[stage]), phase ^ 1u, abort_flag, p.err_word)) {
             ok = false;
             break;
@@ -392,14 +469,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t phase = 0;
       bool ok = true;
       int it = 0;
-      for (int u = unit0; u < total && ok; u += units, ++it) {
+      Walk walk(p, unit0, units);
+      for (Part part; ok && walk.next(p, units, part); ++it) {
         const int buf = it & 1;
         if (!wait_pair(smem_addr(&ctl->acc_empty[buf]), ((it >> 1) & 1u) ^ 1u, abort_flag,
                        p.err_word))
           break;
         tc_fence_after_sync();
         const uint32_t d = tmem + static_cast<uint32_t>(buf * kCols);
-        for (int k = 0; k < p.k_iters; ++k) {
+        for (int k = part.k0; k < part.k1; ++k) {
           if (!wait_pair(smem_addr(&ctl->full[stage]), phase, abort_flag, p.err_word)) {
             ok = false;
             break;
@@ -409,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < kDepth / 16; ++kk)
             umma_bf16_pair(d, slice_desc<kAcrossA>(a0, kk), slice_desc<kAcrossB>(b0, kk), idesc,
-                           (k | kk) != 0 ? 1u : 0u);
+                           k != part.k0 || kk != 0 ? 1u : 0u);
           umma_commit_pair(smem_addr(&ctl->empty[stage]), 0x3);
           if (++stage == kStages) {
             stage = 0;
@@ -433,8 +511,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* const mirror = box + kBoxBytes;
     grid_dependency_wait();  // the gram and the factors
     int it = 0;
-    for (int u = unit0; u < total; u += units, ++it) {
-      const Tile t = tile_of<kSymmetric>(p, u);
+    Walk walk(p, unit0, units);
+    for (Part part; walk.next(p, units, part); ++it) {
+      const Tile t = tile_of<OP>(p, part.tile);
       const int buf = it & 1;
       const int row0 = t.m * kOrthoTile + rank * kRows + quarter * 32;  // of the matrix
       const int row = row0 + lane;
@@ -459,12 +538,71 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after_sync();
       const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) +
                              static_cast<uint32_t>(buf * kCols);
+      // Pieces of the tile that this warp keeps. Where the tile's contraction
+      // is cut, each pair leaves its sums, and the warp that comes last adds
+      // all of them, in the order of the contraction.
+      const int pieces =
+          row0 >= p.rows ? 0 : min(kCols / 64, (p.cols - t.n * kOrthoTile - first * 32 + 31) / 32);
+      int from = unit0, to = unit0;
+      if (part.k1 - part.k0 < p.k_iters && pieces > 0) {
+        const int x = (part.tile - p.whole_tiles) * p.k_iters;
+        from = owner_of(p, x, units);
+        to = owner_of(p, x + p.k_iters - 1, units);
+        int* const counter = p.arrived +
+            ((part.tile - p.whole_tiles) * 2 + rank) * kEpilogueWarps + warp - 2;
+        int before = 0;
+        if (lane == 0) before = *reinterpret_cast<volatile int*>(counter);
+        before = __shfl_sync(0xffffffffu, before, 0);
+        if (before != to - from) {
+          float4* const mine = share_of(p, unit0, unit0 == from, rank, warp - 2) + lane;
 #pragma unroll 1
-      for (int ch = first; ch < first + kCols / 64; ++ch) {
+          for (int i = 0; i < pieces; ++i) {
+            float v[32];
+            tmem_load_32cols(taddr + static_cast<uint32_t>((first + i) * 32), v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              mine[(i * 8 + j) * 32] =
+                  make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+          }
+          __threadfence();
+          __syncwarp();
+          if (lane == 0) before = atomicAdd(counter, 1);
+          before = __shfl_sync(0xffffffffu, before, 0);
+        }
+        if (before == to - from && lane == 0) *counter = 0;  // for the next launch
+        __threadfence();
+        __syncwarp();
+        if (before != to - from) from = to + 1;  // not the last
+      }
+#pragma unroll 1
+      for (int i = 0; from <= to && i < pieces; ++i) {
+        const int ch = first + i;
         const int col = t.n * kOrthoTile + ch * 32;
-        if (row0 >= p.rows || col >= p.cols) break;  // nothing is kept there
         float v[32];
         tmem_load_32cols(taddr + static_cast<uint32_t>(ch * 32), v);
+        if (from < to) {
+          float sum[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) sum[j] = 0.0f;
+          for (int q = from; q <= to; ++q) {
+            if (q == unit0) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) sum[j] += v[j];
+            } else {
+              const float4* const other = share_of(p, q, q == from, rank, warp - 2) + lane;
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const float4 f = __ldcg(other + (i * 8 + j) * 32);
+                sum[4 * j] += f.x;
+                sum[4 * j + 1] += f.y;
+                sum[4 * j + 2] += f.z;
+                sum[4 * j + 3] += f.w;
+              }
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = sum[j];
+        }
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] *= scale;
         if constexpr (OP == OrthoOp::kPoly) {
@@ -547,18 +685,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <OrthoOp OP, class T>
-cudaError_t launch_op(const OrthoGemmParams& p, int sms, cudaStream_t s) {
+cudaError_t launch_op(const OrthoGemmParams& p, cudaStream_t s) {
   const auto kernel = ortho_gemm_kernel<OP, T>;
   cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
-  const int64_t per = OP == OrthoOp::kGram || OP == OrthoOp::kPoly
-                          ? int64_t(p.m_tiles) * (p.m_tiles + 1) / 2
-                          : int64_t(p.m_tiles) * p.n_tiles;
-  const int64_t tiles = per * p.batch;
-  const int64_t pairs = tiles < sms / 2 ? tiles : sms / 2;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * p.units));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = s;
@@ -577,7 +710,7 @@ template <class T>
 cudaError_t launch_copy(const OrthoCopyParams& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
   // CTAs that each find the norm once: six an SM over the batch
-  const int64_t tiles = int64_t(p.n_pad / 64) * (p.m_rows / 64);
+  const int64_t tiles = int64_t((p.n_pad + 127) / 128) * (p.m_rows / 64);
   const int64_t most = std::max<int64_t>(1, 6 * 152 / p.batch);
   cfg.gridDim = dim3(static_cast<unsigned>(std::min(tiles, most)),
                      static_cast<unsigned>(p.batch));
@@ -610,21 +743,21 @@ cudaError_t launch_ortho_copy(const OrthoCopyParams& p, int dtype, cudaStream_t 
   return launch_copy<__half>(p, s);
 }
 
-cudaError_t launch_ortho_gemm(const OrthoGemmParams& p, OrthoOp op, int out_dtype, int sms,
+cudaError_t launch_ortho_gemm(const OrthoGemmParams& p, OrthoOp op, int out_dtype,
                               cudaStream_t s) {
   switch (op) {
     case OrthoOp::kGram:
-      return launch_op<OrthoOp::kGram, __half>(p, sms, s);
+      return launch_op<OrthoOp::kGram, __half>(p, s);
     case OrthoOp::kPoly:
-      return launch_op<OrthoOp::kPoly, __half>(p, sms, s);
+      return launch_op<OrthoOp::kPoly, __half>(p, s);
     case OrthoOp::kMul:
-      return launch_op<OrthoOp::kMul, __half>(p, sms, s);
+      return launch_op<OrthoOp::kMul, __half>(p, s);
     case OrthoOp::kOutWide:
-      return out_dtype == FLCE_BF16 ? launch_op<OrthoOp::kOutWide, __nv_bfloat16>(p, sms, s)
-                                    : launch_op<OrthoOp::kOutWide, __half>(p, sms, s);
+      return out_dtype == FLCE_BF16 ? launch_op<OrthoOp::kOutWide, __nv_bfloat16>(p, s)
+                                    : launch_op<OrthoOp::kOutWide, __half>(p, s);
     case OrthoOp::kOutTall:
-      return out_dtype == FLCE_BF16 ? launch_op<OrthoOp::kOutTall, __nv_bfloat16>(p, sms, s)
-                                    : launch_op<OrthoOp::kOutTall, __half>(p, sms, s);
+      return out_dtype == FLCE_BF16 ? launch_op<OrthoOp::kOutTall, __nv_bfloat16>(p, s)
+                                    : launch_op<OrthoOp::kOutTall, __half>(p, s);
   }
   return cudaErrorInvalidValue;
 }

@@ -90,9 +90,47 @@ flce_status check_problem(const flce_ortho_problem* p) {
   return FLCE_OK;
 }
 
+// How many pairs of CTAs take a product's tiles, and how many of the tiles are
+// cut between pairs.
+struct Split {
+  int64_t units, whole, cut;
+};
+constexpr int64_t kPlanPairs = 80;  // that a workspace is planned for
+constexpr int64_t kMaxParts = 4;    // of a tile where there are fewer tiles than pairs
+
+// A step of 64 along the contraction takes a pair 0.27 us. Cutting costs a tile
+// some 3 us and 1.1 more for each further part, as the sums go through L2, and
+// pairs that no longer walk the contraction together share fewer loads. So
+// tiles are cut where the last round would leave most pairs idle for long:
+// eight grams of 1024 x 4096 (80 tiles, 64 steps) take 38 us cut and 49 whole,
+// the product of 4096 x 4096 (256 tiles) 82 and 89, but its gram (136 tiles)
+// 54 and 50, and that of 4096 x 14336 169 and 152.
+Split split_of(int64_t tiles, int64_t k_iters, int64_t pairs) {
+  if (tiles >= pairs) {
+    const int64_t left = tiles % pairs;
+    // the last round would run with `left` pairs
+    if (left == 0 || 2 * left > pairs || (pairs - left) * k_iters < 24 * pairs)
+      return {pairs, tiles, 0};
+    return {pairs, tiles - pairs - left, pairs + left};
+  }
+  int64_t parts = 1;
+  double best = 0.27 * k_iters;
+  for (int64_t s = 2; s <= kMaxParts && s * tiles <= pairs && 4 * s <= k_iters; ++s) {
+    const double t = 0.27 * k_iters / s + 1.9 + 1.1 * s;
+    if (t < best) {
+      best = t;
+      parts = s;
+    }
+  }
+  return parts > 1 ? Split{parts * tiles, 0, tiles} : Split{tiles, tiles, 0};
+}
+
+constexpr int32_t kArrived = 2 * kPlanPairs * 2 * flce::kOrthoWarps;
+constexpr size_t kArrivedBytes = kArrived * 4;
+
 struct Plan {
   int64_t m, n, m_pad, n_pad, parts;
-  size_t x[2], gram, poly, partial, factor, total;
+  size_t x[2], gram, poly, partial, factor, arrived, shares, total;
 };
 Plan plan_of(const flce_ortho_problem* p) {
   Plan q{};
@@ -102,7 +140,7 @@ Plan plan_of(const flce_ortho_problem* p) {
   q.n_pad = ceil_div(q.n, 64) * 64;
   // shares of at least 8192 values
   q.parts = std::max<int64_t>(
-      1, std::min<int64_t>({512, q.m * q.n / 8192, 4 * 152 / std::max<int64_t>(1, p->batch)}));
+      1, std::min<int64_t>({1024, q.m * q.n / 8192, 8 * 152 / std::max<int64_t>(1, p->batch)}));
   const size_t b = static_cast<size_t>(p->batch);
   const size_t x_bytes = align_256(b * static_cast<size_t>(q.m_pad * q.n_pad) * 2);
   const size_t g_bytes = align_256(b * static_cast<size_t>(q.m_pad * q.m_pad) * 2);
@@ -112,7 +150,12 @@ Plan plan_of(const flce_ortho_problem* p) {
   q.poly = q.gram + g_bytes;
   q.partial = q.poly + g_bytes;
   q.factor = q.partial + align_256(b * static_cast<size_t>(q.parts) * 8);
-  q.total = q.factor + align_256(b * 4);
+  q.arrived = q.factor + align_256(b * 4);
+  q.shares = q.arrived + kArrivedBytes;
+  const int64_t side = q.m_pad / flce::kOrthoTile;
+  const int64_t tiles = p->batch * side * ceil_div(q.n, flce::kOrthoTile);
+  q.total = q.shares + static_cast<size_t>(2 * std::min(kPlanPairs, kMaxParts * tiles)) *
+                           flce::kOrthoShareBytes;
   return q;
 }
 
@@ -201,6 +244,8 @@ flce_status flce_orthogonalize(const flce_ortho_problem* p, const void* src, voi
   c.x_shift = shift_for(bound);
   c.m_rows = static_cast<int32_t>(ceil_div(plan.m, 64) * 64);
   c.factor = reinterpret_cast<float*>(ws + plan.factor);
+  c.arrived = reinterpret_cast<int32_t*>(ws + plan.arrived);
+  c.arrived_count = kArrived;
   cudaError_t e = flce::launch_ortho_norm(c, p->dtype, s);
   if (e != cudaSuccess) return cuda_fail(e, "matrix norm kernel");
   e = flce::launch_ortho_copy(c, p->dtype, s);
@@ -231,6 +276,16 @@ flce_status flce_orthogonalize(const flce_ortho_problem* p, const void* src, voi
   const int32_t m_tiles = static_cast<int32_t>(plan.m_pad / flce::kOrthoTile);
   const int32_t n_tiles = static_cast<int32_t>(ceil_div(plan.n, flce::kOrthoTile));
   const int32_t m_pad = static_cast<int32_t>(plan.m_pad);
+  const int64_t pairs = std::min<int64_t>(kPlanPairs, sms / 2);
+  const auto cut = [&](flce::OrthoGemmParams& g, int64_t tiles) {
+    const Split split = split_of(tiles * p->batch, g.k_iters, pairs);
+    g.units = static_cast<int32_t>(split.units);
+    g.whole_tiles = static_cast<int32_t>(split.whole);
+    g.split_tiles = static_cast<int32_t>(split.cut);
+    g.shares = ws + plan.shares;
+    g.arrived = c.arrived;
+  };
+  const int64_t triangle = int64_t(m_tiles) * (m_tiles + 1) / 2;
   for (int k = 0; k < p->steps; ++k) {
     const float* const abc = p->coefficients + 3 * k;
     const double g_scale = scale_for(bound * bound);
@@ -255,7 +310,8 @@ flce_status flce_orthogonalize(const flce_ortho_problem* p, const void* src, voi
     g.acc_scale = static_cast<float>(g_scale / (x_scale * x_scale));
     g.factor = factor;
     g.factor_square = 1;
-    e = flce::launch_ortho_gemm(g, flce::OrthoOp::kGram, 0, sms, s);
+    cut(g, triangle);
+    e = flce::launch_ortho_gemm(g, flce::OrthoOp::kGram, 0, s);
     if (e != cudaSuccess) return cuda_fail(e, "gram kernel");
 
     g.a_map = g.b_map = g_along;
@@ -266,7 +322,8 @@ flce_status flce_orthogonalize(const flce_ortho_problem* p, const void* src, voi
     g.old = ws + plan.gram;
     g.old_scale = static_cast<float>(abc[1] * p_scale / g_scale);
     g.diag = static_cast<float>(abc[0] * p_scale);
-    e = flce::launch_ortho_gemm(g, flce::OrthoOp::kPoly, 0, sms, s);
+    cut(g, triangle);
+    e = flce::launch_ortho_gemm(g, flce::OrthoOp::kPoly, 0, s);
     if (e != cudaSuccess) return cuda_fail(e, "polynomial kernel");
 
     g.factor = factor;
@@ -295,10 +352,11 @@ flce_status flce_orthogonalize(const flce_ortho_problem* p, const void* src, voi
       g.rows = c.m_rows;
       g.cols = c.n_pad;
     }
+    cut(g, int64_t(m_tiles) * n_tiles);
     const flce::OrthoOp op = !last ? flce::OrthoOp::kMul
                              : tall ? flce::OrthoOp::kOutTall
                                     : flce::OrthoOp::kOutWide;
-    e = flce::launch_ortho_gemm(g, op, p->out_dtype, sms, s);
+    e = flce::launch_ortho_gemm(g, op, p->out_dtype, s);
     if (e != cudaSuccess) return cuda_fail(e, "product kernel");
     x_scale = next_scale;
   }

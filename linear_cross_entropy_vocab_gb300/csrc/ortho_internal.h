@@ -26,6 +26,8 @@ struct OrthoCopyParams {
   float eps;
   int32_t x_shift;   // x holds src / norm times 2^x_shift, but for factor
   int32_t m_rows;    // rows of x that are filled: a multiple of 64
+  int32_t* arrived;  // cleared for the products
+  int32_t arrived_count;
   float* factor;     // [batch]: x = src / (norm + eps) is factor times what x holds
 };
 cudaError_t launch_ortho_norm(const OrthoCopyParams& p, int dtype, cudaStream_t s);
@@ -45,6 +47,10 @@ enum class OrthoOp {
 struct OrthoGemmParams {
   CUtensorMap a_map, b_map, c_map;
   int32_t batch, m_tiles, n_tiles, k_iters;
+  int32_t units;                     // pairs of CTAs
+  int32_t whole_tiles, split_tiles;  // of all tiles, in this order
+  void* shares;      // sums of cut tiles: two of 256 KB for each pair
+  int32_t* arrived;  // [split_tiles][2 CTAs][8 warps], zeros before and after
   int32_t a_stride, b_stride;  // rows of a map between two matrices
   int32_t m_pad;               // rows of c between two matrices
   float acc_scale;             // of the accumulator
@@ -57,9 +63,11 @@ struct OrthoGemmParams {
   int32_t rows, cols;          // of out, or of c: what is stored of a matrix
   int32_t* err_word;
 };
-cudaError_t launch_ortho_gemm(const OrthoGemmParams& p, OrthoOp op, int out_dtype, int sms,
+cudaError_t launch_ortho_gemm(const OrthoGemmParams& p, OrthoOp op, int out_dtype,
                               cudaStream_t s);
 
 constexpr int kOrthoTile = 256;
+constexpr int kOrthoWarps = 8;  // that store a tile, in each CTA
+constexpr int kOrthoShareBytes = kOrthoTile * kOrthoTile * 4;
 
 }  // namespace flce
