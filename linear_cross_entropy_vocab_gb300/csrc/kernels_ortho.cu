@@ -8,11 +8,11 @@
 // diagonal are computed and stored twice, once transposed.
 //
 // Bound by the tensor cores: m^2 n + m^3 + 2 m^2 n operations a step for an
-// m x n matrix, m <= n, against a few passes over it. A persistent kernel runs
-// CTA pairs on 256 x 256 tiles (tcgen05.mma over the pair, operands staged by
-// TMA in a ring of six 32 KB stages, two accumulators in tensor memory, so that
-// a tile is stored behind the next one's products); launches overlap at their
-// ends.
+// m x n matrix, m <= n, against a few passes over it. One persistent kernel
+// runs all steps with CTA pairs on 256 x 256 tiles (tcgen05.mma over the pair,
+// operands staged by TMA in a ring of six 32 KB stages, two accumulators in
+// tensor memory, so that a tile is stored behind the next one's products).
+// Products follow one another by counts in global memory, not by launches.
 //
 // The operands are halves with a power-of-two scale for each product, chosen by
 // the host from the bounds on the singular values, so that nothing leaves the
@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(256) ortho_norm_kernel(const OrthoCopyParams p
   total = team_all<256>(total, buf, SumOp{});
   if (threadIdx.x == 0) p.partial[int64_t(blockIdx.y) * p.parts + blockIdx.x] = total;
   if (blockIdx.x == 0 && blockIdx.y == 0)
-    for (int i = threadIdx.x; i < p.arrived_count; i += 256) p.arrived[i] = 0;
+    for (int i = threadIdx.x; i < p.counts; i += 256) p.count[i] = 0;
 }
 
 // Where the halves of row i from column 8 * c on lie in a 64 x 64 part in
@@ -99,7 +99,6 @@ template <class T>
 __global__ void __launch_bounds__(256) ortho_copy_kernel(const OrthoCopyParams p) {
   __shared__ __align__(16) __half part[2][64 * 64];
   __shared__ double buf[8];
-  grid_launch_dependents();
   grid_dependency_wait();
   const int b = blockIdx.y;
   const double* const partial = p.partial + int64_t(b) * p.parts;
@@ -219,9 +218,10 @@ constexpr int kDepth = 64;  // of a stage: one 128-byte swizzle row of halves
 constexpr int kStages = 6;
 constexpr int kOperandBytes = kRows * kDepth * 2;
 constexpr int kStageBytes = 2 * kOperandBytes;
-constexpr int kEpilogueWarps = kOrthoWarps;  // two a quarter of the rows, with half of the columns each
-constexpr int kThreads = 64 + 32 * kEpilogueWarps;
+constexpr int kWarps = kOrthoWarps;  // of the epilogue: two a quarter of the rows, half of the columns each
+constexpr int kThreads = 64 + 32 * kWarps;
 constexpr int kBoxBytes = 32 * 32 * 2;
+constexpr int kPieces = kCols / 64;  // of 32 columns, for an epilogue warp
 
 struct Ctl {
   uint64_t full[kStages], empty[kStages];
@@ -231,8 +231,7 @@ struct Ctl {
   int abort;
 };
 constexpr int kSmemBytes =
-    1024 + kStages * kStageBytes + kEpilogueWarps * 2 * kBoxBytes +
-    static_cast<int>(sizeof(Ctl));
+    1024 + kStages * kStageBytes + kWarps * 2 * kBoxBytes + static_cast<int>(sizeof(Ctl));
 
 template <bool ACROSS>
 __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* map, uint32_t bar,
@@ -250,57 +249,86 @@ __device__ __forceinline__ uint64_t slice_desc(uint32_t base, int kk) {
                 : smem_desc_sw128(base + kk * 32, 16, 1024);
 }
 
+// Every wait has a limit: past it the CTA gives up, lets what is in flight
+// finish and leaves, and the error word says so.
+__device__ __forceinline__ bool give_up(uint64_t t0, volatile int* abort_flag, int* err_word) {
+  if (*abort_flag) return true;
+  if (globaltimer_ns() - t0 <= kWaitBudgetNs) return false;
+  *abort_flag = 1;
+  if (err_word) atomicOr(err_word, FLCE_DEVERR_TIMEOUT);
+  return true;
+}
 __device__ __forceinline__ bool wait_pair(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                           int* err_word) {
   if (mbar_try_wait_cluster(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t it = 1;; ++it) {
     if (mbar_try_wait_cluster(bar, parity)) return true;
-    if ((it & 63u) == 0u) {
-      if (*abort_flag) return false;
-      if (globaltimer_ns() - t0 > kWaitBudgetNs) {
-        *abort_flag = 1;
-        if (err_word) atomicOr(err_word, FLCE_DEVERR_TIMEOUT);
-        return false;
-      }
-    }
+    if ((it & 63u) == 0u && give_up(t0, abort_flag, err_word)) return false;
   }
 }
-// Lets what is in flight finish, with a limit, whatever the abort flag says.
 __device__ __forceinline__ void drain_pair(uint32_t bar, uint32_t parity) {
   const uint64_t t0 = globaltimer_ns();
   while (!mbar_try_wait_cluster(bar, parity)) {
     if (globaltimer_ns() - t0 > 1000000000ull) break;
   }
 }
+__device__ __forceinline__ int load_acquire(const int* p) {
+  int v;
+  asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ void add_release(int* p, int v) {
+  asm volatile("red.release.gpu.global.add.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+// Orders accesses of global memory by bulk copies and by ordinary instructions.
+__device__ __forceinline__ void fence_proxy_async_global() {
+  asm volatile("fence.proxy.async.global;" ::: "memory");
+}
+
+enum Op { kGram, kPoly, kMul, kOutWide, kOutTall };
+
+// One product of the sequence, as every role walks it: step k's gram,
+// polynomial and product.
+struct Product {
+  int k, kind;        // kind 0 to 2: gram, polynomial, product
+  Op op;
+  int m_tiles, n_tiles, per;  // tiles of a matrix
+  int k_iters;
+};
+__device__ __forceinline__ Product product_of(const OrthoRunParams& p, int i) {
+  Product q;
+  q.k = i / 3;
+  q.kind = i - 3 * q.k;
+  const bool out = q.k + 1 == p.steps;
+  q.op = q.kind == 0 ? kGram : q.kind == 1 ? kPoly : !out ? kMul : p.tall ? kOutTall : kOutWide;
+  q.m_tiles = q.op == kOutTall ? p.n_tiles : p.m_tiles;
+  q.n_tiles = q.kind < 2 || q.op == kOutTall ? p.m_tiles : p.n_tiles;
+  q.per = q.kind < 2 ? p.m_tiles * (p.m_tiles + 1) / 2 : p.m_tiles * p.n_tiles;
+  q.k_iters = q.kind == 0 ? p.k_n : p.k_m;
+  return q;
+}
 
 struct Tile {
   int b, m, n;
 };
-template <OrthoOp OP>
-__device__ __forceinline__ Tile tile_of(const OrthoGemmParams& p, int u) {
+__device__ __forceinline__ Tile tile_of(const Product& q, int u) {
   Tile t;
-  if constexpr (OP == OrthoOp::kGram || OP == OrthoOp::kPoly) {
-    const int per = p.m_tiles * (p.m_tiles + 1) / 2;
-    t.b = u / per;
-    int r = u - t.b * per;
+  t.b = u / q.per;
+  int r = u - t.b * q.per;
+  if (q.kind < 2) {  // the triangle above the diagonal
     t.m = 0;
-    while (r >= p.m_tiles - t.m) {
-      r -= p.m_tiles - t.m;
+    while (r >= q.m_tiles - t.m) {
+      r -= q.m_tiles - t.m;
       ++t.m;
     }
     t.n = t.m + r;
+  } else if (q.op == kOutTall) {  // p stays in L2, x passes once
+    t.m = r / q.n_tiles;
+    t.n = r - t.m * q.n_tiles;
   } else {
-    const int per = p.m_tiles * p.n_tiles;
-    t.b = u / per;
-    const int r = u - t.b * per;
-    if constexpr (OP == OrthoOp::kOutTall) {  // p stays in L2, x passes once
-      t.m = r / p.n_tiles;
-      t.n = r - t.m * p.n_tiles;
-    } else {
-      t.n = r / p.m_tiles;
-      t.m = r - t.n * p.m_tiles;
-    }
+    t.n = r / q.m_tiles;
+    t.m = r - t.n * q.m_tiles;
   }
   return t;
 }
@@ -309,38 +337,88 @@ __device__ __forceinline__ Tile tile_of(const OrthoGemmParams& p, int u) {
 struct Part {
   int tile, k0, k1;
 };
-// The parts of one pair of CTAs. The last `split_tiles` tiles are laid end to
-// end and cut into as many equal stretches as there are pairs, so that all
-// pairs end together; the tiles before them are taken whole, one pair after the
-// other. The stretches come first: what joins their sums runs behind whole
-// tiles' products.
+// The parts of one pair of CTAs. Tiles are taken in turn, over all products:
+// a product's first tile goes to the pair after the last one of the product
+// before. Where a product's tiles are cut, the last `cut` of them are laid end
+// to end and divided into as many equal stretches as there are pairs, so that
+// all pairs end together; the stretches come first, so that what joins their
+// sums runs behind whole tiles' products.
 struct Walk {
-  int at, end, whole;
-  static __device__ __forceinline__ int start(const OrthoGemmParams& p, int unit, int units) {
-    return unit * (p.split_tiles * p.k_iters) / units;  // the host keeps this in 31 bits
+  int at, end, whole, whole_end, stride;
+  static __device__ __forceinline__ int start(const OrthoCut& c, int k_iters, int unit) {
+    return unit * (c.cut * k_iters) / c.units;  // the host keeps this in 31 bits
   }
-  __device__ __forceinline__ Walk(const OrthoGemmParams& p, int unit, int units)
-      : at(start(p, unit, units)), end(start(p, unit + 1, units)), whole(unit) {}
-  __device__ __forceinline__ bool next(const OrthoGemmParams& p, int units, Part& part) {
+  __device__ __forceinline__ Walk(const OrthoRunParams& p, const Product& q, int unit, int turn) {
+    const OrthoCut& c = p.cut[q.kind];
+    at = end = 0;
+    if (c.cut > 0) {
+      if (unit < c.units) {
+        at = start(c, q.k_iters, unit);
+        end = start(c, q.k_iters, unit + 1);
+      }
+      whole = unit;
+      stride = c.units;
+      whole_end = c.whole;
+    } else {
+      whole = unit - turn;
+      if (whole < 0) whole += p.units;
+      stride = p.units;
+      whole_end = q.per * p.batch;
+    }
+  }
+  __device__ __forceinline__ bool next(const Product& q, Part& part) {
     if (at < end) {
-      const int t = at / p.k_iters;
-      part.tile = p.whole_tiles + t;
-      part.k0 = at - t * p.k_iters;
-      part.k1 = min(p.k_iters, part.k0 + end - at);
+      const int t = at / q.k_iters;
+      part.tile = whole_end + t;
+      part.k0 = at - t * q.k_iters;
+      part.k1 = min(q.k_iters, part.k0 + end - at);
       at += part.k1 - part.k0;
       return true;
     }
-    if (whole < p.whole_tiles) {
-      part = {whole, 0, p.k_iters};
-      whole += units;
+    if (whole < whole_end) {
+      part.tile = whole;
+      part.k0 = 0;
+      part.k1 = q.k_iters;
+      whole += stride;
       return true;
     }
     return false;
   }
 };
 // The pair that has iteration x of the stretches.
-__device__ __forceinline__ int owner_of(const OrthoGemmParams& p, int x, int units) {
-  return ((x + 1) * units - 1) / (p.split_tiles * p.k_iters);
+__device__ __forceinline__ int owner_of(const OrthoCut& c, int k_iters, int x) {
+  return ((x + 1) * c.units - 1) / (c.cut * k_iters);
+}
+// The pair that the next product's first tile goes to.
+__device__ __forceinline__ int next_turn(const OrthoRunParams& p, const Product& q, int turn) {
+  return p.cut[q.kind].cut > 0 ? turn : (turn + q.per * p.batch) % p.units;
+}
+
+// What a product reads of a matrix is there once each epilogue warp of each
+// tile of the product before has counted one up. The counts go on over the
+// steps. Where tiles are cut, all matrices count together: the places of their
+// sums are used again by the next product.
+struct Need {
+  const int* count;
+  int least;
+};
+__device__ __forceinline__ int* count_of(const OrthoRunParams& p, int kind, int b) {
+  return p.finished + kind * p.batch + (p.joint ? 0 : b);
+}
+__device__ __forceinline__ Need need_of(const OrthoRunParams& p, const Product& q, int b) {
+  const int before = q.kind == 0 ? 2 : q.kind - 1;
+  const int per = before < 2 ? p.m_tiles * (p.m_tiles + 1) / 2 : p.m_tiles * p.n_tiles;
+  const int times = q.kind == 0 ? q.k : q.k + 1;
+  return {count_of(p, before, b), times * per * 2 * kWarps * (p.joint ? p.batch : 1)};
+}
+__device__ __forceinline__ bool wait_need(const Need& need, volatile int* abort_flag,
+                                          int* err_word) {
+  if (load_acquire(need.count) >= need.least) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (load_acquire(need.count) >= need.least) return true;
+    if ((it & 15u) == 0u && give_up(t0, abort_flag, err_word)) return false;
+  }
 }
 
 // A box of 32 x 32 16-bit values, rows of 64 bytes: the 16-byte pieces of a row
@@ -357,40 +435,279 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t sr
       "r"(src), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
-// Where a pair leaves a warp's sums of a part: of the first part of a tile
-// (which ends the pair's stretch) or of another (which begins it).
-__device__ __forceinline__ float4* share_of(const OrthoGemmParams& p, int unit, bool first,
-                                            int rank, int warp) {
-  const int64_t slot = ((unit * 2 + (first ? 1 : 0)) * 2 + rank) * kEpilogueWarps + warp;
-  return reinterpret_cast<float4*>(p.shares) + slot * (kCols / 64 * 8 * 32);
+// Until all but the last committed store have read shared memory.
+__device__ __forceinline__ void tma_store_wait_read_but_one() {
+  asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
 }
 template <class T>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
-  if constexpr (sizeof(T) == sizeof(__half) && !std::is_same_v<T, __half>) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  if constexpr (std::is_same_v<T, __half>) {
+    const __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
   } else {
-    const __half2 h = __floats2half2_rn(a, b);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
   }
 }
+// Where a pair leaves a warp's sums of a part: of the first part of a tile
+// (which ends the pair's stretch) or of another (which begins it).
+__device__ __forceinline__ float4* share_of(const OrthoRunParams& p, int unit, bool first,
+                                            int rank, int warp) {
+  const int64_t slot = ((unit * 2 + (first ? 1 : 0)) * 2 + rank) * kWarps + warp;
+  return reinterpret_cast<float4*>(p.shares) + slot * (kPieces * 8 * 32);
+}
 
-template <OrthoOp OP, class T>
+// The loads of a part: each CTA its 128 rows of one operand and 128 of the 256
+// of the other.
+struct Ring {
+  int stage;
+  uint32_t phase, armed, last;
+};
+template <Op OP>
+__device__ __forceinline__ bool load_part(const OrthoRunParams& p, const Product& q,
+                                          const Part& part, const Tile& t, uint32_t base, int rank,
+                                          Ctl* ctl, Ring& ring) {
+  constexpr bool kAcrossA = OP == kOutTall, kAcrossB = OP == kMul || OP == kOutWide;
+  const int from = q.k & 1;
+  const CUtensorMap* const a = OP == kGram   ? &p.x_along[from]
+                               : OP == kPoly ? &p.g_along
+                               : kAcrossA    ? &p.x_across[from]
+                                             : &p.p_along;
+  const CUtensorMap* const b = OP == kGram   ? &p.x_along[from]
+                               : OP == kPoly ? &p.g_along
+                               : kAcrossB    ? &p.x_across[from]
+                                             : &p.p_along;
+  const int a_side = t.m * kOrthoTile + rank * kRows, b_side = t.n * kOrthoTile + rank * kRows;
+  const int row0 = t.b * p.m_pad;
+  for (int k = part.k0; k < part.k1; ++k) {
+    const int s = ring.stage;
+    if (!wait_pair(smem_addr(&ctl->empty[s]), ring.phase ^ 1u, &ctl->abort, p.err_word))
+      return false;
+    const uint32_t full_local = smem_addr(&ctl->full[s]);
+    const uint32_t full = map_to_rank(full_local, 0);
+    if (rank == 0) mbar_arrive_expect_tx(full_local, 2 * kStageBytes);
+    const uint32_t dst = base + s * kStageBytes;
+    load_operand<kAcrossA>(dst, a, full, kAcrossA ? a_side : row0 + a_side,
+                           kAcrossA ? row0 + k * kDepth : k * kDepth);
+    load_operand<kAcrossB>(dst + kOperandBytes, b, full, kAcrossB ? b_side : row0 + b_side,
+                           kAcrossB ? row0 + k * kDepth : k * kDepth);
+    ring.armed |= 1u << s;
+    ring.last = (ring.last & ~(1u << s)) | (ring.phase << s);
+    if (++ring.stage == kStages) {
+      ring.stage = 0;
+      ring.phase ^= 1u;
+    }
+  }
+  return true;
+}
+
+template <Op OP>
+__device__ __forceinline__ bool multiply_part(const OrthoRunParams& p, const Part& part,
+                                              uint32_t base, uint32_t d, Ctl* ctl, Ring& ring) {
+  constexpr bool kAcrossA = OP == kOutTall, kAcrossB = OP == kMul || OP == kOutWide;
+  constexpr uint32_t idesc =
+      idesc_f16kind_f32(2 * kRows, kCols, kAcrossA ? 1 : 0, kAcrossB ? 1 : 0, 0);
+  for (int k = part.k0; k < part.k1; ++k) {
+    if (!wait_pair(smem_addr(&ctl->full[ring.stage]), ring.phase, &ctl->abort, p.err_word))
+      return false;
+    tc_fence_after_sync();
+    const uint32_t a0 = base + ring.stage * kStageBytes, b0 = a0 + kOperandBytes;
+#pragma unroll
+    for (int kk = 0; kk < kDepth / 16; ++kk)
+      umma_bf16_pair(d, slice_desc<kAcrossA>(a0, kk), slice_desc<kAcrossB>(b0, kk), idesc,
+                     k != part.k0 || kk != 0 ? 1u : 0u);
+    umma_commit_pair(smem_addr(&ctl->empty[ring.stage]), 0x3);
+    if (++ring.stage == kStages) {
+      ring.stage = 0;
+      ring.phase ^= 1u;
+    }
+  }
+  return true;
+}
+
+// A warp's 32 rows and 128 columns of a part's accumulator: stored, or left for
+// the warp that joins the tile's sums. Returns whether the tile is stored.
+template <Op OP, class T>
+__device__ __forceinline__ bool finish_part(const OrthoRunParams& p, const Product& q,
+                                            const Part& part, const Tile& t, uint32_t taddr,
+                                            int unit, int rank, int warp, int quarter, int first,
+                                            uint8_t* boxes, int lane) {
+  constexpr bool kOut = OP == kOutWide || OP == kOutTall;
+  const int row0 = t.m * kOrthoTile + rank * kRows + quarter * 32;  // of the matrix
+  const int row = row0 + lane;
+  const bool mirrored = (OP == kGram || OP == kPoly) && t.n > t.m;
+  const OrthoStep& st = p.step[q.k];
+  const int rows = kOut ? p.rows : p.m_rows;
+  const int cols = kOut ? p.cols : OP == kMul ? p.n_pad : p.m_rows;
+  float scale = OP == kGram ? st.gram : OP == kPoly ? st.poly : st.product;
+  if ((OP == kGram || OP == kMul || kOut) && q.k == 0) {
+    // the norm's factor belongs to the first step's x
+    const float f = p.factor[t.b];
+    scale *= OP == kGram ? f * f : f;
+  }
+  // Pieces of the tile that this warp keeps. Where the tile's contraction is
+  // cut, each pair leaves its sums, and the warp that comes last adds all of
+  // them, in the order of the contraction.
+  const int pieces =
+      row0 >= rows ? 0 : min(kPieces, (cols - t.n * kOrthoTile - first * 32 + 31) / 32);
+  int from = unit, to = unit;
+  if (part.k1 - part.k0 < q.k_iters) {
+    const OrthoCut& c = p.cut[q.kind];
+    const int x = (part.tile - c.whole) * q.k_iters;
+    from = owner_of(c, q.k_iters, x);
+    to = owner_of(c, q.k_iters, x + q.k_iters - 1);
+    int* const counter = p.arrived + ((part.tile - c.whole) * 2 + rank) * kWarps + warp;
+    int before = 0;
+    if (lane == 0) before = *reinterpret_cast<volatile int*>(counter);
+    before = __shfl_sync(0xffffffffu, before, 0);
+    if (before != to - from) {
+      float4* const mine = share_of(p, unit, unit == from, rank, warp) + lane;
+#pragma unroll 1
+      for (int i = 0; i < pieces; ++i) {
+        float v[32];
+        tmem_load_32cols(taddr + static_cast<uint32_t>((first + i) * 32), v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          mine[(i * 8 + j) * 32] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+      }
+      __threadfence();
+      __syncwarp();
+      if (lane == 0) before = atomicAdd(counter, 1);
+      before = __shfl_sync(0xffffffffu, before, 0);
+    }
+    if (before == to - from && lane == 0) *counter = 0;  // for the next product
+    __threadfence();
+    __syncwarp();
+    if (before != to - from) return false;
+  }
+  const uint4* old = nullptr;
+  uint4 held[4];
+  if constexpr (OP == kPoly) {
+    old = reinterpret_cast<const uint4*>(static_cast<const __half*>(p.gram) +
+                                         (int64_t(t.b) * p.m_pad + row) * p.m_pad +
+                                         t.n * kOrthoTile);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) held[i] = __ldcg(old + 4 * first + i);
+  }
+#pragma unroll 1
+  for (int i = 0; i < pieces; ++i) {
+    const int ch = first + i;
+    const int col = t.n * kOrthoTile + ch * 32;
+    float v[32];
+    tmem_load_32cols(taddr + static_cast<uint32_t>(ch * 32), v);
+    if (from < to) {
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {  // eight columns at a time
+        float sum[8] = {};
+        for (int u = from; u <= to; ++u) {
+          if (u == unit) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum[j] += v[8 * g + j];
+          } else {
+            const float4* const other =
+                share_of(p, u, u == from, rank, warp) + lane + (i * 8 + 2 * g) * 32;
+            const float4 f = __ldcg(other), h = __ldcg(other + 32);
+            sum[0] += f.x, sum[1] += f.y, sum[2] += f.z, sum[3] += f.w;
+            sum[4] += h.x, sum[5] += h.y, sum[6] += h.z, sum[7] += h.w;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[8 * g + j] = sum[j];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] *= scale;
+    if constexpr (OP == kPoly) {
+      const uint32_t w[16] = {held[0].x, held[0].y, held[0].z, held[0].w, held[1].x, held[1].y,
+                              held[1].z, held[1].w, held[2].x, held[2].y, held[2].z, held[2].w,
+                              held[3].x, held[3].y, held[3].z, held[3].w};
+      if (i + 1 < pieces) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) held[j] = __ldcg(old + 4 * (ch + 1) + j);
+      }
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+        v[2 * j] = fmaf(g.x, st.old, v[2 * j]);
+        v[2 * j + 1] = fmaf(g.y, st.old, v[2 * j + 1]);
+      }
+      if (row - col >= 0 && row - col < 32) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (row - col == j) v[j] += st.diag;
+      }
+    }
+    uint32_t w[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) w[j] = pack2<T>(v[2 * j], v[2 * j + 1]);
+    // The boxes' last contents have been taken: both boxes are a piece and its
+    // mirror image, or two pieces in turn.
+    if (lane == 0) {
+      if (mirrored || i == 0)
+        tma_store_wait_read();
+      else
+        tma_store_wait_read_but_one();
+    }
+    __syncwarp();
+    uint8_t* const box = mirrored ? boxes : boxes + (i & 1) * kBoxBytes;
+    uint8_t* const mirror = boxes + kBoxBytes;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      *reinterpret_cast<uint4*>(box + box_at(lane, j)) =
+          make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+    if (mirrored) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        *reinterpret_cast<uint16_t*>(mirror + box_at(j, lane >> 3) + (lane & 7) * 2) =
+            static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
+    }
+    if (kOut && !p.out_mapped) {
+      // rows that no map can describe: 32 values of one after the other
+      __syncwarp();
+      T* const out =
+          static_cast<T*>(p.out) + (int64_t(t.b) * rows + row0) * cols + col + lane;
+      const int some = rows - row0 < 32 ? rows - row0 : 32;
+      if (col + lane < cols) {
+#pragma unroll 8
+        for (int r = 0; r < some; ++r)
+          out[int64_t(r) * cols] =
+              *reinterpret_cast<const T*>(box + box_at(r, lane >> 3) + (lane & 7) * 2);
+      }
+      continue;
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      if constexpr (kOut) {
+        tma_store_3d(&p.out_store, smem_addr(box), col, row0, t.b);
+      } else {
+        const CUtensorMap* const c = OP == kGram   ? &p.g_store
+                                     : OP == kPoly ? &p.p_store
+                                                   : &p.x_store[(q.k & 1) ^ 1];
+        tma_store_2d(c, smem_addr(box), col, t.b * p.m_pad + row0);
+        if (mirrored) tma_store_2d(c, smem_addr(mirror), row0, t.b * p.m_pad + col);
+      }
+      tma_store_commit();
+    }
+  }
+  return true;
+}
+
+// All products of all steps. A grid of CTA pairs, all of them resident (a
+// cooperative launch), walks the products' tiles in order; a tile waits until
+// the product before has finished its matrix, so that matrices of a batch pass
+// one another and nothing but a matrix's own order holds a pair up.
+template <class T>
 __global__ void __launch_bounds__(kThreads, 1)
-    ortho_gemm_kernel(const __grid_constant__ OrthoGemmParams p) {
-  constexpr bool kSymmetric = OP == OrthoOp::kGram || OP == OrthoOp::kPoly;
-  constexpr bool kOut = OP == OrthoOp::kOutWide || OP == OrthoOp::kOutTall;
-  constexpr bool kAcrossA = OP == OrthoOp::kOutTall;
-  constexpr bool kAcrossB = OP == OrthoOp::kMul || OP == OrthoOp::kOutWide;
+    ortho_run_kernel(const __grid_constant__ OrthoRunParams p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* const boxes = smem_raw + (base - raw) + kStages * kStageBytes;
-  Ctl* const ctl = reinterpret_cast<Ctl*>(boxes + kEpilogueWarps * 2 * kBoxBytes);
+  Ctl* const ctl = reinterpret_cast<Ctl*>(boxes + kWarps * 2 * kBoxBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank());
-  const bool leader = rank == 0;
-  const int unit0 = blockIdx.x >> 1, units = gridDim.x >> 1;
+  const int unit = blockIdx.x >> 1;
   volatile int* const abort_flag = &ctl->abort;
 
   if (threadIdx.x == 0) {
@@ -400,15 +717,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_addr(&ctl->acc_full[b]), 1);
-      mbar_init(smem_addr(&ctl->acc_empty[b]), 2 * kEpilogueWarps);  // of both CTAs
+      mbar_init(smem_addr(&ctl->acc_empty[b]), 2 * kWarps);  // of both CTAs
     }
     mbar_init(smem_addr(&ctl->done), 1);
     ctl->abort = 0;
     fence_mbar_init();
   }
   if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&p.a_map);
-    tma_prefetch_desc(&p.b_map);
+    tma_prefetch_desc(&p.x_along[0]);
+    tma_prefetch_desc(&p.g_along);
+    tma_prefetch_desc(&p.p_along);
+    tma_prefetch_desc(&p.x_across[0]);
   }
   if (warp == 1) {
     tmem_alloc_pair(smem_addr(&ctl->tmem), 512);
@@ -418,83 +737,79 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_sync();
   tc_fence_after_sync();
   const uint32_t tmem = ctl->tmem;
-  if (threadIdx.x == 0) grid_launch_dependents();
+  const int products = 3 * p.steps;
+  int turn = 0;
 
   if (warp == 0) {
     if (lane == 0) {
-      // ---- loads: each CTA its 128 rows of a and 128 of b's 256
-      int stage = 0;
-      uint32_t phase = 0, armed = 0, last = 0;
+      Ring ring{};
       bool ok = true;
-      grid_dependency_wait();
-      Walk walk(p, unit0, units);
-      for (Part part; ok && walk.next(p, units, part);) {
-        const Tile t = tile_of<OP>(p, part.tile);
-        const int a_side = t.m * kOrthoTile + rank * kRows;
-        const int b_side = t.n * kOrthoTile + rank * kRows;
-        const int a_base = t.b * p.a_stride, b_base = t.b * p.b_stride;
-        for (int k = part.k0; k < part.k1; ++k) {
-          if (!wait_pair(smem_addr(&ctl->empty[stage]), phase ^ 1u, abort_flag, p.err_word)) {
-            ok = false;
-            break;
+      for (int i = 0; ok && i < products; ++i) {
+        const Product q = product_of(p, i);
+        Walk walk(p, q, unit, turn);
+        int ready = -1;  // the matrix whose operands are known to be there
+        for (Part part; ok && walk.next(q, part);) {
+          const Tile t = tile_of(q, part.tile);
+          if (i > 0 && t.b != ready) {
+            ok = wait_need(need_of(p, q, t.b), abort_flag, p.err_word);
+            if (!ok) break;
+            fence_proxy_async_global();
+            ready = t.b;
           }
-          const uint32_t full_local = smem_addr(&ctl->full[stage]);
-          const uint32_t full = map_to_rank(full_local, 0);
-          if (leader) mbar_arrive_expect_tx(full_local, 2 * kStageBytes);
-          const uint32_t dst = base + stage * kStageBytes;
-          load_operand<kAcrossA>(dst, &p.a_map, full, kAcrossA ? a_side : a_base + a_side,
-                                 kAcrossA ? a_base + k * kDepth : k * kDepth);
-          load_operand<kAcrossB>(dst + kOperandBytes, &p.b_map, full,
-                                 kAcrossB ? b_side : b_base + b_side,
-                                 kAcrossB ? b_base + k * kDepth : k * kDepth);
-          armed |= 1u << stage;
-          last = (last & ~(1u << stage)) | (phase << stage);
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1u;
+          switch (q.op) {
+            case kGram:
+              ok = load_part<kGram>(p, q, part, t, base, rank, ctl, ring);
+              break;
+            case kPoly:
+              ok = load_part<kPoly>(p, q, part, t, base, rank, ctl, ring);
+              break;
+            case kMul:
+            case kOutWide:
+              ok = load_part<kMul>(p, q, part, t, base, rank, ctl, ring);
+              break;
+            case kOutTall:
+              ok = load_part<kOutTall>(p, q, part, t, base, rank, ctl, ring);
+              break;
           }
         }
+        turn = next_turn(p, q, turn);
       }
-      if (!ok && leader) {
+      if (!ok && rank == 0) {
         for (int s = 0; s < kStages; ++s)
-          if (armed & (1u << s)) drain_pair(smem_addr(&ctl->full[s]), (last >> s) & 1u);
+          if (ring.armed & (1u << s)) drain_pair(smem_addr(&ctl->full[s]), (ring.last >> s) & 1u);
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && leader) {
-      // ---- products
-      constexpr uint32_t idesc =
-          idesc_f16kind_f32(2 * kRows, kCols, kAcrossA ? 1 : 0, kAcrossB ? 1 : 0, 0);
-      int stage = 0;
-      uint32_t phase = 0;
+    if (lane == 0 && rank == 0) {
+      Ring ring{};
       bool ok = true;
       int it = 0;
-      Walk walk(p, unit0, units);
-      for (Part part; ok && walk.next(p, units, part); ++it) {
-        const int buf = it & 1;
-        if (!wait_pair(smem_addr(&ctl->acc_empty[buf]), ((it >> 1) & 1u) ^ 1u, abort_flag,
-                       p.err_word))
-          break;
-        tc_fence_after_sync();
-        const uint32_t d = tmem + static_cast<uint32_t>(buf * kCols);
-        for (int k = part.k0; k < part.k1; ++k) {
-          if (!wait_pair(smem_addr(&ctl->full[stage]), phase, abort_flag, p.err_word)) {
-            ok = false;
-            break;
-          }
+      for (int i = 0; ok && i < products; ++i) {
+        const Product q = product_of(p, i);
+        Walk walk(p, q, unit, turn);
+        for (Part part; ok && walk.next(q, part); ++it) {
+          const int buf = it & 1;
+          ok = wait_pair(smem_addr(&ctl->acc_empty[buf]), ((it >> 1) & 1u) ^ 1u, abort_flag,
+                         p.err_word);
+          if (!ok) break;
           tc_fence_after_sync();
-          const uint32_t a0 = base + stage * kStageBytes, b0 = a0 + kOperandBytes;
-#pragma unroll
-          for (int kk = 0; kk < kDepth / 16; ++kk)
-            umma_bf16_pair(d, slice_desc<kAcrossA>(a0, kk), slice_desc<kAcrossB>(b0, kk), idesc,
-                           k != part.k0 || kk != 0 ? 1u : 0u);
-          umma_commit_pair(smem_addr(&ctl->empty[stage]), 0x3);
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1u;
+          const uint32_t d = tmem + static_cast<uint32_t>(buf * kCols);
+          switch (q.op) {
+            case kGram:
+            case kPoly:
+              ok = multiply_part<kGram>(p, part, base, d, ctl, ring);
+              break;
+            case kMul:
+            case kOutWide:
+              ok = multiply_part<kMul>(p, part, base, d, ctl, ring);
+              break;
+            case kOutTall:
+              ok = multiply_part<kOutTall>(p, part, base, d, ctl, ring);
+              break;
           }
+          if (ok) umma_commit_pair(smem_addr(&ctl->acc_full[buf]), 0x3);
         }
-        if (ok) umma_commit_pair(smem_addr(&ctl->acc_full[buf]), 0x3);
+        turn = next_turn(p, q, turn);
       }
       umma_commit_pair(smem_addr(&ctl->done), 0x3);
       drain_pair(smem_addr(&ctl->done), 0);
@@ -503,174 +818,68 @@ __global__ void __launch_bounds__(kThreads, 1)
       drain_pair(smem_addr(&ctl->done), 0);
     }
   } else {
-    // ---- results: a thread has a row of the tile, 32 columns at a time
     const int quarter = warp & 3;
+    const int first = (warp - 2) >> 2 ? kPieces : 0;
     const uint32_t acc_empty = map_to_rank(smem_addr(&ctl->acc_empty[0]), 0);
-    const int first = (warp - 2) >> 2 ? kCols / 64 : 0;  // of the eight pieces of 32 columns
     uint8_t* const box = boxes + (warp - 2) * 2 * kBoxBytes;
-    uint8_t* const mirror = box + kBoxBytes;
-    grid_dependency_wait();  // the gram and the factors
     int it = 0;
-    Walk walk(p, unit0, units);
-    for (Part part; walk.next(p, units, part); ++it) {
-      const Tile t = tile_of<OP>(p, part.tile);
-      const int buf = it & 1;
-      const int row0 = t.m * kOrthoTile + rank * kRows + quarter * 32;  // of the matrix
-      const int row = row0 + lane;
-      const bool mirrored = kSymmetric && t.n > t.m;
-      float scale = p.acc_scale;
-      if (p.factor != nullptr) {
-        const float f = p.factor[t.b];
-        scale *= p.factor_square ? f * f : f;
-      }
-      const uint4* old = nullptr;
-      uint4 held[4];
-      if constexpr (OP == OrthoOp::kPoly) {
-        old = reinterpret_cast<const uint4*>(static_cast<const __half*>(p.old) +
-                                             (int64_t(t.b) * p.m_pad + row) * p.m_pad +
-                                             t.n * kOrthoTile);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) held[i] = old[4 * first + i];
-      }
-      if (!__all_sync(0xffffffffu, wait_pair(smem_addr(&ctl->acc_full[buf]), (it >> 1) & 1u,
-                                             abort_flag, p.err_word)))
-        break;
-      tc_fence_after_sync();
-      const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) +
-                             static_cast<uint32_t>(buf * kCols);
-      // Pieces of the tile that this warp keeps. Where the tile's contraction
-      // is cut, each pair leaves its sums, and the warp that comes last adds
-      // all of them, in the order of the contraction.
-      const int pieces =
-          row0 >= p.rows ? 0 : min(kCols / 64, (p.cols - t.n * kOrthoTile - first * 32 + 31) / 32);
-      int from = unit0, to = unit0;
-      if (part.k1 - part.k0 < p.k_iters && pieces > 0) {
-        const int x = (part.tile - p.whole_tiles) * p.k_iters;
-        from = owner_of(p, x, units);
-        to = owner_of(p, x + p.k_iters - 1, units);
-        int* const counter = p.arrived +
-            ((part.tile - p.whole_tiles) * 2 + rank) * kEpilogueWarps + warp - 2;
-        int before = 0;
-        if (lane == 0) before = *reinterpret_cast<volatile int*>(counter);
-        before = __shfl_sync(0xffffffffu, before, 0);
-        if (before != to - from) {
-          float4* const mine = share_of(p, unit0, unit0 == from, rank, warp - 2) + lane;
-#pragma unroll 1
-          for (int i = 0; i < pieces; ++i) {
-            float v[32];
-            tmem_load_32cols(taddr + static_cast<uint32_t>((first + i) * 32), v);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              mine[(i * 8 + j) * 32] =
-                  make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-          }
+    bool ok = true;
+    for (int i = 0; ok && i < products; ++i) {
+      const Product q = product_of(p, i);
+      Walk walk(p, q, unit, turn);
+      int ready = -1;
+      for (Part part; walk.next(q, part); ++it) {
+        const Tile t = tile_of(q, part.tile);
+        if (q.op == kPoly && t.b != ready) {  // the gram is read here too
+          ok = __all_sync(0xffffffffu,
+                          lane != 0 || wait_need(need_of(p, q, t.b), abort_flag, p.err_word));
+          if (!ok) break;
           __threadfence();
           __syncwarp();
-          if (lane == 0) before = atomicAdd(counter, 1);
-          before = __shfl_sync(0xffffffffu, before, 0);
+          ready = t.b;
         }
-        if (before == to - from && lane == 0) *counter = 0;  // for the next launch
-        __threadfence();
-        __syncwarp();
-        if (before != to - from) from = to + 1;  // not the last
-      }
-#pragma unroll 1
-      for (int i = 0; from <= to && i < pieces; ++i) {
-        const int ch = first + i;
-        const int col = t.n * kOrthoTile + ch * 32;
-        float v[32];
-        tmem_load_32cols(taddr + static_cast<uint32_t>(ch * 32), v);
-        if (from < to) {
-          float sum[32];
-#pragma unroll
-          for (int j = 0; j < 32; ++j) sum[j] = 0.0f;
-          for (int q = from; q <= to; ++q) {
-            if (q == unit0) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) sum[j] += v[j];
-            } else {
-              const float4* const other = share_of(p, q, q == from, rank, warp - 2) + lane;
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const float4 f = __ldcg(other + (i * 8 + j) * 32);
-                sum[4 * j] += f.x;
-                sum[4 * j + 1] += f.y;
-                sum[4 * j + 2] += f.z;
-                sum[4 * j + 3] += f.w;
-              }
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = sum[j];
+        const int buf = it & 1;
+        ok = __all_sync(0xffffffffu, wait_pair(smem_addr(&ctl->acc_full[buf]), (it >> 1) & 1u,
+                                               abort_flag, p.err_word));
+        if (!ok) break;
+        tc_fence_after_sync();
+        const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) +
+                               static_cast<uint32_t>(buf * kCols);
+        bool stored = false;
+        switch (q.op) {
+          case kGram:
+            stored = finish_part<kGram, __half>(p, q, part, t, taddr, unit, rank, warp - 2, quarter,
+                                                first, box, lane);
+            break;
+          case kPoly:
+            stored = finish_part<kPoly, __half>(p, q, part, t, taddr, unit, rank, warp - 2, quarter,
+                                                first, box, lane);
+            break;
+          case kMul:
+            stored = finish_part<kMul, __half>(p, q, part, t, taddr, unit, rank, warp - 2, quarter,
+                                               first, box, lane);
+            break;
+          case kOutWide:
+            finish_part<kOutWide, T>(p, q, part, t, taddr, unit, rank, warp - 2, quarter, first,
+                                     box, lane);
+            break;
+          case kOutTall:
+            finish_part<kOutTall, T>(p, q, part, t, taddr, unit, rank, warp - 2, quarter, first,
+                                     box, lane);
+            break;
         }
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] *= scale;
-        if constexpr (OP == OrthoOp::kPoly) {
-          const uint32_t w[16] = {held[0].x, held[0].y, held[0].z, held[0].w,
-                                  held[1].x, held[1].y, held[1].z, held[1].w,
-                                  held[2].x, held[2].y, held[2].z, held[2].w,
-                                  held[3].x, held[3].y, held[3].z, held[3].w};
-          if (ch + 1 < first + kCols / 64) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) held[i] = old[4 * (ch + 1) + i];
-          }
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-            v[2 * i] = fmaf(g.x, p.old_scale, v[2 * i]);
-            v[2 * i + 1] = fmaf(g.y, p.old_scale, v[2 * i + 1]);
-          }
-          if (row - col >= 0 && row - col < 32) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (row - col == j) v[j] += p.diag;
-          }
-        }
-        uint32_t w[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) w[i] = pack2<T>(v[2 * i], v[2 * i + 1]);
-        // the boxes' last contents have been taken
-        if (lane == 0) tma_store_wait_read();
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<uint4*>(box + box_at(lane, i)) =
-              make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-        if (mirrored) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            *reinterpret_cast<uint16_t*>(mirror + box_at(i, lane >> 3) + (lane & 7) * 2) =
-                static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
-        }
-        if (kOut && !p.out_mapped) {
-          // rows that no map can describe: 32 values of one after the other
-          __syncwarp();
-          T* const out = static_cast<T*>(p.out) +
-                         (int64_t(t.b) * p.rows + row0) * p.cols + col + lane;
-          const int rows = p.rows - row0 < 32 ? p.rows - row0 : 32;
-          if (col + lane < p.cols) {
-#pragma unroll 8
-            for (int r = 0; r < rows; ++r)
-              out[int64_t(r) * p.cols] = *reinterpret_cast<const T*>(
-                  box + box_at(r, lane >> 3) + (lane & 7) * 2);
-          }
-          continue;
-        }
-        fence_proxy_async_smem();
+        tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) {
-          if constexpr (kOut)
-            tma_store_3d(&p.c_map, smem_addr(box), col, row0, t.b);
-          else
-            tma_store_2d(&p.c_map, smem_addr(box), col, t.b * p.m_pad + row0);
-          if (mirrored) tma_store_2d(&p.c_map, smem_addr(mirror), row0, t.b * p.m_pad + col);
-          tma_store_commit();
+          mbar_arrive_cluster(acc_empty + static_cast<uint32_t>(buf * sizeof(uint64_t)));
+          if (stored) {
+            tma_store_wait_all();
+            fence_proxy_async_global();
+            add_release(count_of(p, q.kind, t.b), 1);
+          }
         }
       }
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0)
-        mbar_arrive_cluster(acc_empty + static_cast<uint32_t>(buf * sizeof(uint64_t)));
+      turn = next_turn(p, q, turn);
     }
     if (lane == 0) tma_store_wait_all();
   }
@@ -684,10 +893,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <OrthoOp OP, class T>
-cudaError_t launch_op(const OrthoGemmParams& p, cudaStream_t s) {
-  const auto kernel = ortho_gemm_kernel<OP, T>;
-  cudaError_t e =
+template <class T>
+cudaError_t launch_run(const OrthoRunParams& p, cudaStream_t s) {
+  const auto kernel = ortho_run_kernel<T>;
+  const cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
@@ -699,8 +908,8 @@ cudaError_t launch_op(const OrthoGemmParams& p, cudaStream_t s) {
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeCooperative;
+  attr[1].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, p);
@@ -743,23 +952,8 @@ cudaError_t launch_ortho_copy(const OrthoCopyParams& p, int dtype, cudaStream_t 
   return launch_copy<__half>(p, s);
 }
 
-cudaError_t launch_ortho_gemm(const OrthoGemmParams& p, OrthoOp op, int out_dtype,
-                              cudaStream_t s) {
-  switch (op) {
-    case OrthoOp::kGram:
-      return launch_op<OrthoOp::kGram, __half>(p, s);
-    case OrthoOp::kPoly:
-      return launch_op<OrthoOp::kPoly, __half>(p, s);
-    case OrthoOp::kMul:
-      return launch_op<OrthoOp::kMul, __half>(p, s);
-    case OrthoOp::kOutWide:
-      return out_dtype == FLCE_BF16 ? launch_op<OrthoOp::kOutWide, __nv_bfloat16>(p, s)
-                                    : launch_op<OrthoOp::kOutWide, __half>(p, s);
-    case OrthoOp::kOutTall:
-      return out_dtype == FLCE_BF16 ? launch_op<OrthoOp::kOutTall, __nv_bfloat16>(p, s)
-                                    : launch_op<OrthoOp::kOutTall, __half>(p, s);
-  }
-  return cudaErrorInvalidValue;
+cudaError_t launch_ortho_run(const OrthoRunParams& p, int out_dtype, cudaStream_t s) {
+  return out_dtype == FLCE_BF16 ? launch_run<__nv_bfloat16>(p, s) : launch_run<__half>(p, s);
 }
 
 }  // namespace flce

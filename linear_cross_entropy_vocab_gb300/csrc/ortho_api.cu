@@ -15,7 +15,7 @@ using namespace flce::host;
 
 constexpr int64_t kMaxSide = 1 << 20;
 constexpr int64_t kMaxBatch = 65535;
-constexpr int64_t kMaxSteps = 64;
+constexpr int64_t kMaxSteps = flce::kOrthoMaxSteps;
 
 bool float_type(int32_t d) { return d == FLCE_F32 || d == FLCE_BF16 || d == FLCE_F16; }
 size_t size_of(int32_t d) { return d == FLCE_F32 ? 4 : 2; }
@@ -126,11 +126,10 @@ Split split_of(int64_t tiles, int64_t k_iters, int64_t pairs) {
 }
 
 constexpr int32_t kArrived = 2 * kPlanPairs * 2 * flce::kOrthoWarps;
-constexpr size_t kArrivedBytes = kArrived * 4;
 
 struct Plan {
   int64_t m, n, m_pad, n_pad, parts;
-  size_t x[2], gram, poly, partial, factor, arrived, shares, total;
+  size_t x[2], gram, poly, partial, factor, counts, shares, total;
 };
 Plan plan_of(const flce_ortho_problem* p) {
   Plan q{};
@@ -150,8 +149,8 @@ Plan plan_of(const flce_ortho_problem* p) {
   q.poly = q.gram + g_bytes;
   q.partial = q.poly + g_bytes;
   q.factor = q.partial + align_256(b * static_cast<size_t>(q.parts) * 8);
-  q.arrived = q.factor + align_256(b * 4);
-  q.shares = q.arrived + kArrivedBytes;
+  q.counts = q.factor + align_256(b * 4);
+  q.shares = q.counts + align_256((kArrived + 3 * b) * 4);
   const int64_t side = q.m_pad / flce::kOrthoTile;
   const int64_t tiles = p->batch * side * ceil_div(q.n, flce::kOrthoTile);
   q.total = q.shares + static_cast<size_t>(2 * std::min(kPlanPairs, kMaxParts * tiles)) *
@@ -210,9 +209,9 @@ flce_status flce_orthogonalize(const flce_ortho_problem* p, const void* src, voi
   if (!aligned_to(src, size_of(p->dtype)) || !aligned_to(out, 2) || !aligned_to(err_word, 4))
     return fail(FLCE_ERR_UNSUPPORTED, "a pointer is misaligned for its type");
   const Plan plan = plan_of(p);
-  // coordinates and tile numbers are 32-bit
+  // coordinates are 32-bit, and so are the counts of tiles x 16 warps x 64 steps
   if (p->batch * plan.m_pad > (int64_t(1) << 30) ||
-      p->batch * ceil_div(plan.n, 256) * (plan.m_pad / 256) > (int64_t(1) << 30))
+      p->batch * ceil_div(plan.n, 256) * (plan.m_pad / 256) > (int64_t(1) << 20))
     return fail(FLCE_ERR_UNSUPPORTED, "the batch has too many rows");
   st = check_workspace(workspace, workspace_bytes, plan.total);
   if (st != FLCE_OK) return st;
@@ -244,123 +243,85 @@ flce_status flce_orthogonalize(const flce_ortho_problem* p, const void* src, voi
   c.x_shift = shift_for(bound);
   c.m_rows = static_cast<int32_t>(ceil_div(plan.m, 64) * 64);
   c.factor = reinterpret_cast<float*>(ws + plan.factor);
-  c.arrived = reinterpret_cast<int32_t*>(ws + plan.arrived);
-  c.arrived_count = kArrived;
+  c.count = reinterpret_cast<int32_t*>(ws + plan.counts);
+  c.counts = kArrived + 3 * c.batch;
   cudaError_t e = flce::launch_ortho_norm(c, p->dtype, s);
   if (e != cudaSuccess) return cuda_fail(e, "matrix norm kernel");
   e = flce::launch_ortho_copy(c, p->dtype, s);
   if (e != cudaSuccess) return cuda_fail(e, "matrix copy kernel");
 
-  // the maps of both copies, the gram and the polynomial
+  flce::OrthoRunParams r{};
   const int64_t x_rows = p->batch * plan.m_pad;
-  CUtensorMap x_along[2], x_across[2], x_store[2], g_along, g_store, p_along, p_store;
   const int copies = p->steps > 1 ? 2 : 1;
   for (int i = 0; i < copies; ++i) {
     uint8_t* const x = ws + plan.x[i];
-    if (!make_map(&x_along[i], x, plan.n_pad, x_rows, 64, 128, kLoad) ||
-        !make_map(&x_across[i], x, plan.n_pad, x_rows, 64, 64, kLoad) ||
-        !make_map(&x_store[i], x, plan.n_pad, x_rows, 32, 32, kStore))
+    if (!make_map(&r.x_along[i], x, plan.n_pad, x_rows, 64, 128, kLoad) ||
+        !make_map(&r.x_across[i], x, plan.n_pad, x_rows, 64, 64, kLoad) ||
+        !make_map(&r.x_store[i], x, plan.n_pad, x_rows, 32, 32, kStore))
       return FLCE_ERR_CUDA;
   }
-  if (!make_map(&g_along, ws + plan.gram, plan.m_pad, x_rows, 64, 128, kLoad) ||
-      !make_map(&g_store, ws + plan.gram, plan.m_pad, x_rows, 32, 32, kStore) ||
-      !make_map(&p_along, ws + plan.poly, plan.m_pad, x_rows, 64, 128, kLoad) ||
-      !make_map(&p_store, ws + plan.poly, plan.m_pad, x_rows, 32, 32, kStore))
+  if (!make_map(&r.g_along, ws + plan.gram, plan.m_pad, x_rows, 64, 128, kLoad) ||
+      !make_map(&r.g_store, ws + plan.gram, plan.m_pad, x_rows, 32, 32, kStore) ||
+      !make_map(&r.p_along, ws + plan.poly, plan.m_pad, x_rows, 64, 128, kLoad) ||
+      !make_map(&r.p_store, ws + plan.poly, plan.m_pad, x_rows, 32, 32, kStore))
     return FLCE_ERR_CUDA;
   // maps take rows of whole 16 bytes
   const bool out_mapped = p->cols % 8 == 0 && aligned_to(out, 16);
-  CUtensorMap out_store{};
-  if (out_mapped && !make_map(&out_store, out, p->cols, p->rows, 32, 32, kStore, p->batch))
+  if (out_mapped && !make_map(&r.out_store, out, p->cols, p->rows, 32, 32, kStore, p->batch))
     return FLCE_ERR_CUDA;
 
-  const int32_t m_tiles = static_cast<int32_t>(plan.m_pad / flce::kOrthoTile);
-  const int32_t n_tiles = static_cast<int32_t>(ceil_div(plan.n, flce::kOrthoTile));
-  const int32_t m_pad = static_cast<int32_t>(plan.m_pad);
-  const int64_t pairs = std::min<int64_t>(kPlanPairs, sms / 2);
-  const auto cut = [&](flce::OrthoGemmParams& g, int64_t tiles) {
-    const Split split = split_of(tiles * p->batch, g.k_iters, pairs);
-    g.units = static_cast<int32_t>(split.units);
-    g.whole_tiles = static_cast<int32_t>(split.whole);
-    g.split_tiles = static_cast<int32_t>(split.cut);
-    g.shares = ws + plan.shares;
-    g.arrived = c.arrived;
-  };
-  const int64_t triangle = int64_t(m_tiles) * (m_tiles + 1) / 2;
   for (int k = 0; k < p->steps; ++k) {
     const float* const abc = p->coefficients + 3 * k;
     const double g_scale = scale_for(bound * bound);
     const double p_scale = scale_for(poly_bound(abc[0], abc[1], abc[2], bound * bound));
     bound = step_bound(abc[0], abc[1], abc[2], bound) * (1.0 + 1.0 / 64);
-    const double next_scale = scale_for(bound);
-    const int from = k & 1;
-    const bool last = k + 1 == p->steps;
-    flce::OrthoGemmParams g{};
-    g.batch = static_cast<int32_t>(p->batch);
-    g.m_pad = m_pad;
-    g.a_stride = g.b_stride = m_pad;
-    g.err_word = err_word;
-    // the norm's factor belongs to the first step's x
-    const float* const factor = k == 0 ? c.factor : nullptr;
-
-    g.a_map = g.b_map = x_along[from];
-    g.c_map = g_store;
-    g.m_tiles = g.n_tiles = m_tiles;
-    g.rows = g.cols = c.m_rows;
-    g.k_iters = static_cast<int32_t>(plan.n_pad / 64);
-    g.acc_scale = static_cast<float>(g_scale / (x_scale * x_scale));
-    g.factor = factor;
-    g.factor_square = 1;
-    cut(g, triangle);
-    e = flce::launch_ortho_gemm(g, flce::OrthoOp::kGram, 0, s);
-    if (e != cudaSuccess) return cuda_fail(e, "gram kernel");
-
-    g.a_map = g.b_map = g_along;
-    g.c_map = p_store;
-    g.k_iters = static_cast<int32_t>(ceil_div(plan.m, 64));
-    g.acc_scale = static_cast<float>(abc[2] * p_scale / (g_scale * g_scale));
-    g.factor = nullptr;
-    g.old = ws + plan.gram;
-    g.old_scale = static_cast<float>(abc[1] * p_scale / g_scale);
-    g.diag = static_cast<float>(abc[0] * p_scale);
-    cut(g, triangle);
-    e = flce::launch_ortho_gemm(g, flce::OrthoOp::kPoly, 0, s);
-    if (e != cudaSuccess) return cuda_fail(e, "polynomial kernel");
-
-    g.factor = factor;
-    g.factor_square = 0;
-    if (last && tall) {
-      g.a_map = x_across[from];
-      g.b_map = p_along;
-      g.m_tiles = n_tiles;
-      g.n_tiles = m_tiles;
-    } else {
-      g.a_map = p_along;
-      g.b_map = x_across[from];
-      g.m_tiles = m_tiles;
-      g.n_tiles = n_tiles;
-    }
-    if (last) {
-      g.acc_scale = static_cast<float>(1.0 / (x_scale * p_scale));
-      g.out = out;
-      g.c_map = out_store;
-      g.out_mapped = out_mapped ? 1 : 0;
-      g.rows = c.rows;
-      g.cols = c.cols;
-    } else {
-      g.acc_scale = static_cast<float>(next_scale / (x_scale * p_scale));
-      g.c_map = x_store[1 - from];
-      g.rows = c.m_rows;
-      g.cols = c.n_pad;
-    }
-    cut(g, int64_t(m_tiles) * n_tiles);
-    const flce::OrthoOp op = !last ? flce::OrthoOp::kMul
-                             : tall ? flce::OrthoOp::kOutTall
-                                    : flce::OrthoOp::kOutWide;
-    e = flce::launch_ortho_gemm(g, op, p->out_dtype, s);
-    if (e != cudaSuccess) return cuda_fail(e, "product kernel");
+    const double next_scale = k + 1 == p->steps ? 1.0 : scale_for(bound);
+    flce::OrthoStep& t = r.step[k];
+    t.gram = static_cast<float>(g_scale / (x_scale * x_scale));
+    t.poly = static_cast<float>(abc[2] * p_scale / (g_scale * g_scale));
+    t.old = static_cast<float>(abc[1] * p_scale / g_scale);
+    t.diag = static_cast<float>(abc[0] * p_scale);
+    t.product = static_cast<float>(next_scale / (x_scale * p_scale));
     x_scale = next_scale;
   }
-  return FLCE_OK;
+  r.steps = p->steps;
+  r.batch = c.batch;
+  r.m_tiles = static_cast<int32_t>(plan.m_pad / flce::kOrthoTile);
+  r.n_tiles = static_cast<int32_t>(ceil_div(plan.n, flce::kOrthoTile));
+  r.k_n = static_cast<int32_t>(plan.n_pad / 64);
+  r.k_m = static_cast<int32_t>(ceil_div(plan.m, 64));
+  r.m_pad = c.m_pad;
+  r.m_rows = c.m_rows;
+  r.n_pad = c.n_pad;
+  r.tall = c.tall;
+  r.out_mapped = out_mapped ? 1 : 0;
+  r.rows = c.rows;
+  r.cols = c.cols;
+  r.factor = c.factor;
+  r.gram = ws + plan.gram;
+  r.out = out;
+  r.shares = ws + plan.shares;
+  r.arrived = c.count;
+  r.finished = c.count + kArrived;
+  r.err_word = err_word;
+  const int64_t pairs = std::min<int64_t>(kPlanPairs, sms / 2);
+  const int64_t triangle = p->batch * r.m_tiles * (r.m_tiles + 1) / 2;
+  const int64_t all = p->batch * r.m_tiles * r.n_tiles;
+  // Matrices of a batch fill each other's rounds: their tiles stay whole, unless
+  // there are too few of them all the same.
+  const bool whole = p->batch > 1 && all >= pairs;
+  for (int i = 0; i < 3; ++i) {
+    const int64_t tiles = i < 2 ? triangle : all;
+    const Split split = whole ? Split{std::min(tiles, pairs), tiles, 0}
+                              : split_of(tiles, i == 0 ? r.k_n : r.k_m, pairs);
+    r.cut[i].units = static_cast<int32_t>(split.units);
+    r.cut[i].whole = static_cast<int32_t>(split.whole);
+    r.cut[i].cut = static_cast<int32_t>(split.cut);
+    r.units = std::max(r.units, r.cut[i].units);
+    if (split.cut > 0) r.joint = 1;
+  }
+  e = flce::launch_ortho_run(r, p->out_dtype, s);
+  return e == cudaSuccess ? FLCE_OK : cuda_fail(e, "orthogonalising kernel");
 }
 
 }  // extern "C"
