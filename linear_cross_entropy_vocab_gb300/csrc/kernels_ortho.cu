@@ -580,15 +580,21 @@ __device__ __forceinline__ bool finish_part(const OrthoRunParams& p, const Produ
     __syncwarp();
     if (before != to - from) return false;
   }
-  const uint4* old = nullptr;
-  uint4 held[4];
-  if constexpr (OP == kPoly) {
-    old = reinterpret_cast<const uint4*>(static_cast<const __half*>(p.gram) +
-                                         (int64_t(t.b) * p.m_pad + row) * p.m_pad +
-                                         t.n * kOrthoTile);
+  // The gram's values of this piece and the next: four lanes take 64 bytes of a
+  // row, so that a load touches eight lines and not 32.
+  uint4 held[2][4];
+  const uint4* const old = reinterpret_cast<const uint4*>(
+      static_cast<const __half*>(p.gram) +
+      (int64_t(t.b) * p.m_pad + row0 + (lane >> 2)) * p.m_pad + t.n * kOrthoTile + first * 32 +
+      (lane & 3) * 8);
+  const auto fetch = [&](uint4(&g)[4], int i) {
+    if (OP == kPoly && i < pieces) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) held[i] = __ldcg(old + 4 * first + i);
-  }
+      for (int j = 0; j < 4; ++j) g[j] = __ldcg(old + 4 * i + j * p.m_pad);  // eight rows further
+    }
+  };
+  fetch(held[0], 0);
+  fetch(held[1], 1);
 #pragma unroll 1
   for (int i = 0; i < pieces; ++i) {
     const int ch = first + i;
@@ -617,29 +623,6 @@ __device__ __forceinline__ bool finish_part(const OrthoRunParams& p, const Produ
     }
 #pragma unroll
     for (int j = 0; j < 32; ++j) v[j] *= scale;
-    if constexpr (OP == kPoly) {
-      const uint32_t w[16] = {held[0].x, held[0].y, held[0].z, held[0].w, held[1].x, held[1].y,
-                              held[1].z, held[1].w, held[2].x, held[2].y, held[2].z, held[2].w,
-                              held[3].x, held[3].y, held[3].z, held[3].w};
-      if (i + 1 < pieces) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) held[j] = __ldcg(old + 4 * (ch + 1) + j);
-      }
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-        v[2 * j] = fmaf(g.x, st.old, v[2 * j]);
-        v[2 * j + 1] = fmaf(g.y, st.old, v[2 * j + 1]);
-      }
-      if (row - col >= 0 && row - col < 32) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (row - col == j) v[j] += st.diag;
-      }
-    }
-    uint32_t w[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) w[j] = pack2<T>(v[2 * j], v[2 * j + 1]);
     // The boxes' last contents have been taken: both boxes are a piece and its
     // mirror image, or two pieces in turn.
     if (lane == 0) {
@@ -651,6 +634,33 @@ __device__ __forceinline__ bool finish_part(const OrthoRunParams& p, const Produ
     __syncwarp();
     uint8_t* const box = mirrored ? boxes : boxes + (i & 1) * kBoxBytes;
     uint8_t* const mirror = boxes + kBoxBytes;
+    if constexpr (OP == kPoly) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<uint4*>(box + box_at(8 * j + (lane >> 2), lane & 3)) = held[0][j];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) held[0][j] = held[1][j];
+      fetch(held[1], i + 2);
+      __syncwarp();
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const uint4 w = *reinterpret_cast<const uint4*>(box + box_at(lane, g));
+        const uint32_t h[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
+          v[8 * g + 2 * j] = fmaf(f.x, st.old, v[8 * g + 2 * j]);
+          v[8 * g + 2 * j + 1] = fmaf(f.y, st.old, v[8 * g + 2 * j + 1]);
+        }
+      }
+      if (row0 == col) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] += lane == j ? st.diag : 0.0f;
+      }
+    }
+    uint32_t w[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) w[j] = pack2<T>(v[2 * j], v[2 * j + 1]);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       *reinterpret_cast<uint4*>(box + box_at(lane, j)) =
