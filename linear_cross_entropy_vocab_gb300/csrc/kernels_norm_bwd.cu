@@ -12,7 +12,9 @@
 // adds the CTAs' shares in their order, so that every run gives the same bits.
 // Rows of more than 16384 values take two passes: the means, and then columns
 // by blocks.
+#include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "norm_internal.h"
 #include "norm_rows.cuh"
@@ -21,10 +23,10 @@
 namespace flce {
 namespace {
 
-template <class T, bool VEC, int TEAM, int VECS, int THREADS, int CTAS>
+template <class T, int TEAM, int VECS, int THREADS, int CTAS>
 __global__ void __launch_bounds__(THREADS, CTAS) rms_norm_bwd_kernel(const NormBwdParams p) {
   static_assert(TEAM == 32 || TEAM == THREADS, "a team is a warp or the CTA");
-  using Cols = Columns<TEAM, VEC>;
+  using Cols = Columns<TEAM, false>;
   constexpr int kTeams = THREADS / TEAM;
   __shared__ float sum_buf[2][THREADS / 32];
   __shared__ float share[kTeams > 1 ? kTeams : 1][kTeams > 1 ? TEAM * VECS * 8 : 1];
@@ -111,6 +113,168 @@ __global__ void __launch_bounds__(THREADS, CTAS) rms_norm_bwd_kernel(const NormB
   }
 }
 
+// Through L1: the two halves of eight fp32 values lie in the same sectors for
+// both of their copies (past it, 16384 x 4096 fp32 takes 262 us instead of 171).
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int LEFT>
+__device__ __forceinline__ void copy_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
+// The same for rows of whole groups at 16-byte boundaries, copied to shared
+// memory some rows ahead. Each thread copies what it reads itself, so that
+// nothing but its own copies has to be waited for. R: the type of the sum.
+// 32768 x 4096 bf16: 174 us (6.1 TB/s) with up to 192 KB an SM on their way,
+// 226 with a row ahead in registers, 396 without.
+template <class T, class R, int THREADS, int VECS>
+struct Ring {
+  static constexpr int kT = sizeof(T) == 4 ? 2 : 1, kR = sizeof(R) == 4 ? 2 : 1;  // of 16 bytes
+  static constexpr int kPieces = VECS * (2 * kR + kT);
+  static constexpr int kStage = kPieces * THREADS * 16;
+};
+template <class T, class R, int TEAM, int VECS, int THREADS, int CTAS, int DEPTH>
+__global__ void __launch_bounds__(THREADS, CTAS) rms_norm_bwd_rows_kernel(const NormBwdParams p) {
+  static_assert(TEAM == 32 || TEAM == THREADS, "a team is a warp or the CTA");
+  using Stage = Ring<T, R, THREADS, VECS>;
+  constexpr int kT = Stage::kT, kR = Stage::kR, kPieces = Stage::kPieces;
+  constexpr int kTeams = THREADS / TEAM;
+  extern __shared__ __align__(16) uint4 ring[];
+  __shared__ float sum_buf[2][THREADS / 32];
+  __shared__ float share[kTeams > 1 ? kTeams : 1][kTeams > 1 ? TEAM * VECS * 8 : 1];
+  const int t = static_cast<int>(threadIdx.x) % TEAM;
+  const int team = static_cast<int>(threadIdx.x) / TEAM;
+  const int64_t h = p.h, step = static_cast<int64_t>(gridDim.x) * kTeams;
+  const int e = t * 8;
+  const float inv_h = __fdiv_rn(1.0f, static_cast<float>(h));
+  const bool adds = p.grad_sum != nullptr, weighs = p.weight != nullptr;
+  float acc[VECS][8];
+  Raw<T> w[VECS];
+  int64_t row = static_cast<int64_t>(blockIdx.x) * kTeams + team;
+  grid_launch_dependents();
+#pragma unroll
+  for (int i = 0; i < VECS; ++i) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[i][j] = 0.0f;
+    w[i].clear();
+    if (weighs && !p.weight_wide && e + i * TEAM * 8 < h)
+      w[i].load(static_cast<const T*>(p.weight) + e + i * TEAM * 8);
+  }
+  // piece k of this thread in a stage: of the sum, its gradient and grad_y
+  const auto slot = [&](int stage, int k) {
+    return ring + (stage * kPieces + k) * THREADS + threadIdx.x;
+  };
+  const auto copy = [&](int64_t at, int stage) {
+    if (at < p.n) {
+      const R* const pt = static_cast<const R*>(p.total) + at * p.total_pitch + e;
+      const R* const ps = static_cast<const R*>(p.grad_sum) + at * h + e;
+      const T* const py = static_cast<const T*>(p.grad_y) + at * h + e;
+#pragma unroll
+      for (int i = 0; i < VECS; ++i) {
+        if (e + i * TEAM * 8 >= h) continue;
+#pragma unroll
+        for (int k = 0; k < kR; ++k) {
+          copy_async16(smem_addr(slot(stage, i * kR + k)),
+                       reinterpret_cast<const uint4*>(pt + i * TEAM * 8) + k);
+          if (adds)
+            copy_async16(smem_addr(slot(stage, (VECS + i) * kR + k)),
+                         reinterpret_cast<const uint4*>(ps + i * TEAM * 8) + k);
+        }
+#pragma unroll
+        for (int k = 0; k < kT; ++k)
+          copy_async16(smem_addr(slot(stage, 2 * VECS * kR + i * kT + k)),
+                       reinterpret_cast<const uint4*>(py + i * TEAM * 8) + k);
+      }
+    }
+    copy_async_commit();
+  };
+#pragma unroll
+  for (int d = 0; d < DEPTH - 1; ++d) copy(row + d * step, d);
+  float next_rstd = row < p.n ? p.rstd[row] : 0.0f;
+  int stage = 0;
+  for (int turn = 0; row < p.n; row += step, turn ^= 1) {
+    float unit[VECS][8], u[VECS][8];
+    float dot = 0.0f;
+    const float inv = next_rstd;
+    copy_async_wait<DEPTH - 2>();
+    if (row + step < p.n) next_rstd = p.rstd[row + step];
+#pragma unroll
+    for (int i = 0; i < VECS; ++i) {
+      Raw<R> total;
+      Raw<T> dy;
+      total.clear();
+      dy.clear();
+      if (e + i * TEAM * 8 < h) {
+#pragma unroll
+        for (int k = 0; k < kR; ++k) total.q[k] = *slot(stage, i * kR + k);
+#pragma unroll
+        for (int k = 0; k < kT; ++k) dy.q[k] = *slot(stage, 2 * VECS * kR + i * kT + k);
+      }
+      total.values(unit[i]);
+      dy.values(u[i]);
+      float v[8];
+      if (weighs) {
+        if (p.weight_wide)
+          Columns<TEAM, true>::load(static_cast<const float*>(p.weight), e + i * TEAM * 8, h, v);
+        else
+          w[i].values(v);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        unit[i][j] *= inv;
+        acc[i][j] = fmaf(u[i][j], unit[i][j], acc[i][j]);
+        if (weighs) u[i][j] *= v[j];
+        dot = fmaf(u[i][j], unit[i][j], dot);
+      }
+    }
+    // into the stage that the row before has left
+    copy(row + (DEPTH - 1) * step, stage == 0 ? DEPTH - 1 : stage - 1);
+    // rows in turn use two buffers: a warp that is a row ahead has passed the
+    // barrier of the row before
+    const float mean = team_all<TEAM>(dot, sum_buf[turn], SumOp{}) * inv_h;
+#pragma unroll
+    for (int i = 0; i < VECS; ++i) {
+      const int c = e + i * TEAM * 8;
+      if (c >= h) continue;
+      float g[8] = {};
+      if (adds) {
+        Raw<R> gs;
+#pragma unroll
+        for (int k = 0; k < kR; ++k) gs.q[k] = *slot(stage, (VECS + i) * kR + k);
+        gs.values(g);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        g[j] = fmaf(inv, fmaf(-unit[i][j], mean, u[i][j]), g[j]);
+      if (p.grad_x != nullptr) store8(static_cast<T*>(p.grad_x) + row * h + c, g);
+      if (p.grad_residual != nullptr) store8(static_cast<float*>(p.grad_residual) + row * h + c, g);
+    }
+    if (++stage == DEPTH) stage = 0;
+  }
+  if (p.grad_weight == nullptr) return;
+  if constexpr (kTeams > 1) {
+#pragma unroll
+    for (int i = 0; i < VECS; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) share[team][e + i * TEAM * 8 + j] = acc[i][j];
+    __syncthreads();
+    for (int64_t c = threadIdx.x; c < h; c += THREADS) {
+      float v = share[0][c];
+      for (int k = 1; k < kTeams; ++k) v += share[k][c];
+      p.partial[static_cast<int64_t>(blockIdx.x) * h + c] = v;
+    }
+  } else {
+    float* const out = p.partial + static_cast<int64_t>(blockIdx.x) * h + e;
+#pragma unroll
+    for (int i = 0; i < VECS; ++i)
+      if (e + i * TEAM * 8 < h) store8(out + i * TEAM * 8, acc[i]);
+  }
+}
+
 // grad_w of 32 columns a CTA: its 32 warps take the shares in turn, and their
 // sums are added in order.
 template <class W>
@@ -190,35 +354,82 @@ __global__ void __launch_bounds__(256) norm_bwd_columns_kernel(const NormBwdPara
   }
 }
 
-// CTAs an SM that the row kernel is compiled for.
-constexpr int ctas_of(int threads) { return threads >= 1024 ? 1 : threads >= 512 ? 1 : 512 / threads; }
+// How rows are dealt out: threads of a CTA, groups of eight values a thread,
+// rows of a CTA at a time and CTAs an SM, by the length of a row and the
+// kernel: value by value, groups with a 16-bit sum, groups with an fp32 sum.
+// One group a thread where the sum is fp32 leaves 64 registers a thread and
+// twice the threads: 16384 x 4096 with a bf16 x 220 us, 244 with half of them
+// (both before their copies went through L1; 163 now).
+struct Shape {
+  int threads, vecs, rows, ctas;
+};
+constexpr Shape shape_of(int64_t h, int kind) {
+  if (h <= 256) return {128, 1, 4, kind == 0 ? 4 : 5};
+  if (h <= 512) return {64, 1, 1, kind == 0 ? 8 : 10};
+  if (h <= 1024) return {128, 1, 1, kind == 0 ? 4 : 5};
+  if (kind == 2) {
+    if (h <= 2048) return {256, 1, 1, 4};
+    if (h <= 4096) return {512, 1, 1, 2};
+    if (h <= 8192) return {1024, 1, 1, 1};
+    return {1024, 2, 1, 1};
+  }
+  if (h <= 2048) return {128, 2, 1, 4};
+  if (h <= 4096) return {256, 2, 1, 2};
+  if (h <= 8192) return {512, 2, 1, 1};
+  return {1024, 2, 1, 1};
+}
 
-template <class T, bool VEC, int TEAM, int VECS, int THREADS = TEAM>
-cudaError_t launch_bwd_team(const NormBwdParams& p, int64_t parts, cudaStream_t s) {
-  rms_norm_bwd_kernel<T, VEC, TEAM, VECS, THREADS, ctas_of(THREADS)>
-      <<<static_cast<unsigned>(parts), THREADS, 0, s>>>(p);
+// Value by value, with the shape for rows of H values.
+template <class T, int H>
+cudaError_t launch_bwd_values(const NormBwdParams& p, int64_t parts, cudaStream_t s) {
+  constexpr Shape k = shape_of(H, 0);
+  constexpr int kTeam = k.rows > 1 ? 32 : k.threads;
+  rms_norm_bwd_kernel<T, kTeam, k.vecs, k.threads, k.ctas>
+      <<<static_cast<unsigned>(parts), k.threads, 0, s>>>(p);
   return cudaGetLastError();
 }
-
-struct Shape {
-  int threads, rows;  // of a CTA
-};
-Shape shape_of(int64_t h) {
-  if (h <= 256) return {128, 4};
-  if (h <= 2048) return {128, 1};
-  if (h <= 4096) return {256, 1};
-  if (h <= 8192) return {512, 1};
-  return {1024, 1};
+template <class T, class R, int H>
+cudaError_t launch_bwd_groups(const NormBwdParams& p, int64_t parts, cudaStream_t s) {
+  constexpr Shape k = shape_of(H, sizeof(R) == 4 ? 2 : 1);
+  constexpr int kTeam = k.rows > 1 ? 32 : k.threads;
+  constexpr int kStage = Ring<T, R, k.threads, k.vecs>::kStage;
+  constexpr int kFit = 200 * 1024 / k.ctas / kStage;
+  constexpr int kDepth = kFit > 4 ? 4 : kFit;
+  if constexpr (kDepth < 2) {  // no two rows in shared memory
+    return launch_bwd_values<T, H>(p, parts, s);
+  } else {
+    const auto kernel = rms_norm_bwd_rows_kernel<T, R, kTeam, k.vecs, k.threads, k.ctas, kDepth>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kDepth * kStage);
+    if (e != cudaSuccess) return e;
+    kernel<<<static_cast<unsigned>(parts), k.threads, kDepth * kStage, s>>>(p);
+    return cudaGetLastError();
+  }
 }
 
-template <class T, bool VEC>
-cudaError_t launch_bwd_rows(const NormBwdParams& p, int64_t parts, cudaStream_t s) {
-  if (p.h <= 256) return launch_bwd_team<T, VEC, 32, 1, 128>(p, parts, s);
-  if (p.h <= 1024) return launch_bwd_team<T, VEC, 128, 1>(p, parts, s);
-  if (p.h <= 2048) return launch_bwd_team<T, VEC, 128, 2>(p, parts, s);
-  if (p.h <= 4096) return launch_bwd_team<T, VEC, 256, 2>(p, parts, s);
-  if (p.h <= 8192) return launch_bwd_team<T, VEC, 512, 2>(p, parts, s);
-  return launch_bwd_team<T, VEC, 1024, 2>(p, parts, s);
+template <class T, class R>
+cudaError_t launch_bwd_rows(const NormBwdParams& p, bool groups, int64_t parts, cudaStream_t s) {
+  const auto by_length = [&](auto h) {
+    constexpr int H = decltype(h)::value;
+    return groups ? launch_bwd_groups<T, R, H>(p, parts, s) : launch_bwd_values<T, H>(p, parts, s);
+  };
+  if (p.h <= 256) return by_length(std::integral_constant<int, 256>{});
+  if (p.h <= 512) return by_length(std::integral_constant<int, 512>{});
+  if (p.h <= 1024) return by_length(std::integral_constant<int, 1024>{});
+  if (p.h <= 2048) return by_length(std::integral_constant<int, 2048>{});
+  if (p.h <= 4096) return by_length(std::integral_constant<int, 4096>{});
+  if (p.h <= 8192) return by_length(std::integral_constant<int, 8192>{});
+  return by_length(std::integral_constant<int, 16384>{});
+}
+
+// CTAs that take n rows.
+int64_t parts_of(int64_t n, int64_t h, int kind, int sms) {
+  if (n < 1) return 0;
+  if (h > kNormBwdMaxH) return n < 16 ? n : 16;
+  const Shape k = shape_of(h, kind);
+  const int64_t most = static_cast<int64_t>(sms) * k.ctas;
+  const int64_t need = (n + k.rows - 1) / k.rows;
+  return need < most ? need : most;
 }
 
 bool rows_of_16(const void* p, int64_t pitch, int size) {
@@ -244,7 +455,7 @@ cudaError_t launch_weight(const NormBwdParams& p, int64_t parts, cudaStream_t s)
 template <class T>
 cudaError_t launch_bwd_typed(const NormBwdParams& p, int sms, cudaStream_t s) {
   constexpr int e = sizeof(T);
-  const int64_t parts = norm_bwd_parts(p.n, p.h, sms);
+  int64_t parts = parts_of(p.n, p.h, 0, sms);
   cudaError_t err;
   if (p.h > kNormBwdMaxH) {
     norm_along_kernel<T><<<static_cast<unsigned>(p.n), 1024, 0, s>>>(p);
@@ -255,11 +466,13 @@ cudaError_t launch_bwd_typed(const NormBwdParams& p, int sms, cudaStream_t s) {
     err = cudaGetLastError();
   } else {
     const int wide = p.wide ? 4 : e;
-    const bool vec = p.h % 8 == 0 && rows_of_16(p.grad_y, p.h, e) &&
+    const bool groups = p.h % 8 == 0 && rows_of_16(p.grad_y, p.h, e) &&
                      rows_of_16(p.grad_sum, p.h, wide) &&
                      rows_of_16(p.total, p.total_pitch, wide) && rows_of_16(p.weight, 0, e) &&
                      rows_of_16(p.grad_x, p.h, e) && rows_of_16(p.grad_residual, p.h, 4);
-    err = vec ? launch_bwd_rows<T, true>(p, parts, s) : launch_bwd_rows<T, false>(p, parts, s);
+    if (groups) parts = parts_of(p.n, p.h, wide == 4 ? 2 : 1, sms);
+    err = sizeof(T) < 4 && p.wide ? launch_bwd_rows<T, float>(p, groups, parts, s)
+                                  : launch_bwd_rows<T, T>(p, groups, parts, s);
   }
   if (err != cudaSuccess || p.grad_weight == nullptr) return err;
   return e == 4 || p.weight_wide ? launch_weight<float>(p, parts, s)
@@ -269,12 +482,7 @@ cudaError_t launch_bwd_typed(const NormBwdParams& p, int sms, cudaStream_t s) {
 }  // namespace
 
 int64_t norm_bwd_parts(int64_t n, int64_t h, int sms) {
-  if (n < 1) return 0;
-  if (h > kNormBwdMaxH) return n < 16 ? n : 16;
-  const Shape shape = shape_of(h);
-  const int64_t most = static_cast<int64_t>(sms) * ctas_of(shape.threads);
-  const int64_t need = (n + shape.rows - 1) / shape.rows;
-  return need < most ? need : most;
+  return std::max({parts_of(n, h, 0, sms), parts_of(n, h, 1, sms), parts_of(n, h, 2, sms)});
 }
 
 cudaError_t launch_rms_norm_bwd(const NormBwdParams& p, int dtype, int sms, cudaStream_t s) {

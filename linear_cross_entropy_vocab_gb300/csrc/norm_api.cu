@@ -105,6 +105,7 @@ flce_status flce_rms_norm(const flce_norm_problem* p, const void* x, const void*
   if (st != FLCE_OK || p->n == 0) return st;
   flce::NormParams k = forward_params(p, x, residual, weight, sum_out);
   k.y = y;
+  k.sms = sms;
   k.rstd = rstd_out;
   const cudaError_t e = flce::launch_rms_norm(k, p->dtype, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FLCE_OK : cuda_fail(e, "norm kernel");
@@ -129,6 +130,7 @@ flce_status flce_rms_norm_quantize(const flce_norm_problem* p, const void* x,
   if (st != FLCE_OK || p->n == 0) return st;
   flce::NormParams k = forward_params(p, x, residual, weight, sum_out);
   k.q = q;
+  k.sms = sms;
   k.q_pitch = q_pitch;
   k.scale = scale;
   const cudaError_t e = flce::launch_rms_norm_q(k, p->dtype, static_cast<cudaStream_t>(stream));

@@ -20,7 +20,7 @@ struct NormParams {
   float* scale;
   float* rstd;           // or null
   int64_t n, h, x_pitch, residual_pitch, q_pitch;
-  int32_t wide, weight_wide;
+  int32_t wide, weight_wide, sms;
   float eps;
 };
 cudaError_t launch_rms_norm(const NormParams& p, int dtype, cudaStream_t s);
@@ -40,7 +40,7 @@ struct NormBwdParams {
   int64_t n, h, total_pitch;
   int32_t wide, weight_wide;
 };
-// CTAs that each leave one row of partial sums.
+// The most CTAs that each leave one row of partial sums.
 int64_t norm_bwd_parts(int64_t n, int64_t h, int sms);
 // Rows of more values go through `along`.
 constexpr int64_t kNormBwdMaxH = 16384;

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -75,6 +76,40 @@ __device__ __forceinline__ void store8(__half* p, const float (&v)[8]) {
   }
   *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
+
+// Eight values as they lie in memory.
+template <class T>
+struct Raw {
+  uint4 q[sizeof(T) == 4 ? 2 : 1];
+  __device__ __forceinline__ void load(const T* p) {
+    q[0] = *reinterpret_cast<const uint4*>(p);
+    if constexpr (sizeof(T) == 4) q[1] = *(reinterpret_cast<const uint4*>(p) + 1);
+  }
+  __device__ __forceinline__ void clear() {
+    q[0] = make_uint4(0, 0, 0, 0);
+    if constexpr (sizeof(T) == 4) q[1] = q[0];
+  }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+    if constexpr (sizeof(T) == 4) {
+      const uint32_t w[8] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+    } else {
+      const uint32_t w[4] = {q[0].x, q[0].y, q[0].z, q[0].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (std::is_same_v<T, __half>) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+          v[2 * i] = f.x;
+          v[2 * i + 1] = f.y;
+        } else {
+          v[2 * i] = __uint_as_float(w[i] << 16);
+          v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+      }
+    }
+  }
+};
 
 // Which columns a thread of a team of TEAM holds in its i-th group of eight.
 // VEC: eight neighbours, rows that start at 16-byte boundaries and have whole

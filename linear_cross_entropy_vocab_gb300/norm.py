@@ -59,84 +59,96 @@ def _rows(t: torch.Tensor):
     return t.contiguous(), h
 
 
-def _problem(x, weight, eps, residual, x_pitch, residual_pitch, n, h):
-    code = _DTYPES[x.dtype]
-    return abi.flce_norm_problem(n, h, x_pitch, residual_pitch, code,
-                                 code if residual is None else _DTYPES[residual.dtype],
-                                 code if weight is None else _DTYPES[weight.dtype], eps, 0)
-
-
 def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-def _forward(x, weight, eps, residual, rstd):
-    """(y, sum or None) of checked inputs; fills ``rstd`` where one is given."""
+def _prepare(x, weight, eps, residual):
+    """x, residual and weight as rows, and the problem that they make."""
     x, x_pitch = _rows(x)
     h = x.shape[-1]
-    n = x.numel() // h
-    residual_pitch, total = h, None
+    code = sum_code = weight_code = _DTYPES[x.dtype]
+    residual_pitch = h
     if residual is not None:
         residual, residual_pitch = _rows(residual)
-        total = torch.empty(x.shape, dtype=residual.dtype, device=x.device)
-    if weight is not None and not weight.is_contiguous():
-        weight = weight.contiguous()
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    with on_device(x.device):
-        abi.flce_rms_norm(_problem(x, weight, eps, residual, x_pitch, residual_pitch, n, h),
-                          x.data_ptr(), _ptr(residual), _ptr(weight), y.data_ptr(), _ptr(total),
-                          _ptr(rstd), raw_stream(x.device))
+        sum_code = _DTYPES[residual.dtype]
+    if weight is not None:
+        weight_code = _DTYPES[weight.dtype]
+        if not weight.is_contiguous():
+            weight = weight.contiguous()
+    problem = abi.flce_norm_problem(x.numel() // h, h, x_pitch, residual_pitch, code, sum_code,
+                                    weight_code, eps, 0)
+    return x, weight, residual, problem
+
+
+def _forward(x, weight, residual, problem, rstd):
+    """(y, sum or None); fills ``rstd`` where one is given."""
+    dense = torch.contiguous_format
+    y = torch.empty_like(x, memory_format=dense)
+    total = None if residual is None else torch.empty_like(residual, memory_format=dense)
+    dev = x.device
+    with on_device(dev):
+        abi.flce_rms_norm(problem, x.data_ptr(), _ptr(residual), _ptr(weight), y.data_ptr(),
+                          _ptr(total), _ptr(rstd), raw_stream(dev))
     return y, total
 
 
 class _RmsNorm(torch.autograd.Function):
+    # The backward runs in autograd's own thread, where Python takes several times as long: what
+    # it needs to know is worked out here.
     @staticmethod
     def forward(ctx, x, weight, eps, residual):
-        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-        y, total = _forward(x, weight, eps, residual, rstd)
         ctx.set_materialize_grads(False)
-        ctx.save_for_backward(x if residual is None else total, weight, rstd)
-        ctx.eps = eps
-        ctx.x_dtype = x.dtype
+        x, weight, residual, problem = _prepare(x, weight, eps, residual)
+        rstd = x.new_empty(problem.n, dtype=torch.float32)
+        y, total = _forward(x, weight, residual, problem, rstd)
+        if residual is None:
+            ctx.save_for_backward(x, weight, rstd)
+        else:
+            ctx.save_for_backward(total, weight, rstd)
+            problem.x_pitch = problem.h  # of the sum
+        ctx.plan = problem, abi.flce_rms_norm_backward_workspace_size(problem)
         return y if residual is None else (y, total)
 
     @staticmethod
-    @once_differentiable
     def backward(ctx, grad_y, grad_sum=None):
-        total, weight, rstd = ctx.saved_tensors
-        need_x, need_weight, _, need_residual = ctx.needs_input_grad
-        dev, dtype = total.device, ctx.x_dtype
-        if grad_y is None:  # y is not used: the sum's gradient passes through
-            none = grad_sum is None
-            return (grad_sum.to(dtype) if need_x and not none else None,
-                    torch.zeros_like(weight) if need_weight and not none else None, None,
-                    grad_sum if need_residual else None)
-        total, pitch = _rows(total)
-        h = total.shape[-1]
-        n = total.numel() // h
+        if torch.is_grad_enabled():  # a graph of the backward is asked for
+            return _backward_once(ctx, grad_y, grad_sum)
+        return _backward(ctx, grad_y, grad_sum)
+
+
+def _backward(ctx, grad_y, grad_sum):
+    total, weight, rstd = ctx.saved_tensors
+    need_x, need_weight, _, need_residual = ctx.needs_input_grad
+    problem, ws_bytes = ctx.plan
+    wide = problem.sum_dtype != problem.dtype
+    if grad_y is None:  # y is not used: the sum's gradient passes through
+        if grad_sum is None:
+            return None, None, None, None
+        dtype = next(t for t, code in _DTYPES.items() if code == problem.dtype)
+        return (grad_sum.to(dtype) if need_x else None,
+                torch.zeros_like(weight) if need_weight else None, None,
+                grad_sum if need_residual else None)
+    dev = grad_y.device
+    if not grad_y.is_contiguous():
         grad_y = grad_y.contiguous()
-        grad_sum = None if grad_sum is None else grad_sum.contiguous()
-        weight = None if weight is None else weight.contiguous()
-        wide = total.dtype != dtype
-        # in one type the gradients of x and of the residual are one tensor
-        grad_x = (torch.empty(total.shape, dtype=dtype, device=dev)
-                  if need_x or (need_residual and not wide) else None)
-        grad_residual = (torch.empty(total.shape, dtype=torch.float32, device=dev)
-                         if need_residual and wide else None)
-        grad_weight = torch.empty_like(weight) if need_weight else None
-        code = _DTYPES[dtype]
-        prob = abi.flce_norm_problem(n, h, pitch, h, code, _DTYPES[total.dtype],
-                                     code if weight is None else _DTYPES[weight.dtype], ctx.eps, 0)
-        with on_device(dev):
-            ws_bytes = abi.flce_rms_norm_backward_workspace_size(prob)
-            ws = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=dev)
-            abi.flce_rms_norm_backward(prob, grad_y.data_ptr(), _ptr(grad_sum), total.data_ptr(),
-                                       _ptr(weight), rstd.data_ptr(), _ptr(grad_x),
-                                       _ptr(grad_residual), _ptr(grad_weight), ws.data_ptr(),
-                                       ws_bytes, raw_stream(dev))
-        if need_residual and not wide:
-            grad_residual = grad_x
-        return grad_x if need_x else None, grad_weight, None, grad_residual
+    if grad_sum is not None and not grad_sum.is_contiguous():
+        grad_sum = grad_sum.contiguous()
+    # in one type the gradients of x and of the residual are one tensor
+    grad_x = torch.empty_like(grad_y) if need_x or (need_residual and not wide) else None
+    grad_residual = torch.empty_like(total) if need_residual and wide else None
+    grad_weight = torch.empty_like(weight) if need_weight else None
+    ws = rstd.new_empty((ws_bytes + 3) // 4)
+    with on_device(dev):
+        abi.flce_rms_norm_backward(
+            problem, grad_y.data_ptr(), _ptr(grad_sum), total.data_ptr(), _ptr(weight),
+            rstd.data_ptr(), _ptr(grad_x), _ptr(grad_residual), _ptr(grad_weight), ws.data_ptr(),
+            ws_bytes, raw_stream(dev))
+    return (grad_x if need_x else None, grad_weight, None,
+            grad_residual if wide else grad_x if need_residual else None)
+
+
+_backward_once = once_differentiable(_backward)
 
 
 def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: float = 1e-6, *,
@@ -157,7 +169,8 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: float 
     if forward_ad._current_level < 0 and not (torch.is_grad_enabled() and (
             x.requires_grad or weight is not None and weight.requires_grad
             or residual is not None and residual.requires_grad)):
-        y, total = _forward(x, weight, eps, residual, None)
+        x, weight, residual, problem = _prepare(x, weight, eps, residual)
+        y, total = _forward(x, weight, residual, problem, None)
         return y if residual is None else (y, total)
     return _RmsNorm.apply(x, weight, eps, residual)
 
@@ -173,22 +186,17 @@ def rms_norm_quantize(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
     _check_inputs(x, weight, eps, residual)
     refuse_gradient("rms_norm_quantize", ("x", "weight", "residual"), x, weight, residual)
     lead, h = x.shape[:-1], x.shape[-1]
-    x, x_pitch = _rows(x)
-    n = x.numel() // h
-    residual_pitch, total = h, None
-    if residual is not None:
-        residual, residual_pitch = _rows(residual)
-        total = torch.empty(x.shape, dtype=residual.dtype, device=x.device)
-    if weight is not None and not weight.is_contiguous():
-        weight = weight.contiguous()
+    x, weight, residual, problem = _prepare(x, weight, eps, residual)
+    dev = x.device
+    total = None if residual is None else torch.empty_like(
+        residual, memory_format=torch.contiguous_format)
     q_pitch = (h + 15) // 16 * 16
-    q = torch.empty(n, q_pitch, dtype=torch.int8, device=x.device)
-    scale = torch.empty(lead, dtype=torch.float32, device=x.device)
-    with on_device(x.device):
-        abi.flce_rms_norm_quantize(
-            _problem(x, weight, eps, residual, x_pitch, residual_pitch, n, h), x.data_ptr(),
-            _ptr(residual), _ptr(weight), q.data_ptr(), q_pitch, scale.data_ptr(), _ptr(total),
-            raw_stream(x.device))
+    q = torch.empty(problem.n, q_pitch, dtype=torch.int8, device=dev)
+    scale = x.new_empty(lead, dtype=torch.float32)
+    with on_device(dev):
+        abi.flce_rms_norm_quantize(problem, x.data_ptr(), _ptr(residual), _ptr(weight),
+                                   q.data_ptr(), q_pitch, scale.data_ptr(), _ptr(total),
+                                   raw_stream(dev))
     if q_pitch != h:
         q = q[:, :h]
     if len(lead) != 1:
