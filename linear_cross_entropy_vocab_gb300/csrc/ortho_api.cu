@@ -56,6 +56,26 @@ int shift_for(double bound) {
 }
 double scale_for(double bound) { return std::ldexp(1.0, shift_for(bound)); }
 
+// The scales of each step's operands, and what turns sums into them.
+void fill_steps(const flce_ortho_problem* p, flce::OrthoStep* step) {
+  double bound = 1.0;
+  double x_scale = scale_for(bound);
+  for (int k = 0; k < p->steps; ++k) {
+    const float* const abc = p->coefficients + 3 * k;
+    const double g_scale = scale_for(bound * bound);
+    const double p_scale = scale_for(poly_bound(abc[0], abc[1], abc[2], bound * bound));
+    bound = step_bound(abc[0], abc[1], abc[2], bound) * (1.0 + 1.0 / 64);
+    const double next_scale = k + 1 == p->steps ? 1.0 : scale_for(bound);
+    flce::OrthoStep& t = step[k];
+    t.gram = static_cast<float>(g_scale / (x_scale * x_scale));
+    t.poly = static_cast<float>(abc[2] * p_scale / (g_scale * g_scale));
+    t.old = static_cast<float>(abc[1] * p_scale / g_scale);
+    t.diag = static_cast<float>(abc[0] * p_scale);
+    t.product = static_cast<float>(next_scale / (x_scale * p_scale));
+    x_scale = next_scale;
+  }
+}
+
 flce_status check_problem(const flce_ortho_problem* p) {
   if (p == nullptr) return fail(FLCE_ERR_INVALID_ARG, "problem is NULL");
   if (p->batch < 0 || p->rows < 0 || p->cols < 0)
@@ -128,6 +148,7 @@ Split split_of(int64_t tiles, int64_t k_iters, int64_t pairs) {
 constexpr int32_t kArrived = 2 * kPlanPairs * 2 * flce::kOrthoWarps;
 
 struct Plan {
+  int64_t cluster, slab;  // of matrices that stay in shared memory, else 0
   int64_t m, n, m_pad, n_pad, parts;
   size_t x[2], gram, poly, partial, factor, counts, shares, total;
 };
@@ -135,6 +156,12 @@ Plan plan_of(const flce_ortho_problem* p) {
   Plan q{};
   q.m = std::min(p->rows, p->cols);
   q.n = std::max(p->rows, p->cols);
+  if (q.m <= 128 && q.n <= 512 * flce::kOrthoMaxCluster) {
+    q.cluster = 1;
+    while (q.n > 512 * q.cluster) q.cluster *= 2;
+    q.slab = std::max<int64_t>(64, ceil_div(ceil_div(q.n, q.cluster), 64) * 64);
+    return q;
+  }
   q.m_pad = ceil_div(q.m, flce::kOrthoTile) * flce::kOrthoTile;
   q.n_pad = ceil_div(q.n, 64) * 64;
   // shares of at least 8192 values
@@ -222,8 +249,27 @@ flce_status flce_orthogonalize(const flce_ortho_problem* p, const void* src, voi
   uint8_t* const ws = static_cast<uint8_t*>(workspace);
   const bool tall = p->rows > p->cols;
 
-  double bound = 1.0;
-  double x_scale = scale_for(bound);
+  if (plan.cluster > 0) {
+    flce::OrthoSmallParams k{};
+    fill_steps(p, k.step);
+    k.src = src;
+    k.batch_stride = p->batch_stride;
+    k.row_pitch = p->row_pitch;
+    k.out = out;
+    k.batch = static_cast<int32_t>(p->batch);
+    k.rows = static_cast<int32_t>(p->rows);
+    k.cols = static_cast<int32_t>(p->cols);
+    k.tall = tall ? 1 : 0;
+    k.steps = p->steps;
+    k.cluster = static_cast<int32_t>(plan.cluster);
+    k.slab = static_cast<int32_t>(plan.slab);
+    k.x_shift = shift_for(1.0);
+    k.out_bf16 = p->out_dtype == FLCE_BF16 ? 1 : 0;
+    k.eps = p->eps;
+    k.err_word = err_word;
+    const cudaError_t e = flce::launch_ortho_small(k, p->dtype, s);
+    return e == cudaSuccess ? FLCE_OK : cuda_fail(e, "orthogonalising kernel");
+  }
   flce::OrthoCopyParams c{};
   c.src = src;
   c.batch_stride = p->batch_stride;
@@ -240,7 +286,7 @@ flce_status flce_orthogonalize(const flce_ortho_problem* p, const void* src, voi
   c.partial = reinterpret_cast<double*>(ws + plan.partial);
   c.parts = static_cast<int32_t>(plan.parts);
   c.eps = p->eps;
-  c.x_shift = shift_for(bound);
+  c.x_shift = shift_for(1.0);
   c.m_rows = static_cast<int32_t>(ceil_div(plan.m, 64) * 64);
   c.factor = reinterpret_cast<float*>(ws + plan.factor);
   c.count = reinterpret_cast<int32_t*>(ws + plan.counts);
@@ -270,20 +316,7 @@ flce_status flce_orthogonalize(const flce_ortho_problem* p, const void* src, voi
   if (out_mapped && !make_map(&r.out_store, out, p->cols, p->rows, 32, 32, kStore, p->batch))
     return FLCE_ERR_CUDA;
 
-  for (int k = 0; k < p->steps; ++k) {
-    const float* const abc = p->coefficients + 3 * k;
-    const double g_scale = scale_for(bound * bound);
-    const double p_scale = scale_for(poly_bound(abc[0], abc[1], abc[2], bound * bound));
-    bound = step_bound(abc[0], abc[1], abc[2], bound) * (1.0 + 1.0 / 64);
-    const double next_scale = k + 1 == p->steps ? 1.0 : scale_for(bound);
-    flce::OrthoStep& t = r.step[k];
-    t.gram = static_cast<float>(g_scale / (x_scale * x_scale));
-    t.poly = static_cast<float>(abc[2] * p_scale / (g_scale * g_scale));
-    t.old = static_cast<float>(abc[1] * p_scale / g_scale);
-    t.diag = static_cast<float>(abc[0] * p_scale);
-    t.product = static_cast<float>(next_scale / (x_scale * p_scale));
-    x_scale = next_scale;
-  }
+  fill_steps(p, r.step);
   r.steps = p->steps;
   r.batch = c.batch;
   r.m_tiles = static_cast<int32_t>(plan.m_pad / flce::kOrthoTile);

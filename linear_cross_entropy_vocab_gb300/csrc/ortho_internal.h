@@ -76,4 +76,19 @@ struct OrthoRunParams {
 };
 cudaError_t launch_ortho_run(const OrthoRunParams& p, int out_dtype, cudaStream_t s);
 
+// Matrices with one side of at most 128, each in the shared memory of a cluster
+// of CTAs with `slab` columns each (a multiple of 64, at most 512).
+constexpr int kOrthoMaxCluster = 8;
+struct OrthoSmallParams {
+  OrthoStep step[kOrthoMaxSteps];
+  const void* src;
+  int64_t batch_stride, row_pitch;
+  void* out;  // dense
+  int32_t batch, rows, cols, tall, steps, cluster, slab;
+  int32_t x_shift, out_bf16;
+  float eps;
+  int32_t* err_word;
+};
+cudaError_t launch_ortho_small(const OrthoSmallParams& p, int dtype, cudaStream_t s);
+
 }  // namespace flce

@@ -67,6 +67,9 @@ def _matrices(batch, m, n, dtype, seed=0, scale=1e-3):
 SIZES = [(1, 1, 1), (1, 1, 9), (2, 5, 3), (1, 64, 64), (3, 100, 300), (1, 300, 100), (2, 256, 256),
          (1, 257, 511), (1, 130, 1000), (2, 513, 700), (1, 1000, 260), (5, 96, 64), (1, 1024, 600),
          (1, 64, 5000), (1, 3000, 33), (40, 16, 200), (1, 770, 1300),
+         # one side in shared memory, in clusters of 1 to 8, and just not
+         (1, 128, 512), (2, 128, 513), (3, 1500, 100), (1, 128, 4096), (2, 4090, 65), (1, 7, 4097),
+         (2, 129, 600), (300, 8, 24),
          # tiles whose contraction is cut between CTAs: few, or more than a round
          (1, 1024, 2100), (4, 4000, 700), (90, 20, 1000), (80, 300, 900), (30, 100, 3000)]
 
@@ -133,7 +136,7 @@ def test_addresses_and_strides():
 
 def test_what_surrounds_the_result_stays():
     """Sizes that end inside a tile: nothing is written past the result."""
-    for m, n in ((100, 300), (300, 100), (33, 257)):
+    for m, n in ((100, 300), (300, 100), (33, 257), (700, 99), (130, 257), (300, 400)):
         x = _matrices(2, m, n, torch.bfloat16)
         want = orthogonalize(x)
         import linear_cross_entropy_vocab_gb300.ortho as ortho
@@ -154,8 +157,9 @@ def test_what_surrounds_the_result_stays():
         assert bool((room[:2048] == 7).all()) and bool((room[2048 + 2 * m * n:] == 7).all())
 
 
-def test_extremes():
-    x = _matrices(9, 90, 200, torch.float32, scale=1.0)
+@pytest.mark.parametrize("m,n", [(90, 200), (90, 900), (150, 200)])
+def test_extremes(m, n):
+    x = _matrices(9, m, n, torch.float32, scale=1.0)
     x[0] = 0
     x[1] *= 1e36
     x[2] *= 1e-36
@@ -180,8 +184,9 @@ def test_extremes():
     _check(orthogonalize(tiny)[0], tiny[0])
 
 
-def test_streams_and_graphs():
-    x = _matrices(2, 300, 520, torch.bfloat16)
+@pytest.mark.parametrize("m,n", [(300, 520), (100, 1100)])
+def test_streams_and_graphs(m, n):
+    x = _matrices(2, m, n, torch.bfloat16)
     want = orthogonalize(x)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
@@ -197,7 +202,7 @@ def test_streams_and_graphs():
         with torch.cuda.graph(graphs[i]):
             outs.append(orthogonalize(ins[i] if i == 0 else ins[i].transpose(1, 2)))
     for seed in (3, 4):
-        nx = _matrices(2, 300, 520, torch.bfloat16, seed)
+        nx = _matrices(2, m, n, torch.bfloat16, seed)
         for i in range(2):
             ins[i].copy_(nx)
             graphs[i].replay()

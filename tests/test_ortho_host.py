@@ -24,7 +24,7 @@ def lib():
 def _problem(triples=(QUINTIC,) * 5, **kw):
     flat = [v for triple in triples for v in triple]
     table = (ctypes.c_float * max(len(flat), 1))(*flat)
-    args = dict(batch=2, rows=100, cols=60, batch_stride=6000, row_pitch=60, dtype=abi.FLCE_F32,
+    args = dict(batch=2, rows=300, cols=200, batch_stride=60000, row_pitch=200, dtype=abi.FLCE_F32,
                 out_dtype=abi.FLCE_BF16, steps=len(triples), eps=1e-7,
                 coefficients=ctypes.addressof(table), reserved=0)
     args.update(kw)
@@ -43,7 +43,7 @@ def test_struct_layout():
 
 def test_problem_refusals():
     for bad in (dict(batch=-1), dict(rows=-1), dict(cols=-1), dict(dtype=3), dict(out_dtype=3),
-                dict(out_dtype=abi.FLCE_F32), dict(row_pitch=59), dict(batch_stride=-1),
+                dict(out_dtype=abi.FLCE_F32), dict(row_pitch=199), dict(batch_stride=-1),
                 dict(row_pitch=1 << 50), dict(batch_stride=1 << 60), dict(eps=0.0),
                 dict(eps=math.nan), dict(eps=math.inf), dict(steps=0), dict(steps=65),
                 dict(coefficients=None), dict(reserved=1)):
@@ -89,6 +89,9 @@ def test_workspace_size():
     assert held <= size <= held + (1 << 20) + 160 * 256 * 1024
     small = _problem(batch=1, rows=256, cols=200, row_pitch=200)
     assert abi.flce_orthogonalize_workspace_size(small) <= 3 << 20
+    # none for matrices that stay in shared memory
+    assert abi.flce_orthogonalize_workspace_size(_problem(rows=128, cols=4096, row_pitch=4096)) == 0
+    assert _call(_problem(rows=128), src=None) == INVALID
 
 
 def test_python_refusals():
