@@ -29,6 +29,7 @@
 
 #include "norm_rows.cuh"
 #include "ortho_internal.h"
+#include "ortho_norm.cuh"
 #include "tc_ptx.cuh"
 
 namespace flce {
@@ -105,16 +106,15 @@ __global__ void __launch_bounds__(256) ortho_copy_kernel(const OrthoCopyParams p
   double sum = 0.0;
   for (int i = threadIdx.x; i < p.parts; i += 256) sum += partial[i];
   sum = team_all<256>(sum, buf, SumOp{});
-  const double norm = sqrt(sum) + static_cast<double>(p.eps);
-  // x = src * 2^-e, so that 1/2 < factor <= 1; a norm that is not finite makes
-  // every result NaN
-  int e = 0;
-  float factor = NAN;
-  if (norm < INFINITY) {
-    e = ilogb(norm);
-    factor = static_cast<float>(scalbn(1.0 / norm, e));
+  // by one thread, as 64-bit arithmetic is slow
+  __shared__ int exponent;
+  __shared__ float factor;
+  if (threadIdx.x == 0) {
+    norm_factor(sum, p.eps, exponent, factor);
+    if (blockIdx.x == 0) p.factor[b] = factor;
   }
-  if (blockIdx.x == 0 && threadIdx.x == 0) p.factor[b] = factor;
+  __syncthreads();
+  const int e = exponent;
   // the power of two in two factors, as one could leave the 32-bit range
   const int shift = p.x_shift - e;
   const float scale0 = scalbnf(1.0f, shift / 2), scale1 = scalbnf(1.0f, shift - shift / 2);

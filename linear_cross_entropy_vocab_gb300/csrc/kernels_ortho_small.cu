@@ -17,6 +17,7 @@
 
 #include "norm_rows.cuh"
 #include "ortho_internal.h"
+#include "ortho_norm.cuh"
 #include "tc_ptx.cuh"
 
 namespace flce {
@@ -34,7 +35,8 @@ struct Ctl {
   double squares[kWarps];
   double total[kOrthoMaxCluster];
   uint32_t tmem;
-  int abort;
+  int abort, exponent;
+  float factor;
 };
 
 // Byte offset of the 16-byte piece of columns 8c to 8c + 7 of row r.
@@ -60,8 +62,7 @@ __device__ __forceinline__ void store_cluster_f64(uint32_t addr, double v) {
   asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(addr), "d"(v) : "memory");
 }
 
-// Eight values of x, row i from column j on, or for a tall matrix column j from
-// row i on: `along` consecutive elements of src either way. Zeros outside.
+// Eight values of a row of src from `at` on, zeros past its end.
 template <class T>
 __device__ __forceinline__ void load_piece(const T* row, int at, int len, bool vec, float (&v)[8]) {
   if (vec && at + 8 <= len) {
@@ -103,67 +104,96 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int j0 = rank * p.slab;
   const bool vec = reinterpret_cast<uintptr_t>(src) % 16 == 0 &&
                    p.row_pitch * static_cast<int64_t>(sizeof(T)) % 16 == 0;
-  const int m8 = (m + 7) / 8;
   double squares = 0.0;
-  const auto count = [&](const float(&v)[8]) {
+  // Both passes walk the source alike, 64 columns of x at a time and four pieces
+  // a thread: the squares, and then the halves. A tall matrix gives a thread a
+  // row of src and eight of its columns. (With divisions for the places, 128 x
+  // 512 values took a CTA 29 us to come and go; NNN now.)
+  const auto walk = [&](auto all, auto take) {
+    for (int at = 0; at < p.slab; at += 64) {
+      float v[4][8];
+      const int j = p.tall ? at + (tid & 63) : at + (tid & 7) * 8;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int i = p.tall ? ((tid >> 6) + 4 * q) * 8 : (tid >> 3) + 32 * q;
+        const int r = p.tall ? j0 + j : i, c = p.tall ? i : j0 + j;  // of src
+        if (r < p.rows && c < p.cols) {
+          load_piece(src + int64_t(r) * p.row_pitch, c, p.cols, vec, v[q]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[q][k] = 0.0f;
+        }
+      }
+      all(v);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        take(p.tall ? ((tid >> 6) + 4 * q) * 8 : (tid >> 3) + 32 * q, j, v[q]);
+    }
+  };
+  const auto count = [&](const float(&v)[4][8]) {
+    // 32 squares in 32 bits, or in 64 where those do not hold them
     float sum = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) sum = fmaf(v[k], v[k], sum);
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum = fmaf(v[q][k], v[q][k], sum);
     double wide = sum;
     if (!(sum < 3.0e38f && sum > 1.0e-30f)) {
       wide = 0.0;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) wide += static_cast<double>(v[k]) * v[k];
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) wide += static_cast<double>(v[q][k]) * v[q][k];
     }
     squares += wide;
   };
-  // Both passes walk the source alike: the squares, and then the halves.
-  const auto walk = [&](auto take) {
-    if (p.tall) {  // a lane a row of src, eight of its columns
-      for (int u = tid; u < p.slab * m8; u += kThreads) {
-        const int i = u / p.slab * 8, j = u % p.slab;
-        float v[8] = {};
-        if (j0 + j < n) load_piece(src + int64_t(j0 + j) * p.row_pitch, i, m, vec, v);
-        take(i, j, v);
-      }
-    } else {
-      const int pieces = p.slab / 8;
-      for (int u = tid; u < m * pieces; u += kThreads) {
-        const int i = u / pieces, j = u % pieces * 8;
-        float v[8];
-        load_piece(src + int64_t(i) * p.row_pitch, j0 + j, n, vec, v);
-        take(i, j, v);
+  // Whole aligned pieces that the registers hold are loaded at once and once.
+  constexpr int kHeld = sizeof(T) == 4 ? 4 : 8;  // of 64 columns
+  const bool held = vec && p.cols % 8 == 0 && p.slab <= kHeld * 64;
+  Raw<T> raws[kHeld][4];
+  if (held) {
+#pragma unroll
+    for (int g = 0; g < kHeld; ++g) {
+      const int j = p.tall ? g * 64 + (tid & 63) : g * 64 + (tid & 7) * 8;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int i = p.tall ? ((tid >> 6) + 4 * q) * 8 : (tid >> 3) + 32 * q;
+        const int r = p.tall ? j0 + j : i, c = p.tall ? i : j0 + j;
+        if (g * 64 < p.slab && r < p.rows && c < p.cols)
+          raws[g][q].load(src + int64_t(r) * p.row_pitch + c);
+        else
+          raws[g][q].clear();
       }
     }
-  };
-  walk([&](int, int, const float(&v)[8]) { count(v); });
-  // zeros where no row is written
-  for (int u = tid; u < (kSide - m8 * 8) * (p.slab / 8); u += kThreads)
-    *reinterpret_cast<uint4*>(x + piece_of(m8 * 8 + u / (p.slab / 8), u % (p.slab / 8))) =
-        make_uint4(0, 0, 0, 0);
-  if (!p.tall)
-    for (int u = tid; u < (m8 * 8 - m) * (p.slab / 8); u += kThreads)
-      *reinterpret_cast<uint4*>(x + piece_of(m + u / (p.slab / 8), u % (p.slab / 8))) =
-          make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int g = 0; g < kHeld; ++g) {
+      float v[4][8];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) raws[g][q].values(v[q]);
+      if (g * 64 < p.slab) count(v);
+    }
+  } else {
+    walk(count, [](int, int, const float(&)[8]) {});
+  }
   squares = team_all<kThreads>(squares, ctl->squares, SumOp{});
   if (tid < ranks)
     store_cluster_f64(map_to_rank(smem_addr(&ctl->total[rank]), tid), squares);
   cluster_sync();
   const uint32_t tmem = ctl->tmem;
-  double total = 0.0;
-  for (int k = 0; k < ranks; ++k) total += ctl->total[k];
-  const double norm = sqrt(total) + static_cast<double>(p.eps);
-  // as in the copy of larger matrices: x = src * 2^(x_shift - e), and a factor
-  // in (1/2, 1] that is applied to the first step's sums
-  int e = 0;
-  float factor = NAN;
-  if (norm < INFINITY) {
-    e = ilogb(norm);
-    factor = static_cast<float>(scalbn(1.0 / norm, e));
+  // As in the copy of larger matrices: x = src * 2^(x_shift - e), and a factor
+  // in (1/2, 1] that is applied to the first step's sums. By one thread, as
+  // 64-bit arithmetic is slow.
+  if (tid == 0) {
+    double total = 0.0;
+    for (int k = 0; k < ranks; ++k) total += ctl->total[k];
+    norm_factor(total, p.eps, ctl->exponent, ctl->factor);
   }
+  __syncthreads();
+  const int e = ctl->exponent;
+  const float factor = ctl->factor;
   const int shift = p.x_shift - e;
   const float scale0 = scalbnf(1.0f, shift / 2), scale1 = scalbnf(1.0f, shift - shift / 2);
-  walk([&](int i, int j, const float(&v)[8]) {
+  const auto put = [&](int i, int j, const float(&v)[8]) {
     if (p.tall) {
 #pragma unroll
       for (int k = 0; k < 8; ++k)
@@ -176,7 +206,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         w[k] = half2_bits(v[2 * k] * scale0 * scale1, v[2 * k + 1] * scale0 * scale1);
       *reinterpret_cast<uint4*>(x + piece_of(i, j >> 3)) = make_uint4(w[0], w[1], w[2], w[3]);
     }
-  });
+  };
+  if (held) {
+#pragma unroll
+    for (int g = 0; g < kHeld; ++g) {
+      const int j = p.tall ? g * 64 + (tid & 63) : g * 64 + (tid & 7) * 8;
+      if (g * 64 < p.slab) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float v[8];
+          raws[g][q].values(v);
+          put(p.tall ? ((tid >> 6) + 4 * q) * 8 : (tid >> 3) + 32 * q, j, v);
+        }
+      }
+    }
+  } else {
+    walk([](const float(&)[4][8]) {}, put);
+  }
   fence_proxy_async_all();
   __syncthreads();
 
@@ -341,27 +387,34 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // ---- the result, from shared memory
   uint16_t* const out = static_cast<uint16_t*>(p.out) + int64_t(b) * p.rows * p.cols;
-  if (p.tall) {
-    for (int u = tid; u < p.slab * m; u += kThreads) {
-      const int i = u % m, j = u / m;
-      if (j0 + j < n)
-        out[int64_t(j0 + j) * p.cols + i] =
-            *reinterpret_cast<const uint16_t*>(x + piece_of(i, j >> 3) + (j & 7) * 2);
-    }
-  } else if (p.cols % 8 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0) {
-    const int pieces = p.slab / 8;
-    for (int u = tid; u < m * pieces; u += kThreads) {
-      const int i = u / pieces, c = u % pieces;
-      if (j0 + c * 8 < n)
-        *reinterpret_cast<uint4*>(out + int64_t(i) * p.cols + j0 + c * 8) =
-            *reinterpret_cast<const uint4*>(x + piece_of(i, c));
-    }
-  } else {
-    for (int u = tid; u < m * p.slab; u += kThreads) {
-      const int i = u / p.slab, j = u % p.slab;
-      if (j0 + j < n)
-        out[int64_t(i) * p.cols + j0 + j] =
-            *reinterpret_cast<const uint16_t*>(x + piece_of(i, j >> 3) + (j & 7) * 2);
+  const auto value = [&](int i, int j) {
+    return *reinterpret_cast<const uint16_t*>(x + piece_of(i, j >> 3) + (j & 7) * 2);
+  };
+  const bool whole = p.cols % 8 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0;
+  for (int at = 0; at < p.slab && j0 + at < n; at += 64) {
+    if (p.tall) {  // a row of out is a column of x
+      const int i = tid & 127;
+#pragma unroll 8
+      for (int q = 0; q < 32; ++q) {
+        const int j = at + (tid >> 7) + 2 * q;
+        if (i < m && j0 + j < n) out[int64_t(j0 + j) * p.cols + i] = value(i, j);
+      }
+    } else if (whole) {
+      const int j = at + (tid & 7) * 8;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int i = (tid >> 3) + 32 * q;
+        if (i < m && j0 + j < n)
+          *reinterpret_cast<uint4*>(out + int64_t(i) * p.cols + j0 + j) =
+              *reinterpret_cast<const uint4*>(x + piece_of(i, j >> 3));
+      }
+    } else {
+      const int j = at + (tid & 63);
+#pragma unroll 8
+      for (int q = 0; q < 32; ++q) {
+        const int i = (tid >> 6) + 4 * q;
+        if (i < m && j0 + j < n) out[int64_t(i) * p.cols + j0 + j] = value(i, j);
+      }
     }
   }
   tc_fence_before_sync();

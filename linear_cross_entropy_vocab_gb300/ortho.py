@@ -9,6 +9,7 @@ The work runs in libflce.so (``flce_orthogonalize``).
 from __future__ import annotations
 
 import array
+import itertools
 from typing import Optional, Sequence, Tuple
 
 import torch
@@ -25,6 +26,15 @@ _DTYPES = {torch.float32: abi.FLCE_F32, torch.bfloat16: abi.FLCE_BF16,
 # Five steps that lift small singular values quickly: those above 0.002 of the norm end between
 # 0.68 and 1.21.
 NEWTON_SCHULZ = ((3.4445, -4.7750, 2.0315),) * 5
+
+
+def _table(coefficients):
+    """The coefficients as 32-bit floats in host memory, and the number of steps."""
+    if any(len(triple) != 3 for triple in coefficients):
+        raise ValueError("coefficients must be triples")
+    if not 1 <= len(coefficients) <= 64:
+        raise ValueError("coefficients must have 1 to 64 triples")
+    return array.array("f", itertools.chain.from_iterable(coefficients)), len(coefficients)
 
 
 def orthogonalize(x: torch.Tensor, *,
@@ -52,14 +62,7 @@ def orthogonalize(x: torch.Tensor, *,
         out_dtype = torch.bfloat16 if x.dtype == torch.float32 else x.dtype
     if out_dtype not in (torch.bfloat16, torch.float16):
         raise TypeError(f"out_dtype must be bfloat16 or float16, not {out_dtype}")
-    table = array.array("f")
-    for triple in coefficients:
-        if len(triple) != 3:
-            raise ValueError("coefficients must be triples")
-        table.extend(triple)
-    steps = len(table) // 3
-    if not 1 <= steps <= 64:
-        raise ValueError("coefficients must have 1 to 64 triples")
+    table, steps = _table(coefficients)
     eps = float(eps)
     if not 1.1754944e-38 <= eps <= 3.4028234e38:
         raise ValueError("eps must be finite and at least 2^-126")
