@@ -584,8 +584,9 @@ typedef struct flce_ortho_problem {
 } flce_ortho_problem;
 
 /* Bytes of device workspace flce_orthogonalize() needs (0 if `p` is invalid):
- * about 4 bytes for each element of src and 4 for each of x x^T, with sides
- * rounded up to 256. */
+ * about 4 bytes for each element of src and 4 or 8 for each of x x^T, with sides
+ * rounded up to 256, and up to 42 MB for sums; none where one side is at most
+ * 128 and the other at most 4096. */
 size_t flce_orthogonalize_workspace_size(const flce_ortho_problem* p);
 
 /* out [batch][rows][cols], dense, sharing no memory with src. */

@@ -286,26 +286,23 @@ __device__ __forceinline__ void fence_proxy_async_global() {
   asm volatile("fence.proxy.async.global;" ::: "memory");
 }
 
-enum Op { kGram, kPoly, kMul, kOutWide, kOutTall };
-
-// One product of the sequence, as every role walks it: step k's gram,
-// polynomial and product.
+// One product of the sequence, as every role walks it.
 struct Product {
-  int k, kind;        // kind 0 to 2: gram, polynomial, product
-  Op op;
+  OrthoOp op;
+  bool symmetric;
   int m_tiles, n_tiles, per;  // tiles of a matrix
   int k_iters;
+  const OrthoProduct* with;
 };
 __device__ __forceinline__ Product product_of(const OrthoRunParams& p, int i) {
   Product q;
-  q.k = i / 3;
-  q.kind = i - 3 * q.k;
-  const bool out = q.k + 1 == p.steps;
-  q.op = q.kind == 0 ? kGram : q.kind == 1 ? kPoly : !out ? kMul : p.tall ? kOutTall : kOutWide;
-  q.m_tiles = q.op == kOutTall ? p.n_tiles : p.m_tiles;
-  q.n_tiles = q.kind < 2 || q.op == kOutTall ? p.m_tiles : p.n_tiles;
-  q.per = q.kind < 2 ? p.m_tiles * (p.m_tiles + 1) / 2 : p.m_tiles * p.n_tiles;
-  q.k_iters = q.kind == 0 ? p.k_n : p.k_m;
+  q.with = &p.product[i];
+  q.op = static_cast<OrthoOp>(q.with->op);
+  q.symmetric = q.op <= OrthoOp::kPoly;
+  q.m_tiles = q.op == OrthoOp::kOutTall ? p.n_tiles : p.m_tiles;
+  q.n_tiles = q.symmetric || q.op == OrthoOp::kOutTall ? p.m_tiles : p.n_tiles;
+  q.per = q.symmetric ? p.m_tiles * (p.m_tiles + 1) / 2 : p.m_tiles * p.n_tiles;
+  q.k_iters = q.op == OrthoOp::kGram ? p.k_n : p.k_m;
   return q;
 }
 
@@ -316,14 +313,14 @@ __device__ __forceinline__ Tile tile_of(const Product& q, int u) {
   Tile t;
   t.b = u / q.per;
   int r = u - t.b * q.per;
-  if (q.kind < 2) {  // the triangle above the diagonal
+  if (q.symmetric) {  // the triangle above the diagonal
     t.m = 0;
     while (r >= q.m_tiles - t.m) {
       r -= q.m_tiles - t.m;
       ++t.m;
     }
     t.n = t.m + r;
-  } else if (q.op == kOutTall) {  // p stays in L2, x passes once
+  } else if (q.op == OrthoOp::kOutTall) {  // p stays in L2, x passes once
     t.m = r / q.n_tiles;
     t.n = r - t.m * q.n_tiles;
   } else {
@@ -349,7 +346,7 @@ struct Walk {
     return unit * (c.cut * k_iters) / c.units;  // the host keeps this in 31 bits
   }
   __device__ __forceinline__ Walk(const OrthoRunParams& p, const Product& q, int unit, int turn) {
-    const OrthoCut& c = p.cut[q.kind];
+    const OrthoCut& c = p.cut[q.with->cut];
     at = end = 0;
     if (c.cut > 0) {
       if (unit < c.units) {
@@ -391,25 +388,22 @@ __device__ __forceinline__ int owner_of(const OrthoCut& c, int k_iters, int x) {
 }
 // The pair that the next product's first tile goes to.
 __device__ __forceinline__ int next_turn(const OrthoRunParams& p, const Product& q, int turn) {
-  return p.cut[q.kind].cut > 0 ? turn : (turn + q.per * p.batch) % p.units;
+  return p.cut[q.with->cut].cut > 0 ? turn : (turn + q.per * p.batch) % p.units;
 }
 
 // What a product reads of a matrix is there once each epilogue warp of each
-// tile of the product before has counted one up. The counts go on over the
-// steps. Where tiles are cut, all matrices count together: the places of their
-// sums are used again by the next product.
+// tile of the products before has counted one up. Where tiles are cut, all
+// matrices count together: the places of their sums are used again by the next
+// product.
 struct Need {
   const int* count;
   int least;
 };
-__device__ __forceinline__ int* count_of(const OrthoRunParams& p, int kind, int b) {
-  return p.finished + kind * p.batch + (p.joint ? 0 : b);
+__device__ __forceinline__ int* count_of(const OrthoRunParams& p, int b) {
+  return p.finished + (p.joint ? 0 : b);
 }
 __device__ __forceinline__ Need need_of(const OrthoRunParams& p, const Product& q, int b) {
-  const int before = q.kind == 0 ? 2 : q.kind - 1;
-  const int per = before < 2 ? p.m_tiles * (p.m_tiles + 1) / 2 : p.m_tiles * p.n_tiles;
-  const int times = q.kind == 0 ? q.k : q.k + 1;
-  return {count_of(p, before, b), times * per * 2 * kWarps * (p.joint ? p.batch : 1)};
+  return {count_of(p, b), q.with->need};
 }
 __device__ __forceinline__ bool wait_need(const Need& need, volatile int* abort_flag,
                                           int* err_word) {
@@ -463,20 +457,13 @@ struct Ring {
   int stage;
   uint32_t phase, armed, last;
 };
-template <Op OP>
+template <OrthoOp OP>
 __device__ __forceinline__ bool load_part(const OrthoRunParams& p, const Product& q,
                                           const Part& part, const Tile& t, uint32_t base, int rank,
                                           Ctl* ctl, Ring& ring) {
-  constexpr bool kAcrossA = OP == kOutTall, kAcrossB = OP == kMul || OP == kOutWide;
-  const int from = q.k & 1;
-  const CUtensorMap* const a = OP == kGram   ? &p.x_along[from]
-                               : OP == kPoly ? &p.g_along
-                               : kAcrossA    ? &p.x_across[from]
-                                             : &p.p_along;
-  const CUtensorMap* const b = OP == kGram   ? &p.x_along[from]
-                               : OP == kPoly ? &p.g_along
-                               : kAcrossB    ? &p.x_across[from]
-                                             : &p.p_along;
+  constexpr bool kAcrossA = OP == OrthoOp::kOutTall, kAcrossB = OP == OrthoOp::kMul || OP == OrthoOp::kOutWide;
+  const CUtensorMap* const a = kAcrossA ? &p.across[q.with->a] : &p.along[q.with->a];
+  const CUtensorMap* const b = kAcrossB ? &p.across[q.with->b] : &p.along[q.with->b];
   const int a_side = t.m * kOrthoTile + rank * kRows, b_side = t.n * kOrthoTile + rank * kRows;
   const int row0 = t.b * p.m_pad;
   for (int k = part.k0; k < part.k1; ++k) {
@@ -501,10 +488,10 @@ __device__ __forceinline__ bool load_part(const OrthoRunParams& p, const Product
   return true;
 }
 
-template <Op OP>
+template <OrthoOp OP>
 __device__ __forceinline__ bool multiply_part(const OrthoRunParams& p, const Part& part,
                                               uint32_t base, uint32_t d, Ctl* ctl, Ring& ring) {
-  constexpr bool kAcrossA = OP == kOutTall, kAcrossB = OP == kMul || OP == kOutWide;
+  constexpr bool kAcrossA = OP == OrthoOp::kOutTall, kAcrossB = OP == OrthoOp::kMul || OP == OrthoOp::kOutWide;
   constexpr uint32_t idesc =
       idesc_f16kind_f32(2 * kRows, kCols, kAcrossA ? 1 : 0, kAcrossB ? 1 : 0, 0);
   for (int k = part.k0; k < part.k1; ++k) {
@@ -527,23 +514,23 @@ __device__ __forceinline__ bool multiply_part(const OrthoRunParams& p, const Par
 
 // A warp's 32 rows and 128 columns of a part's accumulator: stored, or left for
 // the warp that joins the tile's sums. Returns whether the tile is stored.
-template <Op OP, class T>
+template <OrthoOp OP, class T>
 __device__ __forceinline__ bool finish_part(const OrthoRunParams& p, const Product& q,
                                             const Part& part, const Tile& t, uint32_t taddr,
                                             int unit, int rank, int warp, int quarter, int first,
                                             uint8_t* boxes, int lane) {
-  constexpr bool kOut = OP == kOutWide || OP == kOutTall;
+  constexpr bool kOut = OP == OrthoOp::kOutWide || OP == OrthoOp::kOutTall;
   const int row0 = t.m * kOrthoTile + rank * kRows + quarter * 32;  // of the matrix
   const int row = row0 + lane;
-  const bool mirrored = (OP == kGram || OP == kPoly) && t.n > t.m;
-  const OrthoStep& st = p.step[q.k];
+  const bool mirrored = OP <= OrthoOp::kPoly && t.n > t.m;
+  const OrthoProduct& with = *q.with;
   const int rows = kOut ? p.rows : p.m_rows;
-  const int cols = kOut ? p.cols : OP == kMul ? p.n_pad : p.m_rows;
-  float scale = OP == kGram ? st.gram : OP == kPoly ? st.poly : st.product;
-  if ((OP == kGram || OP == kMul || kOut) && q.k == 0) {
-    // the norm's factor belongs to the first step's x
+  const int cols = kOut ? p.cols : OP == OrthoOp::kMul ? p.n_pad : p.m_rows;
+  float scale = with.scale;
+  if (with.power != 0) {
+    // the norm's factor belongs to the first x
     const float f = p.factor[t.b];
-    scale *= OP == kGram ? f * f : f;
+    scale *= with.power == 2 ? f * f : f;
   }
   // Pieces of the tile that this warp keeps. Where the tile's contraction is
   // cut, each pair leaves its sums, and the warp that comes last adds all of
@@ -552,7 +539,7 @@ __device__ __forceinline__ bool finish_part(const OrthoRunParams& p, const Produ
       row0 >= rows ? 0 : min(kPieces, (cols - t.n * kOrthoTile - first * 32 + 31) / 32);
   int from = unit, to = unit;
   if (part.k1 - part.k0 < q.k_iters) {
-    const OrthoCut& c = p.cut[q.kind];
+    const OrthoCut& c = p.cut[q.with->cut];
     const int x = (part.tile - c.whole) * q.k_iters;
     from = owner_of(c, q.k_iters, x);
     to = owner_of(c, q.k_iters, x + q.k_iters - 1);
@@ -588,7 +575,7 @@ __device__ __forceinline__ bool finish_part(const OrthoRunParams& p, const Produ
       (int64_t(t.b) * p.m_pad + row0 + (lane >> 2)) * p.m_pad + t.n * kOrthoTile + first * 32 +
       (lane & 3) * 8);
   const auto fetch = [&](uint4(&g)[4], int i) {
-    if (OP == kPoly && i < pieces) {
+    if (OP == OrthoOp::kPoly && i < pieces) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) g[j] = __ldcg(old + 4 * i + j * p.m_pad);  // eight rows further
     }
@@ -634,7 +621,7 @@ __device__ __forceinline__ bool finish_part(const OrthoRunParams& p, const Produ
     __syncwarp();
     uint8_t* const box = mirrored ? boxes : boxes + (i & 1) * kBoxBytes;
     uint8_t* const mirror = boxes + kBoxBytes;
-    if constexpr (OP == kPoly) {
+    if constexpr (OP == OrthoOp::kPoly) {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         *reinterpret_cast<uint4*>(box + box_at(8 * j + (lane >> 2), lane & 3)) = held[0][j];
@@ -649,13 +636,13 @@ __device__ __forceinline__ bool finish_part(const OrthoRunParams& p, const Produ
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
-          v[8 * g + 2 * j] = fmaf(f.x, st.old, v[8 * g + 2 * j]);
-          v[8 * g + 2 * j + 1] = fmaf(f.y, st.old, v[8 * g + 2 * j + 1]);
+          v[8 * g + 2 * j] = fmaf(f.x, with.old, v[8 * g + 2 * j]);
+          v[8 * g + 2 * j + 1] = fmaf(f.y, with.old, v[8 * g + 2 * j + 1]);
         }
       }
       if (row0 == col) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] += lane == j ? st.diag : 0.0f;
+        for (int j = 0; j < 32; ++j) v[j] += lane == j ? with.diag : 0.0f;
       }
     }
     uint32_t w[16];
@@ -689,11 +676,9 @@ __device__ __forceinline__ bool finish_part(const OrthoRunParams& p, const Produ
     __syncwarp();
     if (lane == 0) {
       if constexpr (kOut) {
-        tma_store_3d(&p.out_store, smem_addr(box), col, row0, t.b);
+        tma_store_3d(&p.store[with.c], smem_addr(box), col, row0, t.b);
       } else {
-        const CUtensorMap* const c = OP == kGram   ? &p.g_store
-                                     : OP == kPoly ? &p.p_store
-                                                   : &p.x_store[(q.k & 1) ^ 1];
+        const CUtensorMap* const c = &p.store[with.c];
         tma_store_2d(c, smem_addr(box), col, t.b * p.m_pad + row0);
         if (mirrored) tma_store_2d(c, smem_addr(mirror), row0, t.b * p.m_pad + col);
       }
@@ -734,10 +719,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&p.x_along[0]);
-    tma_prefetch_desc(&p.g_along);
-    tma_prefetch_desc(&p.p_along);
-    tma_prefetch_desc(&p.x_across[0]);
+    tma_prefetch_desc(&p.along[kOrthoX0]);
+    tma_prefetch_desc(&p.along[kOrthoGram]);
+    tma_prefetch_desc(&p.along[kOrthoP0]);
+    tma_prefetch_desc(&p.across[kOrthoX0]);
   }
   if (warp == 1) {
     tmem_alloc_pair(smem_addr(&ctl->tmem), 512);
@@ -747,14 +732,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_sync();
   tc_fence_after_sync();
   const uint32_t tmem = ctl->tmem;
-  const int products = 3 * p.steps;
   int turn = 0;
 
   if (warp == 0) {
     if (lane == 0) {
       Ring ring{};
       bool ok = true;
-      for (int i = 0; ok && i < products; ++i) {
+      for (int i = 0; ok && i < p.products; ++i) {
         const Product q = product_of(p, i);
         Walk walk(p, q, unit, turn);
         int ready = -1;  // the matrix whose operands are known to be there
@@ -767,18 +751,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             ready = t.b;
           }
           switch (q.op) {
-            case kGram:
-              ok = load_part<kGram>(p, q, part, t, base, rank, ctl, ring);
+            case OrthoOp::kGram:
+            case OrthoOp::kSquare:
+            case OrthoOp::kPoly:
+              ok = load_part<OrthoOp::kGram>(p, q, part, t, base, rank, ctl, ring);
               break;
-            case kPoly:
-              ok = load_part<kPoly>(p, q, part, t, base, rank, ctl, ring);
+            case OrthoOp::kMul:
+            case OrthoOp::kOutWide:
+              ok = load_part<OrthoOp::kMul>(p, q, part, t, base, rank, ctl, ring);
               break;
-            case kMul:
-            case kOutWide:
-              ok = load_part<kMul>(p, q, part, t, base, rank, ctl, ring);
-              break;
-            case kOutTall:
-              ok = load_part<kOutTall>(p, q, part, t, base, rank, ctl, ring);
+            case OrthoOp::kOutTall:
+              ok = load_part<OrthoOp::kOutTall>(p, q, part, t, base, rank, ctl, ring);
               break;
           }
         }
@@ -794,7 +777,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Ring ring{};
       bool ok = true;
       int it = 0;
-      for (int i = 0; ok && i < products; ++i) {
+      for (int i = 0; ok && i < p.products; ++i) {
         const Product q = product_of(p, i);
         Walk walk(p, q, unit, turn);
         for (Part part; ok && walk.next(q, part); ++it) {
@@ -805,16 +788,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after_sync();
           const uint32_t d = tmem + static_cast<uint32_t>(buf * kCols);
           switch (q.op) {
-            case kGram:
-            case kPoly:
-              ok = multiply_part<kGram>(p, part, base, d, ctl, ring);
+            case OrthoOp::kGram:
+            case OrthoOp::kSquare:
+            case OrthoOp::kPoly:
+              ok = multiply_part<OrthoOp::kGram>(p, part, base, d, ctl, ring);
               break;
-            case kMul:
-            case kOutWide:
-              ok = multiply_part<kMul>(p, part, base, d, ctl, ring);
+            case OrthoOp::kMul:
+            case OrthoOp::kOutWide:
+              ok = multiply_part<OrthoOp::kMul>(p, part, base, d, ctl, ring);
               break;
-            case kOutTall:
-              ok = multiply_part<kOutTall>(p, part, base, d, ctl, ring);
+            case OrthoOp::kOutTall:
+              ok = multiply_part<OrthoOp::kOutTall>(p, part, base, d, ctl, ring);
               break;
           }
           if (ok) umma_commit_pair(smem_addr(&ctl->acc_full[buf]), 0x3);
@@ -834,13 +818,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* const box = boxes + (warp - 2) * 2 * kBoxBytes;
     int it = 0;
     bool ok = true;
-    for (int i = 0; ok && i < products; ++i) {
+    for (int i = 0; ok && i < p.products; ++i) {
       const Product q = product_of(p, i);
       Walk walk(p, q, unit, turn);
       int ready = -1;
       for (Part part; walk.next(q, part); ++it) {
         const Tile t = tile_of(q, part.tile);
-        if (q.op == kPoly && t.b != ready) {  // the gram is read here too
+        if (q.op == OrthoOp::kPoly && t.b != ready) {  // the gram is read here too
           ok = __all_sync(0xffffffffu,
                           lane != 0 || wait_need(need_of(p, q, t.b), abort_flag, p.err_word));
           if (!ok) break;
@@ -857,24 +841,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                                static_cast<uint32_t>(buf * kCols);
         bool stored = false;
         switch (q.op) {
-          case kGram:
-            stored = finish_part<kGram, __half>(p, q, part, t, taddr, unit, rank, warp - 2, quarter,
+          case OrthoOp::kGram:
+          case OrthoOp::kSquare:
+            stored = finish_part<OrthoOp::kGram, __half>(p, q, part, t, taddr, unit, rank, warp - 2, quarter,
                                                 first, box, lane);
             break;
-          case kPoly:
-            stored = finish_part<kPoly, __half>(p, q, part, t, taddr, unit, rank, warp - 2, quarter,
+          case OrthoOp::kPoly:
+            stored = finish_part<OrthoOp::kPoly, __half>(p, q, part, t, taddr, unit, rank, warp - 2, quarter,
                                                 first, box, lane);
             break;
-          case kMul:
-            stored = finish_part<kMul, __half>(p, q, part, t, taddr, unit, rank, warp - 2, quarter,
+          case OrthoOp::kMul:
+            stored = finish_part<OrthoOp::kMul, __half>(p, q, part, t, taddr, unit, rank, warp - 2, quarter,
                                                first, box, lane);
             break;
-          case kOutWide:
-            finish_part<kOutWide, T>(p, q, part, t, taddr, unit, rank, warp - 2, quarter, first,
+          case OrthoOp::kOutWide:
+            finish_part<OrthoOp::kOutWide, T>(p, q, part, t, taddr, unit, rank, warp - 2, quarter, first,
                                      box, lane);
             break;
-          case kOutTall:
-            finish_part<kOutTall, T>(p, q, part, t, taddr, unit, rank, warp - 2, quarter, first,
+          case OrthoOp::kOutTall:
+            finish_part<OrthoOp::kOutTall, T>(p, q, part, t, taddr, unit, rank, warp - 2, quarter, first,
                                      box, lane);
             break;
         }
@@ -885,7 +870,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (stored) {
             tma_store_wait_all();
             fence_proxy_async_global();
-            add_release(count_of(p, q.kind, t.b), 1);
+            add_release(count_of(p, t.b), 1);
           }
         }
       }

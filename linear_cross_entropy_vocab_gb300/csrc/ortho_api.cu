@@ -4,6 +4,7 @@
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
+#include <utility>
 
 #include "flce.h"
 #include "host_common.h"
@@ -74,6 +75,92 @@ void fill_steps(const flce_ortho_problem* p, flce::OrthoStep* step) {
     t.product = static_cast<float>(next_scale / (x_scale * p_scale));
     x_scale = next_scale;
   }
+}
+
+// The products of all steps. A group of steps s, s + 1, ... multiplies x by the
+// polynomials of its steps all at once: with the gram A of the group's x, and
+// P = p_s(A), the next step's gram is P A P and its x P x, and all of these
+// commute. So each step after a group's first takes two products for its gram,
+// one for its polynomial and one to gather the polynomials, all m x m.
+//
+// The bounds: singular values grow by step_bound, the gram's values are their
+// squares, and a gathered polynomial's are below the product of the bounds of
+// its parts. Each is held with a power of two of its own.
+int list_products(const flce_ortho_problem* p, bool grouped, bool tall, flce::OrthoProduct* out) {
+  using flce::OrthoOp;
+  constexpr double kSlack = 1.0 + 1.0 / 64;  // for roundings
+  int count = 0;
+  const auto add = [&](OrthoOp op, int a, int b, int c, double scale, int power = 0,
+                       double old = 0.0, double diag = 0.0) {
+    flce::OrthoProduct& t = out[count++];
+    t.op = static_cast<int8_t>(op);
+    t.a = static_cast<int8_t>(a);
+    t.b = static_cast<int8_t>(b);
+    t.c = static_cast<int8_t>(c);
+    t.cut = op == OrthoOp::kGram ? 0 : op <= OrthoOp::kPoly ? 1 : 2;
+    t.power = static_cast<int8_t>(power);
+    t.scale = static_cast<float>(scale);
+    t.old = static_cast<float>(old);
+    t.diag = static_cast<float>(diag);
+  };
+  double bound = 1.0, x_scale = scale_for(bound);
+  int from = flce::kOrthoX0;
+  for (int k = 0; k < p->steps;) {
+    // groups of three, of two at the end
+    const int left = p->steps - k;
+    const int group = !grouped ? 1 : left == 4 ? 2 : std::min(3, left);
+    const int first = k;
+    double g_scale = scale_for(bound * bound);
+    add(OrthoOp::kGram, from, from, flce::kOrthoGram, g_scale / (x_scale * x_scale),
+        k == 0 ? 2 : 0);
+    // the buffers of the gathered polynomial, of a step's own, and a free one
+    int gathered = flce::kOrthoP0, own = flce::kOrthoP1, spare = flce::kOrthoP2;
+    double all = 1.0, all_scale = 1.0;  // its bound and scale
+    for (int s = 0; s < group; ++s, ++k) {
+      const float* const abc = p->coefficients + 3 * k;
+      const double most = poly_bound(abc[0], abc[1], abc[2], bound * bound) * kSlack;
+      const double p_scale = scale_for(most);
+      const int mine = s == 0 ? gathered : own;
+      add(OrthoOp::kPoly, flce::kOrthoGram, flce::kOrthoGram, mine,
+          abc[2] * p_scale / (g_scale * g_scale), 0, abc[1] * p_scale / g_scale,
+          abc[0] * p_scale);
+      const double next = step_bound(abc[0], abc[1], abc[2], bound) * kSlack;
+      if (s + 1 < group) {  // the gram of the next step
+        const double half_scale = scale_for(most * bound * bound);
+        const double next_scale = scale_for(next * next);
+        add(OrthoOp::kSquare, mine, flce::kOrthoGram, spare, half_scale / (p_scale * g_scale));
+        add(OrthoOp::kSquare, spare, mine, flce::kOrthoGram,
+            next_scale / (half_scale * p_scale));
+        g_scale = next_scale;
+      }
+      if (s == 0) {
+        all = most;
+        all_scale = p_scale;
+      } else {
+        all *= most;
+        const double scale = scale_for(all);
+        add(OrthoOp::kSquare, mine, gathered, spare, scale / (p_scale * all_scale));
+        std::swap(gathered, spare);
+        all_scale = scale;
+      }
+      bound = next;
+    }
+    const bool last = k == p->steps;
+    const double next_scale = last ? 1.0 : scale_for(bound);
+    const double scale = next_scale / (x_scale * all_scale);
+    const int power = first == 0 ? 1 : 0;
+    if (last && tall) {
+      add(OrthoOp::kOutTall, from, gathered, flce::kOrthoOut, scale, power);
+    } else if (last) {
+      add(OrthoOp::kOutWide, gathered, from, flce::kOrthoOut, scale, power);
+    } else {
+      const int to = from == flce::kOrthoX0 ? flce::kOrthoX1 : flce::kOrthoX0;
+      add(OrthoOp::kMul, gathered, from, to, scale, power);
+      from = to;
+    }
+    x_scale = next_scale;
+  }
+  return count;
 }
 
 flce_status check_problem(const flce_ortho_problem* p) {
@@ -150,7 +237,8 @@ constexpr int32_t kArrived = 2 * kPlanPairs * 2 * flce::kOrthoWarps;
 struct Plan {
   int64_t cluster, slab;  // of matrices that stay in shared memory, else 0
   int64_t m, n, m_pad, n_pad, parts;
-  size_t x[2], gram, poly, partial, factor, counts, shares, total;
+  size_t buffer[flce::kOrthoBuffers], partial, factor, counts, shares, total;
+  bool grouped;  // several steps on one gram
 };
 Plan plan_of(const flce_ortho_problem* p) {
   Plan q{};
@@ -170,14 +258,22 @@ Plan plan_of(const flce_ortho_problem* p) {
   const size_t b = static_cast<size_t>(p->batch);
   const size_t x_bytes = align_256(b * static_cast<size_t>(q.m_pad * q.n_pad) * 2);
   const size_t g_bytes = align_256(b * static_cast<size_t>(q.m_pad * q.m_pad) * 2);
-  q.x[0] = 0;
-  q.x[1] = x_bytes;
-  q.gram = q.x[1] + (p->steps > 1 ? x_bytes : 0);
-  q.poly = q.gram + g_bytes;
-  q.partial = q.poly + g_bytes;
+  // Steps of one group take one gram and one product with x, 3 m^2 n operations
+  // together, instead of one each, and 3 m^3 more for each step after the first.
+  // Two groups of five steps are three products more than five steps by
+  // themselves, each of which waits some 8 us for the one before.
+  q.grouped = p->steps > 1 &&
+              static_cast<double>(p->batch) * q.m * q.m * (q.n - q.m) > 4.0e9;
+  q.buffer[flce::kOrthoX0] = 0;
+  q.buffer[flce::kOrthoX1] = x_bytes;
+  q.buffer[flce::kOrthoGram] = q.buffer[flce::kOrthoX1] + (p->steps > 1 ? x_bytes : 0);
+  q.buffer[flce::kOrthoP0] = q.buffer[flce::kOrthoGram] + g_bytes;
+  q.buffer[flce::kOrthoP1] = q.buffer[flce::kOrthoP0] + g_bytes;
+  q.buffer[flce::kOrthoP2] = q.buffer[flce::kOrthoP1] + (q.grouped ? g_bytes : 0);
+  q.partial = q.buffer[flce::kOrthoP2] + (q.grouped ? g_bytes : 0);
   q.factor = q.partial + align_256(b * static_cast<size_t>(q.parts) * 8);
   q.counts = q.factor + align_256(b * 4);
-  q.shares = q.counts + align_256((kArrived + 3 * b) * 4);
+  q.shares = q.counts + align_256((kArrived + b) * 4);
   const int64_t side = q.m_pad / flce::kOrthoTile;
   const int64_t tiles = p->batch * side * ceil_div(q.n, flce::kOrthoTile);
   q.total = q.shares + static_cast<size_t>(2 * std::min(kPlanPairs, kMaxParts * tiles)) *
@@ -236,9 +332,9 @@ flce_status flce_orthogonalize(const flce_ortho_problem* p, const void* src, voi
   if (!aligned_to(src, size_of(p->dtype)) || !aligned_to(out, 2) || !aligned_to(err_word, 4))
     return fail(FLCE_ERR_UNSUPPORTED, "a pointer is misaligned for its type");
   const Plan plan = plan_of(p);
-  // coordinates are 32-bit, and so are the counts of tiles x 16 warps x 64 steps
+  // coordinates and the numbers of tiles are 32-bit
   if (p->batch * plan.m_pad > (int64_t(1) << 30) ||
-      p->batch * ceil_div(plan.n, 256) * (plan.m_pad / 256) > (int64_t(1) << 20))
+      p->batch * ceil_div(plan.n, 256) * (plan.m_pad / 256) > (int64_t(1) << 28))
     return fail(FLCE_ERR_UNSUPPORTED, "the batch has too many rows");
   st = check_workspace(workspace, workspace_bytes, plan.total);
   if (st != FLCE_OK) return st;
@@ -282,7 +378,7 @@ flce_status flce_orthogonalize(const flce_ortho_problem* p, const void* src, voi
   c.n = static_cast<int32_t>(plan.n);
   c.m_pad = static_cast<int32_t>(plan.m_pad);
   c.n_pad = static_cast<int32_t>(plan.n_pad);
-  c.x = ws + plan.x[0];
+  c.x = ws + plan.buffer[flce::kOrthoX0];
   c.partial = reinterpret_cast<double*>(ws + plan.partial);
   c.parts = static_cast<int32_t>(plan.parts);
   c.eps = p->eps;
@@ -290,34 +386,25 @@ flce_status flce_orthogonalize(const flce_ortho_problem* p, const void* src, voi
   c.m_rows = static_cast<int32_t>(ceil_div(plan.m, 64) * 64);
   c.factor = reinterpret_cast<float*>(ws + plan.factor);
   c.count = reinterpret_cast<int32_t*>(ws + plan.counts);
-  c.counts = kArrived + 3 * c.batch;
-  cudaError_t e = flce::launch_ortho_norm(c, p->dtype, s);
-  if (e != cudaSuccess) return cuda_fail(e, "matrix norm kernel");
-  e = flce::launch_ortho_copy(c, p->dtype, s);
-  if (e != cudaSuccess) return cuda_fail(e, "matrix copy kernel");
-
+  c.counts = kArrived + c.batch;
   flce::OrthoRunParams r{};
   const int64_t x_rows = p->batch * plan.m_pad;
-  const int copies = p->steps > 1 ? 2 : 1;
-  for (int i = 0; i < copies; ++i) {
-    uint8_t* const x = ws + plan.x[i];
-    if (!make_map(&r.x_along[i], x, plan.n_pad, x_rows, 64, 128, kLoad) ||
-        !make_map(&r.x_across[i], x, plan.n_pad, x_rows, 64, 64, kLoad) ||
-        !make_map(&r.x_store[i], x, plan.n_pad, x_rows, 32, 32, kStore))
+  for (int i = 0; i < flce::kOrthoBuffers; ++i) {
+    if ((i == flce::kOrthoX1 && p->steps == 1) || (i > flce::kOrthoP0 && !plan.grouped)) continue;
+    const bool is_x = i <= flce::kOrthoX1;
+    const int64_t cols = is_x ? plan.n_pad : plan.m_pad;
+    uint8_t* const base = ws + plan.buffer[i];
+    if (!make_map(&r.along[i], base, cols, x_rows, 64, 128, kLoad) ||
+        !make_map(&r.store[i], base, cols, x_rows, 32, 32, kStore) ||
+        (is_x && !make_map(&r.across[i], base, cols, x_rows, 64, 64, kLoad)))
       return FLCE_ERR_CUDA;
   }
-  if (!make_map(&r.g_along, ws + plan.gram, plan.m_pad, x_rows, 64, 128, kLoad) ||
-      !make_map(&r.g_store, ws + plan.gram, plan.m_pad, x_rows, 32, 32, kStore) ||
-      !make_map(&r.p_along, ws + plan.poly, plan.m_pad, x_rows, 64, 128, kLoad) ||
-      !make_map(&r.p_store, ws + plan.poly, plan.m_pad, x_rows, 32, 32, kStore))
-    return FLCE_ERR_CUDA;
   // maps take rows of whole 16 bytes
   const bool out_mapped = p->cols % 8 == 0 && aligned_to(out, 16);
-  if (out_mapped && !make_map(&r.out_store, out, p->cols, p->rows, 32, 32, kStore, p->batch))
+  if (out_mapped && !make_map(&r.store[flce::kOrthoOut], out, p->cols, p->rows, 32, 32, kStore,
+                              p->batch))
     return FLCE_ERR_CUDA;
-
-  fill_steps(p, r.step);
-  r.steps = p->steps;
+  r.products = list_products(p, plan.grouped, tall, r.product);
   r.batch = c.batch;
   r.m_tiles = static_cast<int32_t>(plan.m_pad / flce::kOrthoTile);
   r.n_tiles = static_cast<int32_t>(ceil_div(plan.n, flce::kOrthoTile));
@@ -326,12 +413,11 @@ flce_status flce_orthogonalize(const flce_ortho_problem* p, const void* src, voi
   r.m_pad = c.m_pad;
   r.m_rows = c.m_rows;
   r.n_pad = c.n_pad;
-  r.tall = c.tall;
   r.out_mapped = out_mapped ? 1 : 0;
   r.rows = c.rows;
   r.cols = c.cols;
   r.factor = c.factor;
-  r.gram = ws + plan.gram;
+  r.gram = ws + plan.buffer[flce::kOrthoGram];
   r.out = out;
   r.shares = ws + plan.shares;
   r.arrived = c.count;
@@ -353,6 +439,17 @@ flce_status flce_orthogonalize(const flce_ortho_problem* p, const void* src, voi
     r.units = std::max(r.units, r.cut[i].units);
     if (split.cut > 0) r.joint = 1;
   }
+  int64_t need = 0;
+  for (int i = 0; i < r.products; ++i) {
+    r.product[i].need = static_cast<int32_t>(need);
+    need += (r.product[i].cut < 2 ? triangle : all) / (r.joint ? 1 : p->batch) * 2 *
+            flce::kOrthoWarps;
+  }
+  if (need > 0x7fffffff) return fail(FLCE_ERR_UNSUPPORTED, "too many tiles and steps to count");
+  cudaError_t e = flce::launch_ortho_norm(c, p->dtype, s);
+  if (e != cudaSuccess) return cuda_fail(e, "matrix norm kernel");
+  e = flce::launch_ortho_copy(c, p->dtype, s);
+  if (e != cudaSuccess) return cuda_fail(e, "matrix copy kernel");
   e = flce::launch_ortho_run(r, p->out_dtype, s);
   return e == cudaSuccess ? FLCE_OK : cuda_fail(e, "orthogonalising kernel");
 }

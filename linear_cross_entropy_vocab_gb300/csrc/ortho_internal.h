@@ -44,34 +44,56 @@ struct OrthoStep {
   float poly, old, diag;  // the square, the gram's halves, and on the diagonal
   float product;
 };
+
+enum class OrthoOp : int {
+  kGram,     // c = a a^T over x's columns
+  kSquare,   // c = a b of polynomials of one gram, which commute: symmetric
+  kPoly,     // c = diag I + old a + a a, a the gram
+  kMul,      // c = a x
+  kOutWide,  // out = a x
+  kOutTall,  // out = x^T b, of the transposed copy of a tall matrix
+};
+// The operands and results of products: two copies of x and four m x m
+// matrices; the result of the last.
+enum OrthoBuffer { kOrthoX0, kOrthoX1, kOrthoGram, kOrthoP0, kOrthoP1, kOrthoP2, kOrthoBuffers,
+                   kOrthoOut = kOrthoBuffers };
+struct OrthoProduct {
+  int8_t op, a, b, c;  // OrthoOp, OrthoBuffer
+  int8_t cut;          // of the cuts: 0 kGram, 1 symmetric ones else, 2 with x
+  int8_t power;        // of the norm's factor
+  float scale;         // of the sums
+  float old, diag;     // kPoly
+  int32_t need;        // what a matrix (or all: joint) has counted before
+};
+// Three steps a group (see ortho_api.cu) are eleven products.
+constexpr int kOrthoMaxProducts = 240;
+
 // Of a product's tiles over the whole batch, `whole` are taken whole and `cut`
 // along their contraction, among `units` pairs of CTAs.
 struct OrthoCut {
   int32_t units, whole, cut;
 };
 
-// All steps over all matrices. x alternates between two copies. Sides are
-// padded to tiles; `along` maps have boxes of 64 along the contraction x 128
-// rows, `across` of 64 x 64 with the contraction across rows, `store` of
-// 32 x 32 with 64-byte swizzle.
+// All steps over all matrices. Sides are padded to tiles; `along` maps have boxes
+// of 64 along the contraction x 128 rows, `across` (of x) of 64 x 64 with the
+// contraction across rows, `store` of 32 x 32 with 64-byte swizzle.
 struct OrthoRunParams {
-  CUtensorMap x_along[2], x_across[2], x_store[2];
-  CUtensorMap g_along, g_store, p_along, p_store;  // the gram and the polynomial
-  CUtensorMap out_store;  // [batch][rows][cols], where out_mapped
-  OrthoStep step[kOrthoMaxSteps];
-  OrthoCut cut[3];     // of the gram, the polynomial, the product
-  int32_t steps, batch, units;
+  CUtensorMap along[kOrthoBuffers], across[2];
+  CUtensorMap store[kOrthoBuffers + 1];  // the last: out [batch][rows][cols], where out_mapped
+  OrthoProduct product[kOrthoMaxProducts];
+  OrthoCut cut[3];
+  int32_t products, batch, units;
   int32_t m_tiles, n_tiles;
   int32_t k_n, k_m;    // 64-deep stages along n and along m
   int32_t m_pad, m_rows, n_pad;
-  int32_t tall, out_mapped, rows, cols;  // of out
+  int32_t out_mapped, rows, cols;  // of out
   int32_t joint;       // matrices count together (where tiles are cut)
   const float* factor; // [batch]
   const void* gram;
   void* out;           // dense
   void* shares;        // sums of cut tiles: two of 256 KB for each pair
   int32_t* arrived;    // [cut][2 CTAs][8 warps], zeros before and after
-  int32_t* finished;   // [3][batch], zeros before
+  int32_t* finished;   // [batch], zeros before
   int32_t* err_word;
 };
 cudaError_t launch_ortho_run(const OrthoRunParams& p, int out_dtype, cudaStream_t s);

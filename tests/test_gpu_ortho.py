@@ -4,7 +4,9 @@ Tolerance, to first order in the roundings, all in the 2-norm over the entries. 
 singular values by f(s) = s (a + b s^2 + c s^4); a perturbation of x grows by at most
 D = max |f'(s)| over the range [0, top] of the values. The copy, the gram A, the polynomial p and
 the new x are rounded to halves, by 2^-11 of each entry at most: A's rounding enters p by at most
-|b| + 2 |c| top^2 and then x by top, p's enters x by top. Sums of k products in 32 bits add
+|b| + 2 |c| top^2 and then x by top, p's enters x by top. Steps that share a gram go by the polynomials
+gathered, and the next gram p A p by its two products, each rounded too; the bound taken is the
+larger of both ways. Sums of k products in 32 bits add
 k / 16 * 2^-23, and what halves cannot hold (2^-25 over the scale, which is 2^8 at least) is
 added. The result is rounded once more. Single entries are held to 16 times the mean of that
 bound, which is a sixth of an entry and less.
@@ -23,31 +25,61 @@ pytestmark = pytest.mark.gpu
 TYPES = [torch.float32, torch.bfloat16, torch.float16]
 
 
+def _groups(steps, together):
+    """How many steps each gram serves: three, and two at the end."""
+    sizes = []
+    while sum(sizes) < steps:
+        left = steps - sum(sizes)
+        sizes.append(1 if not together else 2 if left == 4 else min(3, left))
+    return sizes
+
+
 def _steps64(g, coefficients, eps, out_dtype):
     """(result, bound on the 2-norm of the result's error) for one matrix."""
     g = g.double()
-    x = g / (torch.linalg.matrix_norm(g) + eps)
-    if x.shape[0] > x.shape[1]:
-        x = x.t()
-    m, n = x.shape
+    x0 = g / (torch.linalg.matrix_norm(g) + eps)
+    if x0.shape[0] > x0.shape[1]:
+        x0 = x0.t()
+    m, n = x0.shape
     half = 2.0 ** -11 + n / 16 * 2.0 ** -23
     floor = 2.0 ** -33 * math.sqrt(m * n)
-    delta, top = half * float(x.norm()) + floor, 1.0
-    for k, (a, b, c) in enumerate(coefficients):
-        s = torch.linspace(0, top, 4001, dtype=torch.float64)
-        grow = float((a + 3 * b * s ** 2 + 5 * c * s ** 4).abs().max())
-        top_now = top
-        top = float((s * (a + b * s ** 2 + c * s ** 4)).abs().max()) * 1.02
-        gram = x @ x.t()
-        p = a * torch.eye(m, dtype=torch.float64, device=x.device) + b * gram + c * (gram @ gram)
-        x = p @ x
-        local = top_now * (abs(b) + 2 * abs(c) * top_now ** 2) * (half * float(gram.norm()) + floor)
-        local += top_now * (half * float(p.norm()) + floor)
-        delta = grow * delta + local
-        if k + 1 < len(coefficients):
-            delta += half * float(x.norm()) + floor
-    delta += torch.finfo(out_dtype).eps / 2 * float(x.norm()) + floor
-    return (x if x.shape == g.shape else x.t()), delta
+    eye = torch.eye(m, dtype=torch.float64, device=x0.device)
+
+    def rounded(t):
+        return half * float(t.norm()) + floor
+
+    deltas = []
+    for together in (False, True):
+        x, delta, top, k = x0, rounded(x0), 1.0, 0
+        for size in _groups(len(coefficients), together):
+            first = top
+            gram = x @ x.t()
+            d_gram, gathered, d_all, all_ = rounded(gram), eye, 0.0, 1.0
+            for s in range(size):
+                a, b, c = coefficients[k]
+                k += 1
+                t = torch.linspace(0, top, 4001, dtype=torch.float64)
+                delta *= float((a + 3 * b * t ** 2 + 5 * c * t ** 4).abs().max())
+                q = float((a + b * t ** 2 + c * t ** 4).abs().max())
+                p = a * eye + b * gram + c * (gram @ gram)
+                d_p = (abs(b) + 2 * abs(c) * top ** 2) * d_gram + rounded(p)
+                if s + 1 < size:
+                    half_way = p @ gram
+                    d_half = q * d_gram + top ** 2 * d_p + rounded(half_way)
+                    gram = half_way @ p
+                    d_gram = q * d_half + q * top ** 2 * d_p + rounded(gram)
+                d_all = q * d_all + all_ * d_p
+                gathered = p @ gathered
+                if s > 0:
+                    d_all += rounded(gathered)
+                all_ *= q
+                top = float((t * (a + b * t ** 2 + c * t ** 4)).abs().max()) * 1.02
+            x = gathered @ x
+            delta += first * d_all
+            if k < len(coefficients):
+                delta += rounded(x)
+        deltas.append(delta + torch.finfo(out_dtype).eps / 2 * float(x.norm()) + floor)
+    return (x if x.shape == g.shape else x.t()), max(deltas)
 
 
 def _check(got, g, coefficients=NEWTON_SCHULZ, eps=1e-7):
@@ -70,6 +102,8 @@ SIZES = [(1, 1, 1), (1, 1, 9), (2, 5, 3), (1, 64, 64), (3, 100, 300), (1, 300, 1
          # one side in shared memory, in clusters of 1 to 8, and just not
          (1, 128, 512), (2, 128, 513), (3, 1500, 100), (1, 128, 4096), (2, 4090, 65), (1, 7, 4097),
          (2, 129, 600), (300, 8, 24),
+         # steps that share a gram
+         (4, 3000, 700), (1, 1000, 5100), (30, 200, 4100),
          # tiles whose contraction is cut between CTAs: few, or more than a round
          (1, 1024, 2100), (4, 4000, 700), (90, 20, 1000), (80, 300, 900), (30, 100, 3000)]
 
@@ -110,6 +144,14 @@ def test_other_steps(m, n):
     got = orthogonalize(x[0], coefficients=((1.5, -0.5, 0.0),) * 40, out_dtype=torch.float16)
     values = torch.linalg.svdvals(got.double())
     assert float((values - 1).abs().max()) < 2e-2
+
+
+@pytest.mark.parametrize("steps", [1, 2, 3, 4, 6, 7, 8])
+def test_numbers_of_steps(steps):
+    coefficients = tuple((3.0 - 0.2 * k, -3.5 + 0.3 * k, 1.4 - 0.1 * k) for k in range(steps))
+    for x in (_matrices(3, 600, 5000, torch.bfloat16), _matrices(1, 300, 400, torch.bfloat16),
+              _matrices(1, 100, 1000, torch.bfloat16)):
+        _check(orthogonalize(x, coefficients=coefficients)[0], x[0], coefficients)
 
 
 def test_addresses_and_strides():

@@ -84,7 +84,7 @@ def test_pointer_refusals():
 def test_workspace_size():
     p = _problem(batch=3, rows=14336, cols=4096, row_pitch=4096)
     size = abi.flce_orthogonalize_workspace_size(p)
-    held = 3 * (2 * 2 * 4096 * 14336 + 2 * 2 * 4096 * 4096)
+    held = 3 * (2 * 2 * 4096 * 14336 + 4 * 2 * 4096 * 4096)
     # and the sums of tiles whose contraction is cut
     assert held <= size <= held + (1 << 20) + 160 * 256 * 1024
     small = _problem(batch=1, rows=256, cols=200, row_pitch=200)
