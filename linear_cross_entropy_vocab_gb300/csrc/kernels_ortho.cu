@@ -213,7 +213,6 @@ __global__ void __launch_bounds__(256) ortho_copy_kernel(const OrthoCopyParams p
 // ----------------------------------------------------------------- products
 
 constexpr int kRows = 128;  // accumulator rows of a CTA
-constexpr int kCols = 256;
 constexpr int kDepth = 64;  // of a stage: one 128-byte swizzle row of halves
 constexpr int kStages = 6;
 constexpr int kOperandBytes = kRows * kDepth * 2;
@@ -221,7 +220,16 @@ constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kWarps = kOrthoWarps;  // of the epilogue: two a quarter of the rows, half of the columns each
 constexpr int kThreads = 64 + 32 * kWarps;
 constexpr int kBoxBytes = 32 * 32 * 2;
-constexpr int kPieces = kCols / 64;  // of 32 columns, for an epilogue warp
+
+// CG = 2: a pair of CTAs on a tile of 256 x 256, each with 128 of its rows. CG =
+// 1: a CTA on a tile of 128 x 128, for matrices that have too few tiles of 256
+// for the SMs: a tile's products and its way out take half as long, and more
+// SMs have one.
+template <int CG>
+struct Shape {
+  static constexpr int kTile = kRows * CG;
+  static constexpr int kPieces = kTile / 64;  // of 32 columns, for an epilogue warp
+};
 
 struct Ctl {
   uint64_t full[kStages], empty[kStages];
@@ -233,15 +241,34 @@ struct Ctl {
 constexpr int kSmemBytes =
     1024 + kStages * kStageBytes + kWarps * 2 * kBoxBytes + static_cast<int>(sizeof(Ctl));
 
-template <bool ACROSS>
+template <int CG>
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x,
+                                         int y) {
+  if constexpr (CG == 2)
+    tma_load_2d_pair(dst, map, bar, x, y);
+  else
+    tma_load_2d(dst, map, bar, x, y);
+}
+template <int CG, bool ACROSS>
 __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* map, uint32_t bar,
                                              int side, int depth) {
   if constexpr (!ACROSS) {
-    tma_load_2d_pair(dst, map, bar, depth, side);  // {64 deep, 128 rows}
+    load_box<CG>(dst, map, bar, depth, side);  // {64 deep, 128 rows}
   } else {
-    tma_load_2d_pair(dst, map, bar, side, depth);  // two boxes {64, 64 deep}
-    tma_load_2d_pair(dst + 8192, map, bar, side + 64, depth);
+    load_box<CG>(dst, map, bar, side, depth);  // two boxes {64, 64 deep}
+    load_box<CG>(dst + 8192, map, bar, side + 64, depth);
   }
+}
+template <int CG>
+__device__ __forceinline__ void commit(uint32_t bar) {
+  if constexpr (CG == 2)
+    umma_commit_pair(bar, 0x3);
+  else
+    umma_commit(bar);
+}
+template <int CG>
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+  return CG == 2 ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity);
 }
 template <bool ACROSS>
 __device__ __forceinline__ uint64_t slice_desc(uint32_t base, int kk) {
@@ -258,18 +285,20 @@ __device__ __forceinline__ bool give_up(uint64_t t0, volatile int* abort_flag, i
   if (err_word) atomicOr(err_word, FLCE_DEVERR_TIMEOUT);
   return true;
 }
-__device__ __forceinline__ bool wait_pair(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+template <int CG>
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                           int* err_word) {
-  if (mbar_try_wait_cluster(bar, parity)) return true;
+  if (try_wait<CG>(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t it = 1;; ++it) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
+    if (try_wait<CG>(bar, parity)) return true;
     if ((it & 63u) == 0u && give_up(t0, abort_flag, err_word)) return false;
   }
 }
-__device__ __forceinline__ void drain_pair(uint32_t bar, uint32_t parity) {
+template <int CG>
+__device__ __forceinline__ void drain_bar(uint32_t bar, uint32_t parity) {
   const uint64_t t0 = globaltimer_ns();
-  while (!mbar_try_wait_cluster(bar, parity)) {
+  while (!try_wait<CG>(bar, parity)) {
     if (globaltimer_ns() - t0 > 1000000000ull) break;
   }
 }
@@ -445,10 +474,11 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 }
 // Where a pair leaves a warp's sums of a part: of the first part of a tile
 // (which ends the pair's stretch) or of another (which begins it).
+template <int CG>
 __device__ __forceinline__ float4* share_of(const OrthoRunParams& p, int unit, bool first,
                                             int rank, int warp) {
-  const int64_t slot = ((unit * 2 + (first ? 1 : 0)) * 2 + rank) * kWarps + warp;
-  return reinterpret_cast<float4*>(p.shares) + slot * (kPieces * 8 * 32);
+  const int64_t slot = ((unit * 2 + (first ? 1 : 0)) * CG + rank) * kWarps + warp;
+  return reinterpret_cast<float4*>(p.shares) + slot * (Shape<CG>::kPieces * 8 * 32);
 }
 
 // The loads of a part: each CTA its 128 rows of one operand and 128 of the 256
@@ -457,26 +487,27 @@ struct Ring {
   int stage;
   uint32_t phase, armed, last;
 };
-template <OrthoOp OP>
+template <int CG, OrthoOp OP>
 __device__ __forceinline__ bool load_part(const OrthoRunParams& p, const Product& q,
                                           const Part& part, const Tile& t, uint32_t base, int rank,
                                           Ctl* ctl, Ring& ring) {
   constexpr bool kAcrossA = OP == OrthoOp::kOutTall, kAcrossB = OP == OrthoOp::kMul || OP == OrthoOp::kOutWide;
   const CUtensorMap* const a = kAcrossA ? &p.across[q.with->a] : &p.along[q.with->a];
   const CUtensorMap* const b = kAcrossB ? &p.across[q.with->b] : &p.along[q.with->b];
-  const int a_side = t.m * kOrthoTile + rank * kRows, b_side = t.n * kOrthoTile + rank * kRows;
+  constexpr int kTile = Shape<CG>::kTile;
+  const int a_side = t.m * kTile + rank * kRows, b_side = t.n * kTile + rank * kRows;
   const int row0 = t.b * p.m_pad;
   for (int k = part.k0; k < part.k1; ++k) {
     const int s = ring.stage;
-    if (!wait_pair(smem_addr(&ctl->empty[s]), ring.phase ^ 1u, &ctl->abort, p.err_word))
+    if (!wait_bar<CG>(smem_addr(&ctl->empty[s]), ring.phase ^ 1u, &ctl->abort, p.err_word))
       return false;
     const uint32_t full_local = smem_addr(&ctl->full[s]);
-    const uint32_t full = map_to_rank(full_local, 0);
-    if (rank == 0) mbar_arrive_expect_tx(full_local, 2 * kStageBytes);
+    const uint32_t full = CG == 2 ? map_to_rank(full_local, 0) : full_local;
+    if (rank == 0) mbar_arrive_expect_tx(full_local, CG * kStageBytes);
     const uint32_t dst = base + s * kStageBytes;
-    load_operand<kAcrossA>(dst, a, full, kAcrossA ? a_side : row0 + a_side,
+    load_operand<CG, kAcrossA>(dst, a, full, kAcrossA ? a_side : row0 + a_side,
                            kAcrossA ? row0 + k * kDepth : k * kDepth);
-    load_operand<kAcrossB>(dst + kOperandBytes, b, full, kAcrossB ? b_side : row0 + b_side,
+    load_operand<CG, kAcrossB>(dst + kOperandBytes, b, full, kAcrossB ? b_side : row0 + b_side,
                            kAcrossB ? row0 + k * kDepth : k * kDepth);
     ring.armed |= 1u << s;
     ring.last = (ring.last & ~(1u << s)) | (ring.phase << s);
@@ -488,22 +519,26 @@ __device__ __forceinline__ bool load_part(const OrthoRunParams& p, const Product
   return true;
 }
 
-template <OrthoOp OP>
+template <int CG, OrthoOp OP>
 __device__ __forceinline__ bool multiply_part(const OrthoRunParams& p, const Part& part,
                                               uint32_t base, uint32_t d, Ctl* ctl, Ring& ring) {
   constexpr bool kAcrossA = OP == OrthoOp::kOutTall, kAcrossB = OP == OrthoOp::kMul || OP == OrthoOp::kOutWide;
   constexpr uint32_t idesc =
-      idesc_f16kind_f32(2 * kRows, kCols, kAcrossA ? 1 : 0, kAcrossB ? 1 : 0, 0);
+      idesc_f16kind_f32(Shape<CG>::kTile, Shape<CG>::kTile, kAcrossA ? 1 : 0, kAcrossB ? 1 : 0, 0);
   for (int k = part.k0; k < part.k1; ++k) {
-    if (!wait_pair(smem_addr(&ctl->full[ring.stage]), ring.phase, &ctl->abort, p.err_word))
+    if (!wait_bar<CG>(smem_addr(&ctl->full[ring.stage]), ring.phase, &ctl->abort, p.err_word))
       return false;
     tc_fence_after_sync();
     const uint32_t a0 = base + ring.stage * kStageBytes, b0 = a0 + kOperandBytes;
 #pragma unroll
     for (int kk = 0; kk < kDepth / 16; ++kk)
-      umma_bf16_pair(d, slice_desc<kAcrossA>(a0, kk), slice_desc<kAcrossB>(b0, kk), idesc,
-                     k != part.k0 || kk != 0 ? 1u : 0u);
-    umma_commit_pair(smem_addr(&ctl->empty[ring.stage]), 0x3);
+      if constexpr (CG == 2)
+        umma_bf16_pair(d, slice_desc<kAcrossA>(a0, kk), slice_desc<kAcrossB>(b0, kk), idesc,
+                       k != part.k0 || kk != 0 ? 1u : 0u);
+      else
+        umma_bf16(d, slice_desc<kAcrossA>(a0, kk), slice_desc<kAcrossB>(b0, kk), idesc,
+                  k != part.k0 || kk != 0 ? 1u : 0u);
+    commit<CG>(smem_addr(&ctl->empty[ring.stage]));
     if (++ring.stage == kStages) {
       ring.stage = 0;
       ring.phase ^= 1u;
@@ -514,13 +549,14 @@ __device__ __forceinline__ bool multiply_part(const OrthoRunParams& p, const Par
 
 // A warp's 32 rows and 128 columns of a part's accumulator: stored, or left for
 // the warp that joins the tile's sums. Returns whether the tile is stored.
-template <OrthoOp OP, class T>
+template <int CG, OrthoOp OP, class T>
 __device__ __forceinline__ bool finish_part(const OrthoRunParams& p, const Product& q,
                                             const Part& part, const Tile& t, uint32_t taddr,
                                             int unit, int rank, int warp, int quarter, int first,
                                             uint8_t* boxes, int lane) {
+  constexpr int kTile = Shape<CG>::kTile, kPieces = Shape<CG>::kPieces;
   constexpr bool kOut = OP == OrthoOp::kOutWide || OP == OrthoOp::kOutTall;
-  const int row0 = t.m * kOrthoTile + rank * kRows + quarter * 32;  // of the matrix
+  const int row0 = t.m * kTile + rank * kRows + quarter * 32;  // of the matrix
   const int row = row0 + lane;
   const bool mirrored = OP <= OrthoOp::kPoly && t.n > t.m;
   const OrthoProduct& with = *q.with;
@@ -536,19 +572,19 @@ __device__ __forceinline__ bool finish_part(const OrthoRunParams& p, const Produ
   // cut, each pair leaves its sums, and the warp that comes last adds all of
   // them, in the order of the contraction.
   const int pieces =
-      row0 >= rows ? 0 : min(kPieces, (cols - t.n * kOrthoTile - first * 32 + 31) / 32);
+      row0 >= rows ? 0 : min(kPieces, (cols - t.n * kTile - first * 32 + 31) / 32);
   int from = unit, to = unit;
   if (part.k1 - part.k0 < q.k_iters) {
     const OrthoCut& c = p.cut[q.with->cut];
     const int x = (part.tile - c.whole) * q.k_iters;
     from = owner_of(c, q.k_iters, x);
     to = owner_of(c, q.k_iters, x + q.k_iters - 1);
-    int* const counter = p.arrived + ((part.tile - c.whole) * 2 + rank) * kWarps + warp;
+    int* const counter = p.arrived + ((part.tile - c.whole) * CG + rank) * kWarps + warp;
     int before = 0;
     if (lane == 0) before = *reinterpret_cast<volatile int*>(counter);
     before = __shfl_sync(0xffffffffu, before, 0);
     if (before != to - from) {
-      float4* const mine = share_of(p, unit, unit == from, rank, warp) + lane;
+      float4* const mine = share_of<CG>(p, unit, unit == from, rank, warp) + lane;
 #pragma unroll 1
       for (int i = 0; i < pieces; ++i) {
         float v[32];
@@ -572,7 +608,7 @@ __device__ __forceinline__ bool finish_part(const OrthoRunParams& p, const Produ
   uint4 held[2][4];
   const uint4* const old = reinterpret_cast<const uint4*>(
       static_cast<const __half*>(p.gram) +
-      (int64_t(t.b) * p.m_pad + row0 + (lane >> 2)) * p.m_pad + t.n * kOrthoTile + first * 32 +
+      (int64_t(t.b) * p.m_pad + row0 + (lane >> 2)) * p.m_pad + t.n * kTile + first * 32 +
       (lane & 3) * 8);
   const auto fetch = [&](uint4(&g)[4], int i) {
     if (OP == OrthoOp::kPoly && i < pieces) {
@@ -585,7 +621,7 @@ __device__ __forceinline__ bool finish_part(const OrthoRunParams& p, const Produ
 #pragma unroll 1
   for (int i = 0; i < pieces; ++i) {
     const int ch = first + i;
-    const int col = t.n * kOrthoTile + ch * 32;
+    const int col = t.n * kTile + ch * 32;
     float v[32];
     tmem_load_32cols(taddr + static_cast<uint32_t>(ch * 32), v);
     if (from < to) {
@@ -598,7 +634,7 @@ __device__ __forceinline__ bool finish_part(const OrthoRunParams& p, const Produ
             for (int j = 0; j < 8; ++j) sum[j] += v[8 * g + j];
           } else {
             const float4* const other =
-                share_of(p, u, u == from, rank, warp) + lane + (i * 8 + 2 * g) * 32;
+                share_of<CG>(p, u, u == from, rank, warp) + lane + (i * 8 + 2 * g) * 32;
             const float4 f = __ldcg(other), h = __ldcg(other + 32);
             sum[0] += f.x, sum[1] += f.y, sum[2] += f.z, sum[3] += f.w;
             sum[4] += h.x, sum[5] += h.y, sum[6] += h.z, sum[7] += h.w;
@@ -688,11 +724,11 @@ __device__ __forceinline__ bool finish_part(const OrthoRunParams& p, const Produ
   return true;
 }
 
-// All products of all steps. A grid of CTA pairs, all of them resident (a
+// All products of all steps. A grid of CTA pairs (or CTAs), all of them resident (a
 // cooperative launch), walks the products' tiles in order; a tile waits until
 // the product before has finished its matrix, so that matrices of a batch pass
 // one another and nothing but a matrix's own order holds a pair up.
-template <class T>
+template <int CG, class T>
 __global__ void __launch_bounds__(kThreads, 1)
     ortho_run_kernel(const __grid_constant__ OrthoRunParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -701,8 +737,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* const boxes = smem_raw + (base - raw) + kStages * kStageBytes;
   Ctl* const ctl = reinterpret_cast<Ctl*>(boxes + kWarps * 2 * kBoxBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = static_cast<int>(cluster_ctarank());
-  const int unit = blockIdx.x >> 1;
+  constexpr int kTile = Shape<CG>::kTile, kPieces = Shape<CG>::kPieces;
+  const int rank = CG == 2 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int unit = static_cast<int>(blockIdx.x) / CG;
   volatile int* const abort_flag = &ctl->abort;
 
   if (threadIdx.x == 0) {
@@ -712,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_addr(&ctl->acc_full[b]), 1);
-      mbar_init(smem_addr(&ctl->acc_empty[b]), 2 * kWarps);  // of both CTAs
+      mbar_init(smem_addr(&ctl->acc_empty[b]), CG * kWarps);  // of both CTAs
     }
     mbar_init(smem_addr(&ctl->done), 1);
     ctl->abort = 0;
@@ -725,11 +762,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&p.across[kOrthoX0]);
   }
   if (warp == 1) {
-    tmem_alloc_pair(smem_addr(&ctl->tmem), 512);
-    tmem_relinquish_pair();
+    if constexpr (CG == 2) {
+      tmem_alloc_pair(smem_addr(&ctl->tmem), 2 * kTile);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_addr(&ctl->tmem), 2 * kTile);
+      tmem_relinquish();
+    }
   }
   tc_fence_before_sync();
-  cluster_sync();
+  if constexpr (CG == 2)
+    cluster_sync();
+  else
+    __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = ctl->tmem;
   int turn = 0;
@@ -754,14 +799,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             case OrthoOp::kGram:
             case OrthoOp::kSquare:
             case OrthoOp::kPoly:
-              ok = load_part<OrthoOp::kGram>(p, q, part, t, base, rank, ctl, ring);
+              ok = load_part<CG, OrthoOp::kGram>(p, q, part, t, base, rank, ctl, ring);
               break;
             case OrthoOp::kMul:
             case OrthoOp::kOutWide:
-              ok = load_part<OrthoOp::kMul>(p, q, part, t, base, rank, ctl, ring);
+              ok = load_part<CG, OrthoOp::kMul>(p, q, part, t, base, rank, ctl, ring);
               break;
             case OrthoOp::kOutTall:
-              ok = load_part<OrthoOp::kOutTall>(p, q, part, t, base, rank, ctl, ring);
+              ok = load_part<CG, OrthoOp::kOutTall>(p, q, part, t, base, rank, ctl, ring);
               break;
           }
         }
@@ -769,7 +814,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok && rank == 0) {
         for (int s = 0; s < kStages; ++s)
-          if (ring.armed & (1u << s)) drain_pair(smem_addr(&ctl->full[s]), (ring.last >> s) & 1u);
+          if (ring.armed & (1u << s)) drain_bar<CG>(smem_addr(&ctl->full[s]), (ring.last >> s) & 1u);
       }
     }
   } else if (warp == 1) {
@@ -782,39 +827,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         Walk walk(p, q, unit, turn);
         for (Part part; ok && walk.next(q, part); ++it) {
           const int buf = it & 1;
-          ok = wait_pair(smem_addr(&ctl->acc_empty[buf]), ((it >> 1) & 1u) ^ 1u, abort_flag,
+          ok = wait_bar<CG>(smem_addr(&ctl->acc_empty[buf]), ((it >> 1) & 1u) ^ 1u, abort_flag,
                          p.err_word);
           if (!ok) break;
           tc_fence_after_sync();
-          const uint32_t d = tmem + static_cast<uint32_t>(buf * kCols);
+          const uint32_t d = tmem + static_cast<uint32_t>(buf * kTile);
           switch (q.op) {
             case OrthoOp::kGram:
             case OrthoOp::kSquare:
             case OrthoOp::kPoly:
-              ok = multiply_part<OrthoOp::kGram>(p, part, base, d, ctl, ring);
+              ok = multiply_part<CG, OrthoOp::kGram>(p, part, base, d, ctl, ring);
               break;
             case OrthoOp::kMul:
             case OrthoOp::kOutWide:
-              ok = multiply_part<OrthoOp::kMul>(p, part, base, d, ctl, ring);
+              ok = multiply_part<CG, OrthoOp::kMul>(p, part, base, d, ctl, ring);
               break;
             case OrthoOp::kOutTall:
-              ok = multiply_part<OrthoOp::kOutTall>(p, part, base, d, ctl, ring);
+              ok = multiply_part<CG, OrthoOp::kOutTall>(p, part, base, d, ctl, ring);
               break;
           }
-          if (ok) umma_commit_pair(smem_addr(&ctl->acc_full[buf]), 0x3);
+          if (ok) commit<CG>(smem_addr(&ctl->acc_full[buf]));
         }
         turn = next_turn(p, q, turn);
       }
-      umma_commit_pair(smem_addr(&ctl->done), 0x3);
-      drain_pair(smem_addr(&ctl->done), 0);
+      commit<CG>(smem_addr(&ctl->done));
+      drain_bar<CG>(smem_addr(&ctl->done), 0);
     } else if (lane == 0) {
       // the other CTA's products write this one's tensor memory
-      drain_pair(smem_addr(&ctl->done), 0);
+      drain_bar<CG>(smem_addr(&ctl->done), 0);
     }
   } else {
     const int quarter = warp & 3;
     const int first = (warp - 2) >> 2 ? kPieces : 0;
-    const uint32_t acc_empty = map_to_rank(smem_addr(&ctl->acc_empty[0]), 0);
+    uint32_t acc_empty = smem_addr(&ctl->acc_empty[0]);
+    if constexpr (CG == 2) acc_empty = map_to_rank(acc_empty, 0);
     uint8_t* const box = boxes + (warp - 2) * 2 * kBoxBytes;
     int it = 0;
     bool ok = true;
@@ -833,40 +879,44 @@ __global__ void __launch_bounds__(kThreads, 1)
           ready = t.b;
         }
         const int buf = it & 1;
-        ok = __all_sync(0xffffffffu, wait_pair(smem_addr(&ctl->acc_full[buf]), (it >> 1) & 1u,
+        ok = __all_sync(0xffffffffu, wait_bar<CG>(smem_addr(&ctl->acc_full[buf]), (it >> 1) & 1u,
                                                abort_flag, p.err_word));
         if (!ok) break;
         tc_fence_after_sync();
         const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) +
-                               static_cast<uint32_t>(buf * kCols);
+                               static_cast<uint32_t>(buf * kTile);
         bool stored = false;
         switch (q.op) {
           case OrthoOp::kGram:
           case OrthoOp::kSquare:
-            stored = finish_part<OrthoOp::kGram, __half>(p, q, part, t, taddr, unit, rank, warp - 2, quarter,
+            stored = finish_part<CG, OrthoOp::kGram, __half>(p, q, part, t, taddr, unit, rank, warp - 2, quarter,
                                                 first, box, lane);
             break;
           case OrthoOp::kPoly:
-            stored = finish_part<OrthoOp::kPoly, __half>(p, q, part, t, taddr, unit, rank, warp - 2, quarter,
+            stored = finish_part<CG, OrthoOp::kPoly, __half>(p, q, part, t, taddr, unit, rank, warp - 2, quarter,
                                                 first, box, lane);
             break;
           case OrthoOp::kMul:
-            stored = finish_part<OrthoOp::kMul, __half>(p, q, part, t, taddr, unit, rank, warp - 2, quarter,
+            stored = finish_part<CG, OrthoOp::kMul, __half>(p, q, part, t, taddr, unit, rank, warp - 2, quarter,
                                                first, box, lane);
             break;
           case OrthoOp::kOutWide:
-            finish_part<OrthoOp::kOutWide, T>(p, q, part, t, taddr, unit, rank, warp - 2, quarter, first,
+            finish_part<CG, OrthoOp::kOutWide, T>(p, q, part, t, taddr, unit, rank, warp - 2, quarter, first,
                                      box, lane);
             break;
           case OrthoOp::kOutTall:
-            finish_part<OrthoOp::kOutTall, T>(p, q, part, t, taddr, unit, rank, warp - 2, quarter, first,
+            finish_part<CG, OrthoOp::kOutTall, T>(p, q, part, t, taddr, unit, rank, warp - 2, quarter, first,
                                      box, lane);
             break;
         }
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive_cluster(acc_empty + static_cast<uint32_t>(buf * sizeof(uint64_t)));
+          const uint32_t free = acc_empty + static_cast<uint32_t>(buf * sizeof(uint64_t));
+          if constexpr (CG == 2)
+            mbar_arrive_cluster(free);
+          else
+            mbar_arrive(free);
           if (stored) {
             tma_store_wait_all();
             fence_proxy_async_global();
@@ -880,33 +930,39 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before_sync();
   __syncwarp();
-  cluster_sync();
+  if constexpr (CG == 2)
+    cluster_sync();
+  else
+    __syncthreads();
   if (warp == 1) {
     __syncwarp();
     tc_fence_after_sync();
-    tmem_dealloc_pair(tmem, 512);
+    if constexpr (CG == 2)
+      tmem_dealloc_pair(tmem, 2 * kTile);
+    else
+      tmem_dealloc(tmem, 2 * kTile);
   }
 }
 
-template <class T>
+template <int CG, class T>
 cudaError_t launch_run(const OrthoRunParams& p, cudaStream_t s) {
-  const auto kernel = ortho_run_kernel<T>;
+  const auto kernel = ortho_run_kernel<CG, T>;
   const cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * p.units));
+  cfg.gridDim = dim3(static_cast<unsigned>(CG * p.units));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = s;
   cudaLaunchAttribute attr[2]{};
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeCooperative;
-  attr[1].val.cooperative = 1;
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CG;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = CG;  // a cluster where there are pairs
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
@@ -948,7 +1004,10 @@ cudaError_t launch_ortho_copy(const OrthoCopyParams& p, int dtype, cudaStream_t 
 }
 
 cudaError_t launch_ortho_run(const OrthoRunParams& p, int out_dtype, cudaStream_t s) {
-  return out_dtype == FLCE_BF16 ? launch_run<__nv_bfloat16>(p, s) : launch_run<__half>(p, s);
+  if (p.pairs)
+    return out_dtype == FLCE_BF16 ? launch_run<2, __nv_bfloat16>(p, s)
+                                  : launch_run<2, __half>(p, s);
+  return out_dtype == FLCE_BF16 ? launch_run<1, __nv_bfloat16>(p, s) : launch_run<1, __half>(p, s);
 }
 
 }  // namespace flce

@@ -205,14 +205,15 @@ struct Split {
 constexpr int64_t kPlanPairs = 80;  // that a workspace is planned for
 constexpr int64_t kMaxParts = 4;    // of a tile where there are fewer tiles than pairs
 
-// A step of 64 along the contraction takes a pair 0.27 us. Cutting costs a tile
-// some 3 us and 1.1 more for each further part, as the sums go through L2, and
+// A step of 64 along the contraction takes a pair 0.27 us (a CTA on 128 x 128
+// 0.14). Cutting costs a tile some 3 us and 1.1 (0.6) more for each further part, as the sums go through L2, and
 // pairs that no longer walk the contraction together share fewer loads. So
 // tiles are cut where the last round would leave most pairs idle for long:
 // eight grams of 1024 x 4096 (80 tiles, 64 steps) take 38 us cut and 49 whole,
 // the product of 4096 x 4096 (256 tiles) 82 and 89, but its gram (136 tiles)
 // 54 and 50, and that of 4096 x 14336 169 and 152.
-Split split_of(int64_t tiles, int64_t k_iters, int64_t pairs) {
+Split split_of(int64_t tiles, int64_t k_iters, int64_t pairs, bool large) {
+  const double each = large ? 0.27 : 0.14, join = large ? 1.1 : 0.6;
   if (tiles >= pairs) {
     const int64_t left = tiles % pairs;
     // the last round would run with `left` pairs
@@ -221,9 +222,9 @@ Split split_of(int64_t tiles, int64_t k_iters, int64_t pairs) {
     return {pairs, tiles - pairs - left, pairs + left};
   }
   int64_t parts = 1;
-  double best = 0.27 * k_iters;
+  double best = each * k_iters;
   for (int64_t s = 2; s <= kMaxParts && s * tiles <= pairs && 4 * s <= k_iters; ++s) {
-    const double t = 0.27 * k_iters / s + 1.9 + 1.1 * s;
+    const double t = each * k_iters / s + 1.9 + join * s;
     if (t < best) {
       best = t;
       parts = s;
@@ -232,7 +233,7 @@ Split split_of(int64_t tiles, int64_t k_iters, int64_t pairs) {
   return parts > 1 ? Split{parts * tiles, 0, tiles} : Split{tiles, tiles, 0};
 }
 
-constexpr int32_t kArrived = 2 * kPlanPairs * 2 * flce::kOrthoWarps;
+constexpr int32_t kArrived = 2 * (2 * kPlanPairs) * 2 * flce::kOrthoWarps;
 
 struct Plan {
   int64_t cluster, slab;  // of matrices that stay in shared memory, else 0
@@ -406,8 +407,13 @@ flce_status flce_orthogonalize(const flce_ortho_problem* p, const void* src, voi
     return FLCE_ERR_CUDA;
   r.products = list_products(p, plan.grouped, tall, r.product);
   r.batch = c.batch;
-  r.m_tiles = static_cast<int32_t>(plan.m_pad / flce::kOrthoTile);
-  r.n_tiles = static_cast<int32_t>(ceil_div(plan.n, flce::kOrthoTile));
+  // Tiles of 128 where all of a product with x find an SM.
+  const int64_t small = p->batch * ceil_div(plan.m, 128) * ceil_div(plan.n, 128);
+  r.pairs = small > sms ? 1 : 0;
+  const int64_t tile = r.pairs ? flce::kOrthoTile : flce::kOrthoTile / 2;
+  const int64_t ctas = r.pairs ? 2 : 1;  // of a tile
+  r.m_tiles = static_cast<int32_t>(ceil_div(plan.m, tile));
+  r.n_tiles = static_cast<int32_t>(ceil_div(plan.n, tile));
   r.k_n = static_cast<int32_t>(plan.n_pad / 64);
   r.k_m = static_cast<int32_t>(ceil_div(plan.m, 64));
   r.m_pad = c.m_pad;
@@ -423,7 +429,7 @@ flce_status flce_orthogonalize(const flce_ortho_problem* p, const void* src, voi
   r.arrived = c.count;
   r.finished = c.count + kArrived;
   r.err_word = err_word;
-  const int64_t pairs = std::min<int64_t>(kPlanPairs, sms / 2);
+  const int64_t pairs = std::min<int64_t>(2 * kPlanPairs, sms) / ctas;
   const int64_t triangle = p->batch * r.m_tiles * (r.m_tiles + 1) / 2;
   const int64_t all = p->batch * r.m_tiles * r.n_tiles;
   // Matrices of a batch fill each other's rounds: their tiles stay whole, unless
@@ -432,7 +438,7 @@ flce_status flce_orthogonalize(const flce_ortho_problem* p, const void* src, voi
   for (int i = 0; i < 3; ++i) {
     const int64_t tiles = i < 2 ? triangle : all;
     const Split split = whole ? Split{std::min(tiles, pairs), tiles, 0}
-                              : split_of(tiles, i == 0 ? r.k_n : r.k_m, pairs);
+                              : split_of(tiles, i == 0 ? r.k_n : r.k_m, pairs, r.pairs != 0);
     r.cut[i].units = static_cast<int32_t>(split.units);
     r.cut[i].whole = static_cast<int32_t>(split.whole);
     r.cut[i].cut = static_cast<int32_t>(split.cut);
@@ -442,7 +448,7 @@ flce_status flce_orthogonalize(const flce_ortho_problem* p, const void* src, voi
   int64_t need = 0;
   for (int i = 0; i < r.products; ++i) {
     r.product[i].need = static_cast<int32_t>(need);
-    need += (r.product[i].cut < 2 ? triangle : all) / (r.joint ? 1 : p->batch) * 2 *
+    need += (r.product[i].cut < 2 ? triangle : all) / (r.joint ? 1 : p->batch) * ctas *
             flce::kOrthoWarps;
   }
   if (need > 0x7fffffff) return fail(FLCE_ERR_UNSUPPORTED, "too many tiles and steps to count");

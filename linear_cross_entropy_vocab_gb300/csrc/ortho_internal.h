@@ -10,7 +10,7 @@
 
 namespace flce {
 
-constexpr int kOrthoTile = 256;
+constexpr int kOrthoTile = 256;  // or half of it
 constexpr int kOrthoWarps = 8;  // that store a tile, in each CTA
 constexpr int kOrthoShareBytes = kOrthoTile * kOrthoTile * 4;
 constexpr int kOrthoMaxSteps = 64;
@@ -69,7 +69,7 @@ struct OrthoProduct {
 constexpr int kOrthoMaxProducts = 240;
 
 // Of a product's tiles over the whole batch, `whole` are taken whole and `cut`
-// along their contraction, among `units` pairs of CTAs.
+// along their contraction, among `units` pairs of CTAs (or CTAs).
 struct OrthoCut {
   int32_t units, whole, cut;
 };
@@ -83,6 +83,7 @@ struct OrthoRunParams {
   OrthoProduct product[kOrthoMaxProducts];
   OrthoCut cut[3];
   int32_t products, batch, units;
+  int32_t pairs;       // tiles of 256 by CTA pairs, else of 128 by CTAs
   int32_t m_tiles, n_tiles;
   int32_t k_n, k_m;    // 64-deep stages along n and along m
   int32_t m_pad, m_rows, n_pad;
@@ -91,8 +92,8 @@ struct OrthoRunParams {
   const float* factor; // [batch]
   const void* gram;
   void* out;           // dense
-  void* shares;        // sums of cut tiles: two of 256 KB for each pair
-  int32_t* arrived;    // [cut][2 CTAs][8 warps], zeros before and after
+  void* shares;        // sums of cut tiles: two of 256 KB for each pair (64 for each CTA)
+  int32_t* arrived;    // [cut][CTAs of a tile][8 warps], zeros before and after
   int32_t* finished;   // [batch], zeros before
   int32_t* err_word;
 };
