@@ -23,7 +23,7 @@
 namespace flce {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kSide = 128;
 constexpr int kBlockBytes = kSide * 128;  // 64 columns of all rows
@@ -105,17 +105,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool vec = reinterpret_cast<uintptr_t>(src) % 16 == 0 &&
                    p.row_pitch * static_cast<int64_t>(sizeof(T)) % 16 == 0;
   double squares = 0.0;
-  // Both passes walk the source alike, 64 columns of x at a time and four pieces
+  // Both passes walk the source alike, 64 columns of x at a time and two pieces
   // a thread: the squares, and then the halves. A tall matrix gives a thread a
   // row of src and eight of its columns. (With divisions for the places, 128 x
   // 512 values took a CTA 29 us to come and go; NNN now.)
   const auto walk = [&](auto all, auto take) {
     for (int at = 0; at < p.slab; at += 64) {
-      float v[4][8];
+      float v[2][8];
       const int j = p.tall ? at + (tid & 63) : at + (tid & 7) * 8;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int i = p.tall ? ((tid >> 6) + 4 * q) * 8 : (tid >> 3) + 32 * q;
+      for (int q = 0; q < 2; ++q) {
+        const int i = p.tall ? ((tid >> 6) + 8 * q) * 8 : (tid >> 3) + 64 * q;
         const int r = p.tall ? j0 + j : i, c = p.tall ? i : j0 + j;  // of src
         if (r < p.rows && c < p.cols) {
           load_piece(src + int64_t(r) * p.row_pitch, c, p.cols, vec, v[q]);
@@ -126,22 +126,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       all(v);
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        take(p.tall ? ((tid >> 6) + 4 * q) * 8 : (tid >> 3) + 32 * q, j, v[q]);
+      for (int q = 0; q < 2; ++q)
+        take(p.tall ? ((tid >> 6) + 8 * q) * 8 : (tid >> 3) + 64 * q, j, v[q]);
     }
   };
-  const auto count = [&](const float(&v)[4][8]) {
-    // 32 squares in 32 bits, or in 64 where those do not hold them
+  const auto count = [&](const float(&v)[2][8]) {
+    // 16 squares in 32 bits, or in 64 where those do not hold them
     float sum = 0.0f;
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
+    for (int q = 0; q < 2; ++q)
 #pragma unroll
       for (int k = 0; k < 8; ++k) sum = fmaf(v[q][k], v[q][k], sum);
     double wide = sum;
     if (!(sum < 3.0e38f && sum > 1.0e-30f)) {
       wide = 0.0;
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
+      for (int q = 0; q < 2; ++q)
 #pragma unroll
         for (int k = 0; k < 8; ++k) wide += static_cast<double>(v[q][k]) * v[q][k];
     }
@@ -150,14 +150,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Whole aligned pieces that the registers hold are loaded at once and once.
   constexpr int kHeld = sizeof(T) == 4 ? 4 : 8;  // of 64 columns
   const bool held = vec && p.cols % 8 == 0 && p.slab <= kHeld * 64;
-  Raw<T> raws[kHeld][4];
+  Raw<T> raws[kHeld][2];
   if (held) {
 #pragma unroll
     for (int g = 0; g < kHeld; ++g) {
       const int j = p.tall ? g * 64 + (tid & 63) : g * 64 + (tid & 7) * 8;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int i = p.tall ? ((tid >> 6) + 4 * q) * 8 : (tid >> 3) + 32 * q;
+      for (int q = 0; q < 2; ++q) {
+        const int i = p.tall ? ((tid >> 6) + 8 * q) * 8 : (tid >> 3) + 64 * q;
         const int r = p.tall ? j0 + j : i, c = p.tall ? i : j0 + j;
         if (g * 64 < p.slab && r < p.rows && c < p.cols)
           raws[g][q].load(src + int64_t(r) * p.row_pitch + c);
@@ -167,9 +167,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 #pragma unroll
     for (int g = 0; g < kHeld; ++g) {
-      float v[4][8];
+      float v[2][8];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) raws[g][q].values(v[q]);
+      for (int q = 0; q < 2; ++q) raws[g][q].values(v[q]);
       if (g * 64 < p.slab) count(v);
     }
   } else {
@@ -213,21 +213,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int j = p.tall ? g * 64 + (tid & 63) : g * 64 + (tid & 7) * 8;
       if (g * 64 < p.slab) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < 2; ++q) {
           float v[8];
           raws[g][q].values(v);
-          put(p.tall ? ((tid >> 6) + 4 * q) * 8 : (tid >> 3) + 32 * q, j, v);
+          put(p.tall ? ((tid >> 6) + 8 * q) * 8 : (tid >> 3) + 64 * q, j, v);
         }
       }
     }
   } else {
-    walk([](const float(&)[4][8]) {}, put);
+    walk([](const float(&)[2][8]) {}, put);
   }
   fence_proxy_async_all();
   __syncthreads();
 
-  // ---- the steps. A warp has a quarter of the rows and half of the columns.
-  const int row = (warp & 3) * 32 + lane, half = warp >> 2;
+  // ---- the steps. A warp has a quarter of the rows and of the columns.
+  const int row = (warp & 3) * 32 + lane, part = warp >> 2;
   const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
   const uint32_t done = smem_addr(&ctl->done);
   const uint32_t x_at = base, gram_at = smem_addr(gram);
@@ -239,13 +239,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   // what all threads have written to shared memory is there for the products
   const auto written = [&] {
-    fence_proxy_async_all();
+    fence_proxy_async_smem();
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
   };
-  // 32 halves of a row of the gram or the polynomial from column 64 half + 32 g
-  const auto gram_piece = [&](int g, int k) { return gram + piece_of(row, half * 8 + g * 4 + k); };
+  // of the thread's 32 halves of the gram or the polynomial
+  const auto gram_piece = [&](int k) { return gram + piece_of(row, part * 4 + k); };
   for (int s = 0; s < p.steps; ++s) {
     const OrthoStep& st = p.step[s];
     const float f = s == 0 ? factor : 1.0f;
@@ -259,35 +259,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     finished();
     if (ranks == 1) {
-#pragma unroll 1
-      for (int g = 0; g < 2; ++g) {
-        float v[32];
-        tmem_load_32cols(lanes + half * 64 + g * 32, v);
-        const float scale = st.gram * f * f;
+      float v[32];
+      tmem_load_32cols(lanes + part * 32, v);
+      const float scale = st.gram * f * f;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t w[4];
+      for (int k = 0; k < 4; ++k) {
+        uint32_t w[4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            w[q] = half2_bits(v[8 * k + 2 * q] * scale, v[8 * k + 2 * q + 1] * scale);
-          *reinterpret_cast<uint4*>(gram_piece(g, k)) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
+        for (int q = 0; q < 4; ++q)
+          w[q] = half2_bits(v[8 * k + 2 * q] * scale, v[8 * k + 2 * q + 1] * scale);
+        *reinterpret_cast<uint4*>(gram_piece(k)) = make_uint4(w[0], w[1], w[2], w[3]);
       }
     } else {
       // each CTA adds up its share of the rows and sends the halves to all
       const int rows = kSide / ranks, owner = row / rows;
       const uint32_t to = map_to_rank(smem_addr(exchange), owner) +
                           static_cast<uint32_t>((rank * rows + row - owner * rows) * kSide * 4);
-#pragma unroll 1
-      for (int g = 0; g < 2; ++g) {
-        float v[32];
-        tmem_load_32cols(lanes + half * 64 + g * 32, v);
+      float v[32];
+      tmem_load_32cols(lanes + part * 32, v);
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          // pieces of a row turned by its number: rows are 512 bytes apart
-          store_cluster4(to + (((half * 16 + g * 8 + k) ^ (row & 7)) << 4),
-                         make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]));
-      }
+      for (int k = 0; k < 8; ++k)
+        // pieces of a row turned by its number: rows are 512 bytes apart
+        store_cluster4(to + (((part * 8 + k) ^ (row & 7)) << 4),
+                       make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]));
       tc_fence_before_sync();
       cluster_sync();
       tc_fence_after_sync();
@@ -320,20 +314,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       umma_commit(done);
     }
     finished();
-#pragma unroll 1
-    for (int g = 0; g < 2; ++g) {
+    {
       float v[32];
-      tmem_load_32cols(lanes + kSide + half * 64 + g * 32, v);
+      tmem_load_32cols(lanes + kSide + part * 32, v);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        uint4* const at = reinterpret_cast<uint4*>(gram_piece(g, k));
+        uint4* const at = reinterpret_cast<uint4*>(gram_piece(k));
         const uint4 old = *at;
         const uint32_t h[4] = {old.x, old.y, old.z, old.w};
         uint32_t w[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h[q]));
-          const int col = half * 64 + g * 32 + 8 * k + 2 * q;
+          const int col = part * 32 + 8 * k + 2 * q;
           float lo = fmaf(v[8 * k + 2 * q], st.poly, a.x * st.old);
           float hi = fmaf(v[8 * k + 2 * q + 1], st.poly, a.y * st.old);
           lo += row == col ? st.diag : 0.0f;
@@ -362,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool last = s + 1 == p.steps;
     const int groups = p.slab / 32;
 #pragma unroll 1
-    for (int g = half; g < groups; g += 2) {
+    for (int g = part; g < groups; g += 4) {
       float v[32];
       tmem_load_32cols(lanes + g * 32, v);
 #pragma unroll
@@ -395,15 +388,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (p.tall) {  // a row of out is a column of x
       const int i = tid & 127;
 #pragma unroll 8
-      for (int q = 0; q < 32; ++q) {
-        const int j = at + (tid >> 7) + 2 * q;
+      for (int q = 0; q < 16; ++q) {
+        const int j = at + (tid >> 7) + 4 * q;
         if (i < m && j0 + j < n) out[int64_t(j0 + j) * p.cols + i] = value(i, j);
       }
     } else if (whole) {
       const int j = at + (tid & 7) * 8;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int i = (tid >> 3) + 32 * q;
+      for (int q = 0; q < 2; ++q) {
+        const int i = (tid >> 3) + 64 * q;
         if (i < m && j0 + j < n)
           *reinterpret_cast<uint4*>(out + int64_t(i) * p.cols + j0 + j) =
               *reinterpret_cast<const uint4*>(x + piece_of(i, j >> 3));
@@ -411,8 +404,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
       const int j = at + (tid & 63);
 #pragma unroll 8
-      for (int q = 0; q < 32; ++q) {
-        const int i = (tid >> 6) + 4 * q;
+      for (int q = 0; q < 16; ++q) {
+        const int i = (tid >> 6) + 8 * q;
         if (i < m && j0 + j < n) out[int64_t(i) * p.cols + j0 + j] = value(i, j);
       }
     }
