@@ -1,5 +1,6 @@
-"""A small language model's head, trained and then used: the fused loss with clipped gradients, the
-head's weight in 8-bit integers, and a beam search over its logits.
+"""A small language model's head, trained and then used: the norm before the head, the fused loss
+with clipped gradients and an orthogonalised update, the norm's output and the head's weight in
+8-bit integers, and a beam search over its logits.
 
     python examples/train_and_decode.py
 
@@ -16,7 +17,7 @@ import torch
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 from linear_cross_entropy_vocab_gb300 import (  # noqa: E402
     beam_reorder_, beam_select, clip_grad_norm_, fused_linear_cross_entropy, int8_linear,
-    quantize_rows)
+    orthogonalize, quantize_rows, rms_norm, rms_norm_quantize)
 
 VOCAB, HIDDEN, STEPS, LENGTH = 1000, 256, 300, 24
 BEAMS, PROMPT, END = 4, 4, 0  # token 0 ends a sequence
@@ -40,27 +41,37 @@ class Model(torch.nn.Module):
         self.change = torch.nn.Embedding(2 * VOCAB, HIDDEN)
         self.place = torch.nn.Embedding(LENGTH, HIDDEN)
         self.mix = torch.nn.Linear(HIDDEN, HIDDEN)
+        self.norm = torch.nn.Parameter(torch.ones(HIDDEN))
         self.head = torch.nn.Parameter(torch.randn(VOCAB, HIDDEN) * HIDDEN ** -0.5)
 
     def hidden(self, token, before, place):
+        """What the layer adds, in 16 bits, and the stream it is added to, in 32."""
         x = self.token(token) + self.change(token - before + VOCAB) + self.place(place)
-        return x + torch.nn.functional.gelu(self.mix(x))
+        return torch.nn.functional.gelu(self.mix(x)).bfloat16(), x
 
 
 def train(model, generator):
-    optimizer = torch.optim.AdamW(model.parameters(), lr=1e-2, weight_decay=0.0)
+    # the layer's matrix is updated by its orthogonalised momentum, everything else by AdamW
+    mix = model.mix.weight
+    optimizer = torch.optim.AdamW([p for p in model.parameters() if p is not mix], lr=1e-2,
+                                  weight_decay=0.0)
+    momentum = torch.zeros_like(mix)
     losses = []
     for _ in range(STEPS):
         tokens = sequences(256, generator)
         before = torch.cat([tokens[:, :1], tokens[:, :-1]], 1)
         place = torch.arange(LENGTH, device="cuda").expand_as(tokens)
-        hidden = model.hidden(tokens, before, place)[:, 1:-1]
-        loss = fused_linear_cross_entropy(hidden.bfloat16(), model.head.bfloat16(),
+        added, stream = model.hidden(tokens, before, place)
+        hidden, _ = rms_norm(added, model.norm, residual=stream)
+        loss = fused_linear_cross_entropy(hidden[:, 1:-1], model.head.bfloat16(),
                                           tokens[:, 2:], reduction="mean")
-        optimizer.zero_grad()
+        model.zero_grad()
         loss.backward()
         clip_grad_norm_(model.parameters(), 1.0)
         optimizer.step()
+        with torch.no_grad():
+            momentum.mul_(0.95).add_(mix.grad)
+            mix.add_(orthogonalize(momentum), alpha=-0.02)
         losses.append(loss.detach())
     return float(losses[0]), float(losses[-1])
 
@@ -78,9 +89,10 @@ def decode(model, prompts):
     scores[:, 0] = 0.0
     finished = torch.zeros(batch, BEAMS, dtype=torch.bool, device="cuda")
     for at in range(PROMPT, LENGTH):
-        hidden = model.hidden(history[:, at - 1], history[:, at - 2],
-                              torch.full((batch * BEAMS,), at - 1, device="cuda"))
-        logits = int8_linear(hidden.bfloat16(), weight, weight_scale, out_dtype=torch.float32)
+        added, stream = model.hidden(history[:, at - 1], history[:, at - 2],
+                                     torch.full((batch * BEAMS,), at - 1, device="cuda"))
+        hidden, scale, _ = rms_norm_quantize(added, model.norm, residual=stream)
+        logits = int8_linear(hidden, weight, weight_scale, x_scale=scale)
         chosen = beam_select(logits.view(batch, BEAMS, VOCAB), scores, finished=finished,
                              pad_token=END)
         flags = finished.view(-1, 1)
