@@ -407,9 +407,12 @@ flce_status flce_orthogonalize(const flce_ortho_problem* p, const void* src, voi
     return FLCE_ERR_CUDA;
   r.products = list_products(p, plan.grouped, tall, r.product);
   r.batch = c.batch;
-  // Tiles of 128 where all of a product with x find an SM.
+  // Tiles of 128 where all of a product with x find an SM in two rounds: 2048 x
+  // 2048 (256 tiles) takes 274 us with them and 333 with tiles of 256, 1024 x
+  // 4096 (256) 208 and 282; 2500 x 2500 (400) 485 and 401, three of 2049 x 1365
+  // (561) 308 and 286.
   const int64_t small = p->batch * ceil_div(plan.m, 128) * ceil_div(plan.n, 128);
-  r.pairs = small > sms ? 1 : 0;
+  r.pairs = small > 2 * sms ? 1 : 0;
   const int64_t tile = r.pairs ? flce::kOrthoTile : flce::kOrthoTile / 2;
   const int64_t ctas = r.pairs ? 2 : 1;  // of a tile
   r.m_tiles = static_cast<int32_t>(ceil_div(plan.m, tile));

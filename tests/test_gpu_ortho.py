@@ -105,6 +105,8 @@ SIZES = [(1, 1, 1), (1, 1, 9), (2, 5, 3), (1, 64, 64), (3, 100, 300), (1, 300, 1
          # one side in shared memory, in clusters of 1 to 8, and just not
          (1, 128, 512), (2, 128, 513), (3, 1500, 100), (1, 128, 4096), (2, 4090, 65), (1, 7, 4097),
          (2, 129, 600), (300, 8, 24),
+         # tiles of 128 in two rounds, some cut, and just tiles of 256
+         (1, 1300, 2500), (2, 1900, 1200), (1, 2300, 2200),
          # steps that share a gram
          (4, 3000, 700), (1, 1000, 5100), (30, 200, 4100),
          # tiles whose contraction is cut between CTAs: few, or more than a round
