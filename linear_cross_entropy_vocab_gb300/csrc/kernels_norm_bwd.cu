@@ -26,7 +26,7 @@ namespace {
 template <class T, int TEAM, int VECS, int THREADS, int CTAS>
 __global__ void __launch_bounds__(THREADS, CTAS) rms_norm_bwd_kernel(const NormBwdParams p) {
   static_assert(TEAM == 32 || TEAM == THREADS, "a team is a warp or the CTA");
-  using Cols = Columns<TEAM, false>;
+  using Cols = Columns<TEAM>;
   constexpr int kTeams = THREADS / TEAM;
   __shared__ float sum_buf[2][THREADS / 32];
   __shared__ float share[kTeams > 1 ? kTeams : 1][kTeams > 1 ? TEAM * VECS * 8 : 1];
@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) rms_norm_bwd_kernel(const NormB
 #pragma unroll
     for (int i = 0; i < VECS; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) share[team][Cols::first(0, i, t) + j * Cols::kStep] = acc[i][j];
+      for (int j = 0; j < 8; ++j) share[team][Cols::first(0, i, t) + j * TEAM] = acc[i][j];
     __syncthreads();
     for (int64_t c = threadIdx.x; c < h; c += THREADS) {
       float v = share[0][c];
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) rms_norm_bwd_rows_kernel(const 
       float v[8];
       if (weighs) {
         if (p.weight_wide)
-          Columns<TEAM, true>::load(static_cast<const float*>(p.weight), e + i * TEAM * 8, h, v);
+          load_weights(p.weight, e + i * TEAM * 8, h, v);
         else
           w[i].values(v);
       }
@@ -430,10 +430,6 @@ int64_t parts_of(int64_t n, int64_t h, int kind, int sms) {
   const int64_t most = static_cast<int64_t>(sms) * k.ctas;
   const int64_t need = (n + k.rows - 1) / k.rows;
   return need < most ? need : most;
-}
-
-bool rows_of_16(const void* p, int64_t pitch, int size) {
-  return p == nullptr || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && pitch * size % 16 == 0);
 }
 
 template <class W>

@@ -420,19 +420,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <class T>
 cudaError_t launch_small(const OrthoSmallParams& p, cudaStream_t s) {
-  const int need = 1024 + p.slab / 64 * kBlockBytes + kGramBytes +
-                   (p.cluster > 1 ? kExchangeBytes : 0) + static_cast<int>(sizeof(Ctl));
-  // One CTA an SM: CTAs of two clusters that waited for each other's tensor
-  // memory would never end.
-  const int bytes = need > 120 * 1024 ? need : 120 * 1024;
+  // All of an SM's shared memory: where two CTAs share an SM's tensor memory,
+  // those of two clusters could wait for each other's and never end.
+  constexpr int kBytes = 227 * 1024;
+  static_assert(1024 + 512 / 64 * kBlockBytes + kGramBytes + kExchangeBytes +
+                        static_cast<int>(sizeof(Ctl)) <= kBytes,
+                "the widest slab does not fit");
   const auto kernel = ortho_small_kernel<T>;
   const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(p.batch * p.cluster));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(bytes);
+  cfg.dynamicSmemBytes = kBytes;
   cfg.stream = s;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;

@@ -19,10 +19,10 @@
 
 namespace flce {
 
-template <class T, bool QUANT, bool VEC, int TEAM, int VECS, int THREADS>
+template <class T, bool QUANT, int TEAM, int VECS, int THREADS>
 __global__ void __launch_bounds__(THREADS) rms_norm_kernel(const NormParams p) {
   static_assert(TEAM == 32 || TEAM == THREADS, "a team is a warp or the CTA");
-  using Cols = Columns<TEAM, VEC>;
+  using Cols = Columns<TEAM>;
   constexpr int kWarps = THREADS / 32;
   constexpr int kSweep = TEAM * VECS * 8;
   __shared__ float sum_buf[kWarps];
@@ -123,7 +123,6 @@ __global__ void __launch_bounds__(THREADS) rms_norm_kernel(const NormParams p) {
     const float inv = __fdiv_rn(1.0f, scale);
     if (t == 0) p.scale[row] = scale;
     int8_t* const q = p.q + row * p.q_pitch;
-    const bool qvec = (reinterpret_cast<uintptr_t>(q) & 7u) == 0;
     for (int64_t e0 = 0; e0 < h; e0 += kSweep) {
       if (again) {
         load(e0, false);
@@ -134,14 +133,10 @@ __global__ void __launch_bounds__(THREADS) rms_norm_kernel(const NormParams p) {
         const int64_t e = Cols::first(e0, i, t);
         if (e >= h) continue;
         round8(s[i], scale, inv);
-        if constexpr (VEC) {
-          put_bytes(q, e, h, qvec, s[i]);
-        } else {
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (e + j * TEAM < h)
-              q[e + j * TEAM] = static_cast<int8_t>(__float_as_uint(s[i][j]) & 0xffu);
-        }
+        for (int j = 0; j < 8; ++j)
+          if (e + j * TEAM < h)
+            q[e + j * TEAM] = static_cast<int8_t>(__float_as_uint(s[i][j]) & 0xffu);
       }
     }
   }
@@ -231,7 +226,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) rms_norm_rows_kernel(const Norm
       if (weighs) {
         float v[8];
         if (p.weight_wide)
-          Columns<TEAM, true>::load(static_cast<const float*>(p.weight), e + i * TEAM * 8, h, v);
+          load_weights(p.weight, e + i * TEAM * 8, h, v);
         else
           w[i].values(v);
 #pragma unroll
@@ -271,7 +266,7 @@ template <class T, bool QUANT, int TEAM, int VECS, int THREADS = TEAM>
 cudaError_t launch_norm_team(const NormParams& p, cudaStream_t s) {
   constexpr int64_t rows = THREADS / TEAM;  // of a CTA
   const unsigned grid = static_cast<unsigned>((p.n + rows - 1) / rows);
-  rms_norm_kernel<T, QUANT, false, TEAM, VECS, THREADS><<<grid, THREADS, 0, s>>>(p);
+  rms_norm_kernel<T, QUANT, TEAM, VECS, THREADS><<<grid, THREADS, 0, s>>>(p);
   return cudaGetLastError();
 }
 template <class T, class R, bool QUANT, int TEAM, int VECS, int THREADS = TEAM>
@@ -304,11 +299,6 @@ cudaError_t launch_norm_groups(const NormParams& p, cudaStream_t s) {
   if (p.h <= 4096) return launch_norm_stream<T, R, QUANT, 256, 2>(p, s);
   if (p.h <= 8192) return launch_norm_stream<T, R, QUANT, 512, 2>(p, s);
   return launch_norm_stream<T, R, QUANT, 1024, 2>(p, s);
-}
-
-// Whether every row of a tensor starts at a 16-byte boundary.
-inline bool rows_of_16(const void* p, int64_t pitch, int size) {
-  return p == nullptr || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && pitch * size % 16 == 0);
 }
 
 template <class T, bool QUANT>

@@ -111,43 +111,26 @@ struct Raw {
   }
 };
 
-// Which columns a thread of a team of TEAM holds in its i-th group of eight.
-// VEC: eight neighbours, rows that start at 16-byte boundaries and have whole
-// groups. Else column j of the group lies TEAM columns after the one before,
-// so that a warp's loads are neighbours.
-template <int TEAM, bool VEC>
+// A team's columns value by value, for rows that start anywhere: value j of a
+// thread's i-th group of eight lies TEAM columns after the one before, so that a
+// warp's loads are neighbours.
+template <int TEAM>
 struct Columns {
   static __device__ __forceinline__ int64_t first(int64_t e0, int i, int t) {
-    return e0 + (VEC ? (i * TEAM + t) * 8 : i * 8 * TEAM + t);
+    return e0 + i * 8 * TEAM + t;
   }
-  static constexpr int kStep = VEC ? 1 : TEAM;
-
   // Zeros past the row's end.
   template <class T>
   static __device__ __forceinline__ void load(const T* row, int64_t e, int64_t h, float (&v)[8]) {
-    if constexpr (VEC) {
-      if (e < h) {
-        load8(row + e, v);
-        return;
-      }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        v[j] = e + j * TEAM < h ? to_f32(row[e + j * TEAM]) : 0.0f;
-    }
+    for (int j = 0; j < 8; ++j) v[j] = e + j * TEAM < h ? to_f32(row[e + j * TEAM]) : 0.0f;
   }
   template <class T>
   static __device__ __forceinline__ void store(T* row, int64_t e, int64_t h,
                                                const float (&v)[8]) {
-    if constexpr (VEC) {
-      if (e < h) store8(row + e, v);
-    } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (e + j * TEAM < h) row[e + j * TEAM] = from_f32<T>(v[j]);
-    }
+    for (int j = 0; j < 8; ++j)
+      if (e + j * TEAM < h) row[e + j * TEAM] = from_f32<T>(v[j]);
   }
   // A tensor that is fp32 where `wide` and T otherwise.
   template <class T>
@@ -168,6 +151,21 @@ struct Columns {
       store(static_cast<T*>(p) + row_at, e, h, v);
   }
 };
+
+// Eight fp32 weights from column e on; zeros past the row's end.
+__device__ __forceinline__ void load_weights(const void* weight, int e, int64_t h, float (&v)[8]) {
+  if (e < h) {
+    load8(static_cast<const float*>(weight) + e, v);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+}
+
+// Whether every row of a tensor starts at a 16-byte boundary.
+inline bool rows_of_16(const void* p, int64_t pitch, int size) {
+  return p == nullptr || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && pitch * size % 16 == 0);
+}
 
 // The sum (or, for MaxOp, the maximum) of `v` over the team: a warp, or all
 // TEAM threads of the CTA, in a fixed order. `buf` holds a value a warp; calls

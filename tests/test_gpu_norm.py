@@ -269,6 +269,35 @@ def test_some_gradients_only():
     assert torch.equal(gx, ds.bfloat16()) and torch.equal(gr, ds) and not bool(gw.any())
 
 
+def test_one_tensor_in_two_places():
+    x, _, w = _inputs(30, 264, torch.float32, torch.float32)
+    dy, ds = torch.randn_like(x), torch.randn_like(x)
+    want = _backward(x, x.clone(), w, dy, ds)[2]
+    leaf, gain = x.clone().requires_grad_(), w.clone().requires_grad_()
+    y, total = rms_norm(leaf, gain, residual=leaf)
+    gx, gw = torch.autograd.grad([y, total], [leaf, gain], [dy, ds])
+    assert torch.equal(gx, 2 * want["x"]) and torch.equal(gw, want["weight"])
+    # accumulated into leaves, twice: the shared gradient is not written to
+    leaves = [t.clone().requires_grad_() for t in (x, x, w)]
+    for _ in range(2):
+        y, total = rms_norm(leaves[0], leaves[2], residual=leaves[1])
+        torch.autograd.backward([y, total], [dy, ds])
+    assert torch.equal(leaves[0].grad, 2 * want["x"])
+    assert torch.equal(leaves[1].grad, 2 * want["x"])
+    # one after the other, through the stream
+    y, total = rms_norm(leaf, gain, residual=x)
+    y2, total2 = rms_norm(y, gain, residual=total)
+    g = torch.autograd.grad([y2, total2], leaf, [dy, ds])[0]
+    l64 = x.double().requires_grad_()
+    s1 = l64 + x.double()
+    u1 = s1 * torch.rsqrt((s1 * s1).mean(1, keepdim=True) + 1e-6) * w.double()
+    s2 = u1 + s1
+    u2 = s2 * torch.rsqrt((s2 * s2).mean(1, keepdim=True) + 1e-6) * w.double()
+    ref = torch.autograd.grad((u2 * dy.double()).sum() + (s2 * ds.double()).sum(), l64)[0]
+    # two layers of products of 32-bit values, 64 roundings each
+    assert float((g.double() - ref).norm()) <= 128 * U * float(ref.norm()) * 2
+
+
 def test_autograd_rules():
     x, r, w = _inputs(5, 64, torch.float32, torch.float32)
     leaf = x.clone().requires_grad_()
