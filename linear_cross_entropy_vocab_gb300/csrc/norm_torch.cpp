@@ -1,0 +1,225 @@
+// The root-mean-square norm as PyTorch operators over the C ABI: allocation of
+// results, the current stream, and the autograd node. In C++ because these calls
+// are shorter than Python's share of them: autograd runs a node in a thread of
+// its own, where a node written in Python took 100 us more than this one.
+#include <ATen/ATen.h>
+#include <c10/cuda/CUDAGuard.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/autograd/custom_function.h>
+#include <torch/csrc/autograd/functions/basic_ops.h>
+#include <torch/library.h>
+
+#include <memory>
+#include <optional>
+#include <tuple>
+#include <vector>
+
+#include "flce.h"
+
+namespace {
+
+using at::Tensor;
+using torch::autograd::AutogradContext;
+using torch::autograd::variable_list;
+
+int32_t code_of(const Tensor& t) {
+  switch (t.scalar_type()) {
+    case at::kFloat:
+      return FLCE_F32;
+    case at::kBFloat16:
+      return FLCE_BF16;
+    case at::kHalf:
+      return FLCE_F16;
+    default:
+      TORCH_CHECK_TYPE(false, "unsupported dtype ", t.scalar_type());
+  }
+}
+
+void check(flce_status status, const char* call) {
+  TORCH_CHECK(status == FLCE_OK, call, ": ", flce_status_string(status), ": ", flce_last_error());
+}
+
+void* stream_of(const Tensor& t) {
+  return c10::cuda::getCurrentCUDAStream(t.device().index()).stream();
+}
+
+const void* pointer(const Tensor& t) { return t.defined() ? t.const_data_ptr() : nullptr; }
+void* writable(const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
+
+// t [..., H] as rows of contiguous elements at one pitch.
+Tensor rows_of(const Tensor& t, int64_t& pitch) {
+  const int64_t h = t.size(-1);
+  pitch = h;
+  if (t.is_contiguous()) return t;
+  if (t.dim() == 2 && (t.stride(1) == 1 || h == 1) && t.stride(0) >= h) {
+    pitch = t.stride(0);
+    return t;
+  }
+  return t.contiguous();
+}
+
+Tensor empty_as(const Tensor& shape_of, const Tensor& like) {
+  return at::empty(shape_of.sizes(), like.options());
+}
+
+// Inputs as the library takes them.
+struct Inputs {
+  Tensor x, weight, residual;
+  flce_norm_problem problem{};
+};
+Inputs prepare(const Tensor& x, const std::optional<Tensor>& weight, double eps,
+               const std::optional<Tensor>& residual) {
+  Inputs in;
+  flce_norm_problem& p = in.problem;
+  in.x = rows_of(x, p.x_pitch);
+  p.h = x.size(-1);
+  p.n = x.numel() / p.h;
+  p.dtype = p.sum_dtype = p.weight_dtype = code_of(x);
+  p.residual_pitch = p.h;
+  p.eps = static_cast<float>(eps);
+  if (residual) {
+    in.residual = rows_of(*residual, p.residual_pitch);
+    p.sum_dtype = code_of(in.residual);
+  }
+  if (weight) {
+    in.weight = weight->contiguous();
+    p.weight_dtype = code_of(in.weight);
+  }
+  return in;
+}
+
+// (y, sum or undefined); fills rstd where it is defined.
+std::tuple<Tensor, Tensor> forward(const Inputs& in, const Tensor& rstd) {
+  const c10::cuda::CUDAGuard guard(in.x.device());
+  const Tensor y = empty_as(in.x, in.x);
+  const Tensor sum = in.residual.defined() ? empty_as(in.x, in.residual) : Tensor();
+  check(flce_rms_norm(&in.problem, pointer(in.x), pointer(in.residual), pointer(in.weight),
+                      writable(y), writable(sum), static_cast<float*>(writable(rstd)),
+                      stream_of(in.x)),
+        "flce_rms_norm");
+  return {y, sum};
+}
+
+class RmsNorm : public torch::autograd::Function<RmsNorm> {
+ public:
+  static variable_list forward(AutogradContext* ctx, const Tensor& x,
+                               const std::optional<Tensor>& weight, double eps,
+                               const std::optional<Tensor>& residual) {
+    const Inputs in = prepare(x, weight, eps, residual);
+    const Tensor rstd = at::empty({in.problem.n}, x.options().dtype(at::kFloat));
+    auto [y, sum] = ::forward(in, rstd);
+    ctx->set_materialize_grads(false);
+    ctx->save_for_backward({residual ? sum : in.x, in.weight, rstd});
+    ctx->saved_data["eps"] = eps;
+    ctx->saved_data["dtype"] = static_cast<int64_t>(x.scalar_type());
+    if (residual) return {y, sum};
+    return {y};
+  }
+
+  static variable_list backward(AutogradContext* ctx, const variable_list& grads) {
+    const variable_list saved = ctx->get_saved_variables();
+    const Tensor &total = saved[0], &weight = saved[1], &rstd = saved[2];
+    // inputs that are tensors are counted
+    size_t input = 0;
+    const bool need_x = ctx->needs_input_grad(input++);
+    const bool need_weight = weight.defined() && ctx->needs_input_grad(input++);
+    const bool need_residual = grads.size() > 1 && ctx->needs_input_grad(input);
+    Tensor grad_y = grads[0], grad_sum = grads.size() > 1 ? grads[1] : Tensor();
+    const auto dtype = static_cast<at::ScalarType>(ctx->saved_data["dtype"].toInt());
+    const bool wide = total.scalar_type() != dtype;
+    Tensor grad_x, grad_weight, grad_residual;
+    if (!grad_y.defined()) {  // y is not used: the sum's gradient passes through
+      if (grad_sum.defined()) {
+        if (need_x) grad_x = grad_sum.to(dtype);
+        if (need_weight) grad_weight = at::zeros_like(weight);
+        if (need_residual) grad_residual = grad_sum;
+      }
+    } else {
+      const c10::cuda::CUDAGuard guard(total.device());
+      grad_y = grad_y.contiguous();
+      if (grad_sum.defined()) grad_sum = grad_sum.contiguous();
+      // in one type the gradients of x and of the residual are one tensor
+      if (need_x || (need_residual && !wide)) grad_x = empty_as(total, grad_y);
+      if (need_residual && wide) grad_residual = empty_as(total, total);
+      if (need_weight) grad_weight = at::empty_like(weight);
+      flce_norm_problem p{};
+      p.h = total.size(-1);
+      p.n = rstd.numel();
+      p.x_pitch = p.residual_pitch = p.h;
+      if (!total.is_contiguous()) p.x_pitch = total.stride(0);  // rows_of has seen to the rest
+      p.dtype = code_of(grad_y);
+      p.sum_dtype = code_of(total);
+      p.weight_dtype = weight.defined() ? code_of(weight) : p.dtype;
+      p.eps = static_cast<float>(ctx->saved_data["eps"].toDouble());
+      const size_t bytes = flce_rms_norm_backward_workspace_size(&p);
+      const Tensor workspace =
+          at::empty({static_cast<int64_t>(bytes)}, total.options().dtype(at::kByte));
+      check(flce_rms_norm_backward(&p, pointer(grad_y), pointer(grad_sum), pointer(total),
+                                   pointer(weight), static_cast<const float*>(pointer(rstd)),
+                                   writable(grad_x), writable(grad_residual),
+                                   writable(grad_weight), writable(workspace), bytes,
+                                   stream_of(total)),
+            "flce_rms_norm_backward");
+      if (need_residual && !wide) grad_residual = grad_x;
+      if (!need_x) grad_x = Tensor();
+    }
+    variable_list out{grad_x, grad_weight, Tensor(), grad_residual};
+    if (at::GradMode::is_enabled()) {
+      // a graph of the backward is asked for: its outputs refuse to go further
+      variable_list some;
+      for (const Tensor& t : out)
+        if (t.defined()) some.push_back(t);
+      const auto refuse = std::make_shared<torch::autograd::DelayedError>(
+          "rms_norm cannot be differentiated twice", static_cast<int64_t>(some.size()));
+      for (Tensor& t : some) t = t.detach().requires_grad_();
+      some = (*refuse)(std::move(some));
+      size_t next = 0;
+      for (Tensor& t : out)
+        if (t.defined()) t = some[next++];
+    }
+    return out;
+  }
+};
+
+std::vector<Tensor> rms_norm(const Tensor& x, const std::optional<Tensor>& weight, double eps,
+                             const std::optional<Tensor>& residual, bool differentiable) {
+  if (differentiable) return RmsNorm::apply(x, weight, eps, residual);
+  const Inputs in = prepare(x, weight, eps, residual);
+  auto [y, sum] = forward(in, Tensor());
+  if (residual) return {y, sum};
+  return {y};
+}
+
+std::vector<Tensor> rms_norm_quantize(const Tensor& x, const std::optional<Tensor>& weight,
+                                      double eps, const std::optional<Tensor>& residual) {
+  const Inputs in = prepare(x, weight, eps, residual);
+  const flce_norm_problem& p = in.problem;
+  const c10::cuda::CUDAGuard guard(x.device());
+  // rows at multiples of 16 bytes, as the 8-bit layer reads them best
+  const int64_t pitch = (p.h + 15) / 16 * 16;
+  Tensor q = at::empty({p.n, pitch}, x.options().dtype(at::kChar));
+  const auto lead = x.sizes().slice(0, x.dim() - 1);
+  const Tensor scale = at::empty(lead, x.options().dtype(at::kFloat));
+  const Tensor sum = residual ? empty_as(in.x, in.residual) : Tensor();
+  check(flce_rms_norm_quantize(&p, pointer(in.x), pointer(in.residual), pointer(in.weight),
+                               static_cast<int8_t*>(writable(q)), pitch,
+                               static_cast<float*>(writable(scale)), writable(sum), stream_of(x)),
+        "flce_rms_norm_quantize");
+  if (pitch != p.h) q = q.narrow(1, 0, p.h);
+  if (lead.empty())
+    q = q.select(0, 0);
+  else if (lead.size() > 1)
+    q = q.unflatten(0, lead);
+  if (residual) return {q, scale, sum};
+  return {q, scale};
+}
+
+}  // namespace
+
+TORCH_LIBRARY(flce, m) {
+  m.def("rms_norm(Tensor x, Tensor? weight, float eps, Tensor? residual, bool differentiable) "
+        "-> Tensor[]",
+        &rms_norm);
+  m.def("rms_norm_quantize(Tensor x, Tensor? weight, float eps, Tensor? residual) -> Tensor[]",
+        &rms_norm_quantize);
+}

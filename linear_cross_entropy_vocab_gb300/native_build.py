@@ -3,7 +3,9 @@
 The translation units are compiled in parallel and linked into
 ``linear_cross_entropy_vocab_gb300/_build/libflce.so``; the CUDA runtime is
 linked statically and the driver's tensor-map encoder is looked up at run
-time, so the library needs no libcuda at link time.
+time, so the library needs no libcuda at link time. Beside it lies
+``libflce_torch.so``: the operators that are registered with PyTorch, compiled
+by the host compiler against the installed PyTorch and linked to libflce.so.
 """
 from __future__ import annotations
 
@@ -18,6 +20,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libflce.so")
+TORCH_LIB = os.path.join(BUILD, "libflce_torch.so")
+TORCH_SOURCE = "norm_torch.cpp"
 
 SOURCES = ["flce_api.cu", "kernels_tc.cu", "kernels_simt.cu", "kernels_rows.cu",
            "grads_api.cu", "kernels_grads.cu", "beam_api.cu", "kernels_beam.cu",
@@ -44,10 +48,43 @@ def _inputs():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(TORCH_LIB)):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(TORCH_LIB))
     return all(os.path.getmtime(f) <= t for f in _inputs())
+
+
+def _compile_torch() -> str:
+    """The object file of the operators that are registered with PyTorch."""
+    import torch
+
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        raise RuntimeError("no C++ compiler found (g++)")
+    include = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
+    obj = os.path.join(BUILD, "norm_torch.o")
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-I", INCLUDE, "-isystem", include, "-isystem",
+           os.path.join(include, "torch", "csrc", "api", "include"), "-isystem", cuda,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-c",
+           os.path.join(CSRC, TORCH_SOURCE), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cxx} failed on {TORCH_SOURCE}:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_torch(obj: str) -> None:
+    import torch
+
+    tmp = TORCH_LIB + ".tmp"
+    cmd = [shutil.which("g++") or shutil.which("c++"), "-shared", "-o", tmp, obj, "-L", BUILD,
+           "-lflce", "-L", os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_cpu",
+           "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, TORCH_LIB)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -67,14 +104,17 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(r.stdout, r.stderr)
         return obj
 
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        torch_obj = ex.submit(_compile_torch)
         objs = list(ex.map(compile_one, SOURCES))
+        torch_obj = torch_obj.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_torch(torch_obj)
     return LIB
 
 

@@ -5,31 +5,31 @@
 
 ``rms_norm`` gives y (and s) with their gradients, ``rms_norm_quantize`` gives y in 8-bit integers
 as int8_linear takes them. The work runs in libflce.so (``flce_rms_norm``,
-``flce_rms_norm_quantize``, ``flce_rms_norm_backward``).
+``flce_rms_norm_quantize``, ``flce_rms_norm_backward``), called by the operators of
+libflce_torch.so.
 """
 from __future__ import annotations
 
+import os
 from typing import Optional
 
 import torch
 from torch.autograd import forward_ad
-from torch.autograd.function import once_differentiable
 
-from . import abi
+from . import abi, native_build
 from ._autograd import refuse_gradient
-from ._stream import on_device, raw_stream
 
 __all__ = ["rms_norm", "rms_norm_quantize"]
 
-_DTYPES = {torch.float32: abi.FLCE_F32, torch.bfloat16: abi.FLCE_BF16,
-           torch.float16: abi.FLCE_F16}
+_DTYPES = (torch.float32, torch.bfloat16, torch.float16)
+_MAX_H = 1 << 24
 
 
 def _check_inputs(x, weight, eps, residual) -> None:
     if x.dtype not in _DTYPES:
         raise TypeError(f"unsupported dtype {x.dtype}: use float32, bfloat16 or float16")
-    if x.dim() < 1 or x.shape[-1] < 1:
-        raise ValueError("x must be (..., H) with H of at least 1")
+    if x.dim() < 1 or not 1 <= x.shape[-1] <= _MAX_H:
+        raise ValueError("x must be (..., H) with H of at least 1 and at most 2^24")
     if weight is not None:
         if weight.shape != x.shape[-1:]:
             raise ValueError("weight must be (H,)")
@@ -49,106 +49,22 @@ def _check_inputs(x, weight, eps, residual) -> None:
             raise ValueError(f"{name} is on {t.device}, x on {x.device}")
 
 
-def _rows(t: torch.Tensor):
-    """``t`` [..., H] as rows of contiguous elements at one pitch: (tensor, pitch)."""
-    h = t.shape[-1]
-    if t.is_contiguous():
-        return t, h
-    if t.dim() == 2 and (t.stride(1) == 1 or h == 1) and t.stride(0) >= h:
-        return t, t.stride(0)
-    return t.contiguous(), h
+_ops = None
 
 
-def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
-
-
-def _prepare(x, weight, eps, residual):
-    """x, residual and weight as rows, and the problem that they make."""
-    x, x_pitch = _rows(x)
-    h = x.shape[-1]
-    code = sum_code = weight_code = _DTYPES[x.dtype]
-    residual_pitch = h
-    if residual is not None:
-        residual, residual_pitch = _rows(residual)
-        sum_code = _DTYPES[residual.dtype]
-    if weight is not None:
-        weight_code = _DTYPES[weight.dtype]
-        if not weight.is_contiguous():
-            weight = weight.contiguous()
-    problem = abi.flce_norm_problem(x.numel() // h, h, x_pitch, residual_pitch, code, sum_code,
-                                    weight_code, eps, 0)
-    return x, weight, residual, problem
-
-
-def _forward(x, weight, residual, problem, rstd):
-    """(y, sum or None); fills ``rstd`` where one is given."""
-    dense = torch.contiguous_format
-    y = torch.empty_like(x, memory_format=dense)
-    total = None if residual is None else torch.empty_like(residual, memory_format=dense)
-    dev = x.device
-    with on_device(dev):
-        abi.flce_rms_norm(problem, x.data_ptr(), _ptr(residual), _ptr(weight), y.data_ptr(),
-                          _ptr(total), _ptr(rstd), raw_stream(dev))
-    return y, total
-
-
-class _RmsNorm(torch.autograd.Function):
-    # The backward runs in autograd's own thread, where Python takes several times as long: what
-    # it needs to know is worked out here.
-    @staticmethod
-    def forward(ctx, x, weight, eps, residual):
-        ctx.set_materialize_grads(False)
-        x, weight, residual, problem = _prepare(x, weight, eps, residual)
-        rstd = x.new_empty(problem.n, dtype=torch.float32)
-        y, total = _forward(x, weight, residual, problem, rstd)
-        if residual is None:
-            ctx.save_for_backward(x, weight, rstd)
-        else:
-            ctx.save_for_backward(total, weight, rstd)
-            problem.x_pitch = problem.h  # of the sum
-        ctx.plan = problem, abi.flce_rms_norm_backward_workspace_size(problem)
-        return y if residual is None else (y, total)
-
-    @staticmethod
-    def backward(ctx, grad_y, grad_sum=None):
-        if torch.is_grad_enabled():  # a graph of the backward is asked for
-            return _backward_once(ctx, grad_y, grad_sum)
-        return _backward(ctx, grad_y, grad_sum)
-
-
-def _backward(ctx, grad_y, grad_sum):
-    total, weight, rstd = ctx.saved_tensors
-    need_x, need_weight, _, need_residual = ctx.needs_input_grad
-    problem, ws_bytes = ctx.plan
-    wide = problem.sum_dtype != problem.dtype
-    if grad_y is None:  # y is not used: the sum's gradient passes through
-        if grad_sum is None:
-            return None, None, None, None
-        dtype = next(t for t, code in _DTYPES.items() if code == problem.dtype)
-        return (grad_sum.to(dtype) if need_x else None,
-                torch.zeros_like(weight) if need_weight else None, None,
-                grad_sum if need_residual else None)
-    dev = grad_y.device
-    if not grad_y.is_contiguous():
-        grad_y = grad_y.contiguous()
-    if grad_sum is not None and not grad_sum.is_contiguous():
-        grad_sum = grad_sum.contiguous()
-    # in one type the gradients of x and of the residual are one tensor
-    grad_x = torch.empty_like(grad_y) if need_x or (need_residual and not wide) else None
-    grad_residual = torch.empty_like(total) if need_residual and wide else None
-    grad_weight = torch.empty_like(weight) if need_weight else None
-    ws = rstd.new_empty((ws_bytes + 3) // 4)
-    with on_device(dev):
-        abi.flce_rms_norm_backward(
-            problem, grad_y.data_ptr(), _ptr(grad_sum), total.data_ptr(), _ptr(weight),
-            rstd.data_ptr(), _ptr(grad_x), _ptr(grad_residual), _ptr(grad_weight), ws.data_ptr(),
-            ws_bytes, raw_stream(dev))
-    return (grad_x if need_x else None, grad_weight, None,
-            grad_residual if wide else grad_x if need_residual else None)
-
-
-_backward_once = once_differentiable(_backward)
+def _operators():
+    """torch.ops.flce, which libflce_torch.so registers. Raises if it is missing."""
+    global _ops
+    if _ops is None:
+        abi.load()
+        path = native_build.TORCH_LIB
+        if not os.path.exists(path):
+            raise RuntimeError(
+                f"{path} is missing: build the CUDA library first "
+                "(python -m linear_cross_entropy_vocab_gb300.native_build)")
+        torch.ops.load_library(path)
+        _ops = torch.ops.flce.rms_norm.default, torch.ops.flce.rms_norm_quantize.default
+    return _ops
 
 
 def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: float = 1e-6, *,
@@ -166,13 +82,11 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: float 
     """
     eps = float(eps)
     _check_inputs(x, weight, eps, residual)
-    if forward_ad._current_level < 0 and not (torch.is_grad_enabled() and (
-            x.requires_grad or weight is not None and weight.requires_grad
-            or residual is not None and residual.requires_grad)):
-        x, weight, residual, problem = _prepare(x, weight, eps, residual)
-        y, total = _forward(x, weight, residual, problem, None)
-        return y if residual is None else (y, total)
-    return _RmsNorm.apply(x, weight, eps, residual)
+    differentiable = forward_ad._current_level >= 0 or torch.is_grad_enabled() and (
+        x.requires_grad or weight is not None and weight.requires_grad
+        or residual is not None and residual.requires_grad)
+    got = _operators()[0](x, weight, eps, residual, differentiable)
+    return got[0] if residual is None else tuple(got)
 
 
 def rms_norm_quantize(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
@@ -185,20 +99,4 @@ def rms_norm_quantize(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
     eps = float(eps)
     _check_inputs(x, weight, eps, residual)
     refuse_gradient("rms_norm_quantize", ("x", "weight", "residual"), x, weight, residual)
-    lead, h = x.shape[:-1], x.shape[-1]
-    x, weight, residual, problem = _prepare(x, weight, eps, residual)
-    dev = x.device
-    total = None if residual is None else torch.empty_like(
-        residual, memory_format=torch.contiguous_format)
-    q_pitch = (h + 15) // 16 * 16
-    q = torch.empty(problem.n, q_pitch, dtype=torch.int8, device=dev)
-    scale = x.new_empty(lead, dtype=torch.float32)
-    with on_device(dev):
-        abi.flce_rms_norm_quantize(problem, x.data_ptr(), _ptr(residual), _ptr(weight),
-                                   q.data_ptr(), q_pitch, scale.data_ptr(), _ptr(total),
-                                   raw_stream(dev))
-    if q_pitch != h:
-        q = q[:, :h]
-    if len(lead) != 1:
-        q = q.unflatten(0, lead) if lead else q[0]
-    return (q, scale) if residual is None else (q, scale, total)
+    return tuple(_operators()[1](x, weight, eps, residual))
