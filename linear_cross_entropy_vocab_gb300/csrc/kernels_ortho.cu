@@ -231,10 +231,14 @@ struct Shape {
   static constexpr int kPieces = kTile / 64;  // of 32 columns, for an epilogue warp
 };
 
+constexpr int kSlots = 4;  // items on their way to the roles
+
 struct Ctl {
   uint64_t full[kStages], empty[kStages];
   uint64_t acc_full[2], acc_empty[2];
   uint64_t done;
+  uint64_t item_full[kSlots], item_empty[kSlots];
+  int item[kSlots];  // an item's number, or -1: none left
   uint32_t tmem;
   int abort;
 };
@@ -363,62 +367,123 @@ __device__ __forceinline__ Tile tile_of(const Product& q, int u) {
 struct Part {
   int tile, k0, k1;
 };
-// The parts of one pair of CTAs. Tiles are taken in turn, over all products:
-// a product's first tile goes to the pair after the last one of the product
-// before. Where a product's tiles are cut, the last `cut` of them are laid end
-// to end and divided into as many equal stretches as there are pairs, so that
-// all pairs end together; the stretches come first, so that what joins their
-// sums runs behind whole tiles' products.
-struct Walk {
-  int at, end, whole, whole_end, stride;
-  static __device__ __forceinline__ int start(const OrthoCut& c, int k_iters, int unit) {
-    return unit * (c.cut * k_iters) / c.units;  // the host keeps this in 31 bits
-  }
-  __device__ __forceinline__ Walk(const OrthoRunParams& p, const Product& q, int unit, int turn) {
-    const OrthoCut& c = p.cut[q.with->cut];
-    at = end = 0;
-    if (c.cut > 0) {
-      if (unit < c.units) {
-        at = start(c, q.k_iters, unit);
-        end = start(c, q.k_iters, unit + 1);
-      }
-      whole = unit;
-      stride = c.units;
-      whole_end = c.whole;
-    } else {
-      whole = unit - turn;
-      if (whole < 0) whole += p.units;
-      stride = p.units;
-      whole_end = q.per * p.batch;
-    }
-  }
-  __device__ __forceinline__ bool next(const Product& q, Part& part) {
-    if (at < end) {
-      const int t = at / q.k_iters;
-      part.tile = whole_end + t;
-      part.k0 = at - t * q.k_iters;
-      part.k1 = min(q.k_iters, part.k0 + end - at);
-      at += part.k1 - part.k0;
-      return true;
-    }
-    if (whole < whole_end) {
-      part.tile = whole;
-      part.k0 = 0;
-      part.k1 = q.k_iters;
-      whole += stride;
-      return true;
-    }
-    return false;
-  }
-};
-// The pair that has iteration x of the stretches.
+// Where stretch `unit` of a product's cut tiles begins: they are laid end to end
+// and divided into equal stretches.
+__device__ __forceinline__ int stretch(const OrthoCut& c, int k_iters, int unit) {
+  return unit * (c.cut * k_iters) / c.units;  // the host keeps this in 31 bits
+}
+// The stretch that has iteration x.
 __device__ __forceinline__ int owner_of(const OrthoCut& c, int k_iters, int x) {
   return ((x + 1) * c.units - 1) / (c.cut * k_iters);
 }
-// The pair that the next product's first tile goes to.
-__device__ __forceinline__ int next_turn(const OrthoRunParams& p, const Product& q, int turn) {
-  return p.cut[q.with->cut].cut > 0 ? turn : (turn + q.per * p.batch) % p.units;
+__device__ __forceinline__ void store_cluster(uint32_t addr, int v) {
+  asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
+
+// What a pair of CTAs (or a CTA) works on, as one of its roles meets it: items,
+// numbered over all products, each a stretch or a whole tile, a product's
+// stretches first (what joins their sums then runs behind whole tiles'
+// products). Pairs draw the numbers from a counter: the loading thread (of the
+// even CTA) draws when it has issued the loads of the item before, and hands the
+// number to all roles through a ring of slots. (Drawn one item ahead, two tiles
+// of one product went to a pair while others waited for the product: 2500 x 2500
+// took 664 us instead of 404.) An item waits for items of smaller numbers
+// only, and every pair takes its items in order, so that the smallest unfinished
+// one never waits: pairs that have not started yet hold nobody up.
+enum class Role { kDrawer, kThread, kWarp };
+template <int CG, Role ROLE>
+struct Feed {
+  const OrthoRunParams& p;
+  Ctl* const ctl;
+  const int rank, lane;
+  Product q;
+  int i = 0;             // the product's number
+  int base = 0, count;   // its first item, and how many it has
+  int at = 0, end = 0;   // what is left of a stretch
+  int unit = 0;          // the stretch
+  int slot = 0;
+  uint32_t phase = 0;
+
+  __device__ __forceinline__ int items_of(const Product& of) const {
+    const OrthoCut& c = p.cut[of.with->cut];
+    return c.cut > 0 ? c.units + c.whole : of.per * p.batch;
+  }
+  __device__ __forceinline__ Feed(const OrthoRunParams& p_, Ctl* ctl_, int rank_, int lane_)
+      : p(p_), ctl(ctl_), rank(rank_), lane(lane_), q(product_of(p_, 0)) {
+    count = items_of(q);
+  }
+  __device__ __forceinline__ void advance() {
+    if (++slot == kSlots) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+  // Draws a number, or -1 past the last item, and puts it into the next slot of
+  // all CTAs.
+  __device__ __forceinline__ bool draw(int& u) {
+    u = atomicAdd(p.ticket, 1);
+    if (!wait_bar<CG>(smem_addr(&ctl->item_empty[slot]), phase ^ 1u, &ctl->abort, p.err_word))
+      return false;
+    if (u >= p.items) u = -1;
+    const uint32_t to = smem_addr(&ctl->item[slot]), bar = smem_addr(&ctl->item_full[slot]);
+    if constexpr (CG == 2) {
+      store_cluster(map_to_rank(to, 1), u);
+      mbar_arrive_cluster(map_to_rank(bar, 1));
+    }
+    *reinterpret_cast<volatile int*>(&ctl->item[slot]) = u;
+    mbar_arrive(bar);
+    advance();
+    return true;
+  }
+  // The next part and its product `q`. False when none are left or a wait gave
+  // up. All lanes of a Role::kWarp call it together.
+  __device__ __forceinline__ bool next(Part& part) {
+    if (at >= end) {
+      int u;
+      if constexpr (ROLE == Role::kDrawer) {
+        if (!draw(u)) return false;
+      } else {
+        const bool here = wait_bar<CG>(smem_addr(&ctl->item_full[slot]), phase, &ctl->abort,
+                                       p.err_word);
+        if (ROLE == Role::kWarp ? !__all_sync(0xffffffffu, here) : !here) return false;
+        u = *reinterpret_cast<volatile int*>(&ctl->item[slot]);
+        if constexpr (ROLE == Role::kWarp) __syncwarp();
+        if (lane == 0) {
+          const uint32_t bar = smem_addr(&ctl->item_empty[slot]);
+          if (CG == 1 || rank == 0)
+            mbar_arrive(bar);
+          else
+            mbar_arrive_cluster(map_to_rank(bar, 0));
+        }
+        advance();
+      }
+      if (u < 0) return false;
+      while (u >= base + count) {
+        base += count;
+        q = product_of(p, ++i);
+        count = items_of(q);
+      }
+      u -= base;
+      const OrthoCut& c = p.cut[q.with->cut];
+      const int stretches = c.cut > 0 ? c.units : 0;
+      if (u >= stretches) {
+        part.tile = u - stretches;
+        part.k0 = 0;
+        part.k1 = q.k_iters;
+        return true;
+      }
+      unit = u;
+      at = stretch(c, q.k_iters, u);
+      end = stretch(c, q.k_iters, u + 1);
+    }
+    const int t = at / q.k_iters;
+    part.tile = p.cut[q.with->cut].whole + t;
+    part.k0 = at - t * q.k_iters;
+    part.k1 = min(q.k_iters, part.k0 + end - at);
+    at += part.k1 - part.k0;
+    return true;
+  }
+};
 
 // What a product reads of a matrix is there once each epilogue warp of each
 // tile of the products before has counted one up. Where tiles are cut, all
@@ -724,10 +789,10 @@ __device__ __forceinline__ bool finish_part(const OrthoRunParams& p, const Produ
   return true;
 }
 
-// All products of all steps. A grid of CTA pairs (or CTAs), all of them resident (a
-// cooperative launch), walks the products' tiles in order; a tile waits until
-// the product before has finished its matrix, so that matrices of a batch pass
-// one another and nothing but a matrix's own order holds a pair up.
+// All products of all steps: pairs of CTAs (or CTAs), as many as there are SMs
+// for, draw their tiles in order; a tile waits until the products before have
+// finished its matrix, so that matrices of a batch pass one another and nothing
+// but a matrix's own order holds a pair up.
 template <int CG, class T>
 __global__ void __launch_bounds__(kThreads, 1)
     ortho_run_kernel(const __grid_constant__ OrthoRunParams p) {
@@ -739,7 +804,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kTile = Shape<CG>::kTile, kPieces = Shape<CG>::kPieces;
   const int rank = CG == 2 ? static_cast<int>(cluster_ctarank()) : 0;
-  const int unit = static_cast<int>(blockIdx.x) / CG;
   volatile int* const abort_flag = &ctl->abort;
 
   if (threadIdx.x == 0) {
@@ -752,6 +816,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_addr(&ctl->acc_empty[b]), CG * kWarps);  // of both CTAs
     }
     mbar_init(smem_addr(&ctl->done), 1);
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(smem_addr(&ctl->item_full[i]), 1);
+      // the product thread, the odd CTA's loading thread, the epilogue warps
+      mbar_init(smem_addr(&ctl->item_empty[i]), CG + CG * kWarps);
+    }
     ctl->abort = 0;
     fence_mbar_init();
   }
@@ -777,23 +846,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = ctl->tmem;
-  int turn = 0;
-
   if (warp == 0) {
     if (lane == 0) {
       Ring ring{};
       bool ok = true;
-      for (int i = 0; ok && i < p.products; ++i) {
-        const Product q = product_of(p, i);
-        Walk walk(p, q, unit, turn);
-        int ready = -1;  // the matrix whose operands are known to be there
-        for (Part part; ok && walk.next(q, part);) {
+      const auto load = [&](auto&& feed) {
+        int product = 0, ready = -1;  // the matrix whose operands are known to be there
+        for (Part part; ok && feed.next(part);) {
+          const Product& q = feed.q;
           const Tile t = tile_of(q, part.tile);
-          if (i > 0 && t.b != ready) {
+          if (feed.i > 0 && (t.b != ready || feed.i != product)) {
             ok = wait_need(need_of(p, q, t.b), abort_flag, p.err_word);
             if (!ok) break;
             fence_proxy_async_global();
             ready = t.b;
+            product = feed.i;
           }
           switch (q.op) {
             case OrthoOp::kGram:
@@ -810,45 +877,46 @@ __global__ void __launch_bounds__(kThreads, 1)
               break;
           }
         }
-        turn = next_turn(p, q, turn);
-      }
-      if (!ok && rank == 0) {
+      };
+      if (rank == 0)
+        load(Feed<CG, Role::kDrawer>(p, ctl, rank, 0));
+      else
+        load(Feed<CG, Role::kThread>(p, ctl, rank, 0));
+      if (*abort_flag && rank == 0) {
         for (int s = 0; s < kStages; ++s)
-          if (ring.armed & (1u << s)) drain_bar<CG>(smem_addr(&ctl->full[s]), (ring.last >> s) & 1u);
+          if (ring.armed & (1u << s))
+            drain_bar<CG>(smem_addr(&ctl->full[s]), (ring.last >> s) & 1u);
       }
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
       Ring ring{};
-      bool ok = true;
+      Feed<CG, Role::kThread> feed(p, ctl, rank, 0);
       int it = 0;
-      for (int i = 0; ok && i < p.products; ++i) {
-        const Product q = product_of(p, i);
-        Walk walk(p, q, unit, turn);
-        for (Part part; ok && walk.next(q, part); ++it) {
-          const int buf = it & 1;
-          ok = wait_bar<CG>(smem_addr(&ctl->acc_empty[buf]), ((it >> 1) & 1u) ^ 1u, abort_flag,
-                         p.err_word);
-          if (!ok) break;
-          tc_fence_after_sync();
-          const uint32_t d = tmem + static_cast<uint32_t>(buf * kTile);
-          switch (q.op) {
-            case OrthoOp::kGram:
-            case OrthoOp::kSquare:
-            case OrthoOp::kPoly:
-              ok = multiply_part<CG, OrthoOp::kGram>(p, part, base, d, ctl, ring);
-              break;
-            case OrthoOp::kMul:
-            case OrthoOp::kOutWide:
-              ok = multiply_part<CG, OrthoOp::kMul>(p, part, base, d, ctl, ring);
-              break;
-            case OrthoOp::kOutTall:
-              ok = multiply_part<CG, OrthoOp::kOutTall>(p, part, base, d, ctl, ring);
-              break;
-          }
-          if (ok) commit<CG>(smem_addr(&ctl->acc_full[buf]));
+      for (Part part; feed.next(part); ++it) {
+        const int buf = it & 1;
+        if (!wait_bar<CG>(smem_addr(&ctl->acc_empty[buf]), ((it >> 1) & 1u) ^ 1u, abort_flag,
+                          p.err_word))
+          break;
+        tc_fence_after_sync();
+        const uint32_t d = tmem + static_cast<uint32_t>(buf * kTile);
+        bool ok = true;
+        switch (feed.q.op) {
+          case OrthoOp::kGram:
+          case OrthoOp::kSquare:
+          case OrthoOp::kPoly:
+            ok = multiply_part<CG, OrthoOp::kGram>(p, part, base, d, ctl, ring);
+            break;
+          case OrthoOp::kMul:
+          case OrthoOp::kOutWide:
+            ok = multiply_part<CG, OrthoOp::kMul>(p, part, base, d, ctl, ring);
+            break;
+          case OrthoOp::kOutTall:
+            ok = multiply_part<CG, OrthoOp::kOutTall>(p, part, base, d, ctl, ring);
+            break;
         }
-        turn = next_turn(p, q, turn);
+        if (!ok) break;
+        commit<CG>(smem_addr(&ctl->acc_full[buf]));
       }
       commit<CG>(smem_addr(&ctl->done));
       drain_bar<CG>(smem_addr(&ctl->done), 0);
@@ -862,69 +930,66 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t acc_empty = smem_addr(&ctl->acc_empty[0]);
     if constexpr (CG == 2) acc_empty = map_to_rank(acc_empty, 0);
     uint8_t* const box = boxes + (warp - 2) * 2 * kBoxBytes;
-    int it = 0;
-    bool ok = true;
-    for (int i = 0; ok && i < p.products; ++i) {
-      const Product q = product_of(p, i);
-      Walk walk(p, q, unit, turn);
-      int ready = -1;
-      for (Part part; walk.next(q, part); ++it) {
-        const Tile t = tile_of(q, part.tile);
-        if (q.op == OrthoOp::kPoly && t.b != ready) {  // the gram is read here too
-          ok = __all_sync(0xffffffffu,
-                          lane != 0 || wait_need(need_of(p, q, t.b), abort_flag, p.err_word));
-          if (!ok) break;
-          __threadfence();
-          __syncwarp();
-          ready = t.b;
-        }
-        const int buf = it & 1;
-        ok = __all_sync(0xffffffffu, wait_bar<CG>(smem_addr(&ctl->acc_full[buf]), (it >> 1) & 1u,
-                                               abort_flag, p.err_word));
-        if (!ok) break;
-        tc_fence_after_sync();
-        const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) +
-                               static_cast<uint32_t>(buf * kTile);
-        bool stored = false;
-        switch (q.op) {
-          case OrthoOp::kGram:
-          case OrthoOp::kSquare:
-            stored = finish_part<CG, OrthoOp::kGram, __half>(p, q, part, t, taddr, unit, rank, warp - 2, quarter,
-                                                first, box, lane);
-            break;
-          case OrthoOp::kPoly:
-            stored = finish_part<CG, OrthoOp::kPoly, __half>(p, q, part, t, taddr, unit, rank, warp - 2, quarter,
-                                                first, box, lane);
-            break;
-          case OrthoOp::kMul:
-            stored = finish_part<CG, OrthoOp::kMul, __half>(p, q, part, t, taddr, unit, rank, warp - 2, quarter,
-                                               first, box, lane);
-            break;
-          case OrthoOp::kOutWide:
-            finish_part<CG, OrthoOp::kOutWide, T>(p, q, part, t, taddr, unit, rank, warp - 2, quarter, first,
-                                     box, lane);
-            break;
-          case OrthoOp::kOutTall:
-            finish_part<CG, OrthoOp::kOutTall, T>(p, q, part, t, taddr, unit, rank, warp - 2, quarter, first,
-                                     box, lane);
-            break;
-        }
-        tc_fence_before_sync();
+    Feed<CG, Role::kWarp> feed(p, ctl, rank, lane);
+    int it = 0, product = 0, ready = -1;
+    for (Part part; feed.next(part); ++it) {
+      const Product& q = feed.q;
+      const Tile t = tile_of(q, part.tile);
+      if (q.op == OrthoOp::kPoly && (t.b != ready || feed.i != product)) {
+        // the gram is read here too
+        if (!__all_sync(0xffffffffu,
+                        lane != 0 || wait_need(need_of(p, q, t.b), abort_flag, p.err_word)))
+          break;
+        __threadfence();
         __syncwarp();
-        if (lane == 0) {
-          const uint32_t free = acc_empty + static_cast<uint32_t>(buf * sizeof(uint64_t));
-          if constexpr (CG == 2)
-            mbar_arrive_cluster(free);
-          else
-            mbar_arrive(free);
-          if (stored) {
-            tma_store_wait_all();
-            fence_proxy_async_global();
-            add_release(count_of(p, t.b), 1);
-          }
+        ready = t.b;
+        product = feed.i;
+      }
+      const int buf = it & 1;
+      if (!__all_sync(0xffffffffu, wait_bar<CG>(smem_addr(&ctl->acc_full[buf]), (it >> 1) & 1u,
+                                                abort_flag, p.err_word)))
+        break;
+      tc_fence_after_sync();
+      const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) +
+                             static_cast<uint32_t>(buf * kTile);
+      bool stored = false;
+      switch (q.op) {
+        case OrthoOp::kGram:
+        case OrthoOp::kSquare:
+          stored = finish_part<CG, OrthoOp::kGram, __half>(p, q, part, t, taddr, feed.unit, rank,
+                                                           warp - 2, quarter, first, box, lane);
+          break;
+        case OrthoOp::kPoly:
+          stored = finish_part<CG, OrthoOp::kPoly, __half>(p, q, part, t, taddr, feed.unit, rank,
+                                                           warp - 2, quarter, first, box, lane);
+          break;
+        case OrthoOp::kMul:
+          stored = finish_part<CG, OrthoOp::kMul, __half>(p, q, part, t, taddr, feed.unit, rank,
+                                                          warp - 2, quarter, first, box, lane);
+          break;
+        case OrthoOp::kOutWide:
+          finish_part<CG, OrthoOp::kOutWide, T>(p, q, part, t, taddr, feed.unit, rank, warp - 2,
+                                                quarter, first, box, lane);
+          break;
+        case OrthoOp::kOutTall:
+          finish_part<CG, OrthoOp::kOutTall, T>(p, q, part, t, taddr, feed.unit, rank, warp - 2,
+                                                quarter, first, box, lane);
+          break;
+      }
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        const uint32_t free = acc_empty + static_cast<uint32_t>(buf * sizeof(uint64_t));
+        if constexpr (CG == 2)
+          mbar_arrive_cluster(free);
+        else
+          mbar_arrive(free);
+        if (stored) {
+          tma_store_wait_all();
+          fence_proxy_async_global();
+          add_release(count_of(p, t.b), 1);
         }
       }
-      turn = next_turn(p, q, turn);
     }
     if (lane == 0) tma_store_wait_all();
   }
@@ -955,14 +1020,12 @@ cudaError_t launch_run(const OrthoRunParams& p, cudaStream_t s) {
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = s;
-  cudaLaunchAttribute attr[2]{};
-  attr[0].id = cudaLaunchAttributeCooperative;
-  attr[0].val.cooperative = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = CG;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = CG;  // a cluster where there are pairs
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = CG;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = CG - 1;  // a cluster where there are pairs
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 

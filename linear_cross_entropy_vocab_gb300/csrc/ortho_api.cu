@@ -274,7 +274,7 @@ Plan plan_of(const flce_ortho_problem* p) {
   q.partial = q.buffer[flce::kOrthoP2] + (q.grouped ? g_bytes : 0);
   q.factor = q.partial + align_256(b * static_cast<size_t>(q.parts) * 8);
   q.counts = q.factor + align_256(b * 4);
-  q.shares = q.counts + align_256((kArrived + b) * 4);
+  q.shares = q.counts + align_256((kArrived + b + 1) * 4);
   const int64_t side = q.m_pad / flce::kOrthoTile;
   const int64_t tiles = p->batch * side * ceil_div(q.n, flce::kOrthoTile);
   q.total = q.shares + static_cast<size_t>(2 * std::min(kPlanPairs, kMaxParts * tiles)) *
@@ -387,7 +387,7 @@ flce_status flce_orthogonalize(const flce_ortho_problem* p, const void* src, voi
   c.m_rows = static_cast<int32_t>(ceil_div(plan.m, 64) * 64);
   c.factor = reinterpret_cast<float*>(ws + plan.factor);
   c.count = reinterpret_cast<int32_t*>(ws + plan.counts);
-  c.counts = kArrived + c.batch;
+  c.counts = kArrived + c.batch + 1;
   flce::OrthoRunParams r{};
   const int64_t x_rows = p->batch * plan.m_pad;
   for (int i = 0; i < flce::kOrthoBuffers; ++i) {
@@ -431,6 +431,7 @@ flce_status flce_orthogonalize(const flce_ortho_problem* p, const void* src, voi
   r.shares = ws + plan.shares;
   r.arrived = c.count;
   r.finished = c.count + kArrived;
+  r.ticket = r.finished + c.batch;
   r.err_word = err_word;
   const int64_t pairs = std::min<int64_t>(2 * kPlanPairs, sms) / ctas;
   const int64_t triangle = p->batch * r.m_tiles * (r.m_tiles + 1) / 2;
@@ -448,13 +449,16 @@ flce_status flce_orthogonalize(const flce_ortho_problem* p, const void* src, voi
     r.units = std::max(r.units, r.cut[i].units);
     if (split.cut > 0) r.joint = 1;
   }
-  int64_t need = 0;
+  int64_t need = 0, items = 0;
   for (int i = 0; i < r.products; ++i) {
+    const flce::OrthoCut& c = r.cut[r.product[i].cut];
+    items += c.cut > 0 ? c.units + c.whole : r.product[i].cut < 2 ? triangle : all;
     r.product[i].need = static_cast<int32_t>(need);
     need += (r.product[i].cut < 2 ? triangle : all) / (r.joint ? 1 : p->batch) * ctas *
             flce::kOrthoWarps;
   }
-  if (need > 0x7fffffff) return fail(FLCE_ERR_UNSUPPORTED, "too many tiles and steps to count");
+  r.items = static_cast<int32_t>(items);
+  if (need > 0x7fffffff || items > 0x7fff0000) return fail(FLCE_ERR_UNSUPPORTED, "too many tiles and steps to count");
   cudaError_t e = flce::launch_ortho_norm(c, p->dtype, s);
   if (e != cudaSuccess) return cuda_fail(e, "matrix norm kernel");
   e = flce::launch_ortho_copy(c, p->dtype, s);

@@ -82,7 +82,9 @@ struct OrthoRunParams {
   CUtensorMap store[kOrthoBuffers + 1];  // the last: out [batch][rows][cols], where out_mapped
   OrthoProduct product[kOrthoMaxProducts];
   OrthoCut cut[3];
-  int32_t products, batch, units;
+  int32_t products, batch;
+  int32_t units, items;  // pairs of CTAs in the grid, and what they draw
+  int32_t* ticket;       // 0 before
   int32_t pairs;       // tiles of 256 by CTA pairs, else of 128 by CTAs
   int32_t m_tiles, n_tiles;
   int32_t k_n, k_m;    // 64-deep stages along n and along m
