@@ -3,9 +3,11 @@
 // are shorter than Python's share of them: autograd runs a node in a thread of
 // its own, where a node written in Python took 100 us more than this one.
 #include <ATen/ATen.h>
+#include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/custom_function.h>
+#include <torch/csrc/autograd/functions/accumulate_grad.h>
 #include <torch/csrc/autograd/functions/basic_ops.h>
 #include <torch/library.h>
 
@@ -46,16 +48,18 @@ void* stream_of(const Tensor& t) {
 const void* pointer(const Tensor& t) { return t.defined() ? t.const_data_ptr() : nullptr; }
 void* writable(const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
 
-// t [..., H] as rows of contiguous elements at one pitch.
+// t [..., H] as rows of contiguous elements at one pitch: as it is, where its
+// leading dimensions are steps of one (a slice of wider rows), or a copy.
 Tensor rows_of(const Tensor& t, int64_t& pitch) {
   const int64_t h = t.size(-1);
   pitch = h;
   if (t.is_contiguous()) return t;
-  if (t.dim() == 2 && (t.stride(1) == 1 || h == 1) && t.stride(0) >= h) {
-    pitch = t.stride(0);
-    return t;
-  }
-  return t.contiguous();
+  bool rows = t.dim() > 1 && (t.stride(-1) == 1 || h == 1) && t.stride(-2) >= h;
+  for (int64_t i = 0; rows && i + 2 < t.dim(); ++i)
+    rows = t.stride(i) == t.stride(i + 1) * t.size(i + 1);
+  if (!rows) return t.contiguous();
+  pitch = t.stride(-2);
+  return t;
 }
 
 Tensor empty_as(const Tensor& shape_of, const Tensor& like) {
@@ -100,6 +104,27 @@ std::tuple<Tensor, Tensor> forward(const Inputs& in, const Tensor& rstd) {
   return {y, sum};
 }
 
+// Refuses a backward that is captured while an eager graph of the same leaves
+// lives: their accumulators keep the stream that they were made on, autograd
+// would make that one wait for the captured one, and where it is the default
+// stream the capture is lost and the process with it.
+void refuse_lost_capture() {
+  if (c10::cuda::currentStreamCaptureStatusMayInitCtx() == c10::cuda::CaptureStatus::None) return;
+  const auto node = torch::autograd::get_current_node();
+  if (node == nullptr) return;
+  for (size_t i = 0; i < node->num_outputs(); ++i) {
+    torch::autograd::Node* const next = node->next_edge(i).function.get();
+    if (dynamic_cast<torch::autograd::AccumulateGrad*>(next) == nullptr ||
+        !node->task_should_compute_output(i))
+      continue;
+    const auto stream = next->stream();
+    TORCH_CHECK(!stream || *stream != c10::cuda::getDefaultCUDAStream(stream->device_index()),
+                "rms_norm: a captured backward needs leaves without another graph; drop the "
+                "outputs of earlier calls on the default stream before the capture, or make "
+                "them on the captured stream");
+  }
+}
+
 class RmsNorm : public torch::autograd::Function<RmsNorm> {
  public:
   static variable_list forward(AutogradContext* ctx, const Tensor& x,
@@ -117,6 +142,7 @@ class RmsNorm : public torch::autograd::Function<RmsNorm> {
   }
 
   static variable_list backward(AutogradContext* ctx, const variable_list& grads) {
+    refuse_lost_capture();
     const variable_list saved = ctx->get_saved_variables();
     const Tensor &total = saved[0], &weight = saved[1], &rstd = saved[2];
     // inputs that are tensors are counted
@@ -146,7 +172,7 @@ class RmsNorm : public torch::autograd::Function<RmsNorm> {
       p.h = total.size(-1);
       p.n = rstd.numel();
       p.x_pitch = p.residual_pitch = p.h;
-      if (!total.is_contiguous()) p.x_pitch = total.stride(0);  // rows_of has seen to the rest
+      if (!total.is_contiguous()) p.x_pitch = total.stride(-2);  // rows_of has seen to the rest
       p.dtype = code_of(grad_y);
       p.sum_dtype = code_of(total);
       p.weight_dtype = weight.defined() ? code_of(weight) : p.dtype;

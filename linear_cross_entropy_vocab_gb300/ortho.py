@@ -50,8 +50,9 @@ def orthogonalize(x: torch.Tensor, *,
     most 1, below 16. Products are taken of 11-bit values with 32-bit sums: the result is within
     about 1.5e-3 of itself, more where a few singular values are far above the others. A matrix
     of zeros stays one; one that holds a NaN or an infinity becomes NaN. It has no gradient: an x
-    that asks for one is refused. Sides are at most 2^20. ``err_word`` (one int32, which the
-    caller clears and reads) gets FLCE_DEVERR_TIMEOUT if a kernel gave up waiting.
+    that asks for one is refused. Sides are at most 2^20, and the matrices
+    of a call at most 65535. ``err_word`` (one int32, which the caller clears and reads) gets
+    FLCE_DEVERR_TIMEOUT if a kernel gave up waiting.
     """
     code = _DTYPES.get(x.dtype)
     if code is None:

@@ -352,6 +352,47 @@ def test_streams_and_graph():
         assert torch.equal(q, wq[0]) and torch.equal(scale, wq[1])
 
 
+def test_slices_of_wider_rows():
+    g = torch.Generator("cuda").manual_seed(3)
+    wide = torch.randn(3, 5, 2 * 264, generator=g, device="cuda")
+    dy, ds = (torch.randn(3, 5, 264, generator=g, device="cuda") for _ in range(2))
+    w = 1 + 0.3 * torch.randn(264, generator=g, device="cuda")
+    for part in (wide[..., 264:], wide[:, 1:4, :264], wide.transpose(0, 1)[..., :264],
+                 wide[:, 2:3, :264], wide[..., ::2]):
+        up, us = dy[:, :part.shape[1]], ds[:, :part.shape[1]]
+        if part.shape[:2] != up.shape[:2]:
+            up, us = dy.transpose(0, 1), ds.transpose(0, 1)
+        results = []
+        for view in (part, part.contiguous()):
+            x, r = view.detach().requires_grad_(), (view * 2).detach().requires_grad_()
+            outs = [rms_norm(x, w), *rms_norm(x, w, residual=view), *rms_norm(r, w, residual=x)]
+            results.append(outs + list(torch.autograd.grad(
+                outs, [x, r], [up, up, us, up, us])) + list(rms_norm_quantize(x.detach(), w)))
+        for a, b in zip(*results):
+            assert torch.equal(a, b)
+
+
+def test_captured_backward_beside_an_eager_graph():
+    x = torch.randn(8, 264, device="cuda").requires_grad_()
+    dy = torch.randn(8, 264, device="cuda")
+    kept = rms_norm(x)
+    want, = torch.autograd.grad(rms_norm(x), x, dy)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with pytest.raises(RuntimeError, match="captured backward"):
+        with torch.cuda.graph(graph):
+            rms_norm(x).backward(dy)
+    assert x.grad is None
+    del kept
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        rms_norm(x).backward(dy)
+    x.grad.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(x.grad, want)
+
+
 def test_into_the_8_bit_head():
     x, r, w = _inputs(20, 1000, torch.bfloat16, torch.bfloat16)
     head_q, head_scale = quantize_rows(torch.randn(333, 1000, device="cuda").bfloat16())
