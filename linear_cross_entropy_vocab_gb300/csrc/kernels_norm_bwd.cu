@@ -285,8 +285,10 @@ __global__ void __launch_bounds__(1024) norm_weight_kernel(const float* partial,
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   float v = 0.0f;
-  if (c < h)
+  if (c < h) {
+#pragma unroll 8
     for (int64_t k = warp; k < parts; k += 32) v += partial[k * h + c];
+  }
   buf[warp][lane] = v;
   __syncthreads();
   v = buf[lane][warp];

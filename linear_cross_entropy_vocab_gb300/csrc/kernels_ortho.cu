@@ -97,7 +97,7 @@ __device__ __forceinline__ int piece_at(int i, int c) { return i * 64 + ((c ^ (i
 // matrix, and rows that do not start at 16-byte boundaries, go through shared
 // memory.
 template <class T>
-__global__ void __launch_bounds__(256) ortho_copy_kernel(const OrthoCopyParams p) {
+__global__ void __launch_bounds__(256, sizeof(T) == 4 ? 3 : 4) ortho_copy_kernel(const OrthoCopyParams p) {
   __shared__ __align__(16) __half part[2][64 * 64];
   __shared__ double buf[8];
   grid_dependency_wait();
@@ -172,29 +172,50 @@ __global__ void __launch_bounds__(256) ortho_copy_kernel(const OrthoCopyParams p
           part[k >> 1][piece_at(c8 * 8 + j, dr >> 3) + (dr & 7)] = half_of(v[k][j]);
       }
     } else {
-      // rows that start anywhere: the nine aligned pieces that hold 64 values
-      for (int u9 = threadIdx.x; u9 < halves * 64 * 9; u9 += 256) {
-        const int line = u9 / 9, g = line >> 6, dr = line & 63;
+      // rows that start anywhere: the nine aligned pieces that hold 64 values,
+      // all of a thread's loads before its stores
+      constexpr int kEach = (2 * 64 * 9 + 255) / 256;
+      Raw<T> raw[kEach];
+      const auto place = [&](int k, int& g, int& dr, int& dc, const T*& row) {
+        const int u9 = k * 256 + threadIdx.x, line = u9 / 9;
+        g = line >> 6;
+        dr = line & 63;
         const int r = s0 + dr + (p.tall ? 64 * g : 0), c0 = t0 + (p.tall ? 0 : 64 * g);
-        const T* const row = src + int64_t(r) * p.row_pitch;
+        row = src + int64_t(r) * p.row_pitch;
         const int phase = static_cast<int>(reinterpret_cast<uintptr_t>(row) / sizeof(T)) & 7;
-        const int c = c0 - ((c0 + phase) & 7) + (u9 - line * 9) * 8;
-        float v[8] = {};
-        if (r < p.rows) {
-          if (c >= 0 && c + 8 <= p.cols) {
-            load8(row + c, v);
-          } else {
+        dc = (u9 - line * 9) * 8 - ((c0 + phase) & 7);
+        row += c0 + dc;
+        return c0 + dc;
+      };
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (c + j >= 0 && c + j < p.cols) v[j] = to_f32(row[c + j]);
-          }
+      for (int k = 0; k < kEach; ++k) {
+        int g, dr, dc;
+        const T* at;
+        const int c = place(k, g, dr, dc, at);
+        const bool in = g < halves && s0 + dr + (p.tall ? 64 * g : 0) < p.rows;
+        if (in && c >= 0 && c + 8 <= p.cols) {
+          raw[k].load(at);
+        } else {
+          float v[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] = in && c + j >= 0 && c + j < p.cols ? to_f32(at[j]) : 0.0f;
+          store8(reinterpret_cast<T*>(raw[k].q), v);
         }
+      }
+#pragma unroll
+      for (int k = 0; k < kEach; ++k) {
+        int g, dr, dc;
+        const T* at;
+        place(k, g, dr, dc, at);
+        if (g >= halves) continue;
+        float v[8];
+        raw[k].values(v);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const int dc = c + j - c0;
-          if (dc < 0 || dc >= 64) continue;
-          const int i = p.tall ? dc : dr, at = p.tall ? dr : dc;
-          part[g][piece_at(i, at >> 3) + (at & 7)] = half_of(v[j]);
+          const int d = dc + j;
+          if (d < 0 || d >= 64) continue;
+          const int i = p.tall ? d : dr, to = p.tall ? dr : d;
+          part[g][piece_at(i, to >> 3) + (to & 7)] = half_of(v[j]);
         }
       }
     }
