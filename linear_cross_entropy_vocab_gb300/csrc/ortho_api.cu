@@ -409,21 +409,27 @@ flce_status flce_orthogonalize(const flce_ortho_problem* p, const void* src, voi
   r.batch = c.batch;
   // Tiles of 128, one to an SM, or of 256, one to a pair of SMs. The small ones
   // take half as long to come and go, which counts where products are short and
-  // wait for each other; the large ones load half as much for an operation,
-  // which counts over many rounds. So small ones are taken where a product with
-  // x has two rounds of them, or a symmetric product one round (a quarter more
-  // in a batch, whose matrices fill each other's rounds) and the product with x
-  // not too many. Small and large, us: 2048 x 2048 (136 tiles of a gram, 256 of
-  // a product with x) 278 and 333; 2048 x 4096 (136, 512) 356 and 474; 1024 x
-  // 8192 (36, 512) 242 and 297; four of 1024 x 4096 (144, 1024) 293 and 318; 1536
-  // x 16384 (78, 1536) 519 and 458; 2304 x 2304 (171, 324) 389 and 368; 2500 x
-  // 2500 (210, 400) 493 and 406; six of 777 x 1555 (168, 546) 226 and 242; three
-  // of 2049 x 1365 (198, 561) 312 and 299.
+  // wait for each other, and pad less; the large ones load half as much for an
+  // operation, which counts over many rounds. So small ones are taken
+  // - where a product with x has two rounds of them: 2048 x 2048 takes 278 us,
+  //   with large ones 333;
+  // - where a symmetric product has one round (a quarter more in a batch, whose
+  //   matrices fill each other's rounds) and the product with x not too many: 2048
+  //   x 4096 356 and 474, 1024 x 8192 242 and 297, four of 1024 x 4096 293 and 318,
+  //   six of 777 x 1555 226 and 242 (but 1536 x 16384, 10 rounds, 519 and 458; 2304
+  //   x 2304 389 and 368; three of 2049 x 1365 312 and 299);
+  // - for short contractions: 100 of 384 x 384 278 and 380, 128 of 256 x 512 225
+  //   and 253;
+  // - in a batch where they pad to five sixths at most: ten of 640 x 900 167 and 197,
+  //   fourteen of 640 x 640 165 and 192 (but eight of 1000 x 1000 254 and 237).
   const int64_t side = ceil_div(plan.m, 128);
   const int64_t gram_tiles = p->batch * side * (side + 1) / 2;
   const int64_t x_tiles = p->batch * side * ceil_div(plan.n, 128);
-  const bool small = x_tiles <= 2 * sms || (gram_tiles <= sms && x_tiles <= 7 * sms) ||
-                     (p->batch > 1 && 4 * gram_tiles <= 5 * sms && x_tiles <= 4 * sms);
+  const int64_t x_large = p->batch * ceil_div(plan.m, 256) * ceil_div(plan.n, 256);
+  const bool small =
+      plan.m <= 384 || x_tiles <= 2 * sms || (gram_tiles <= sms && x_tiles <= 7 * sms) ||
+      (p->batch > 1 && ((4 * gram_tiles <= 5 * sms && x_tiles <= 4 * sms) ||
+                        (6 * x_tiles <= 5 * 4 * x_large && x_tiles <= 7 * sms)));
   r.pairs = small ? 0 : 1;
   const int64_t tile = r.pairs ? flce::kOrthoTile : flce::kOrthoTile / 2;
   const int64_t ctas = r.pairs ? 2 : 1;  // of a tile

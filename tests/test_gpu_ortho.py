@@ -111,7 +111,9 @@ SIZES = [(1, 1, 1), (1, 1, 9), (2, 5, 3), (1, 64, 64), (3, 100, 300), (1, 300, 1
          (4, 3000, 700), (1, 1000, 5100), (30, 200, 4100),
          # tiles whose contraction is cut between CTAs: few, or more than a round
          (1, 1024, 2100), (4, 4000, 700), (90, 20, 1000), (80, 300, 900), (30, 100, 3000),
-         (1, 300, 20000), (1, 400, 40000)]
+         (1, 300, 20000), (1, 400, 40000), (20, 640, 500),
+         # tiles of 256, some in a batch, with steps that share a gram and without
+         (8, 1000, 1000), (8, 1000, 2700), (2, 2701, 2050), (1, 4100, 2300), (17, 700, 4000)]
 
 
 @pytest.mark.parametrize("dtype", TYPES)
