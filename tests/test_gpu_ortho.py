@@ -158,6 +158,7 @@ def test_other_steps(m, n):
 def test_numbers_of_steps(steps):
     coefficients = tuple((3.0 - 0.2 * k, -3.5 + 0.3 * k, 1.4 - 0.1 * k) for k in range(steps))
     for x in (_matrices(3, 600, 5000, torch.bfloat16), _matrices(1, 300, 400, torch.bfloat16),
+              _matrices(8, 1000, 2700, torch.bfloat16), _matrices(8, 1000, 1000, torch.bfloat16),
               _matrices(1, 100, 1000, torch.bfloat16)):
         _check(orthogonalize(x, coefficients=coefficients)[0], x[0], coefficients, batch=len(x))
 
@@ -234,7 +235,7 @@ def test_extremes(m, n):
     _check(orthogonalize(tiny)[0], tiny[0])
 
 
-@pytest.mark.parametrize("m,n", [(300, 520), (100, 1100)])
+@pytest.mark.parametrize("m,n", [(300, 520), (100, 1100), (2000, 2200)])
 def test_streams_and_graphs(m, n):
     x = _matrices(2, m, n, torch.bfloat16)
     want = orthogonalize(x)
