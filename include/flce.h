@@ -579,7 +579,10 @@ typedef struct flce_ortho_problem {
   int32_t steps;        /* 1 to 64 */
   float eps;            /* finite, at least FLT_MIN */
   const float* coefficients; /* steps x (a, b, c), in host memory, read within the
-                                call; singular values stay in 1e-4 to 16 */
+                                call; the largest singular value stays in 1e-4
+                                to 16 and |a + b t + c t^2| below 1e4 for its
+                                square, and within 1.5 times what they reach
+                                where each step's values are larger by 2^-9 */
   int64_t reserved;     /* 0 */
 } flce_ortho_problem;
 

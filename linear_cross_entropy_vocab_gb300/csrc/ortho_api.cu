@@ -49,7 +49,7 @@ double step_bound(double a, double b, double c, double top) {
 }
 
 // The power of two that takes values up to `bound` to at most 2^14: halves
-// reach 65504, and roundings add little to a bound.
+// reach 65504, which leaves what roundings add to a bound a factor of four.
 int shift_for(double bound) {
   int e = 0;
   std::frexp(bound, &e);  // bound < 2^e
@@ -57,16 +57,55 @@ int shift_for(double bound) {
 }
 double scale_for(double bound) { return std::ldexp(1.0, shift_for(bound)); }
 
-// The scales of each step's operands, and what turns sums into them.
-void fill_steps(const flce_ortho_problem* p, flce::OrthoStep* step) {
-  double bound = 1.0;
-  double x_scale = scale_for(bound);
+// What the steps do to singular values, from which everything else is planned:
+// bounds on them before each step (and after the last), and on the step's
+// polynomial of their squares, both of the formula without roundings.
+struct Bounds {
+  double top[kMaxSteps + 1], poly[kMaxSteps];
+};
+// Roundings move a singular value: by up to 2^-11 of it where x is rounded, and
+// up to four times as much where the gram and a polynomial are that is larger
+// elsewhere than for this value. The steps that follow must not make much of it.
+// Above the largest value that a schedule is made for, its polynomials may rise
+// twelve times as fast as the value itself, and five such steps turn 2^-11 into
+// anything (noise of 12 x 20 values was off by up to 93 %, a constant matrix
+// became NaN). So schedules have to bear kMoved before every step, as those with
+// the usual safety factor of 1.01 do.
+constexpr double kMoved = 1.0 / 512;
+constexpr double kMost = 1.5;  // times a bound, by moved values; products of three of them stay below 4
+// Fills `b`. The step whose bounds do not hold, or -1; `moved` says whether
+// that is by moved values alone.
+int find_bounds(const flce_ortho_problem* p, Bounds* b, bool* moved) {
+  b->top[0] = 1.0;
+  *moved = false;
+  double with = 1.0;  // top[k], moved
   for (int k = 0; k < p->steps; ++k) {
     const float* const abc = p->coefficients + 3 * k;
-    const double g_scale = scale_for(bound * bound);
-    const double p_scale = scale_for(poly_bound(abc[0], abc[1], abc[2], bound * bound));
-    bound = step_bound(abc[0], abc[1], abc[2], bound) * (1.0 + 1.0 / 64);
-    const double next_scale = k + 1 == p->steps ? 1.0 : scale_for(bound);
+    const double top = b->top[k];
+    const double poly = poly_bound(abc[0], abc[1], abc[2], top * top);
+    const double next = step_bound(abc[0], abc[1], abc[2], top);
+    b->poly[k] = poly;
+    b->top[k + 1] = next;
+    if (!(poly <= 1.0e4) || !(next <= 16.0) || !(next >= 1.0e-4)) return k;
+    with *= 1.0 + kMoved;
+    const double poly_with = poly_bound(abc[0], abc[1], abc[2], with * with);
+    with = step_bound(abc[0], abc[1], abc[2], with);
+    if (!(poly_with <= kMost * poly) || !(with <= kMost * next)) {
+      *moved = true;
+      return k;
+    }
+  }
+  return -1;
+}
+
+// The scales of each step's operands, and what turns sums into them.
+void fill_steps(const flce_ortho_problem* p, const Bounds& b, flce::OrthoStep* step) {
+  double x_scale = scale_for(b.top[0]);
+  for (int k = 0; k < p->steps; ++k) {
+    const float* const abc = p->coefficients + 3 * k;
+    const double g_scale = scale_for(b.top[k] * b.top[k]);
+    const double p_scale = scale_for(b.poly[k]);
+    const double next_scale = k + 1 == p->steps ? 1.0 : scale_for(b.top[k + 1]);
     flce::OrthoStep& t = step[k];
     t.gram = static_cast<float>(g_scale / (x_scale * x_scale));
     t.poly = static_cast<float>(abc[2] * p_scale / (g_scale * g_scale));
@@ -83,12 +122,12 @@ void fill_steps(const flce_ortho_problem* p, flce::OrthoStep* step) {
 // commute. So each step after a group's first takes two products for its gram,
 // one for its polynomial and one to gather the polynomials, all m x m.
 //
-// The bounds: singular values grow by step_bound, the gram's values are their
-// squares, and a gathered polynomial's are below the product of the bounds of
-// its parts. Each is held with a power of two of its own.
-int list_products(const flce_ortho_problem* p, bool grouped, bool tall, flce::OrthoProduct* out) {
+// The gram's values are below the squares of the singular values' bound, and a
+// gathered polynomial's below the product of the bounds of its parts. Each is
+// held with a power of two of its own.
+int list_products(const flce_ortho_problem* p, const Bounds& b, bool grouped, bool tall,
+                  flce::OrthoProduct* out) {
   using flce::OrthoOp;
-  constexpr double kSlack = 1.0 + 1.0 / 64;  // for roundings
   int count = 0;
   const auto add = [&](OrthoOp op, int a, int b, int c, double scale, int power = 0,
                        double old = 0.0, double diag = 0.0) {
@@ -103,14 +142,14 @@ int list_products(const flce_ortho_problem* p, bool grouped, bool tall, flce::Or
     t.old = static_cast<float>(old);
     t.diag = static_cast<float>(diag);
   };
-  double bound = 1.0, x_scale = scale_for(bound);
+  double x_scale = scale_for(b.top[0]);
   int from = flce::kOrthoX0;
   for (int k = 0; k < p->steps;) {
     // groups of three, of two at the end
     const int left = p->steps - k;
     const int group = !grouped ? 1 : left == 4 ? 2 : std::min(3, left);
     const int first = k;
-    double g_scale = scale_for(bound * bound);
+    double g_scale = scale_for(b.top[k] * b.top[k]);
     add(OrthoOp::kGram, from, from, flce::kOrthoGram, g_scale / (x_scale * x_scale),
         k == 0 ? 2 : 0);
     // the buffers of the gathered polynomial, of a step's own, and a free one
@@ -118,15 +157,14 @@ int list_products(const flce_ortho_problem* p, bool grouped, bool tall, flce::Or
     double all = 1.0, all_scale = 1.0;  // its bound and scale
     for (int s = 0; s < group; ++s, ++k) {
       const float* const abc = p->coefficients + 3 * k;
-      const double most = poly_bound(abc[0], abc[1], abc[2], bound * bound) * kSlack;
+      const double most = b.poly[k], top = b.top[k], next = b.top[k + 1];
       const double p_scale = scale_for(most);
       const int mine = s == 0 ? gathered : own;
       add(OrthoOp::kPoly, flce::kOrthoGram, flce::kOrthoGram, mine,
           abc[2] * p_scale / (g_scale * g_scale), 0, abc[1] * p_scale / g_scale,
           abc[0] * p_scale);
-      const double next = step_bound(abc[0], abc[1], abc[2], bound) * kSlack;
       if (s + 1 < group) {  // the gram of the next step
-        const double half_scale = scale_for(most * bound * bound);
+        const double half_scale = scale_for(most * top * top);
         const double next_scale = scale_for(next * next);
         add(OrthoOp::kSquare, mine, flce::kOrthoGram, spare, half_scale / (p_scale * g_scale));
         add(OrthoOp::kSquare, spare, mine, flce::kOrthoGram,
@@ -143,10 +181,9 @@ int list_products(const flce_ortho_problem* p, bool grouped, bool tall, flce::Or
         std::swap(gathered, spare);
         all_scale = scale;
       }
-      bound = next;
     }
     const bool last = k == p->steps;
-    const double next_scale = last ? 1.0 : scale_for(bound);
+    const double next_scale = last ? 1.0 : scale_for(b.top[k]);
     const double scale = next_scale / (x_scale * all_scale);
     const int power = first == 0 ? 1 : 0;
     if (last && tall) {
@@ -163,7 +200,8 @@ int list_products(const flce_ortho_problem* p, bool grouped, bool tall, flce::Or
   return count;
 }
 
-flce_status check_problem(const flce_ortho_problem* p) {
+// Fills `b` where it returns FLCE_OK.
+flce_status check_problem(const flce_ortho_problem* p, Bounds* b) {
   if (p == nullptr) return fail(FLCE_ERR_INVALID_ARG, "problem is NULL");
   if (p->batch < 0 || p->rows < 0 || p->cols < 0)
     return fail(FLCE_ERR_INVALID_ARG, "batch = %lld, rows = %lld, cols = %lld",
@@ -184,15 +222,15 @@ flce_status check_problem(const flce_ortho_problem* p) {
   if (p->steps < 1 || p->steps > kMaxSteps || p->coefficients == nullptr)
     return fail(FLCE_ERR_INVALID_ARG, "1 to %lld steps, with coefficients for each",
                 (long long)kMaxSteps);
-  double bound = 1.0;  // of the singular values before each step
-  for (int k = 0; k < p->steps; ++k) {
-    const float* const abc = p->coefficients + 3 * k;
-    const double poly = poly_bound(abc[0], abc[1], abc[2], bound * bound);
-    bound = step_bound(abc[0], abc[1], abc[2], bound);
-    if (!(poly <= 1.0e4) || !(bound <= 16.0) || !(bound >= 1.0e-4))
-      return fail(FLCE_ERR_UNSUPPORTED,
-                  "the coefficients of step %d take singular values up to %g", k, bound);
-  }
+  bool moved = false;
+  const int bad = find_bounds(p, b, &moved);
+  if (bad >= 0 && moved)
+    return fail(FLCE_ERR_UNSUPPORTED,
+                "step %d magnifies roundings of the largest singular values past its range: give "
+                "the steps a safety factor, as a / 1.01, b / 1.01^3, c / 1.01^5", bad);
+  if (bad >= 0)
+    return fail(FLCE_ERR_UNSUPPORTED,
+                "the coefficients of step %d take singular values up to %g", bad, b->top[bad + 1]);
   if (p->reserved != 0) return fail(FLCE_ERR_INVALID_ARG, "reserved is not 0");
   return FLCE_OK;
 }
@@ -320,7 +358,8 @@ constexpr CUtensorMapSwizzle kStore = CU_TENSOR_MAP_SWIZZLE_64B;
 extern "C" {
 
 size_t flce_orthogonalize_workspace_size(const flce_ortho_problem* p) {
-  if (check_problem(p) != FLCE_OK) return 0;
+  Bounds bounds;
+  if (check_problem(p, &bounds) != FLCE_OK) return 0;
   return plan_of(p).total;
 }
 
@@ -328,7 +367,8 @@ flce_status flce_orthogonalize(const flce_ortho_problem* p, const void* src, voi
                                int32_t* err_word, void* workspace, size_t workspace_bytes,
                                void* stream) {
   clear_error();
-  flce_status st = check_problem(p);
+  Bounds bounds;
+  flce_status st = check_problem(p, &bounds);
   if (st != FLCE_OK) return st;
   const bool empty = p->batch == 0 || p->rows == 0 || p->cols == 0;
   if (!empty && (src == nullptr || out == nullptr))
@@ -351,7 +391,7 @@ flce_status flce_orthogonalize(const flce_ortho_problem* p, const void* src, voi
 
   if (plan.cluster > 0) {
     flce::OrthoSmallParams k{};
-    fill_steps(p, k.step);
+    fill_steps(p, bounds, k.step);
     k.src = src;
     k.batch_stride = p->batch_stride;
     k.row_pitch = p->row_pitch;
@@ -408,7 +448,7 @@ flce_status flce_orthogonalize(const flce_ortho_problem* p, const void* src, voi
   if (out_mapped && !make_map(&r.store[flce::kOrthoOut], out, p->cols, p->rows, 32, 32, kStore,
                               p->batch))
     return FLCE_ERR_CUDA;
-  r.products = list_products(p, plan.grouped, tall, r.product);
+  r.products = list_products(p, bounds, plan.grouped, tall, r.product);
   r.batch = c.batch;
   // Tiles of 128, one to an SM, or of 256, one to a pair of SMs. The small ones
   // take half as long to come and go, which counts where products are short and

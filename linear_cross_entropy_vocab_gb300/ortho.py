@@ -46,13 +46,16 @@ def orthogonalize(x: torch.Tensor, *,
 
     x is float32, bfloat16 or float16; the result [..., M, N] is bfloat16 or float16
     (``out_dtype``, by default x's type, bfloat16 for float32). ``coefficients`` has a triple for
-    each step, at most 64; they have to keep the singular values, of which the first step's are at
-    most 1, below 16. Products are taken of 11-bit values with 32-bit sums: the result is within
-    about 1.5e-3 of itself, more where a few singular values are far above the others. A matrix
-    of zeros stays one; one that holds a NaN or an infinity becomes NaN. It has no gradient: an x
-    that asks for one is refused. Sides are at most 2^20, and the matrices
-    of a call at most 65535. ``err_word`` (one int32, which the caller clears and reads) gets
-    FLCE_DEVERR_TIMEOUT if a kernel gave up waiting.
+    each step, at most 64. They have to keep the largest singular value, which is at most 1 before
+    the first step, in 1e-4 to 16, and each step's a + b t + c t^2 (t its square) below 1e4 in
+    magnitude, and both within 1.5 times that where every step finds its values larger by 2^-9:
+    schedules that are tuned step by step need their safety factor (a / 1.01, b / 1.01^3,
+    c / 1.01^5); without it they magnify roundings and are refused. Products are taken of 11-bit
+    values with 32-bit sums: the result is within about 1.5e-3 of itself, more where a few singular
+    values are far above the others. A matrix of zeros stays one; one that holds a NaN or an
+    infinity becomes NaN. It has no gradient: an x that asks for one is refused. Sides are at most
+    2^20, and the matrices of a call at most 65535. ``err_word`` (one int32, which the caller
+    clears and reads) gets FLCE_DEVERR_TIMEOUT if a kernel gave up waiting.
     """
     code = _DTYPES.get(x.dtype)
     if code is None:

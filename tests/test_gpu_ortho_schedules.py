@@ -1,0 +1,67 @@
+"""Orthogonalising with schedules that are tuned step by step, against the steps in 64 bits.
+
+Tolerance: 1 % of the result's 2-norm, whatever the kernels plan and however they group steps. Each
+product's operands are halves, so a step moves a singular value by some 2^-12 of the polynomial's
+largest value, which is four to eight times what it multiplies by; the next steps' polynomials rise
+at most twelve times as fast as their value where they are steepest, and fall as fast between, so
+that a few values of many are off by a per cent or two and most by 1e-3.
+"""
+import pytest
+import torch
+
+from linear_cross_entropy_vocab_gb300 import orthogonalize
+from linear_cross_entropy_vocab_gb300.abi import FlceError
+from test_ortho_schedules_host import TUNED, TUNED8, safe
+
+pytestmark = pytest.mark.gpu
+
+SCHEDULES = {"tuned5": safe(TUNED[:-1]) + TUNED[-1:], "tuned5_all": safe(TUNED),
+             "tuned8": safe(TUNED8[:-1]) + TUNED8[-1:],
+             "top": ((1.0, 0.5, 0.0), (0.3, 0.163, 0.0)) * 3}
+# in one CTA's shared memory, in a cluster's, by tiles of 128 and of 256, with steps that share a gram
+SIZES = [(1, 100, 300), (2, 128, 1100), (2, 3000, 90), (1, 300, 520), (1, 2300, 2200),
+         (1, 1000, 5100), (4, 3000, 700)]
+
+
+def steps64(g, coefficients, eps=1e-7):
+    x = g.double()
+    x = x / (torch.linalg.matrix_norm(x) + eps)
+    tall = x.shape[0] > x.shape[1]
+    x = x.t() if tall else x
+    for a, b, c in coefficients:
+        gram = x @ x.t()
+        x = a * x + (b * gram + c * (gram @ gram)) @ x
+    return x.t() if tall else x
+
+
+def matrices(kind, batch, m, n, dtype=torch.float32):
+    """Noise, or noise with what many examples have in common, of some rank."""
+    g = torch.Generator("cuda").manual_seed(m + 3 * n)
+    x = torch.randn(batch, m, n, generator=g, device="cuda")
+    if kind == "momentum":
+        rank = max(1, min(m, n) // 32)
+        u = torch.randn(batch, m, rank, generator=g, device="cuda")
+        v = torch.randn(batch, rank, n, generator=g, device="cuda")
+        x.baddbmm_(u, v, alpha=2.0 * rank ** -0.5)
+    return (x * 1e-3).to(dtype)
+
+
+@pytest.mark.parametrize("name", SCHEDULES)
+@pytest.mark.parametrize("batch,m,n", SIZES)
+def test_against_64_bits(batch, m, n, name):
+    x = matrices("noise", batch, m, n)
+    err = torch.zeros((), dtype=torch.int32, device="cuda")
+    got = orthogonalize(x, coefficients=SCHEDULES[name], out_dtype=torch.float16, err_word=err)
+    for i in {0, batch - 1}:
+        want = steps64(x[i], SCHEDULES[name])
+        off = float((got[i].double() - want).norm() / want.norm())
+        assert off <= 1e-2, off
+    assert int(err) == 0
+
+
+@pytest.mark.parametrize("m,n", [(100, 300), (300, 520), (700, 3000)])
+def test_schedules_that_magnify_roundings_are_refused(m, n):
+    x = matrices("noise", 1, m, n)
+    for coefficients in (TUNED, TUNED8):
+        with pytest.raises(FlceError, match="safety factor"):
+            orthogonalize(x, coefficients=coefficients)
