@@ -122,6 +122,14 @@ void fill_steps(const flce_ortho_problem* p, const Bounds& b, flce::OrthoStep* s
 // commute. So each step after a group's first takes two products for its gram,
 // one for its polynomial and one to gather the polynomials, all m x m.
 //
+// Roundings of a gram, of 2^-12 of it, are noise in the directions of small
+// singular values too, and there P on both sides magnifies them by the square of
+// its largest value. A group goes on while that is below 12^2 (11.9 before the
+// third of the default steps): with the published tuned steps, of 8.2, 4.1 and 3.9,
+// three in a group put noise of 0.3 to 1.0 (the 2-norm, for singular values as
+// 1 / k^2) where steps by themselves and groups of two put 0.2.
+constexpr double kCarried = 12.0;
+
 // The gram's values are below the squares of the singular values' bound, and a
 // gathered polynomial's below the product of the bounds of its parts. Each is
 // held with a power of two of its own.
@@ -147,7 +155,10 @@ int list_products(const flce_ortho_problem* p, const Bounds& b, bool grouped, bo
   for (int k = 0; k < p->steps;) {
     // groups of three, of two at the end
     const int left = p->steps - k;
-    const int group = !grouped ? 1 : left == 4 ? 2 : std::min(3, left);
+    const int most = !grouped ? 1 : left == 4 ? 2 : std::min(3, left);
+    int group = 1;
+    for (double carried = b.poly[k]; group < most && carried <= kCarried; ++group)
+      carried *= b.poly[k + group];
     const int first = k;
     double g_scale = scale_for(b.top[k] * b.top[k]);
     add(OrthoOp::kGram, from, from, flce::kOrthoGram, g_scale / (x_scale * x_scale),
