@@ -565,9 +565,11 @@ flce_status flce_rms_norm_backward(const flce_norm_problem* p, const void* grad_
  * (with x^T x on the other side for more rows than columns, which gives the
  * same). The norm is held in fp64, sums in fp32; between the products x, x x^T
  * and the polynomial are held in halves (11 bits) with a power-of-two scale of
- * their own, so that the result is within about 1.5e-3 of itself, more where a
- * few singular values are far above the others. A matrix that holds a NaN or
- * an infinity gives NaN.
+ * their own. With the steps (3.4445, -4.7750, 2.0315) five times the result of
+ * noise, or of noise with a few larger directions, is within 2.5e-3 of itself
+ * (3e-3 in bf16). Where singular values lie far apart, noise of a 2-norm of 2^-12
+ * times the product of the a comes to it, in the directions of the smallest. A
+ * matrix that holds a NaN or an infinity gives NaN.
  */
 typedef struct flce_ortho_problem {
   int64_t batch;        /* matrices, at most 65535 */

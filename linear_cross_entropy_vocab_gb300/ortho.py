@@ -51,11 +51,14 @@ def orthogonalize(x: torch.Tensor, *,
     magnitude, and both within 1.5 times that where every step finds its values larger by 2^-9:
     schedules that are tuned step by step need their safety factor (a / 1.01, b / 1.01^3,
     c / 1.01^5); without it they magnify roundings and are refused. Products are taken of 11-bit
-    values with 32-bit sums: the result is within about 1.5e-3 of itself, more where a few singular
-    values are far above the others. A matrix of zeros stays one; one that holds a NaN or an
-    infinity becomes NaN. It has no gradient: an x that asks for one is refused. Sides are at most
-    2^20, and the matrices of a call at most 65535. ``err_word`` (one int32, which the caller
-    clears and reads) gets FLCE_DEVERR_TIMEOUT if a kernel gave up waiting.
+    values with 32-bit sums: with the default steps the result of noise, or of noise with a few
+    larger directions, is within 2.5e-3 of itself in the 2-norm (3e-3 in bfloat16). Where singular
+    values lie far apart, noise comes to that in the directions of the smallest, of a 2-norm of
+    2^-12 times the product of the a (0.12 with the default steps, where each singular value near 1
+    counts 1). A matrix of zeros stays one; one that holds a NaN or an infinity becomes NaN. It has
+    no gradient: an x that asks for one is refused. Sides are at most 2^20, and the matrices of a
+    call at most 65535. ``err_word`` (one int32, which the caller clears and reads) gets
+    FLCE_DEVERR_TIMEOUT if a kernel gave up waiting.
     """
     code = _DTYPES.get(x.dtype)
     if code is None:
