@@ -2,7 +2,14 @@
 // results, the current stream, and the autograd node. In C++ because these calls
 // are shorter than Python's share of them: autograd runs a node in a thread of
 // its own, where a node written in Python took 100 us more than this one.
+//
+// rms_norm calls the library itself for ordinary tensors. Where something
+// listens to what is dispatched (tracing, torch.compile, fake tensors, a mode) it
+// calls rms_norm_forward and rms_norm_backward through the dispatcher, which have
+// a form for tensors without data.
 #include <ATen/ATen.h>
+#include <ATen/TensorSubclassLikeUtils.h>
+#include <ATen/core/dispatch/Dispatcher.h>
 #include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -103,6 +110,119 @@ std::tuple<Tensor, Tensor> forward(const Inputs& in, const Tensor& rstd) {
         "flce_rms_norm");
   return {y, sum};
 }
+Tensor empty_rstd(const Inputs& in) {
+  return at::empty({in.problem.n}, in.x.options().dtype(at::kFloat));
+}
+
+struct Gradients {
+  Tensor x, residual, weight;  // those that are asked for
+};
+// In one type the gradients of x and of the residual are one tensor, `x`.
+Gradients gradients(const Tensor& upstream, const Tensor& upstream_sum, const Tensor& normalised,
+                    const Tensor& gain, const Tensor& rstd, double eps, bool need_x,
+                    bool need_residual, bool need_weight) {
+  const c10::cuda::CUDAGuard guard(normalised.device());
+  flce_norm_problem p{};
+  const Tensor total = rows_of(normalised, p.x_pitch), grad_y = upstream.contiguous();
+  const Tensor grad_sum = upstream_sum.defined() ? upstream_sum.contiguous() : upstream_sum;
+  const Tensor weight = gain.defined() ? gain.contiguous() : gain;
+  Gradients g;
+  if (need_x) g.x = empty_as(total, grad_y);
+  if (need_residual) g.residual = empty_as(total, total);
+  if (need_weight) g.weight = at::empty_like(weight);
+  p.h = total.size(-1);
+  p.n = rstd.numel();
+  p.residual_pitch = p.h;
+  p.dtype = code_of(grad_y);
+  p.sum_dtype = code_of(total);
+  p.weight_dtype = weight.defined() ? code_of(weight) : p.dtype;
+  p.eps = static_cast<float>(eps);
+  const size_t bytes = flce_rms_norm_backward_workspace_size(&p);
+  const Tensor workspace =
+      at::empty({static_cast<int64_t>(bytes)}, total.options().dtype(at::kByte));
+  check(flce_rms_norm_backward(&p, pointer(grad_y), pointer(grad_sum), pointer(total),
+                               pointer(weight), static_cast<const float*>(pointer(rstd)),
+                               writable(g.x), writable(g.residual), writable(g.weight),
+                               writable(workspace), bytes, stream_of(total)),
+        "flce_rms_norm_backward");
+  return g;
+}
+
+// The same as operators without an autograd formula: (y, rstd) or (y, rstd, sum),
+// and those gradients that are asked for, in the order of their flags.
+std::vector<Tensor> rms_norm_forward(const Tensor& x, const std::optional<Tensor>& weight,
+                                     double eps, const std::optional<Tensor>& residual) {
+  const Inputs in = prepare(x, weight, eps, residual);
+  const Tensor rstd = empty_rstd(in);
+  auto [y, sum] = forward(in, rstd);
+  if (residual) return {y, rstd, sum};
+  return {y, rstd};
+}
+std::vector<Tensor> rms_norm_forward_meta(const Tensor& x, const std::optional<Tensor>&, double,
+                                          const std::optional<Tensor>& residual) {
+  const auto sizes = x.sym_sizes();
+  const c10::SymInt n = x.sym_numel() / sizes.back();
+  std::vector<Tensor> out{at::empty_symint(sizes, x.options()),
+                          at::empty_symint({n}, x.options().dtype(at::kFloat))};
+  if (residual) out.push_back(at::empty_symint(sizes, residual->options()));
+  return out;
+}
+
+std::vector<Tensor> defined(const Gradients& g) {
+  std::vector<Tensor> out;
+  for (const Tensor& t : {g.x, g.residual, g.weight})
+    if (t.defined()) out.push_back(t);
+  return out;
+}
+std::vector<Tensor> rms_norm_backward(const Tensor& grad_y, const std::optional<Tensor>& grad_sum,
+                                      const Tensor& total, const std::optional<Tensor>& weight,
+                                      const Tensor& rstd, double eps, bool need_x,
+                                      bool need_residual, bool need_weight) {
+  return defined(gradients(grad_y, grad_sum.value_or(Tensor()), total, weight.value_or(Tensor()),
+                           rstd, eps, need_x, need_residual, need_weight));
+}
+std::vector<Tensor> rms_norm_backward_meta(const Tensor& grad_y, const std::optional<Tensor>&,
+                                           const Tensor& total,
+                                           const std::optional<Tensor>& weight, const Tensor&,
+                                           double, bool need_x, bool need_residual,
+                                           bool need_weight) {
+  Gradients g;
+  if (need_x) g.x = at::empty_symint(total.sym_sizes(), grad_y.options());
+  if (need_residual) g.residual = at::empty_symint(total.sym_sizes(), total.options());
+  if (need_weight) g.weight = at::empty_symint(weight->sym_sizes(), weight->options());
+  return defined(g);
+}
+
+// Whether a call on these tensors goes through the dispatcher.
+template <class... Optional>
+bool listened_to(const Tensor& t, const Optional&... others) {
+  return at::isTensorSubclassLike(t) || ((others && at::isTensorSubclassLike(*others)) || ...);
+}
+template <class F>
+auto operator_of(const char* name) {
+  return c10::Dispatcher::singleton().findSchemaOrThrow(name, "").typed<F>();
+}
+std::vector<Tensor> dispatch_forward(const Tensor& x, const std::optional<Tensor>& weight,
+                                     double eps, const std::optional<Tensor>& residual) {
+  static const auto op = operator_of<decltype(rms_norm_forward)>("flce::rms_norm_forward");
+  return op.call(x, weight, eps, residual);
+}
+Gradients dispatch_gradients(const Tensor& grad_y, const Tensor& grad_sum, const Tensor& total,
+                             const Tensor& weight, const Tensor& rstd, double eps, bool need_x,
+                             bool need_residual, bool need_weight) {
+  static const auto op = operator_of<decltype(rms_norm_backward)>("flce::rms_norm_backward");
+  const auto given = [](const Tensor& t) {
+    return t.defined() ? std::optional<Tensor>(t) : std::nullopt;
+  };
+  const std::vector<Tensor> got = op.call(grad_y, given(grad_sum), total, given(weight), rstd, eps,
+                                          need_x, need_residual, need_weight);
+  Gradients g;
+  size_t next = 0;
+  if (need_x) g.x = got[next++];
+  if (need_residual) g.residual = got[next++];
+  if (need_weight) g.weight = got[next++];
+  return g;
+}
 
 // Refuses a backward that is captured while an eager graph of the same leaves
 // lives: their accumulators keep the stream that they were made on, autograd
@@ -130,11 +250,19 @@ class RmsNorm : public torch::autograd::Function<RmsNorm> {
   static variable_list forward(AutogradContext* ctx, const Tensor& x,
                                const std::optional<Tensor>& weight, double eps,
                                const std::optional<Tensor>& residual) {
-    const Inputs in = prepare(x, weight, eps, residual);
-    const Tensor rstd = at::empty({in.problem.n}, x.options().dtype(at::kFloat));
-    auto [y, sum] = ::forward(in, rstd);
+    Tensor y, sum;
     ctx->set_materialize_grads(false);
-    ctx->save_for_backward({residual ? sum : in.x, in.weight, rstd});
+    if (listened_to(x, weight, residual)) {
+      const std::vector<Tensor> got = dispatch_forward(x, weight, eps, residual);
+      y = got[0];
+      if (residual) sum = got[2];
+      ctx->save_for_backward({residual ? sum : x, weight.value_or(Tensor()), got[1]});
+    } else {
+      const Inputs in = prepare(x, weight, eps, residual);
+      const Tensor rstd = empty_rstd(in);
+      std::tie(y, sum) = ::forward(in, rstd);
+      ctx->save_for_backward({residual ? sum : in.x, in.weight, rstd});
+    }
     ctx->saved_data["eps"] = eps;
     ctx->saved_data["dtype"] = static_cast<int64_t>(x.scalar_type());
     if (residual) return {y, sum};
@@ -142,15 +270,16 @@ class RmsNorm : public torch::autograd::Function<RmsNorm> {
   }
 
   static variable_list backward(AutogradContext* ctx, const variable_list& grads) {
-    refuse_lost_capture();
     const variable_list saved = ctx->get_saved_variables();
     const Tensor &total = saved[0], &weight = saved[1], &rstd = saved[2];
+    const bool plain = !at::isTensorSubclassLike(grads[0].defined() ? grads[0] : total);
+    if (plain) refuse_lost_capture();
     // inputs that are tensors are counted
     size_t input = 0;
     const bool need_x = ctx->needs_input_grad(input++);
     const bool need_weight = weight.defined() && ctx->needs_input_grad(input++);
     const bool need_residual = grads.size() > 1 && ctx->needs_input_grad(input);
-    Tensor grad_y = grads[0], grad_sum = grads.size() > 1 ? grads[1] : Tensor();
+    const Tensor grad_y = grads[0], grad_sum = grads.size() > 1 ? grads[1] : Tensor();
     const auto dtype = static_cast<at::ScalarType>(ctx->saved_data["dtype"].toInt());
     const bool wide = total.scalar_type() != dtype;
     Tensor grad_x, grad_weight, grad_residual;
@@ -161,31 +290,13 @@ class RmsNorm : public torch::autograd::Function<RmsNorm> {
         if (need_residual) grad_residual = grad_sum;
       }
     } else {
-      const c10::cuda::CUDAGuard guard(total.device());
-      grad_y = grad_y.contiguous();
-      if (grad_sum.defined()) grad_sum = grad_sum.contiguous();
       // in one type the gradients of x and of the residual are one tensor
-      if (need_x || (need_residual && !wide)) grad_x = empty_as(total, grad_y);
-      if (need_residual && wide) grad_residual = empty_as(total, total);
-      if (need_weight) grad_weight = at::empty_like(weight);
-      flce_norm_problem p{};
-      p.h = total.size(-1);
-      p.n = rstd.numel();
-      p.x_pitch = p.residual_pitch = p.h;
-      if (!total.is_contiguous()) p.x_pitch = total.stride(-2);  // rows_of has seen to the rest
-      p.dtype = code_of(grad_y);
-      p.sum_dtype = code_of(total);
-      p.weight_dtype = weight.defined() ? code_of(weight) : p.dtype;
-      p.eps = static_cast<float>(ctx->saved_data["eps"].toDouble());
-      const size_t bytes = flce_rms_norm_backward_workspace_size(&p);
-      const Tensor workspace =
-          at::empty({static_cast<int64_t>(bytes)}, total.options().dtype(at::kByte));
-      check(flce_rms_norm_backward(&p, pointer(grad_y), pointer(grad_sum), pointer(total),
-                                   pointer(weight), static_cast<const float*>(pointer(rstd)),
-                                   writable(grad_x), writable(grad_residual),
-                                   writable(grad_weight), writable(workspace), bytes,
-                                   stream_of(total)),
-            "flce_rms_norm_backward");
+      Gradients g = (plain ? gradients : dispatch_gradients)(
+          grad_y, grad_sum, total, weight, rstd, ctx->saved_data["eps"].toDouble(),
+          need_x || (need_residual && !wide), need_residual && wide, need_weight);
+      grad_x = g.x;
+      grad_residual = g.residual;
+      grad_weight = g.weight;
       if (need_residual && !wide) grad_residual = grad_x;
       if (!need_x) grad_x = Tensor();
     }
@@ -210,6 +321,11 @@ class RmsNorm : public torch::autograd::Function<RmsNorm> {
 std::vector<Tensor> rms_norm(const Tensor& x, const std::optional<Tensor>& weight, double eps,
                              const std::optional<Tensor>& residual, bool differentiable) {
   if (differentiable) return RmsNorm::apply(x, weight, eps, residual);
+  if (listened_to(x, weight, residual)) {
+    const std::vector<Tensor> got = dispatch_forward(x, weight, eps, residual);
+    if (residual) return {got[0], got[2]};
+    return {got[0]};
+  }
   const Inputs in = prepare(x, weight, eps, residual);
   auto [y, sum] = forward(in, Tensor());
   if (residual) return {y, sum};
@@ -239,6 +355,18 @@ std::vector<Tensor> rms_norm_quantize(const Tensor& x, const std::optional<Tenso
   if (residual) return {q, scale, sum};
   return {q, scale};
 }
+std::vector<Tensor> rms_norm_quantize_meta(const Tensor& x, const std::optional<Tensor>&, double,
+                                           const std::optional<Tensor>& residual) {
+  const auto sizes = x.sym_sizes();
+  std::vector<c10::SymInt> strides(sizes.size(), 1);
+  c10::SymInt stride = (sizes.back() + 15) / 16 * 16;
+  for (size_t i = sizes.size() - 1; i-- > 0; stride = stride * sizes[i]) strides[i] = stride;
+  std::vector<Tensor> out{
+      at::empty_strided_symint(sizes, strides, x.options().dtype(at::kChar)),
+      at::empty_symint(sizes.slice(0, sizes.size() - 1), x.options().dtype(at::kFloat))};
+  if (residual) out.push_back(at::empty_symint(sizes, residual->options()));
+  return out;
+}
 
 }  // namespace
 
@@ -246,6 +374,18 @@ TORCH_LIBRARY(flce, m) {
   m.def("rms_norm(Tensor x, Tensor? weight, float eps, Tensor? residual, bool differentiable) "
         "-> Tensor[]",
         &rms_norm);
-  m.def("rms_norm_quantize(Tensor x, Tensor? weight, float eps, Tensor? residual) -> Tensor[]",
-        &rms_norm_quantize);
+  m.def("rms_norm_forward(Tensor x, Tensor? weight, float eps, Tensor? residual) -> Tensor[]");
+  m.def("rms_norm_backward(Tensor grad_y, Tensor? grad_sum, Tensor total, Tensor? weight, "
+        "Tensor rstd, float eps, bool need_x, bool need_residual, bool need_weight) -> Tensor[]");
+  m.def("rms_norm_quantize(Tensor x, Tensor? weight, float eps, Tensor? residual) -> Tensor[]");
+}
+TORCH_LIBRARY_IMPL(flce, CUDA, m) {
+  m.impl("rms_norm_forward", &rms_norm_forward);
+  m.impl("rms_norm_backward", &rms_norm_backward);
+  m.impl("rms_norm_quantize", &rms_norm_quantize);
+}
+TORCH_LIBRARY_IMPL(flce, Meta, m) {
+  m.impl("rms_norm_forward", &rms_norm_forward_meta);
+  m.impl("rms_norm_backward", &rms_norm_backward_meta);
+  m.impl("rms_norm_quantize", &rms_norm_quantize_meta);
 }

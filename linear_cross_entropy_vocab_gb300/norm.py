@@ -78,7 +78,8 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: float 
     2^-126; H is at most 2^24.
 
     x, weight and residual get gradients from those of y and s; the backward reads s as it is
-    stored, and gives the same bits in every run. It cannot be differentiated again.
+    stored, and gives the same bits in every run. It cannot be differentiated again. torch.compile
+    and other tracers see ``flce::rms_norm_forward`` and ``flce::rms_norm_backward``.
     """
     eps = float(eps)
     _check_inputs(x, weight, eps, residual)

@@ -1,0 +1,150 @@
+"""The norm's operators where tensors have no data: fake tensors, tracing, torch.compile."""
+import os
+import subprocess
+import sys
+
+import pytest
+import torch
+from torch._subclasses.fake_tensor import FakeTensorMode
+from torch.fx.experimental.proxy_tensor import make_fx
+
+from linear_cross_entropy_vocab_gb300 import native_build, rms_norm, rms_norm_quantize
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+SHAPES = [(20,), (3, 16), (2, 3, 40), (2, 1, 4, 33)]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    native_build.build()
+
+
+def _inputs(shape, residual, make=torch.empty):
+    x = make(shape, device="cuda", dtype=torch.bfloat16)
+    r = None if residual is None else make(shape, device="cuda", dtype=residual)
+    return x, make(shape[-1:], device="cuda", dtype=torch.float32), r
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+def test_fake_tensors(shape):
+    for residual in (None, torch.bfloat16, torch.float32):
+        with FakeTensorMode():
+            x, w, r = _inputs(shape, residual)
+            got = rms_norm(x.requires_grad_(), w, residual=r)
+            y, s = got if r is not None else (got, None)
+            assert y.requires_grad and y.shape == shape and y.dtype == x.dtype and y.is_cuda and y.is_contiguous()
+            assert s is None or (s.shape == shape and s.dtype == residual)
+            with torch.no_grad():
+                got = rms_norm(x, w, residual=r)
+                assert (got if r is None else got[0]).shape == shape
+                q, scale, *s = rms_norm_quantize(x, w, residual=r)
+            pitch = (shape[-1] + 15) // 16 * 16
+            assert q.shape == shape and q.dtype == torch.int8 and scale.shape == shape[:-1]
+            assert scale.dtype == torch.float32 and q.stride(-1) == 1
+            assert len(shape) == 1 or q.stride(-2) == pitch
+            assert len(s) == (r is not None)
+
+
+@pytest.mark.gpu  # autograd's threads ask for the device
+@pytest.mark.parametrize("shape", SHAPES)
+def test_gradients_of_fake_tensors(shape):
+    for residual in (None, torch.bfloat16, torch.float32):
+        with FakeTensorMode():
+            x, w, r = _inputs(shape, residual)
+            leaves = [t.requires_grad_() for t in (x, w, r) if t is not None]
+            got = rms_norm(x, w, residual=r)
+            outs = [got] if r is None else list(got)
+            grads = torch.autograd.grad(outs, leaves, [torch.empty_like(t) for t in outs])
+            for leaf, grad in zip(leaves, grads):
+                assert grad.shape == leaf.shape and grad.dtype == leaf.dtype
+
+
+@pytest.mark.gpu
+def test_a_traced_training_step():
+    """What a tracer sees: both directions as operators, with no data touched."""
+    def step(x, w, r, dy, ds):
+        y, s = rms_norm(x, w, residual=r)
+        return torch.autograd.grad([y, s], [x, w, r], [dy, ds])
+
+    with FakeTensorMode() as mode:
+        x, w, r = (t.requires_grad_() for t in _inputs((4, 6, 40), torch.float32))
+        dy, ds = torch.empty_like(x), torch.empty_like(r)
+        with mode:
+            graph = make_fx(step)(x, w, r, dy, ds)
+    names = [str(n.target) for n in graph.graph.nodes if n.op == "call_function"]
+    assert "flce.rms_norm_forward.default" in names
+    assert "flce.rms_norm_backward.default" in names
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dynamic", [False, True])
+@pytest.mark.parametrize("residual", [None, torch.bfloat16, torch.float32])
+def test_compiled(residual, dynamic):
+    """The same bits as without compilation, in both directions and in 8 bits."""
+    def step(x, w, r):
+        got = rms_norm(x * 2, w, residual=r)
+        y, s = got if r is not None else (got, x)
+        return (y * y).sum() + s.float().sum() * 0.5, y
+
+    def quantize(x, w, r):
+        with torch.no_grad():
+            return [t + 0 for t in rms_norm_quantize(x, w, residual=r)]
+
+    rms_norm(torch.ones(1, 8, device="cuda"))  # loads the library
+    torch._dynamo.reset()
+    compiled = torch.compile(step, backend="aot_eager", fullgraph=True, dynamic=dynamic)
+    compiled_q = torch.compile(quantize, backend="aot_eager", fullgraph=True, dynamic=dynamic)
+    for shape in ((6, 64), (9, 64), (5, 33)):
+        g = torch.Generator("cuda").manual_seed(len(shape) + shape[0])
+        x, w, r = _inputs(shape, residual, lambda *a, **k: torch.randn(*a, generator=g, **k))
+        leaves = [t.requires_grad_() for t in (x, w, r) if t is not None]
+        results = []
+        for f in (step, compiled):
+            loss, y = f(x, w, r)
+            results.append([y.detach(), *torch.autograd.grad(loss, leaves)])
+        for a, b in zip(*results):
+            assert torch.equal(a, b)
+        for a, b in zip(quantize(x, w, r), compiled_q(x, w, r)):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+def test_compiled_as_the_first_call():
+    """Where the library is not loaded yet."""
+    code = ("import torch\n"
+            "from linear_cross_entropy_vocab_gb300 import rms_norm\n"
+            "f = torch.compile(lambda x, w: rms_norm(x, w) * 2, backend='aot_eager')\n"
+            "x = torch.randn(5, 64, device='cuda').requires_grad_()\n"
+            "w = torch.rand(64, device='cuda').requires_grad_()\n"
+            "y = f(x, w)\n"
+            "got = [y, *torch.autograd.grad(y.sum(), (x, w))]\n"
+            "z = rms_norm(x, w) * 2\n"
+            "want = [z, *torch.autograd.grad(z.sum(), (x, w))]\n"
+            "assert all(torch.equal(a, b) for a, b in zip(got, want))\n")
+    done = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True,
+                          timeout=600)
+    assert done.returncode == 0, done.stderr[-3000:]
+
+
+@pytest.mark.gpu
+def test_operators_by_themselves():
+    """Through the dispatcher they do what the call does, strided inputs included."""
+    g = torch.Generator("cuda").manual_seed(1)
+    for shape in SHAPES:
+        for residual in (None, torch.bfloat16, torch.float32):
+            x, w, r = _inputs(shape, residual,
+                              lambda *a, **k: torch.randn(*a, generator=g, **k))
+            x = torch.stack([x, x], -1)[..., 0]  # elements two apart
+            rms_norm(x, w, residual=r)
+            out = torch.ops.flce.rms_norm_forward(x, w, 1e-6, r)
+            leaves = [t.detach().requires_grad_() for t in (x, w, r) if t is not None]
+            got = rms_norm(leaves[0], leaves[1], residual=leaves[2] if r is not None else None)
+            y, s = got if r is not None else (got, None)
+            assert torch.equal(y, out[0]) and (s is None or torch.equal(s, out[2]))
+            dy = torch.randn(shape, generator=g, device="cuda").bfloat16()
+            want = torch.autograd.grad(y, leaves, dy)
+            wide = residual == torch.float32
+            back = torch.ops.flce.rms_norm_backward(dy, None, x if s is None else s.detach(), w,
+                                                    out[1], 1e-6, True, wide, True)
+            assert torch.equal(back[0], want[0]) and torch.equal(back[-1], want[1])
+            assert not wide or torch.equal(back[1], want[2])
