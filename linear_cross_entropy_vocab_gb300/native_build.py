@@ -5,14 +5,17 @@ The translation units are compiled in parallel and linked into
 linked statically and the driver's tensor-map encoder is looked up at run
 time, so the library needs no libcuda at link time. Beside it lies
 ``libflce_torch.so``: the operators that are registered with PyTorch, compiled
-by the host compiler against the installed PyTorch and linked to libflce.so.
+by the host compiler against the installed PyTorch and linked to libflce.so. It works with that
+PyTorch alone, so ``libflce_torch.json`` says which one it was.
 """
 from __future__ import annotations
 
 import concurrent.futures
+import json
 import os
 import shutil
 import subprocess
+from typing import Optional
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -22,6 +25,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libflce.so")
 TORCH_LIB = os.path.join(BUILD, "libflce_torch.so")
 TORCH_SOURCE = "norm_torch.cpp"
+TORCH_STAMP = os.path.join(BUILD, "libflce_torch.json")
 
 SOURCES = ["flce_api.cu", "kernels_tc.cu", "kernels_simt.cu", "kernels_rows.cu",
            "grads_api.cu", "kernels_grads.cu", "beam_api.cu", "kernels_beam.cu",
@@ -47,8 +51,27 @@ def _inputs():
     return files
 
 
+def _installed_torch() -> dict:
+    """What libflce_torch.so depends on beside its sources."""
+    import torch
+
+    return {"version": str(torch.__version__), "git": torch.version.git_version,
+            "cxx11_abi": bool(torch.compiled_with_cxx11_abi())}
+
+
+def torch_mismatch() -> Optional[str]:
+    """Why libflce_torch.so does not go with the installed PyTorch, or None."""
+    try:
+        with open(TORCH_STAMP) as f:
+            built = dict(json.load(f))
+    except (OSError, ValueError, TypeError):
+        return "it does not say which PyTorch it was built against"
+    return ", ".join(f"{k} {built.get(k)} when it was built, {v} here"
+                     for k, v in _installed_torch().items() if built.get(k) != v) or None
+
+
 def up_to_date() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(TORCH_LIB)):
+    if not (os.path.exists(LIB) and os.path.exists(TORCH_LIB)) or torch_mismatch():
         return False
     t = min(os.path.getmtime(LIB), os.path.getmtime(TORCH_LIB))
     return all(os.path.getmtime(f) <= t for f in _inputs())
@@ -84,7 +107,13 @@ def _link_torch(obj: str) -> None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    # the stamp is away while the library and it may disagree
+    if os.path.exists(TORCH_STAMP):
+        os.remove(TORCH_STAMP)
     os.replace(tmp, TORCH_LIB)
+    with open(TORCH_STAMP + ".tmp", "w") as f:
+        json.dump(_installed_torch(), f)
+    os.replace(TORCH_STAMP + ".tmp", TORCH_STAMP)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:

@@ -62,6 +62,11 @@ def _operators():
             raise RuntimeError(
                 f"{path} is missing: build the CUDA library first "
                 "(python -m linear_cross_entropy_vocab_gb300.native_build)")
+        why = native_build.torch_mismatch()
+        if why is not None:
+            raise RuntimeError(
+                f"{path} is of another PyTorch ({why}): build the CUDA library again "
+                "(python -m linear_cross_entropy_vocab_gb300.native_build)")
         torch.ops.load_library(path)
         _ops = torch.ops.flce.rms_norm.default, torch.ops.flce.rms_norm_quantize.default
     return _ops
