@@ -239,6 +239,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     phase ^= 1u;
     tc_fence_after_sync();
   };
+  // Once a wait has given up no more products are issued, and what is left of
+  // the steps is walked through with whatever is there: every CTA of the cluster
+  // has to come to all of its barriers.
+  const auto issues = [&] {
+    return tid == 0 && *static_cast<volatile int*>(&ctl->abort) == 0;
+  };
+  uint32_t issued = 0;  // groups of products, by thread 0
   // what all threads have written to shared memory is there for the products
   const auto written = [&] {
     fence_proxy_async_smem();
@@ -251,13 +258,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   for (int s = 0; s < p.steps; ++s) {
     const OrthoStep& st = p.step[s];
     const float f = s == 0 ? factor : 1.0f;
-    if (tid == 0) {
+    if (issues()) {
       constexpr uint32_t idesc = idesc_f16kind_f32(kSide, kSide, 0, 0, 0);
       for (int k = 0; k < p.slab / 16; ++k) {
         const uint64_t d = smem_desc_sw128(x_at + (k >> 2) * kBlockBytes + (k & 3) * 32, 16, 1024);
         umma_bf16(tmem, d, d, idesc, k != 0 ? 1u : 0u);
       }
       umma_commit(done);
+      ++issued;
     }
     finished();
     if (ranks == 1) {
@@ -305,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       cluster_sync();
     }
     written();
-    if (tid == 0) {
+    if (issues()) {
       constexpr uint32_t idesc = idesc_f16kind_f32(kSide, kSide, 0, 0, 0);
 #pragma unroll
       for (int k = 0; k < kSide / 16; ++k) {
@@ -314,6 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         umma_bf16(tmem + kSide, d, d, idesc, k != 0 ? 1u : 0u);
       }
       umma_commit(done);
+      ++issued;
     }
     finished();
     {
@@ -339,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     written();
-    if (tid == 0) {
+    if (issues()) {
       for (int c = 0; c < p.slab; c += 256) {
         const int cols = p.slab - c < 256 ? p.slab - c : 256;
         const uint32_t idesc = idesc_f16kind_f32(kSide, cols, 0, 1, 0);
@@ -351,6 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     idesc, k != 0 ? 1u : 0u);
       }
       umma_commit(done);
+      ++issued;
     }
     finished();
     const float scale = st.product * f;
@@ -410,6 +420,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int i = (tid >> 6) + 8 * q;
         if (i < m && j0 + j < n) out[int64_t(i) * p.cols + j0 + j] = value(i, j);
       }
+    }
+  }
+  if (tid == 0 && ctl->abort != 0 && issued > 0) {
+    // the last products, which may still write to tensor memory
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(done, (issued - 1) & 1u) && globaltimer_ns() - t0 < 1000000000ull) {
     }
   }
   tc_fence_before_sync();
