@@ -599,6 +599,16 @@ flce_status flce_orthogonalize(const flce_ortho_problem* p, const void* src, voi
                                int32_t* err_word, void* workspace,
                                size_t workspace_bytes, void* stream);
 
+/* Self-test of what the tiled kernel does when a wait runs out (see
+ * flce_selftest_wait_timeout): the same call on a problem that does not stay in
+ * shared memory, whose second product waits for a count that nothing makes, with
+ * a limit of budget_s seconds (0 < budget_s <= 1) for each wait. On completion
+ * *err_word has FLCE_DEVERR_TIMEOUT set; out is not complete. Nothing faults. */
+flce_status flce_selftest_orthogonalize_timeout(const flce_ortho_problem* p, const void* src,
+                                                void* out, int32_t* err_word, void* workspace,
+                                                size_t workspace_bytes, double budget_s,
+                                                void* stream);
+
 /* ------------------------------------------------------------------------
  * Per-kernel timing, for measurement tools (not part of the method; the
  * pages describe no profiler). While enabled, every kernel launch made by

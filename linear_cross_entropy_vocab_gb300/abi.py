@@ -81,6 +81,7 @@ EXPORTS = (
     "flce_rms_norm_backward",
     "flce_orthogonalize_workspace_size",
     "flce_orthogonalize",
+    "flce_selftest_orthogonalize_timeout",
     "flce_selftest_wait_timeout",
     "flce_status_string",
     "flce_last_error",
@@ -318,6 +319,9 @@ def load() -> ctypes.CDLL:
         lib.flce_orthogonalize.argtypes = [ctypes.POINTER(flce_ortho_problem)] + [_P] * 4 + [
             ctypes.c_size_t, _P]
         lib.flce_orthogonalize.restype = ctypes.c_int
+        lib.flce_selftest_orthogonalize_timeout.argtypes = [
+            ctypes.POINTER(flce_ortho_problem)] + [_P] * 4 + [ctypes.c_size_t, ctypes.c_double, _P]
+        lib.flce_selftest_orthogonalize_timeout.restype = ctypes.c_int
         lib.flce_selftest_wait_timeout.argtypes = [_P, _P, ctypes.c_double, _P]
         lib.flce_selftest_wait_timeout.restype = ctypes.c_int
         lib.flce_status_string.argtypes = [ctypes.c_int]
@@ -563,6 +567,15 @@ def flce_orthogonalize(p, src, out, err_word, workspace, workspace_bytes, stream
                                    workspace_bytes, stream)
     if check:
         _check(st, "flce_orthogonalize")
+    return st
+
+
+def flce_selftest_orthogonalize_timeout(p, src, out, err_word, workspace, workspace_bytes,
+                                        budget_s, stream, check=True) -> int:
+    st = load().flce_selftest_orthogonalize_timeout(ctypes.byref(p), src, out, err_word, workspace,
+                                                    workspace_bytes, float(budget_s), stream)
+    if check:
+        _check(st, "flce_selftest_orthogonalize_timeout")
     return st
 
 

@@ -323,21 +323,22 @@ __device__ __forceinline__ uint64_t slice_desc(uint32_t base, int kk) {
 
 // Every wait has a limit: past it the CTA gives up, lets what is in flight
 // finish and leaves, and the error word says so.
-__device__ __forceinline__ bool give_up(uint64_t t0, volatile int* abort_flag, int* err_word) {
+__device__ __forceinline__ bool give_up(uint64_t t0, volatile int* abort_flag,
+                                        const OrthoRunParams& p) {
   if (*abort_flag) return true;
-  if (globaltimer_ns() - t0 <= kWaitBudgetNs) return false;
+  if (globaltimer_ns() - t0 <= p.wait_ns) return false;
   *abort_flag = 1;
-  if (err_word) atomicOr(err_word, FLCE_DEVERR_TIMEOUT);
+  if (p.err_word) atomicOr(p.err_word, FLCE_DEVERR_TIMEOUT);
   return true;
 }
 template <int CG>
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                          int* err_word) {
+                                         const OrthoRunParams& p) {
   if (try_wait<CG>(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t it = 1;; ++it) {
     if (try_wait<CG>(bar, parity)) return true;
-    if ((it & 63u) == 0u && give_up(t0, abort_flag, err_word)) return false;
+    if ((it & 63u) == 0u && give_up(t0, abort_flag, p)) return false;
   }
 }
 template <int CG>
@@ -463,7 +464,7 @@ struct Feed {
   // all CTAs.
   __device__ __forceinline__ bool draw(int& u) {
     u = atomicAdd(p.ticket, 1);
-    if (!wait_bar<CG>(smem_addr(&ctl->item_empty[slot]), phase ^ 1u, &ctl->abort, p.err_word))
+    if (!wait_bar<CG>(smem_addr(&ctl->item_empty[slot]), phase ^ 1u, &ctl->abort, p))
       return false;
     if (u >= p.items) u = -1;
     const uint32_t to = smem_addr(&ctl->item[slot]), bar = smem_addr(&ctl->item_full[slot]);
@@ -484,8 +485,7 @@ struct Feed {
       if constexpr (ROLE == Role::kDrawer) {
         if (!draw(u)) return false;
       } else {
-        const bool here = wait_bar<CG>(smem_addr(&ctl->item_full[slot]), phase, &ctl->abort,
-                                       p.err_word);
+        const bool here = wait_bar<CG>(smem_addr(&ctl->item_full[slot]), phase, &ctl->abort, p);
         if (ROLE == Role::kWarp ? !__all_sync(0xffffffffu, here) : !here) return false;
         u = *reinterpret_cast<volatile int*>(&ctl->item[slot]);
         if constexpr (ROLE == Role::kWarp) __syncwarp();
@@ -541,12 +541,12 @@ __device__ __forceinline__ Need need_of(const OrthoRunParams& p, const Product& 
   return {count_of(p, b), q.with->need};
 }
 __device__ __forceinline__ bool wait_need(const Need& need, volatile int* abort_flag,
-                                          int* err_word) {
+                                          const OrthoRunParams& p) {
   if (load_acquire(need.count) >= need.least) return true;
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t it = 1;; ++it) {
     if (load_acquire(need.count) >= need.least) return true;
-    if ((it & 15u) == 0u && give_up(t0, abort_flag, err_word)) return false;
+    if ((it & 15u) == 0u && give_up(t0, abort_flag, p)) return false;
   }
 }
 
@@ -605,7 +605,7 @@ __device__ __forceinline__ bool load_part(const OrthoRunParams& p, const Product
   const int row0 = t.b * p.m_pad;
   for (int k = part.k0; k < part.k1; ++k) {
     const int s = ring.stage;
-    if (!wait_bar<CG>(smem_addr(&ctl->empty[s]), ring.phase ^ 1u, &ctl->abort, p.err_word))
+    if (!wait_bar<CG>(smem_addr(&ctl->empty[s]), ring.phase ^ 1u, &ctl->abort, p))
       return false;
     const uint32_t full_local = smem_addr(&ctl->full[s]);
     const uint32_t full = CG == 2 ? map_to_rank(full_local, 0) : full_local;
@@ -632,7 +632,7 @@ __device__ __forceinline__ bool multiply_part(const OrthoRunParams& p, const Par
   constexpr uint32_t idesc =
       idesc_f16kind_f32(Shape<CG>::kTile, Shape<CG>::kTile, kAcrossA ? 1 : 0, kAcrossB ? 1 : 0, 0);
   for (int k = part.k0; k < part.k1; ++k) {
-    if (!wait_bar<CG>(smem_addr(&ctl->full[ring.stage]), ring.phase, &ctl->abort, p.err_word))
+    if (!wait_bar<CG>(smem_addr(&ctl->full[ring.stage]), ring.phase, &ctl->abort, p))
       return false;
     tc_fence_after_sync();
     const uint32_t a0 = base + ring.stage * kStageBytes, b0 = a0 + kOperandBytes;
@@ -897,7 +897,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const Product& q = feed.q;
           const Tile t = tile_of(q, part.tile);
           if (feed.i > 0 && (t.b != ready || feed.i != product)) {
-            ok = wait_need(need_of(p, q, t.b), abort_flag, p.err_word);
+            ok = wait_need(need_of(p, q, t.b), abort_flag, p);
             if (!ok) break;
             fence_proxy_async_global();
             ready = t.b;
@@ -937,7 +937,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (Part part; feed.next(part); ++it) {
         const int buf = it & 1;
         if (!wait_bar<CG>(smem_addr(&ctl->acc_empty[buf]), ((it >> 1) & 1u) ^ 1u, abort_flag,
-                          p.err_word))
+                          p))
           break;
         tc_fence_after_sync();
         const uint32_t d = tmem + static_cast<uint32_t>(buf * kTile);
@@ -978,8 +978,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Tile t = tile_of(q, part.tile);
       if (q.op == OrthoOp::kPoly && (t.b != ready || feed.i != product)) {
         // the gram is read here too
-        if (!__all_sync(0xffffffffu,
-                        lane != 0 || wait_need(need_of(p, q, t.b), abort_flag, p.err_word)))
+        if (!__all_sync(0xffffffffu, lane != 0 || wait_need(need_of(p, q, t.b), abort_flag, p)))
           break;
         __threadfence();
         __syncwarp();
@@ -988,7 +987,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int buf = it & 1;
       if (!__all_sync(0xffffffffu, wait_bar<CG>(smem_addr(&ctl->acc_full[buf]), (it >> 1) & 1u,
-                                                abort_flag, p.err_word)))
+                                                abort_flag, p)))
         break;
       tc_fence_after_sync();
       const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) +

@@ -364,20 +364,12 @@ bool make_map(CUtensorMap* map, const void* base, int64_t inner, int64_t outer,
 constexpr CUtensorMapSwizzle kLoad = CU_TENSOR_MAP_SWIZZLE_128B;
 constexpr CUtensorMapSwizzle kStore = CU_TENSOR_MAP_SWIZZLE_64B;
 
-}  // namespace
+constexpr uint64_t kWaitNs = 4000000000ull;  // of a tile's products and less: 4 s
 
-extern "C" {
-
-size_t flce_orthogonalize_workspace_size(const flce_ortho_problem* p) {
-  Bounds bounds;
-  if (check_problem(p, &bounds) != FLCE_OK) return 0;
-  return plan_of(p).total;
-}
-
-flce_status flce_orthogonalize(const flce_ortho_problem* p, const void* src, void* out,
-                               int32_t* err_word, void* workspace, size_t workspace_bytes,
-                               void* stream) {
-  clear_error();
+// `lost`: each product after the first waits for one count that never comes.
+flce_status orthogonalize(const flce_ortho_problem* p, const void* src, void* out,
+                          int32_t* err_word, void* workspace, size_t workspace_bytes,
+                          void* stream, uint64_t wait_ns, bool lost) {
   Bounds bounds;
   flce_status st = check_problem(p, &bounds);
   if (st != FLCE_OK) return st;
@@ -400,6 +392,8 @@ flce_status flce_orthogonalize(const flce_ortho_problem* p, const void* src, voi
   uint8_t* const ws = static_cast<uint8_t*>(workspace);
   const bool tall = p->rows > p->cols;
 
+  if (lost && plan.cluster > 0)
+    return fail(FLCE_ERR_UNSUPPORTED, "the matrices stay in shared memory");
   if (plan.cluster > 0) {
     flce::OrthoSmallParams k{};
     fill_steps(p, bounds, k.step);
@@ -504,6 +498,7 @@ flce_status flce_orthogonalize(const flce_ortho_problem* p, const void* src, voi
   r.arrived = c.count;
   r.finished = c.count + kArrived;
   r.ticket = r.finished + c.batch;
+  r.wait_ns = wait_ns;
   r.err_word = err_word;
   const int64_t pairs = std::min<int64_t>(2 * kPlanPairs, sms) / ctas;
   const int64_t triangle = p->batch * r.m_tiles * (r.m_tiles + 1) / 2;
@@ -525,18 +520,47 @@ flce_status flce_orthogonalize(const flce_ortho_problem* p, const void* src, voi
   for (int i = 0; i < r.products; ++i) {
     const flce::OrthoCut& c = r.cut[r.product[i].cut];
     items += c.cut > 0 ? c.units + c.whole : r.product[i].cut < 2 ? triangle : all;
-    r.product[i].need = static_cast<int32_t>(need);
+    r.product[i].need = static_cast<int32_t>(need) + (lost && i > 0 ? 1 << 30 : 0);
     need += (r.product[i].cut < 2 ? triangle : all) / (r.joint ? 1 : p->batch) * ctas *
             flce::kOrthoWarps;
   }
   r.items = static_cast<int32_t>(items);
-  if (need > 0x7fffffff || items > 0x7fff0000) return fail(FLCE_ERR_UNSUPPORTED, "too many tiles and steps to count");
+  if (need > (lost ? 1 << 30 : 0x7fffffff) || items > 0x7fff0000) return fail(FLCE_ERR_UNSUPPORTED, "too many tiles and steps to count");
   cudaError_t e = flce::launch_ortho_norm(c, p->dtype, s);
   if (e != cudaSuccess) return cuda_fail(e, "matrix norm kernel");
   e = flce::launch_ortho_copy(c, p->dtype, s);
   if (e != cudaSuccess) return cuda_fail(e, "matrix copy kernel");
   e = flce::launch_ortho_run(r, p->out_dtype, s);
   return e == cudaSuccess ? FLCE_OK : cuda_fail(e, "orthogonalising kernel");
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t flce_orthogonalize_workspace_size(const flce_ortho_problem* p) {
+  Bounds bounds;
+  if (check_problem(p, &bounds) != FLCE_OK) return 0;
+  return plan_of(p).total;
+}
+
+flce_status flce_orthogonalize(const flce_ortho_problem* p, const void* src, void* out,
+                               int32_t* err_word, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+  clear_error();
+  return orthogonalize(p, src, out, err_word, workspace, workspace_bytes, stream, kWaitNs, false);
+}
+
+flce_status flce_selftest_orthogonalize_timeout(const flce_ortho_problem* p, const void* src,
+                                                void* out, int32_t* err_word, void* workspace,
+                                                size_t workspace_bytes, double budget_s,
+                                                void* stream) {
+  clear_error();
+  if (err_word == nullptr) return fail(FLCE_ERR_INVALID_ARG, "err_word is required");
+  if (!(budget_s > 0.0) || budget_s > 1.0)
+    return fail(FLCE_ERR_INVALID_ARG, "budget_s must be in (0, 1] seconds");
+  return orthogonalize(p, src, out, err_word, workspace, workspace_bytes, stream,
+                       static_cast<uint64_t>(budget_s * 1e9), true);
 }
 
 }  // extern "C"

@@ -97,6 +97,7 @@ struct OrthoRunParams {
   void* shares;        // sums of cut tiles: two of 256 KB for each pair (64 for each CTA)
   int32_t* arrived;    // [cut][CTAs of a tile][8 warps], zeros before and after
   int32_t* finished;   // [batch], zeros before
+  uint64_t wait_ns;    // after which a wait gives up
   int32_t* err_word;
 };
 cudaError_t launch_ortho_run(const OrthoRunParams& p, int out_dtype, cudaStream_t s);

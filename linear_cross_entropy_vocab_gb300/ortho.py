@@ -58,7 +58,8 @@ def orthogonalize(x: torch.Tensor, *,
     counts 1). A matrix of zeros stays one; one that holds a NaN or an infinity becomes NaN. It has
     no gradient: an x that asks for one is refused. Sides are at most 2^20, and the matrices of a
     call at most 65535. ``err_word`` (one int32, which the caller clears and reads) gets
-    FLCE_DEVERR_TIMEOUT if a kernel gave up waiting.
+    FLCE_DEVERR_TIMEOUT if a kernel gave up waiting, after 4 seconds, and left the result
+    incomplete; without it that is not reported.
     """
     code = _DTYPES.get(x.dtype)
     if code is None:
