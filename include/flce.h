@@ -514,8 +514,11 @@ flce_status flce_qlinear(const flce_qproblem* p, const void* x, const float* x_s
  *   grad_s = grad_sum + rstd * (u - unit * (1/h) sum_h u * unit)
  *   grad_weight_h = sum_i grad_y_ih * unit_ih    (the same bits in every run)
  *
- * and grad_s is the gradient of x and of the residual. Rows of outputs and of
- * grad_y and grad_sum lie h elements apart.
+ * and grad_s is the gradient of x and of the residual. A sum that its type
+ * stores as an infinity makes its row's gradients and its column's grad_weight
+ * infinite or NaN, although y is finite. The last bit of y may depend on whether
+ * rows lie at 16-byte boundaries. Rows of outputs and of grad_y and grad_sum lie
+ * h elements apart.
  */
 typedef struct flce_norm_problem {
   int64_t n, h;            /* n >= 0; 1 <= h <= 2^24 */

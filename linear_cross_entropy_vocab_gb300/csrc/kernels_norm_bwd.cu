@@ -13,6 +13,14 @@
 // Rows of more than 16384 values take two passes: the means, and then columns
 // by blocks. 32768 x 4096 bf16 with both gradients: 171 us (6.3 TB/s), and 6 us
 // for the second kernel.
+//
+// Both kernels, by the library's call in turn: 8192 x 8192 bf16 98 us (5.5 TB/s),
+// with an fp32 sum 164 (6.6), fp32 195 (5.5). Above 8192 values 1024 threads
+// have two groups of eight each, which 64 registers do not hold (180 to 260 bytes
+// of spills), and two rows with an fp32 sum do not fit into shared memory, so
+// that those go value by value: 4096 x 16384 bf16 139 us (3.9), with an fp32 sum
+// 281 (3.8), fp32 239 (4.5). Value by value for other reasons: 16384 x 2049 fp32 128
+// (4.2) and bf16 216 (1.3), 4096 x 20000 bf16 415 (1.6).
 #include <algorithm>
 #include <cstdint>
 #include <type_traits>
@@ -398,7 +406,7 @@ cudaError_t launch_bwd_groups(const NormBwdParams& p, int64_t parts, cudaStream_
   constexpr int kStage = Ring<T, R, k.threads, k.vecs>::kStage;
   constexpr int kFit = 200 * 1024 / k.ctas / kStage;
   constexpr int kDepth = kFit > 4 ? 4 : kFit;
-  if constexpr (kDepth < 2) {  // no two rows in shared memory
+  if constexpr (kDepth < 2) {  // no two rows in shared memory: above 8192 values, an fp32 sum
     return launch_bwd_values<T, H>(p, parts, s);
   } else {
     const auto kernel = rms_norm_bwd_rows_kernel<T, R, kTeam, k.vecs, k.threads, k.ctas, kDepth>;

@@ -7,9 +7,19 @@
 // Bound by memory: one pass. A team of threads (a warp, or a CTA of 128 to 1024
 // threads) takes a row and keeps its sums in registers, in 32 bits and not
 // rounded, between the mean and the output; rows of more than 16384 values are
-// read a second time. The squares are summed in 32 bits over at most 32 values
-// a thread and then by a tree. 16384 x 3584 fp16 with a residual take 68 us (6.9
-// TB/s), 8192 x 4096 bf16 to 8 bits 42 us (5.6 TB/s).
+// read a second time. The squares are summed in 32 bits, over at most 32 values
+// a thread in each sweep of up to 16384 values, over a thread's sweeps one after
+// the other (1024 for the longest row), and then by a tree.
+//
+// With a residual, by the library's call in turn: 16384 x 3584 fp16 73 us (6.4 TB/s),
+// 8192 x 8192 bf16 90 (6.0), 4096 x 16384 bf16 89 (6.0) and fp32 232 (4.6: 1024
+// threads hold 64 registers each, and the fp32 form spills 264 bytes of them, the
+// 8-bit one 304); to 8 bits 8192 x 4096 bf16 42 us (5.6), 8192 x 8192 116
+// (4.0), 4096 x 16384 103 (4.6). Rows of more than 16384 values and rows that are not at
+// 16-byte boundaries go value by value: 4096 x 20000 bf16 347 us (1.9) and fp32
+// 347 (3.8), 16384 x 2049 bf16 142 (1.9) and fp32 97 (5.6). The two ways add
+// squares and divide by h in different orders: a row's last bit may differ
+// between them.
 #pragma once
 
 #include <cstdint>

@@ -79,12 +79,14 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: float 
 
     x [..., H] is float32, bfloat16 or float16, and y has its type. ``residual`` is of x's shape
     and of its type or float32; s has the residual's type. ``weight`` [H] is of x's type or
-    float32 (None: ones). y is computed from the unrounded sum, in 32 bits. ``eps`` is at least
-    2^-126; H is at most 2^24.
+    float32 (None: ones). y is computed from the unrounded sum, in 32 bits; its last bit may
+    depend on whether rows lie at 16-byte boundaries. ``eps`` is at least 2^-126; H is at most 2^24.
 
     x, weight and residual get gradients from those of y and s; the backward reads s as it is
-    stored, and gives the same bits in every run. It cannot be differentiated again. torch.compile
-    and other tracers see ``flce::rms_norm_forward`` and ``flce::rms_norm_backward``.
+    stored, and gives the same bits in every run. Where s leaves float16's range it is stored as an
+    infinity, and the row's gradients and the weight's of that column are not finite, although y is:
+    a float32 residual keeps them. It cannot be differentiated again. torch.compile and other tracers see ``flce::rms_norm_forward``
+    and ``flce::rms_norm_backward``.
     """
     eps = float(eps)
     _check_inputs(x, weight, eps, residual)
