@@ -1074,7 +1074,7 @@ cudaError_t launch_copy(const OrthoCopyParams& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
   // CTAs that each find the norm once: six an SM over the batch
   const int64_t tiles = int64_t((p.n_pad + 127) / 128) * (p.m_rows / 64);
-  const int64_t most = std::max<int64_t>(1, 6 * 152 / p.batch);
+  const int64_t most = std::max<int64_t>(1, 6 * kOrthoPlanSms / p.batch);
   cfg.gridDim = dim3(static_cast<unsigned>(std::min(tiles, most)),
                      static_cast<unsigned>(p.batch));
   cfg.blockDim = dim3(256);

@@ -305,8 +305,9 @@ Plan plan_of(const flce_ortho_problem* p) {
   // Shares of 4096 values while the batch has two or fewer for an SM, of 8192 to
   // five CTAs an SM.
   q.parts = q.m * q.n / 4096;
-  if (q.parts * p->batch > 2 * 152)
-    q.parts = std::min<int64_t>(q.m * q.n / 8192, 5 * 152 / std::max<int64_t>(1, p->batch));
+  if (q.parts * p->batch > 2 * flce::kOrthoPlanSms)
+    q.parts = std::min<int64_t>(q.m * q.n / 8192,
+                                5 * flce::kOrthoPlanSms / std::max<int64_t>(1, p->batch));
   q.parts = std::max<int64_t>(1, q.parts);
   const size_t b = static_cast<size_t>(p->batch);
   const size_t x_bytes = align_256(b * static_cast<size_t>(q.m_pad * q.n_pad) * 2);

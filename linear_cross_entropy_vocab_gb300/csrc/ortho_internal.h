@@ -14,6 +14,10 @@ constexpr int kOrthoTile = 256;  // or half of it
 constexpr int kOrthoWarps = 8;  // that store a tile, in each CTA
 constexpr int kOrthoShareBytes = kOrthoTile * kOrthoTile * 4;
 constexpr int kOrthoMaxSteps = 64;
+// The SMs that the norm's and the copy's shares are planned for. The workspace and
+// the order of the norm's sums go by it, so it is not the device's own number:
+// with that, results and sizes would depend on the device.
+constexpr int kOrthoPlanSms = 152;
 
 // The matrices as the caller has them, and their copy in halves: x[b] is
 // [m_pad][n_pad] with m <= n, the transpose of src[b] where `tall`, zeros
