@@ -13,13 +13,13 @@ import torch
 
 from linear_cross_entropy_vocab_gb300 import orthogonalize
 from linear_cross_entropy_vocab_gb300.abi import FlceError
-from test_ortho_schedules_host import TUNED, TUNED8, safe
+from test_ortho_schedules_host import STEPWISE, TUNED, TUNED8, safe
 
 pytestmark = pytest.mark.gpu
 
 SCHEDULES = {"tuned5": safe(TUNED[:-1]) + TUNED[-1:], "tuned5_all": safe(TUNED),
              "tuned8": safe(TUNED8[:-1]) + TUNED8[-1:],
-             "top": ((1.0, 0.5, 0.0), (0.3, 0.163, 0.0)) * 3}
+             "stepwise": STEPWISE, "top": ((1.0, 0.5, 0.0), (0.3, 0.163, 0.0)) * 3}
 # in one CTA's shared memory, in a cluster's, by tiles of 128 and of 256, with steps that share a gram
 SIZES = [(1, 100, 300), (2, 128, 1100), (2, 3000, 90), (1, 300, 520), (1, 2300, 2200),
          (1, 1000, 5100), (4, 3000, 700)]

@@ -10,6 +10,9 @@ from linear_cross_entropy_vocab_gb300 import abi, native_build
 TUNED = ((8.2872, -23.5959, 17.3004), (4.1071, -2.9478, 0.5448), (3.9487, -2.9089, 0.5518),
          (3.3184, -2.4885, 0.5100), (2.3007, -1.6690, 0.4188))
 TUNED8 = TUNED + ((1.8913, -1.2680, 0.3768), (1.875, -1.25, 0.375), (1.875, -1.25, 0.375))
+# another one, whose steps differ less
+STEPWISE = ((4.0848, -6.8946, 2.9270), (3.9505, -6.3029, 2.6377), (3.7418, -5.5913, 2.3037),
+            (2.8769, -3.1427, 1.2046), (2.8366, -3.0525, 1.2012))
 FAKE = 0x10000  # never dereferenced
 
 
@@ -52,7 +55,7 @@ def test_schedules_that_magnify_roundings_are_refused():
 def test_schedules_that_settle_are_taken():
     for triples in (((3.4445, -4.7750, 2.0315),) * 5, ((3.4445, -4.7750, 2.0315),) * 64,
                     ((1.5, -0.5, 0.0),) * 64, ((1.875, -1.25, 0.375),) * 64, ((1.0, 0.0, 0.0),) * 64,
-                    ((2.0, -1.5, 0.5),) * 6, TUNED[:1], TUNED[:2],
+                    ((2.0, -1.5, 0.5),) * 6, TUNED[:1], TUNED[:2], STEPWISE,
                     # the largest value at the top of each interval, 1 and 1.5 in turn
                     ((1.0, 0.5, 0.0), (0.3, 0.163, 0.0)) * 3):
         assert _call(triples)[0] == abi.FLCE_ERR_WORKSPACE, triples
