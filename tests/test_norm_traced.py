@@ -1,4 +1,5 @@
 """The norm's operators where tensors have no data: fake tensors, tracing, torch.compile."""
+import contextlib
 import os
 import subprocess
 import sys
@@ -7,6 +8,7 @@ import pytest
 import torch
 from torch._subclasses.fake_tensor import FakeTensorMode
 from torch.fx.experimental.proxy_tensor import make_fx
+from torch.utils._python_dispatch import TorchDispatchMode
 
 from linear_cross_entropy_vocab_gb300 import native_build, rms_norm, rms_norm_quantize
 
@@ -124,6 +126,39 @@ def test_compiled_as_the_first_call():
     done = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True,
                           timeout=600)
     assert done.returncode == 0, done.stderr[-3000:]
+
+
+class _Listener(TorchDispatchMode):
+    def __init__(self):
+        super().__init__()
+        self.seen = []
+
+    def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+        self.seen.append(str(func))
+        return func(*args, **(kwargs or {}))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("forward", [False, True])
+@pytest.mark.parametrize("backward", [False, True])
+def test_a_mode_that_listens_to_one_direction(forward, backward):
+    g = torch.Generator("cuda").manual_seed(2)
+    wide = torch.randn(6, 2, 70, generator=g, device="cuda")
+    dy = torch.randn(6, 70, generator=g, device="cuda")
+    for x in (wide[:, 0], wide[:, 1, ::2], wide.permute(1, 0, 2)[0]):
+        leaf = x.detach().requires_grad_()
+        w = torch.rand(x.shape[-1], generator=g, device="cuda").requires_grad_()
+        up = dy[:, :x.shape[-1]]
+        want = rms_norm(leaf, w)
+        want = [want, *torch.autograd.grad(want, (leaf, w), up)]
+        listener = _Listener()
+        with listener if forward else contextlib.nullcontext():
+            y = rms_norm(leaf, w)
+        with listener if backward else contextlib.nullcontext():
+            got = [y, *torch.autograd.grad(y, (leaf, w), up)]
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert ("flce.rms_norm_forward.default" in listener.seen) == forward
+        assert ("flce.rms_norm_backward.default" in listener.seen) == backward
 
 
 @pytest.mark.gpu
