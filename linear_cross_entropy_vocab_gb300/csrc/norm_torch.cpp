@@ -55,6 +55,36 @@ void* stream_of(const Tensor& t) {
 const void* pointer(const Tensor& t) { return t.defined() ? t.const_data_ptr() : nullptr; }
 void* writable(const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
 
+// Shapes, for calls of the operators themselves: the Python layer has checked its
+// own. The kernels go by x's shape (total's, backwards).
+void check_like(const char* name, const Tensor& t, const Tensor& x) {
+  TORCH_CHECK_VALUE(t.sym_sizes() == x.sym_sizes() && t.device() == x.device(), name,
+                    " must be of x's shape and on its device");
+}
+void check_inputs(const Tensor& x, const std::optional<Tensor>& weight,
+                  const std::optional<Tensor>& residual) {
+  TORCH_CHECK_VALUE(x.dim() >= 1 && x.sym_sizes().back() >= 1,
+                    "x must be (..., H) with H of at least 1");
+  if (weight)
+    TORCH_CHECK_VALUE(weight->dim() == 1 && weight->sym_sizes()[0] == x.sym_sizes().back() &&
+                          weight->device() == x.device(),
+                      "weight must be (H,) and on x's device");
+  if (residual) check_like("residual", *residual, x);
+}
+void check_gradients(const Tensor& grad_y, const std::optional<Tensor>& grad_sum,
+                     const Tensor& total, const std::optional<Tensor>& weight, const Tensor& rstd,
+                     bool need_weight) {
+  check_inputs(total, weight, grad_sum);
+  check_like("grad_y", grad_y, total);
+  TORCH_CHECK_VALUE(rstd.scalar_type() == at::kFloat && rstd.dim() == 1 && rstd.is_contiguous() &&
+                        rstd.sym_numel() * total.sym_sizes().back() == total.sym_numel() &&
+                        rstd.device() == total.device(),
+                    "rstd must have a float32 for each row");
+  TORCH_CHECK_VALUE(!grad_sum || grad_sum->scalar_type() == total.scalar_type(),
+                    "grad_sum must be of total's type");
+  TORCH_CHECK_VALUE(weight || !need_weight, "a gradient of no weight is asked for");
+}
+
 // t [..., H] as rows of contiguous elements at one pitch: as it is, where its
 // leading dimensions are steps of one (a slice of wider rows), or a copy.
 Tensor rows_of(const Tensor& t, int64_t& pitch) {
@@ -152,14 +182,16 @@ Gradients gradients(const Tensor& upstream, const Tensor& upstream_sum, const Te
 // and those gradients that are asked for, in the order of their flags.
 std::vector<Tensor> rms_norm_forward(const Tensor& x, const std::optional<Tensor>& weight,
                                      double eps, const std::optional<Tensor>& residual) {
+  check_inputs(x, weight, residual);
   const Inputs in = prepare(x, weight, eps, residual);
   const Tensor rstd = empty_rstd(in);
   auto [y, sum] = forward(in, rstd);
   if (residual) return {y, rstd, sum};
   return {y, rstd};
 }
-std::vector<Tensor> rms_norm_forward_meta(const Tensor& x, const std::optional<Tensor>&, double,
-                                          const std::optional<Tensor>& residual) {
+std::vector<Tensor> rms_norm_forward_meta(const Tensor& x, const std::optional<Tensor>& weight,
+                                          double, const std::optional<Tensor>& residual) {
+  check_inputs(x, weight, residual);
   const auto sizes = x.sym_sizes();
   const c10::SymInt n = x.sym_numel() / sizes.back();
   std::vector<Tensor> out{at::empty_symint(sizes, x.options()),
@@ -178,14 +210,17 @@ std::vector<Tensor> rms_norm_backward(const Tensor& grad_y, const std::optional<
                                       const Tensor& total, const std::optional<Tensor>& weight,
                                       const Tensor& rstd, double eps, bool need_x,
                                       bool need_residual, bool need_weight) {
+  check_gradients(grad_y, grad_sum, total, weight, rstd, need_weight);
   return defined(gradients(grad_y, grad_sum.value_or(Tensor()), total, weight.value_or(Tensor()),
                            rstd, eps, need_x, need_residual, need_weight));
 }
-std::vector<Tensor> rms_norm_backward_meta(const Tensor& grad_y, const std::optional<Tensor>&,
+std::vector<Tensor> rms_norm_backward_meta(const Tensor& grad_y,
+                                           const std::optional<Tensor>& grad_sum,
                                            const Tensor& total,
-                                           const std::optional<Tensor>& weight, const Tensor&,
-                                           double, bool need_x, bool need_residual,
-                                           bool need_weight) {
+                                           const std::optional<Tensor>& weight,
+                                           const Tensor& rstd, double, bool need_x,
+                                           bool need_residual, bool need_weight) {
+  check_gradients(grad_y, grad_sum, total, weight, rstd, need_weight);
   Gradients g;
   if (need_x) g.x = at::empty_symint(total.sym_sizes(), grad_y.options());
   if (need_residual) g.residual = at::empty_symint(total.sym_sizes(), total.options());
@@ -320,6 +355,7 @@ class RmsNorm : public torch::autograd::Function<RmsNorm> {
 
 std::vector<Tensor> rms_norm(const Tensor& x, const std::optional<Tensor>& weight, double eps,
                              const std::optional<Tensor>& residual, bool differentiable) {
+  check_inputs(x, weight, residual);
   if (differentiable) return RmsNorm::apply(x, weight, eps, residual);
   if (listened_to(x, weight, residual)) {
     const std::vector<Tensor> got = dispatch_forward(x, weight, eps, residual);
@@ -334,6 +370,7 @@ std::vector<Tensor> rms_norm(const Tensor& x, const std::optional<Tensor>& weigh
 
 std::vector<Tensor> rms_norm_quantize(const Tensor& x, const std::optional<Tensor>& weight,
                                       double eps, const std::optional<Tensor>& residual) {
+  check_inputs(x, weight, residual);
   const Inputs in = prepare(x, weight, eps, residual);
   const flce_norm_problem& p = in.problem;
   const c10::cuda::CUDAGuard guard(x.device());
@@ -355,8 +392,9 @@ std::vector<Tensor> rms_norm_quantize(const Tensor& x, const std::optional<Tenso
   if (residual) return {q, scale, sum};
   return {q, scale};
 }
-std::vector<Tensor> rms_norm_quantize_meta(const Tensor& x, const std::optional<Tensor>&, double,
-                                           const std::optional<Tensor>& residual) {
+std::vector<Tensor> rms_norm_quantize_meta(const Tensor& x, const std::optional<Tensor>& weight,
+                                           double, const std::optional<Tensor>& residual) {
+  check_inputs(x, weight, residual);
   const auto sizes = x.sym_sizes();
   std::vector<c10::SymInt> strides(sizes.size(), 1);
   c10::SymInt stride = (sizes.back() + 15) / 16 * 16;

@@ -72,7 +72,7 @@ struct Bounds {
 // became NaN). So schedules have to bear kMoved before every step, as those with
 // the usual safety factor of 1.01 do.
 constexpr double kMoved = 1.0 / 512;
-constexpr double kMost = 1.5;  // times a bound, by moved values; products of three of them stay below 4
+constexpr double kMost = 1.5;  // times a bound, by moved values: 1.5^3 stays below 4
 // Fills `b`. The step whose bounds do not hold, or -1; `moved` says whether
 // that is by moved values alone.
 int find_bounds(const flce_ortho_problem* p, Bounds* b, bool* moved) {
@@ -365,7 +365,8 @@ bool make_map(CUtensorMap* map, const void* base, int64_t inner, int64_t outer,
 constexpr CUtensorMapSwizzle kLoad = CU_TENSOR_MAP_SWIZZLE_128B;
 constexpr CUtensorMapSwizzle kStore = CU_TENSOR_MAP_SWIZZLE_64B;
 
-constexpr uint64_t kWaitNs = 4000000000ull;  // of a tile's products and less: 4 s
+// After which a wait gives up. The longest one is for some tiles' products.
+constexpr uint64_t kWaitNs = 4000000000ull;  // 4 s
 
 // `lost`: each product after the first waits for one count that never comes.
 flce_status orthogonalize(const flce_ortho_problem* p, const void* src, void* out,
@@ -526,7 +527,8 @@ flce_status orthogonalize(const flce_ortho_problem* p, const void* src, void* ou
             flce::kOrthoWarps;
   }
   r.items = static_cast<int32_t>(items);
-  if (need > (lost ? 1 << 30 : 0x7fffffff) || items > 0x7fff0000) return fail(FLCE_ERR_UNSUPPORTED, "too many tiles and steps to count");
+  if (need > (lost ? 1 << 30 : 0x7fffffff) || items > 0x7fff0000)
+    return fail(FLCE_ERR_UNSUPPORTED, "too many tiles and steps to count");
   cudaError_t e = flce::launch_ortho_norm(c, p->dtype, s);
   if (e != cudaSuccess) return cuda_fail(e, "matrix norm kernel");
   e = flce::launch_ortho_copy(c, p->dtype, s);

@@ -47,6 +47,47 @@ def test_fake_tensors(shape):
             assert len(s) == (r is not None)
 
 
+def _refusals(make):
+    """Calls of the operators themselves whose shapes do not fit: nothing may be launched."""
+    x, w, r = make(4, 40), make(40), make(4, 40)
+    rstd = make(4)
+    ops = torch.ops.flce
+    for bad_w, bad_r in ((make(39), r), (make(1, 40), r), (w, make(40)), (w, make(3, 40)),
+                         (w, make(4, 1))):
+        for call in (ops.rms_norm_forward, ops.rms_norm_quantize,
+                     lambda *a: ops.rms_norm(*a, False)):
+            with pytest.raises(ValueError, match="weight must|residual must"):
+                call(x, bad_w, 1e-6, bad_r)
+    for call in (ops.rms_norm_forward, ops.rms_norm_quantize):
+        with pytest.raises(ValueError, match="H of at least 1"):
+            call(make(4, 0), None, 1e-6, None)
+    good = dict(grad_y=x, grad_sum=r, total=x, weight=w, rstd=rstd, eps=1e-6, need_x=True,
+                need_residual=False, need_weight=True)
+    for bad in (dict(grad_y=make(4, 39)), dict(grad_sum=make(2, 40)), dict(weight=make(41)),
+                dict(rstd=make(3)), dict(rstd=make(4, 1)), dict(rstd=make(8)[::2]),
+                dict(rstd=make(4).half()), dict(total=make(5, 40)), dict(weight=None),
+                dict(grad_sum=r.half())):
+        with pytest.raises(ValueError):
+            ops.rms_norm_backward(**{**good, **bad})
+
+
+def test_refusals_of_the_operators():
+    with FakeTensorMode():
+        rms_norm(torch.empty(2, 8, device="cuda"))  # loads the library
+        _refusals(lambda *shape: torch.empty(shape, device="cuda"))
+
+
+@pytest.mark.gpu
+def test_refusals_of_the_operators_on_a_gpu():
+    rms_norm(torch.ones(1, 8, device="cuda"))
+    _refusals(lambda *shape: torch.ones(shape, device="cuda"))
+    x = torch.ones(4, 40, device="cuda")
+    with pytest.raises(ValueError, match="device"):
+        torch.ops.flce.rms_norm_forward(x, torch.ones(40), 1e-6, None)
+    with pytest.raises(ValueError, match="each row"):
+        torch.ops.flce.rms_norm_backward(x, None, x, None, torch.ones(4), 1e-6, True, False, False)
+
+
 @pytest.mark.gpu  # autograd's threads ask for the device
 @pytest.mark.parametrize("shape", SHAPES)
 def test_gradients_of_fake_tensors(shape):
