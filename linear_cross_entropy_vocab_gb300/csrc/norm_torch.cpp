@@ -422,6 +422,13 @@ TORCH_LIBRARY_IMPL(flce, CUDA, m) {
   m.impl("rms_norm_backward", &rms_norm_backward);
   m.impl("rms_norm_quantize", &rms_norm_quantize);
 }
+// None of these has a formula of its own: autograd is passed over, which its
+// fallback would do in some microseconds.
+TORCH_LIBRARY_IMPL(flce, Autograd, m) {
+  m.impl("rms_norm_forward", torch::CppFunction::makeFallthrough());
+  m.impl("rms_norm_backward", torch::CppFunction::makeFallthrough());
+  m.impl("rms_norm_quantize", torch::CppFunction::makeFallthrough());
+}
 TORCH_LIBRARY_IMPL(flce, Meta, m) {
   m.impl("rms_norm_forward", &rms_norm_forward_meta);
   m.impl("rms_norm_backward", &rms_norm_backward_meta);
