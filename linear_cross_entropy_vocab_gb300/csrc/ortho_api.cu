@@ -68,9 +68,9 @@ struct Bounds {
 // elsewhere than for this value. The steps that follow must not make much of it.
 // Above the largest value that a schedule is made for, its polynomials may rise
 // twelve times as fast as the value itself, and five such steps turn 2^-11 into
-// anything (noise of 12 x 20 values was off by up to 93 %, a constant matrix
-// became NaN). So schedules have to bear kMoved before every step, as those with
-// the usual safety factor of 1.01 do.
+// anything (64-bit arithmetic with every operand rounded to halves: noise of 12 x
+// 20 values off by up to 93 %, a constant matrix NaN). So schedules have to bear
+// kMoved before every step, as those with the usual safety factor of 1.01 do.
 constexpr double kMoved = 1.0 / 512;
 constexpr double kMost = 1.5;  // times a bound, by moved values: 1.5^3 stays below 4
 // Fills `b`. The step whose bounds do not hold, or -1; `moved` says whether
